@@ -10,7 +10,11 @@
  * the tree acceptance without a workspace, and sv_ngram_draft proposes prompt-lookup
  * drafts on the device; sv_lm_head is the LM-head projection on the tensor cores, and
  * sv_accept_chain_lmhead / sv_accept_tree_lmhead fuse it with the acceptance (the target
- * rows' statistics come from the projection's epilogue).
+ * rows' statistics come from the projection's epilogue).  Around the cache:
+ * sv_block_tables extends a paged cache's block tables and makes the slot map of the new
+ * tokens, sv_qk_norm_rope / sv_tree_qk_norm_rope turn a projection's rows into the rotated
+ * Q, K and V that the cache and the attention take, and sv_window_attention is the tree
+ * attention of layers with a sliding window and sinks.
  *
  * Conventions shared by every entry point
  *  - Every tensor argument is caller-owned DEVICE memory, dense row-major in the layout
@@ -153,6 +157,98 @@ int sv_tree_attention_path(sv_dtype dt, int N, int Hq, int Hkv, int D, int block
  * prefix the cache can hold (Lmax, or max_blocks*block_size when paged). */
 size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
                                         int max_prefix);
+
+/* Tree attention with a sliding window and sinks, for models whose layers keep only the last
+ * `window` positions and the first few tokens in view.  Node n of sequence b stands at
+ * position P = prefix_len[b] + depth(n).  Its keys are
+ *   the prefix positions p with P - p < window or p < sinks, and
+ *   the tree nodes j on its root path (n itself among them) with depth(n) - depth(j) < window
+ *   or prefix_len[b] + depth(j) < sinks,
+ * so no row is ever empty.  out = softmax(scale * q . K^T) V over those keys; with
+ * window > prefix_len[b] + depth(n) that is sv_tree_attention.  N = 1 is the decoding of one
+ * token per sequence.  window >= 1 (else SV_ERR_INVALID_ARG), 0 <= sinks <= SV_MAX_SINKS.
+ * Cache positions that no row of a sequence sees are not read into its result, and their
+ * blocks need not exist: pages that lie wholly before the window of the root (position
+ * prefix_len[b] - window + 1) and after the sinks may have any entry in the block table, so
+ * they can be freed and used again.  Every other argument, the layouts, the kernels' shapes
+ * and the workspace's rules (zero-filled before its first use; stream-ordered sharing, also
+ * with sv_tree_attention) as sv_tree_attention; a paged block_size that is not a multiple of
+ * 16 and B or Hkv above 65535 are SV_ERR_UNSUPPORTED.
+ * A NaN or infinity in the V row of a key that some rows of a sequence see can also reach
+ * its other rows of the same KV head (0 * NaN).
+ * Workspace: sv_window_attention_workspace_size() bytes (max_prefix as there). */
+#define SV_MAX_SINKS 64
+sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                              const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                              const int32_t *parent, int parent_stride, float scale, int window,
+                              int sinks, void *out, void *workspace, size_t workspace_bytes,
+                              void *stream);
+size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
+                                          int max_prefix, int window);
+
+/* --------------------------------------------------------- into the KV cache */
+
+/* Block tables and slot maps from request lengths, on the device.  Request b has length[b]
+ * tokens in a paged cache and is about to add new_tokens[b].  The call appends the pages it
+ * lacks to its row of block_table and says where every new token goes:
+ *   pages held:   ceil(length[b] / block_size)   (entries that are there are only read)
+ *   pages added:  ceil((length[b] + new_tokens[b]) / block_size) - pages held, the next ids of
+ *                 free_blocks from free_head[0] on, in request order
+ *   new token i of request b is entry t = token_start[b] + i of the flat maps:
+ *                 positions[t] = length[b] + i
+ *                 slots[t] = block_table[b][positions[t] / block_size] * block_size
+ *                            + positions[t] % block_size    (a row of the pool)
+ * length, new_tokens [B]; free_blocks [num_free]; free_head [1], or NULL for 0; block_table
+ * [B,max_blocks], read and extended (entries past the pages a request needs are left as they
+ * are); all int32 in device memory.  Outputs: out_token_start [B+1] (exclusive sums of
+ * new_tokens, the last one the total), out_slots and out_positions [T] (entries past the
+ * total are -1; 16-byte aligned; NULL when T = 0), out_free_head [1] = free_head + pages
+ * added (may pass num_free: the shortage is the difference).  out_free_head must not be
+ * free_head itself.  length is not advanced: calling again with the same inputs gives the
+ * same tables.  B <= SV_MAX_TABLE_BATCH, num_blocks * block_size < 2^31.
+ * Device status: SV_DEV_BAD_BLOCK when free ids run out or an id (held or free) lies outside
+ * the pool (table entry and slots -1), SV_DEV_BAD_PREFIX for a length or total outside
+ * [0, max_blocks * block_size], a negative new_tokens (taken as 0) or more new tokens than T
+ * (their pages are given out, their slots not written). */
+#define SV_MAX_TABLE_BATCH 8192
+sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_tokens, int block_size,
+                          int max_blocks, int num_blocks, const int32_t *free_blocks, int num_free,
+                          const int32_t *free_head, int32_t *block_table, int T,
+                          int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
+                          int32_t *out_free_head, void *stream);
+
+/* Per-head norms of queries and keys with the position rotation, in one pass.  Row t of qkv
+ * (rows ld elements apart, ld >= (Hq + 2 Hkv) * D) is a token's projection: Hq query heads,
+ * Hkv key heads, Hkv value heads of D elements.  Each query and key head x becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (q_weight or k_weight, float32 [D]),
+ * then its first `rot` elements turn by the token's position: with i < rot/2 and angle
+ * position * inv_freq[i], the pair (y_i, y_{i + rot/2}), or with interleaved != 0 the pair
+ * (y_{2i}, y_{2i+1}), becomes (a cos - b sin, a sin + b cos).  Values are copied.  fp32
+ * between the load and the one rounding at the store; angles are exact to the accuracy of
+ * inv_freq (float64 [rot/2], finite) at any position.
+ * positions [T] int32: a token with a negative position is padding, of which nothing is
+ * read or written.  Outputs: q_out [T,Hq,D]; k_out and v_out [num_rows,Hkv,D], token t in row
+ * slots[t] (int32 [T], as sv_block_tables makes them: a paged pool seen as num_blocks *
+ * block_size rows; a negative slot writes no K/V; slots of one call must differ), or with
+ * slots NULL in row t (num_rows >= T).  A slot >= num_rows is skipped and sets
+ * SV_DEV_BAD_BLOCK.  Outputs must not overlap qkv (SV_ERR_INVALID_ARG).
+ * dt: SV_BF16 or SV_F32.  D in {64, 128}; rot a multiple of 16 up to D; qkv, the outputs and
+ * the rows of qkv 16-byte aligned.  No workspace. */
+sv_status sv_qk_norm_rope(sv_dtype dt, int T, int Hq, int Hkv, int D, int rot, int interleaved,
+                          const void *qkv, int64_t ld, const float *q_weight, const float *k_weight,
+                          float eps, const double *inv_freq, const int32_t *positions,
+                          const int32_t *slots, int64_t num_rows, void *q_out, void *k_out,
+                          void *v_out, void *stream);
+
+/* The same for the rows of a candidate tree: qkv [B*N] rows (ld apart), row b*N + n node n of
+ * sequence b at position prefix_len[b] + depth(n) (prefix_len [B] int32, a negative one taken
+ * as 0 with SV_DEV_BAD_PREFIX).  parent, parent_stride as under "Trees" above.  Outputs: the
+ * q [B,N,Hq,D], k_tree and v_tree [B,N,Hkv,D] of the attention calls. */
+sv_status sv_tree_qk_norm_rope(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, int rot,
+                               int interleaved, const void *qkv, int64_t ld, const float *q_weight,
+                               const float *k_weight, float eps, const double *inv_freq,
+                               const int32_t *prefix_len, const int32_t *parent, int parent_stride,
+                               void *q_out, void *k_out, void *v_out, void *stream);
 
 /* ----------------------------------------------------------------- acceptance */
 

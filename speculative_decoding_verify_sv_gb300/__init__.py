@@ -8,6 +8,7 @@ kernels; there is no CPU fallback: if the library is missing the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -22,7 +23,8 @@ __all__ = [
     "sv_accept_workspace_size", "sv_accept_tree_noalloc", "sv_commit_kv", "sv_accept_tree_commit",
     "sv_accept_chain_commit", "sv_accept_tree_recursive", "sv_ngram_draft", "sv_tree_prepare", "sv_read_device_status",
     "sv_lm_head", "sv_accept_lmhead_workspace_size", "sv_accept_chain_lmhead", "sv_accept_tree_lmhead",
-    "sv_accept_typical", "sv_set_wait_limit_ns", "sv_get_wait_limit_ns", "sv_inject_launch_failures",
+    "sv_window_attention", "sv_window_attention_workspace_size", "sv_block_tables", "sv_qk_norm_rope",
+    "sv_tree_qk_norm_rope", "sv_accept_typical", "sv_set_wait_limit_ns", "sv_get_wait_limit_ns", "sv_inject_launch_failures",
     "sv_version", "sv_kernel_launches", "GREEDY", "EXACT", "Q_PROBS_F32", "Q_LOGITS", "Q_DRAFT_ONEHOT", "SV_MAX_TREE_NODES",
 ]
 
@@ -34,6 +36,7 @@ SV_F32, SV_BF16 = 0, 1
 GREEDY, EXACT = 0, 1
 Q_PROBS_F32, Q_LOGITS, Q_DRAFT_ONEHOT = 0, 1, 2  # q as probabilities, draft logits, one-hot drafts
 SV_MAX_TREE_NODES = 64
+SV_MAX_SINKS, SV_MAX_TABLE_BATCH = 64, 8192
 SV_DEV_BAD_TOKEN, SV_DEV_BAD_BLOCK, SV_DEV_BAD_PREFIX, SV_DEV_ZERO_DRAFT_PROB = 1, 2, 4, 8
 SV_DEV_TIMEOUT, SV_DEV_LAYOUT, SV_DEV_BAD_TREE = 0x10, 0x20, 0x40
 
@@ -73,6 +76,7 @@ def load_library():
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(_LIB_PATH)
         P, I, F, U64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64, ctypes.c_size_t
+        I64 = ctypes.c_int64
         lib.sv_tree_attention.argtypes = [I, I, I, I, I, I, P, P, P, _KVCacheC, P, I, F, P, P, SZ, P]
         lib.sv_tree_attention_workspace_size.argtypes = [I, I, I, I, I, I, I]
         lib.sv_tree_attention_path.argtypes = [I, I, I, I, I, I]
@@ -109,13 +113,20 @@ def load_library():
         lib.sv_tree_prepare.argtypes = [I, P, P, P]
         lib.sv_read_device_status.argtypes = [P, P]
         lib.sv_ngram_draft.argtypes = [I, I, P, P, I, I, I, P, P, P]
+        lib.sv_window_attention.argtypes = [I, I, I, I, I, I, P, P, P, _KVCacheC, P, I, F, I, I, P, P, SZ, P]
+        lib.sv_window_attention_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
+        lib.sv_window_attention_workspace_size.restype = SZ
+        lib.sv_block_tables.argtypes = [I, P, P, I, I, I, P, I, P, P, I, P, P, P, P, P]
+        lib.sv_qk_norm_rope.argtypes = [I, I, I, I, I, I, I, P, I64, P, P, F, P, P, P, I64, P, P, P, P]
+        lib.sv_tree_qk_norm_rope.argtypes = [I, I, I, I, I, I, I, I, P, I64, P, P, F, P, P, P, I, P, P, P, P]
         lib.sv_last_error.restype = ctypes.c_char_p
         lib.sv_version.restype = ctypes.c_char_p
         lib.sv_kernel_launches.restype = ctypes.c_uint64
         for fn in ("sv_tree_attention", "sv_accept_chain", "sv_accept_tree", "sv_commit_kv",
                    "sv_tree_prepare", "sv_read_device_status", "sv_accept_tree_noalloc",
                    "sv_accept_tree_commit", "sv_accept_chain_commit", "sv_ngram_draft",
-                   "sv_accept_tree_recursive"):
+                   "sv_accept_tree_recursive", "sv_window_attention", "sv_block_tables",
+                   "sv_qk_norm_rope", "sv_tree_qk_norm_rope"):
             getattr(lib, fn).restype = ctypes.c_int32
         _lib = lib
         return lib
@@ -226,6 +237,43 @@ class KVCache:
         return self.block_table.shape[1] * int(self.block_size)
 
 
+def _int32(x, name: str) -> int:
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} = {x} is not a 32-bit number")
+    return x
+
+
+def _cache_shapes(cache: KVCache, q, B, Hkv, D):
+    """The cache belongs to these sequences and heads: contiguous [B,Lmax,Hkv,D], or pages of
+    block_size rows with a table row per sequence."""
+    if cache.k.dtype != q.dtype:
+        raise TypeError("cache dtype differs from q")
+    if cache.k.dim() != 4 or tuple(cache.k.shape[2:]) != (Hkv, D):
+        raise ValueError(f"cache.k has shape {tuple(cache.k.shape)}, expected [..., ..., {Hkv}, {D}]")
+    if cache.prefix_len.shape != (B,):
+        raise ValueError(f"cache.prefix_len must be [B={B}]")
+    if cache.block_table is None:
+        if cache.k.shape[0] != B:
+            raise ValueError(f"cache.k has {cache.k.shape[0]} sequences, q has {B}")
+    elif cache.block_table.dim() != 2 or cache.block_table.shape[0] != B:
+        raise ValueError(f"cache.block_table must be [B={B}, max_blocks]")
+    elif cache.k.shape[1] != int(cache.block_size):
+        raise ValueError(f"cache.k has blocks of {cache.k.shape[1]} rows, block_size is {cache.block_size}")
+
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on_device(*tensors):
+    """The context of a call on these tensors' device, which must be one and the same."""
+    dev = tensors[0].device
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one call works on one device")
+    return _NO_SWITCH if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
 def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], zero: bool = False):
     if nbytes == 0:
         return workspace, 0
@@ -272,6 +320,167 @@ def sv_tree_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, out=None
                                  cs, par, pstride, float(scale), _ptr(out), _ptr(workspace), ws_bytes,
                                  _stream(stream)))
     return out
+
+
+def sv_window_attention_workspace_size(dtype, B, N, Hq, Hkv, D, max_prefix, window) -> int:
+    dt = SV_BF16 if dtype == torch.bfloat16 else SV_F32
+    return int(load_library().sv_window_attention_workspace_size(dt, B, N, Hq, Hkv, D, max_prefix, window))
+
+
+def sv_window_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, window, sinks=0, out=None,
+                        workspace=None, stream=None) -> torch.Tensor:
+    """Tree attention over the last ``window`` positions and the first ``sinks`` ones; arguments
+    and result as sv_tree_attention.  A node at position P = prefix_len + depth sees a prefix
+    position (or a node of its root path) p iff P - p < window or p < sinks."""
+    lib = load_library()
+    _dev(q, "q", (torch.bfloat16, torch.float32))
+    B, N, Hq, D = q.shape
+    Hkv = k_tree.shape[2]
+    _dev(k_tree, "k_tree", q.dtype, (B, N, Hkv, D))
+    _dev(v_tree, "v_tree", q.dtype, (B, N, Hkv, D))
+    _cache_shapes(cache, q, B, Hkv, D)
+    if out is None:
+        out = torch.empty_like(q)
+    _dev(out, "out", q.dtype, q.shape)
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
+    cs = cache.c_struct()
+    ws_need = int(lib.sv_window_attention_workspace_size(_dt(q), B, N, Hq, Hkv, D, cache.max_prefix, window))
+    # a workspace passed in must have been zero-filled before its first use
+    workspace, ws_bytes = _workspace(ws_need, q.device, workspace, zero=True)
+    par, pstride, _ = _tree_arg(parent, B, N)
+    with _on_device(q, k_tree, v_tree, cache.k, cache.v, cache.prefix_len, cache.block_table, out, workspace,
+                    parent):
+        _check(lib.sv_window_attention(_dt(q), B, N, Hq, Hkv, D, _ptr(q), _ptr(k_tree), _ptr(v_tree), cs, par,
+                                       pstride, float(scale), window, sinks, _ptr(out), _ptr(workspace),
+                                       ws_bytes, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------- into the KV cache
+
+def sv_block_tables(length, new_tokens, block_table, free_blocks, block_size, num_blocks, num_slots,
+                    free_head=None, outs=None, stream=None) -> dict:
+    """Extend a paged cache's block tables for ``new_tokens`` [B] more tokens per request
+    (``length`` [B] are in it) with pages of ``free_blocks`` from ``free_head`` [1] on, and make
+    the new tokens' slot map.  block_table [B,max_blocks] is written in place.  Returns a dict of
+    int32 device tensors: token_start [B+1], slots and positions [num_slots] (-1 past the
+    total), free_head [1] (the advanced head, never the one passed in)."""
+    lib = load_library()
+    _dev(length, "length", torch.int32)
+    if length.dim() != 1:
+        raise ValueError("length must be [B]")
+    B = length.shape[0]
+    _dev(new_tokens, "new_tokens", torch.int32, (B,))
+    _dev(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [B={B}, max_blocks]")
+    _dev(free_blocks, "free_blocks", torch.int32)
+    if free_head is not None:
+        _dev(free_head, "free_head", torch.int32, (1,))
+    T = _int32(num_slots, "num_slots")
+    if T < 0:
+        raise ValueError(f"num_slots = {T}")
+    outs = {} if outs is None else outs
+    for name, shape in (("token_start", (B + 1,)), ("slots", (T,)), ("positions", (T,)), ("free_head", (1,))):
+        if name not in outs:
+            outs[name] = torch.empty(shape, dtype=torch.int32, device=length.device)
+        _dev(outs[name], name, torch.int32, shape)
+    with _on_device(length, new_tokens, block_table, free_blocks, free_head, *outs.values()):
+        _check(lib.sv_block_tables(B, _ptr(length), _ptr(new_tokens), _int32(block_size, "block_size"),
+                                   block_table.shape[1], _int32(num_blocks, "num_blocks"), _ptr(free_blocks),
+                                   free_blocks.numel(), _ptr(free_head), _ptr(block_table), T,
+                                   _ptr(outs["token_start"]), _ptr(outs["slots"]), _ptr(outs["positions"]),
+                                   _ptr(outs["free_head"]), _stream(stream)))
+    return outs
+
+
+def _rope_args(qkv, lead, Hq, Hkv, q_weight, k_weight, inv_freq):
+    """(D, rot, row stride) of a projection qkv [*lead, (Hq + 2 Hkv) * D] with evenly spaced rows."""
+    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
+        raise TypeError("qkv must be a CUDA tensor")
+    if qkv.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"qkv has dtype {qkv.dtype}, expected bfloat16 or float32")
+    _dev(q_weight, "q_weight", torch.float32)
+    D = q_weight.numel()
+    _dev(q_weight, "q_weight", torch.float32, (D,))
+    _dev(k_weight, "k_weight", torch.float32, (D,))
+    _dev(inv_freq, "inv_freq", torch.float64)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot/2]")
+    width = (Hq + 2 * Hkv) * D
+    if qkv.dim() != lead + 1 or qkv.shape[-1] != width:
+        raise ValueError(f"qkv has shape {tuple(qkv.shape)}, expected {lead} leading dimensions and rows of {width}")
+    if qkv.numel() == 0:
+        return D, 2 * inv_freq.numel(), width
+    rows, ld = 1, width
+    for n, step in zip(reversed(qkv.shape[:-1]), reversed(qkv.stride()[:-1])):
+        if n == 1:
+            continue
+        if rows == 1:
+            ld = step
+        elif step != rows * ld:
+            raise ValueError("the rows of qkv must be evenly spaced")
+        rows *= n
+    if qkv.stride(-1) != 1 or ld < width:
+        raise ValueError("the rows of qkv must be contiguous and apart")
+    return D, 2 * inv_freq.numel(), ld
+
+
+def sv_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, positions, eps=1e-6, interleaved=False,
+                    slots=None, q_out=None, k_out=None, v_out=None, stream=None):
+    """Per-head norms of queries and keys and their rotation: qkv [T,(Hq+2Hkv)*D] (rows may be
+    slices of a wider projection), weights float32 [D], inv_freq float64 [rot/2], positions [T]
+    int32 (negative: padding).  Returns (q [T,Hq,D], k, v): k and v are k_out and v_out
+    [..., Hkv, D] (a KV cache, paged or not), token t in row slots[t]; without slots row t."""
+    lib = load_library()
+    D, rot, ld = _rope_args(qkv, 1, Hq, Hkv, q_weight, k_weight, inv_freq)
+    T = qkv.shape[0]
+    _dev(positions, "positions", torch.int32, (T,))
+    if slots is not None:
+        _dev(slots, "slots", torch.int32, (T,))
+        if k_out is None or v_out is None:
+            raise ValueError("slots need k_out and v_out")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=qkv.dtype, device=qkv.device)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, D), dtype=qkv.dtype, device=qkv.device)
+    if v_out is None:
+        v_out = torch.empty((T, Hkv, D), dtype=qkv.dtype, device=qkv.device)
+    _dev(q_out, "q_out", qkv.dtype, (T, Hq, D))
+    _dev(k_out, "k_out", qkv.dtype)
+    _dev(v_out, "v_out", qkv.dtype, k_out.shape)
+    if k_out.dim() < 3 or tuple(k_out.shape[-2:]) != (Hkv, D):
+        raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected [..., {Hkv}, {D}]")
+    with _on_device(qkv, q_weight, k_weight, inv_freq, positions, slots, q_out, k_out, v_out):
+        _check(lib.sv_qk_norm_rope(_dt(qkv), T, Hq, Hkv, D, rot, int(bool(interleaved)), _ptr(qkv), ld,
+                                   _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), _ptr(positions),
+                                   _ptr(slots), k_out.numel() // (Hkv * D), _ptr(q_out), _ptr(k_out), _ptr(v_out),
+                                   _stream(stream)))
+    return q_out, k_out, v_out
+
+
+def sv_tree_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, prefix_len, parent, eps=1e-6,
+                         interleaved=False, outs=None, stream=None):
+    """sv_qk_norm_rope for the rows of a candidate tree: qkv [B,N,(Hq+2Hkv)*D], node n of
+    sequence b at position prefix_len[b] + depth(n).  Returns (q, k_tree, v_tree), the inputs of
+    sv_tree_attention and sv_window_attention (``outs``: those three, to write into)."""
+    lib = load_library()
+    D, rot, ld = _rope_args(qkv, 2, Hq, Hkv, q_weight, k_weight, inv_freq)
+    B, N = qkv.shape[:2]
+    _dev(prefix_len, "prefix_len", torch.int32, (B,))
+    if outs is None:
+        outs = tuple(torch.empty((B, N, h, D), dtype=qkv.dtype, device=qkv.device) for h in (Hq, Hkv, Hkv))
+    q, k, v = outs
+    _dev(q, "q", qkv.dtype, (B, N, Hq, D))
+    _dev(k, "k_tree", qkv.dtype, (B, N, Hkv, D))
+    _dev(v, "v_tree", qkv.dtype, (B, N, Hkv, D))
+    par, pstride, _ = _tree_arg(parent, B, N)
+    with _on_device(qkv, q_weight, k_weight, inv_freq, prefix_len, q, k, v, parent):
+        _check(lib.sv_tree_qk_norm_rope(_dt(qkv), B, N, Hq, Hkv, D, rot, int(bool(interleaved)), _ptr(qkv), ld,
+                                        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq),
+                                        _ptr(prefix_len), par, pstride, _ptr(q), _ptr(k), _ptr(v),
+                                        _stream(stream)))
+    return q, k, v
 
 
 # ------------------------------------------------------------------ acceptance

@@ -11,6 +11,12 @@
 // cp.async pipeline and both products run on bf16 tensor cores with fp32 accumulators
 // and an online softmax.  Splits of the prefix merge in a second kernel by
 // log-sum-exp weights.
+//
+// The WIN instances add a sliding window with sinks: node n at position P = L_b + depth(n)
+// sees a prefix position p (or a tree node at position p on its root path) iff P - p < window
+// or p < sinks.  The prefix tiles then cover [first, L_b), first = L_b - window + 1 being the
+// earliest position in any row's window, and the sinks before `first` are one more tile
+// beside the tree's (no position is read twice, and none outside these ranges at all).
 #include <atomic>
 #include <cfloat>
 
@@ -49,7 +55,7 @@ __device__ __forceinline__ int clamp_prefix(const AttnParams &p, int b) {
   return L;
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) {
   constexpr int LDS = D + 8;  // padded row stride (elements): conflict-free ldmatrix
   constexpr int CH = D / 8;   // 16-byte chunks per row
@@ -71,10 +77,13 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
   const int kvh = blockIdx.y, b = blockIdx.z;
 
   const int L = clamp_prefix(p, b);
-  const int k_begin = split * p.chunk;
+  const int first = WIN ? window_first(L, p.window) : 0;
+  const int n_sinks = WIN ? min(p.sinks, first) : 0;  // sinks before the window's tiles
+  const int k_begin = first + split * p.chunk;
   const int k_end = min(L, k_begin + p.chunk);
   const int n_pref = k_end > k_begin ? (k_end - k_begin + kTileKeys - 1) / kTileKeys : 0;
-  const int has_tree = split == 0 ? 1 : 0;
+  // split 0 starts with the tree's tile and, when there are any, the sinks' tile
+  const int has_tree = split == 0 ? (n_sinks > 0 ? 2 : 1) : 0;
   const int n_tiles = n_pref + has_tree;
 
   // sequence b's tree (shared, or its own row): ancestor masks of its nodes
@@ -101,7 +110,9 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
 
   auto load_tile = [&](int t, int stage) {
     const bool tree = has_tree && t == 0;
-    const int base = k_begin + (t - has_tree) * kTileKeys;
+    const bool sink = WIN && has_tree == 2 && t == 1;
+    const int base = sink ? 0 : k_begin + (t - has_tree) * kTileKeys;
+    const int end = sink ? n_sinks : k_end;
     bf16 *dk = sK + stage * kTileKeys * LDS;
     bf16 *dv = sV + stage * kTileKeys * LDS;
     for (int c = tid; c < kTileKeys * CH; c += kThreads) {
@@ -115,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
         sv = gvt + off;
       } else {
         const int pos = base + r;
-        valid = pos < k_end;
+        valid = pos < end;
         long long row = 0;
         if (valid) {
           row = cache_row(p, b, pos);
@@ -155,6 +166,15 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
     const int R = mt * kRowsPerCta + r_lo + 8 * i;
     anc[i] = R < p.M ? sAnc[R / p.G] : 0ull;
   }
+  // the first prefix position in each row's window, and the window's cut of its root path
+  int lo[2] = {0, 0};
+  if constexpr (WIN) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lo[i] = window_first(L + max(__popcll(anc[i]) - 1, 0), p.window);
+      anc[i] = window_ancestors(anc[i], L, p.window, p.sinks);
+    }
+  }
 
   float o[D / 8][4];
 #pragma unroll
@@ -173,7 +193,9 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
     const bf16 *tk = sK + stage * kTileKeys * LDS;
     const bf16 *tv = sV + stage * kTileKeys * LDS;
     const bool tree = has_tree && t == 0;
-    const int base = k_begin + (t - has_tree) * kTileKeys;
+    const bool sink = WIN && has_tree == 2 && t == 1;
+    const int base = sink ? 0 : k_begin + (t - has_tree) * kTileKeys;
+    const int end = sink ? n_sinks : k_end;
 
     float sc[kTileKeys / 8][4];
 #pragma unroll
@@ -199,7 +221,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int kk = nt * 8 + 2 * (lane & 3) + e;
-          const bool ok = tree ? ((anc[i] >> kk) & 1ull) != 0 : (base + kk < k_end);
+          bool ok = tree ? ((anc[i] >> kk) & 1ull) != 0 : (base + kk < end);
+          if (WIN && !tree) ok = ok && (base + kk >= lo[i] || base + kk < p.sinks);
           const float x = ok ? sc[nt][2 * i + e] * p.scale_log2 : -INFINITY;
           sc[nt][2 * i + e] = x;
           mx = fmaxf(mx, x);
@@ -321,7 +344,7 @@ __host__ __device__ constexpr int f32_stages() { return D == 64 ? 8 : 6; }
 template <int D>
 __host__ __device__ constexpr size_t f32_stage_floats() { return (size_t)kF32Keys * (D + 4) + (size_t)kF32Keys * D; }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) {
   constexpr int KC = kF32Keys, ST = f32_stages<D>();
   constexpr int KS = D + 4;                 // K row stride in shared memory (floats)
@@ -358,8 +381,14 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   const bool live = R < p.M;
   const int n = live ? R / p.G : 0, hq = kvh * p.G + (live ? R % p.G : 0);
 
-  // chunk c: prefix positions [32c, 32c + 32) for c < nP, then tree nodes from 32 (c - nP)
-  const int nP = (L + KC - 1) / KC, nT = (p.N + KC - 1) / KC, nC = nP + nT;
+  // chunk c: prefix positions [32c, 32c + 32) for c < nP, then tree nodes from 32 (c - nP).
+  // With a window the prefix chunks start at `first`, after nS chunks of the sinks before it.
+  const int first = WIN ? window_first(L, p.window) : 0;
+  const int n_sinks = WIN ? min(p.sinks, first) : 0, nS = (n_sinks + KC - 1) / KC;
+  const int nP = nS + (L - first + KC - 1) / KC, nT = (p.N + KC - 1) / KC, nC = nP + nT;
+  // the prefix position of key `key` of chunk c < nP, and where the chunk's range ends
+  auto chunk_pos = [&](int c, int key) { return c < nS ? c * KC + key : first + (c - nS) * KC + key; };
+  auto chunk_end = [&](int c) { return c < nS ? n_sinks : L; };
   auto stage_k = [&](int st) { return f32_ring + (size_t)st * f32_stage_floats<D>(); };
   auto stage_v = [&](int st) { return f32_ring + (size_t)st * f32_stage_floats<D>() + KC * KS; };
   auto issue = [&](int c, int st) {
@@ -370,8 +399,8 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
       const float *srck = gkc, *srcv = gvc;  // any valid address when nothing is read
       bool ok = false;
       if (c < nP) {
-        const int pos = c * KC + key;
-        if (pos < L) {
+        const int pos = chunk_pos(c, key);
+        if (pos < chunk_end(c)) {
           const long long row = cache_row(p, b, pos);
           if (row >= 0) {
             const size_t off = ((size_t)row * p.Hkv + kvh) * D + 4 * d4;
@@ -406,7 +435,12 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   for (int i = lane; i < D; i += 32)
     sQ[warp][i] = live ? gq[(((size_t)b * p.N + n) * p.Hq + hq) * D + i] : 0.f;
   __syncthreads();  // sQ, sAnc
-  const uint64_t anc = sAnc[n];
+  uint64_t anc = sAnc[n];
+  int lo = 0;  // the first prefix position in this row's window
+  if constexpr (WIN) {
+    lo = window_first(L + max(__popcll(anc) - 1, 0), p.window);
+    anc = window_ancestors(anc, L, p.window, p.sinks);
+  }
   float m = -INFINITY, l = 0.f, o[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) o[i] = 0.f;
@@ -419,9 +453,10 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
       const float *sk = stage_k(st), *sv = stage_v(st);
       // lane j scores key j of the chunk
       const bool tree_chunk = c >= nP;
-      const int j = tree_chunk ? (c - nP) * KC + lane : c * KC + lane;
+      const int j = tree_chunk ? (c - nP) * KC + lane : chunk_pos(c, lane);
       bool vis = sValid[st][lane] != 0;
       if (tree_chunk) vis = vis && ((anc >> j) & 1ull);
+      else if (WIN) vis = vis && (j >= lo || j < p.sinks);
       const float4 *kr = reinterpret_cast<const float4 *>(sk + lane * KS);
       const float4 *qr = reinterpret_cast<const float4 *>(sQ[warp]);
       float dot = 0.f;
@@ -468,37 +503,37 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   for (int i = 0; i < PL; ++i) dst[lane + 32 * i] = o[i] * inv;
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_f32(const AttnParams &p, cudaStream_t s) {
   const size_t smem = (size_t)f32_stages<D>() * f32_stage_floats<D>() * sizeof(float);
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D>,
+    const cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D, WIN>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   dim3 grid((p.M + kThreads / 32 - 1) / (kThreads / 32), p.Hkv, p.B);
-  attn_f32_kernel<D><<<grid, kThreads, smem, s>>>(p);
+  attn_f32_kernel<D, WIN><<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_mma(const AttnParams &p, cudaStream_t s) {
   const size_t smem = attn_smem_bytes<D>();
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<D>,
+    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<D, WIN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   dim3 grid(p.m_tiles * p.splits, p.Hkv, p.B);
-  attn_mma_kernel<D><<<grid, kThreads, smem, s>>>(p);
+  attn_mma_kernel<D, WIN><<<grid, kThreads, smem, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   attn_combine_kernel<D><<<dim3(p.M, p.Hkv, p.B), D, 0, s>>>(p);
@@ -535,8 +570,12 @@ AttnPlan attn_plan(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, int max_pr
 }
 
 cudaError_t launch_attention(sv_dtype dt, const AttnParams &p, cudaStream_t s) {
-  if (dt == SV_F32) return p.D == 64 ? launch_f32<64>(p, s) : launch_f32<128>(p, s);
-  return p.D == 64 ? launch_mma<64>(p, s) : launch_mma<128>(p, s);
+  if (p.window > 0) {
+    if (dt == SV_F32) return p.D == 64 ? launch_f32<64, true>(p, s) : launch_f32<128, true>(p, s);
+    return p.D == 64 ? launch_mma<64, true>(p, s) : launch_mma<128, true>(p, s);
+  }
+  if (dt == SV_F32) return p.D == 64 ? launch_f32<64, false>(p, s) : launch_f32<128, false>(p, s);
+  return p.D == 64 ? launch_mma<64, false>(p, s) : launch_mma<128, false>(p, s);
 }
 
 }  // namespace sv

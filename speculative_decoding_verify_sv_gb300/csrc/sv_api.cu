@@ -42,6 +42,7 @@ sv_status cuda_fail(cudaError_t e, const char *what) {
 }
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxGridZ = 65535;  // largest y and z extents of a launch grid
 
 // The tensor-core attention kernel's limit on a wait for progress (sv_set_wait_limit_ns).
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;
@@ -234,11 +235,12 @@ int sv_tree_attention_path(sv_dtype dt, int N, int Hq, int Hkv, int D, int block
   return sv::tc_eligible(dt, N, Hq, Hkv, D, block_size) ? 1 : 0;
 }
 
-sv_status sv_tree_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
-                            const void *k_tree, const void *v_tree, sv_kv_cache cache,
-                            const int32_t *parent, int parent_stride, float scale, void *out,
-                            void *workspace, size_t workspace_bytes, void *stream) {
-  const CallRange range("sv_tree_attention");
+// Tree attention over the whole prefix (window = 0) or over a sliding window with sinks.
+static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                                const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                                const int32_t *parent, int parent_stride, float scale, int window,
+                                int sinks, void *out, void *workspace, size_t workspace_bytes,
+                                void *stream) {
   if (dt != SV_F32 && dt != SV_BF16) return fail(SV_ERR_UNSUPPORTED, "dtype %d not supported", (int)dt);
   if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
     return fail(SV_ERR_INVALID_ARG, "bad sizes B=%d Hq=%d Hkv=%d", B, Hq, Hkv);
@@ -254,8 +256,9 @@ sv_status sv_tree_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, c
   if (!std::isfinite(scale)) return fail(SV_ERR_INVALID_ARG, "scale is not finite");
   if (B == 0) return SV_OK;
   const int max_prefix = max_prefix_of(cache);
-  const sv::AttnPlan plan = sv::attn_plan(dt, B, N, Hq, Hkv, D, max_prefix, num_sms());
-  const bool use_tc = sv::tc_eligible(dt, N, Hq, Hkv, D, cache.block_table ? cache.block_size : 0);
+  const int span = window > 0 && window - 1 < max_prefix ? window - 1 : max_prefix;
+  const sv::AttnPlan plan = sv::attn_plan(dt, B, N, Hq, Hkv, D, span, num_sms());
+  const bool use_tc = window == 0 && sv::tc_eligible(dt, N, Hq, Hkv, D, cache.block_table ? cache.block_size : 0);
   const sv::TcPlan tplan = use_tc ? sv::tc_plan(B, N, Hq, Hkv, D, num_sms()) : sv::TcPlan{};
   const size_t ws_need = use_tc ? tplan.ws_bytes : plan.ws_bytes;
   if (ws_need > 0) {
@@ -293,6 +296,8 @@ sv_status sv_tree_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, c
   p.Mpad = plan.Mpad;
   p.splits = plan.splits;
   p.chunk = plan.chunk;
+  p.window = window;
+  p.sinks = sinks;
   p.scale = scale;
   p.scale_log2 = scale * sv::kLog2e;
   p.tree = tree;
@@ -312,6 +317,44 @@ sv_status sv_tree_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, c
   }
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return SV_OK;
+}
+
+sv_status sv_tree_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                            const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                            const int32_t *parent, int parent_stride, float scale, void *out,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+  const CallRange range("sv_tree_attention");
+  return attention_call(dt, B, N, Hq, Hkv, D, q, k_tree, v_tree, cache, parent, parent_stride, scale, 0,
+                        0, out, workspace, workspace_bytes, stream);
+}
+
+size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
+                                          int max_prefix, int window) {
+  if (window < 1) return 0;
+  return sv_tree_attention_workspace_size(dt, B, N, Hq, Hkv, D,
+                                          window - 1 < max_prefix ? window - 1 : max_prefix);
+}
+
+sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                              const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                              const int32_t *parent, int parent_stride, float scale, int window,
+                              int sinks, void *out, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  const CallRange range("sv_window_attention");
+  if (window < 1) return fail(SV_ERR_INVALID_ARG, "window = %d (at least 1: a token sees itself)", window);
+  if (sinks < 0) return fail(SV_ERR_INVALID_ARG, "sinks = %d", sinks);
+  if (sinks > SV_MAX_SINKS)
+    return fail(SV_ERR_UNSUPPORTED, "sinks = %d (supported 0..%d)", sinks, SV_MAX_SINKS);
+  if (B > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "B = %d (supported up to %d)", B, kMaxGridZ);
+  if (Hkv > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "Hkv = %d (supported up to %d)", Hkv, kMaxGridZ);
+  const long long cap = cache.block_table ? (long long)cache.max_blocks * cache.block_size : cache.Lmax;
+  if (cap > INT32_MAX - 2 * SV_MAX_TREE_NODES)
+    return fail(SV_ERR_UNSUPPORTED, "the cache holds up to %lld positions (supported %d)", cap,
+                INT32_MAX - 2 * SV_MAX_TREE_NODES);
+  if (cache.block_table && cache.block_size > 0 && cache.block_size % 16 != 0)
+    return fail(SV_ERR_UNSUPPORTED, "block_size = %d must be a multiple of 16", cache.block_size);
+  return attention_call(dt, B, N, Hq, Hkv, D, q, k_tree, v_tree, cache, parent, parent_stride, scale,
+                        window, sinks, out, workspace, workspace_bytes, stream);
 }
 
 // ----------------------------------------------------------------- acceptance
@@ -684,6 +727,141 @@ sv_status sv_ngram_draft(int B, int Lmax, const int32_t *history, const int32_t 
   if (e != cudaSuccess) return cuda_fail(e, "n-gram draft launch");
   sv::count_launches(1);
   return SV_OK;
+}
+
+// --------------------------------------------------------------- block tables
+
+sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_tokens, int block_size,
+                          int max_blocks, int num_blocks, const int32_t *free_blocks, int num_free,
+                          const int32_t *free_head, int32_t *block_table, int T,
+                          int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
+                          int32_t *out_free_head, void *stream) {
+  const CallRange range("sv_block_tables");
+  if (B < 0 || T < 0 || num_free < 0)
+    return fail(SV_ERR_INVALID_ARG, "B = %d, T = %d, num_free = %d", B, T, num_free);
+  if (B > SV_MAX_TABLE_BATCH)
+    return fail(SV_ERR_UNSUPPORTED, "B = %d (supported up to %d)", B, SV_MAX_TABLE_BATCH);
+  if (block_size < 1 || max_blocks < 1 || num_blocks < 1)
+    return fail(SV_ERR_INVALID_ARG, "block_size, max_blocks and num_blocks must be >= 1");
+  if ((long long)num_blocks * block_size > INT32_MAX)
+    return fail(SV_ERR_UNSUPPORTED, "a pool of %d blocks of %d has more than 2^31 - 1 rows", num_blocks, block_size);
+  if (B > 0 && (!length || !new_tokens || !block_table || !out_token_start || !out_free_head ||
+                (T > 0 && (!out_slots || !out_positions)) || (num_free > 0 && !free_blocks)))
+    return fail(SV_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(out_slots) || !aligned16(out_positions))
+    return fail(SV_ERR_INVALID_ARG, "out_slots and out_positions must be 16-byte aligned");
+  if (free_head && free_head == out_free_head)
+    return fail(SV_ERR_INVALID_ARG, "out_free_head must not be free_head (every part of the call reads it)");
+  if (B == 0) return SV_OK;  // an empty batch: nothing to launch, no device needed
+  sv::TableParams p{length, new_tokens, free_blocks, free_head, block_table, out_token_start, out_slots,
+                    out_positions, out_free_head, status_word(), B, T, block_size, max_blocks, num_blocks, num_free};
+  if (!p.status) return fail(SV_ERR_CUDA, "no CUDA device");
+  const cudaError_t e = take_injected_failure()
+                            ? cudaErrorLaunchFailure
+                            : sv::launch_block_tables(p, num_sms(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block table launch");
+  sv::count_launches(1);
+  return SV_OK;
+}
+
+// --------------------------------------------------- Q/K norms and the rotation
+
+// (static: linkage of the block, not part of the ABI)
+static sv_status rope_call(sv_dtype dt, int D, sv::RopeParams &p, long long T, void *stream) {
+  if (dt != SV_F32 && dt != SV_BF16) return fail(SV_ERR_UNSUPPORTED, "dtype %d not supported", (int)dt);
+  if (p.Hq < 1 || p.Hkv < 1) return fail(SV_ERR_INVALID_ARG, "bad sizes Hq=%d Hkv=%d", p.Hq, p.Hkv);
+  if (D != 64 && D != 128) return fail(SV_ERR_UNSUPPORTED, "head dim %d (supported 64, 128)", D);
+  if (p.rot < 16 || p.rot > D || p.rot % 16 != 0)
+    return fail(SV_ERR_UNSUPPORTED, "rotary dim %d (supported: multiples of 16 up to the head dim %d)", p.rot, D);
+  if (T > INT32_MAX) return fail(SV_ERR_UNSUPPORTED, "%lld tokens", T);
+  const long long width = ((long long)p.Hq + 2ll * p.Hkv) * D, esize = dt == SV_BF16 ? 2 : 4;
+  if (width > INT32_MAX) return fail(SV_ERR_UNSUPPORTED, "a token's row of %lld elements", width);
+  if (p.ld < width) return fail(SV_ERR_INVALID_ARG, "ld = %lld is below the row's %lld elements", p.ld, width);
+  if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return fail(SV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (p.ld * esize % 16 != 0)
+    return fail(SV_ERR_INVALID_ARG, "ld = %lld: rows must be 16-byte aligned", p.ld);
+  if (T > 0 && (!p.qkv || !p.q_weight || !p.k_weight || !p.inv_freq || !p.q_out || !p.k_out || !p.v_out))
+    return fail(SV_ERR_INVALID_ARG, "a pointer argument is NULL");
+  if (!aligned16(p.qkv) || !aligned16(p.q_out) || !aligned16(p.k_out) || !aligned16(p.v_out))
+    return fail(SV_ERR_INVALID_ARG, "qkv, q_out, k_out and v_out must be 16-byte aligned");
+  if (T == 0) return SV_OK;  // no tokens: nothing to launch, no device needed
+  const char *in0 = static_cast<const char *>(p.qkv), *in1 = in0 + ((T - 1) * p.ld + width) * esize;
+  auto overlaps = [&](const void *o, long long bytes) {
+    const char *o0 = static_cast<const char *>(o);
+    return o0 < in1 && in0 < o0 + bytes;
+  };
+  const long long kv_bytes = p.num_rows * p.Hkv * D * esize;
+  if (overlaps(p.q_out, T * p.Hq * D * esize) || overlaps(p.k_out, kv_bytes) || overlaps(p.v_out, kv_bytes))
+    return fail(SV_ERR_INVALID_ARG, "an output overlaps qkv");
+  p.T = (int)T;
+  p.status = status_word();
+  if (!p.status) return fail(SV_ERR_CUDA, "no CUDA device");
+  const cudaError_t e = take_injected_failure()
+                            ? cudaErrorLaunchFailure
+                            : sv::launch_qk_norm_rope(dt, D, p, num_sms(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "Q/K norm and rotation launch");
+  sv::count_launches(1);
+  return SV_OK;
+}
+
+sv_status sv_qk_norm_rope(sv_dtype dt, int T, int Hq, int Hkv, int D, int rot, int interleaved,
+                          const void *qkv, int64_t ld, const float *q_weight, const float *k_weight,
+                          float eps, const double *inv_freq, const int32_t *positions,
+                          const int32_t *slots, int64_t num_rows, void *q_out, void *k_out,
+                          void *v_out, void *stream) {
+  const CallRange range("sv_qk_norm_rope");
+  if (T < 0 || num_rows < 0)
+    return fail(SV_ERR_INVALID_ARG, "T = %d, num_rows = %lld", T, (long long)num_rows);
+  if (T > 0 && !positions) return fail(SV_ERR_INVALID_ARG, "positions is NULL");
+  if (!slots && num_rows < T)
+    return fail(SV_ERR_INVALID_ARG, "num_rows = %lld is below T = %d (no slots)", (long long)num_rows, T);
+  sv::RopeParams p{};
+  p.qkv = qkv;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.slots = slots;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.ld = ld;
+  p.num_rows = num_rows;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.rot = rot;
+  p.interleaved = interleaved != 0;
+  p.eps = eps;
+  return rope_call(dt, D, p, T, stream);
+}
+
+sv_status sv_tree_qk_norm_rope(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, int rot,
+                               int interleaved, const void *qkv, int64_t ld, const float *q_weight,
+                               const float *k_weight, float eps, const double *inv_freq,
+                               const int32_t *prefix_len, const int32_t *parent, int parent_stride,
+                               void *q_out, void *k_out, void *v_out, void *stream) {
+  const CallRange range("sv_tree_qk_norm_rope");
+  if (B < 0) return fail(SV_ERR_INVALID_ARG, "B = %d", B);
+  sv::RopeParams p{};
+  const sv_status st = tree_arg(N, parent, parent_stride, &p.tree);
+  if (st != SV_OK) return st;
+  if (B > 0 && !prefix_len) return fail(SV_ERR_INVALID_ARG, "prefix_len is NULL");
+  p.qkv = qkv;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.inv_freq = inv_freq;
+  p.prefix_len = prefix_len;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.ld = ld;
+  p.num_rows = (long long)B * N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.rot = rot;
+  p.interleaved = interleaved != 0;
+  p.eps = eps;
+  return rope_call(dt, D, p, (long long)B * N, stream);
 }
 
 // --------------------------------------------------------------------- commit

@@ -74,6 +74,29 @@ __device__ __forceinline__ bool tree_walk_seq(const Tree &t, int b, int c, uint6
   return false;
 }
 
+// ---------------------------------------------------------- sliding window
+
+// The first prefix position in the window of the root (depth 0, position L); deeper nodes
+// see that much less.
+__device__ __forceinline__ int window_first(int L, int window) {
+  return L >= window ? L - window + 1 : 0;
+}
+
+// The tree nodes that a node sees under the window: of its root path (ancestor mask anc,
+// itself included, prefix length L), those less than `window` positions before it, and
+// those at a position below `sinks`.  Parents come before their children, so the mask's
+// bits in ascending order are the path's depths 0, 1, ...
+__device__ __forceinline__ uint64_t window_ancestors(uint64_t anc, int L, int window, int sinks) {
+  int drop = __popcll(anc) - window;  // the depths [0, drop) are out of the window
+  uint64_t m = anc, seen = anc;
+  for (int d = 0; d < drop; ++d) {
+    const uint64_t low = m & (0ull - m);
+    m ^= low;
+    if (L + d >= sinks) seen ^= low;
+  }
+  return seen;
+}
+
 // ------------------------------------------------------------ element access
 
 // Widen 8 packed bf16 (one 16-byte vector) to float; element i at bits [16i, 16i+16).

@@ -41,6 +41,10 @@ struct AttnParams {
   int Lmax, block_size, max_blocks, num_blocks, cap;  // cap = largest valid prefix
   int M, m_tiles, Mpad;  // query rows per (b, kv head) = N*G, tiles of 64 rows
   int splits, chunk;     // prefix split: split s covers [s*chunk, (s+1)*chunk)
+  // sliding window (0 = the whole prefix) and the first `sinks` positions that stay visible
+  // outside it; with a window the splits cover [first + s*chunk, ...), first the earliest
+  // position in the root's window
+  int window, sinks;
   float scale_log2;      // softmax scale * log2(e)
   float scale;
   Tree tree;
@@ -175,6 +179,38 @@ cudaError_t launch_accept_stats(sv_dtype dt, const AcceptParams &p, cudaStream_t
 cudaError_t launch_accept_recursive(sv_dtype dt, const AcceptParams &p, cudaStream_t s);
 
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t s);
+
+// ------------------------------------------- block tables, Q/K norms and rotation
+
+struct TableParams {
+  const int32_t *length, *new_tokens;  // [B]
+  const int32_t *free_blocks;          // [num_free]
+  const int32_t *free_head;            // [1] or NULL (0)
+  int32_t *block_table;                // [B,max_blocks]
+  int32_t *token_start;                // [B+1]
+  int32_t *slots, *positions;          // [T]
+  int32_t *out_free_head;              // [1]
+  unsigned int *status;
+  int B, T, block_size, max_blocks, num_blocks, num_free;
+};
+cudaError_t launch_block_tables(const TableParams &p, int num_sms, cudaStream_t s);
+
+struct RopeParams {
+  const void *qkv;                     // T rows, ld elements apart
+  const float *q_weight, *k_weight;    // [D]
+  const double *inv_freq;              // [rot/2]
+  const int32_t *positions;            // [T], or NULL: prefix_len[b] + depth of the tree's node
+  const int32_t *slots;                // [T] rows of k_out / v_out, or NULL: row t
+  const int32_t *prefix_len;           // [B] (tree form)
+  void *q_out, *k_out, *v_out;
+  unsigned int *status;
+  long long ld, num_rows;              // num_rows: rows of k_out / v_out
+  int T, Hq, Hkv, rot, interleaved;
+  int split;                           // warps per token (set at the launch)
+  float eps;
+  Tree tree;                           // (tree form; T = B * tree.N)
+};
+cudaError_t launch_qk_norm_rope(sv_dtype dt, int D, RopeParams p, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- LM head
 

@@ -15,7 +15,8 @@ import torch
 
 from . import (EXACT, GREEDY, Q_LOGITS, KVCache, sv_accept_chain, sv_accept_chain_commit,
                sv_accept_tree, sv_accept_tree_commit, sv_accept_workspace_size, sv_commit_kv,
-               sv_tree_attention, sv_tree_attention_workspace_size)
+               sv_tree_attention, sv_tree_attention_workspace_size, sv_window_attention,
+               sv_window_attention_workspace_size)
 
 
 # inputs of the attention call (the rest feed the acceptance)
@@ -33,12 +34,15 @@ class VerifyStep:
     """Buffers and calls of one verify step for a fixed batch shape.
 
     chain=True uses sv_accept_chain (parent must be a chain); otherwise sv_accept_tree.
+    window: the layer's sliding window (its attention is then sv_window_attention, with the
+    first ``sinks`` positions kept visible); None attends to the whole prefix.
     """
 
     def __init__(self, parent: Sequence[int], B: int, Hq: int, Hkv: int, D: int, V: int,
                  cache: KVCache, dtype=torch.bfloat16, mode=EXACT, q_kind=Q_LOGITS,
                  temperature: float = 1.0, top_k: int = 0, chain: bool = False,
-                 device: Optional[torch.device] = None, top_p: float = 1.0):
+                 device: Optional[torch.device] = None, top_p: float = 1.0,
+                 window: Optional[int] = None, sinks: int = 0):
         self.parent = list(parent)
         self.N = len(self.parent)
         self.Dmax = max(_depths(self.parent))
@@ -46,9 +50,15 @@ class VerifyStep:
         self.cache, self.dtype, self.mode, self.q_kind = cache, dtype, mode, q_kind
         self.temperature, self.top_k, self.chain = temperature, top_k, chain
         self.top_p = top_p
+        self.window, self.sinks = window, sinks
+        if window is None and sinks:
+            raise ValueError("sinks go with a window")
         self.device = device or cache.k.device
         self.scale = D ** -0.5
-        ws = sv_tree_attention_workspace_size(dtype, B, self.N, Hq, Hkv, D, cache.max_prefix)
+        if window is None:
+            ws = sv_tree_attention_workspace_size(dtype, B, self.N, Hq, Hkv, D, cache.max_prefix)
+        else:
+            ws = sv_window_attention_workspace_size(dtype, B, self.N, Hq, Hkv, D, cache.max_prefix, window)
         # zero before first use: the kernel keeps completion words in it
         self.attn_ws = torch.zeros(max(ws, 16), dtype=torch.uint8, device=self.device)
         self.attn_splits = ws > 0
@@ -76,6 +86,9 @@ class VerifyStep:
         return 1 + 2
 
     def attention(self, q, k_tree, v_tree, stream=None):
+        if self.window is not None:
+            return sv_window_attention(q, k_tree, v_tree, self.cache, self.parent, self.scale, self.window,
+                                       sinks=self.sinks, out=self.out, workspace=self.attn_ws, stream=stream)
         return sv_tree_attention(q, k_tree, v_tree, self.cache, self.parent, self.scale,
                                  out=self.out, workspace=self.attn_ws, stream=stream)
 
