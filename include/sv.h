@@ -166,7 +166,8 @@ size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int H
  *   or prefix_len[b] + depth(j) < sinks,
  * so no row is ever empty.  out = softmax(scale * q . K^T) V over those keys; with
  * window > prefix_len[b] + depth(n) that is sv_tree_attention.  N = 1 is the decoding of one
- * token per sequence.  window >= 1 (else SV_ERR_INVALID_ARG), 0 <= sinks <= SV_MAX_SINKS.
+ * token per sequence.  window >= 1 and scale > 0 (else SV_ERR_INVALID_ARG), 0 <= sinks <=
+ * SV_MAX_SINKS.
  * Cache positions that no row of a sequence sees are not read into its result, and their
  * blocks need not exist: pages that lie wholly before the window of the root (position
  * prefix_len[b] - window + 1) and after the sinks may have any entry in the block table, so

@@ -169,6 +169,12 @@ sv_status check_cache(const sv_kv_cache &c, bool writable, int B) {
   return SV_OK;
 }
 
+// The general attention kernel keeps its partials behind the words that the tensor-core
+// kernel's calls count in (the workspace's first 256 bytes), so that calls of either kind may
+// share a workspace.
+constexpr size_t kGeneralWsOffset = 256;
+size_t general_ws_bytes(const sv::AttnPlan &pl) { return pl.ws_bytes > 0 ? kGeneralWsOffset + pl.ws_bytes : 0; }
+
 }  // namespace
 
 extern "C" {
@@ -220,7 +226,7 @@ size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int H
                                         int max_prefix) {
   if (B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_prefix < 0)
     return 0;
-  size_t ws = sv::attn_plan(dt, B, N, Hq, Hkv, D, max_prefix, num_sms()).ws_bytes;
+  size_t ws = general_ws_bytes(sv::attn_plan(dt, B, N, Hq, Hkv, D, max_prefix, num_sms()));
   if (dt == SV_BF16 && (D == 64 || D == 128)) {
     const size_t tc = sv::tc_plan(B, N, Hq, Hkv, D, num_sms()).ws_bytes;
     if (tc > ws) ws = tc;
@@ -258,9 +264,9 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
   const int max_prefix = max_prefix_of(cache);
   const int span = window > 0 && window - 1 < max_prefix ? window - 1 : max_prefix;
   const sv::AttnPlan plan = sv::attn_plan(dt, B, N, Hq, Hkv, D, span, num_sms());
-  const bool use_tc = window == 0 && sv::tc_eligible(dt, N, Hq, Hkv, D, cache.block_table ? cache.block_size : 0);
+  const bool use_tc = sv::tc_eligible(dt, N, Hq, Hkv, D, cache.block_table ? cache.block_size : 0);
   const sv::TcPlan tplan = use_tc ? sv::tc_plan(B, N, Hq, Hkv, D, num_sms()) : sv::TcPlan{};
-  const size_t ws_need = use_tc ? tplan.ws_bytes : plan.ws_bytes;
+  const size_t ws_need = use_tc ? tplan.ws_bytes : general_ws_bytes(plan);
   if (ws_need > 0) {
     if (!workspace || workspace_bytes < ws_need)
       return fail(SV_ERR_WORKSPACE, "attention workspace %zu bytes, need %zu", workspace_bytes,
@@ -309,7 +315,7 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
     if (e == cudaSuccess) sv::count_launches(1);
   } else {
     if (plan.ws_bytes > 0) {
-      p.part_o = static_cast<float *>(workspace);
+      p.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + kGeneralWsOffset);
       p.part_ml = p.part_o + (size_t)B * Hkv * plan.splits * plan.Mpad * D;
     }
     e = take_injected_failure() ? cudaErrorLaunchFailure : sv::launch_attention(dt, p, static_cast<cudaStream_t>(stream));
@@ -345,6 +351,7 @@ sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
   if (sinks < 0) return fail(SV_ERR_INVALID_ARG, "sinks = %d", sinks);
   if (sinks > SV_MAX_SINKS)
     return fail(SV_ERR_UNSUPPORTED, "sinks = %d (supported 0..%d)", sinks, SV_MAX_SINKS);
+  if (!(scale > 0.f)) return fail(SV_ERR_INVALID_ARG, "scale must be positive");
   if (B > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "B = %d (supported up to %d)", B, kMaxGridZ);
   if (Hkv > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "Hkv = %d (supported up to %d)", Hkv, kMaxGridZ);
   const long long cap = cache.block_table ? (long long)cache.max_blocks * cache.block_size : cache.Lmax;

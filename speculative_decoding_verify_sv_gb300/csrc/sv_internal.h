@@ -82,6 +82,10 @@ struct TcParams {
   float scale_log2;
   Tree tree;
   unsigned long long wait_ns;  // a wait for progress gives up after this long
+  // sliding window: 16-row boxes of the cache (sinks), the window, the sinks, and the power of
+  // two that a unit's first tile starts at a multiple of
+  CUtensorMap tm_ks, tm_vs;
+  int window, sinks, win_align;
 };
 
 struct TcPlan {

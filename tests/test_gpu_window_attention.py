@@ -218,6 +218,11 @@ def test_refusals_and_empty_batch(cuda_ok):
         with pytest.raises(sv.SVError) as e:
             _call(inp, par, window, sinks)
         assert e.value.code == code
+    for scale in (0.0, -0.1, float("nan"), float("inf")):
+        with pytest.raises(sv.SVError) as e:
+            sv.sv_window_attention(inp["q"], inp["k_tree"], inp["v_tree"],
+                                   sv.KVCache(inp["cache_k"], inp["cache_v"], inp["prefix_len"]), par, scale, 4)
+        assert e.value.code == sv.SV_ERR_INVALID_ARG
     with pytest.raises(ValueError):
         _call(inp, par, 2 ** 31, 0)
     with pytest.raises(ValueError):
