@@ -177,7 +177,9 @@ size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int H
  * 16 and B or Hkv above 65535 are SV_ERR_UNSUPPORTED.
  * A NaN or infinity in the V row of a key that some rows of a sequence see can also reach
  * its other rows of the same KV head (0 * NaN).
- * Workspace: sv_window_attention_workspace_size() bytes (max_prefix as there). */
+ * Workspace: sv_window_attention_workspace_size() bytes (max_prefix as there; 0 for float32, for up
+ * to 32 query rows per KV head, and where few or short windows make the kernel without one
+ * the faster). */
 #define SV_MAX_SINKS 64
 sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
                               const void *k_tree, const void *v_tree, sv_kv_cache cache,

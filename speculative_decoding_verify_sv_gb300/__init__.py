@@ -8,7 +8,7 @@ kernels; there is no CPU fallback: if the library is missing the calls raise.
 """
 from __future__ import annotations
 
-import contextlib
+import array
 import ctypes
 import os
 import threading
@@ -68,6 +68,8 @@ def library_path() -> str:
 def load_library():
     """Load libsv.so (built by ``__graft_entry__.build()``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -244,34 +246,73 @@ def _int32(x, name: str) -> int:
     return x
 
 
-def _cache_shapes(cache: KVCache, q, B, Hkv, D):
-    """The cache belongs to these sequences and heads: contiguous [B,Lmax,Hkv,D], or pages of
-    block_size rows with a table row per sequence."""
-    if cache.k.dtype != q.dtype:
+# The operators around the cache are called once per layer, or for a single token, where the
+# call's host side is what counts: their wrappers check a tensor and take its pointer in one
+# step, take the current stream's handle as it is, and hand plain numbers to the library.
+
+def _arg(t, name: str, dtype, shape, dev: int) -> int:
+    """The pointer of a contiguous CUDA tensor of this type and shape on device ``dev``."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or t.shape != shape \
+            or not t.is_contiguous():
+        _dev(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}: one call works on one device")
+    return t.data_ptr()
+
+
+def _home(t, name: str) -> int:
+    """The device index of a call, that of its first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _launch(fn, dev: int, stream, *args) -> None:
+    """fn(*args, stream) on device ``dev``, on its current stream unless one is given."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    code = fn(*args, int(stream))
+    if code != SV_OK:
+        _check(code)
+
+
+def _tree_ptr(parent, B: int, N: int, dev: int):
+    """(what to keep alive, pointer, parent_stride) of a tree argument, as _tree_arg takes it."""
+    if isinstance(parent, torch.Tensor):
+        if parent.is_cuda:
+            ptr, stride, _ = _tree_arg(parent, B, N)
+            if parent.get_device() != dev:
+                raise ValueError(f"parent is on {parent.device}, the other tensors on cuda:{dev}")
+            return parent, ptr, stride
+        parent = parent.tolist()
+    rows = array.array("i", parent)
+    if len(rows) != N:
+        raise ValueError(f"parent has {len(rows)} entries, the tree has {N} rows")
+    return rows, rows.buffer_info()[0], 0
+
+
+def _cache_arg(cache: KVCache, dtype, B: int, Hkv: int, D: int, dev: int) -> _KVCacheC:
+    """The cache of these sequences and heads: contiguous [B,Lmax,Hkv,D], or pages of block_size
+    rows with a table row per sequence."""
+    k, table = cache.k, cache.block_table
+    if k.dtype is not dtype:
         raise TypeError("cache dtype differs from q")
-    if cache.k.dim() != 4 or tuple(cache.k.shape[2:]) != (Hkv, D):
-        raise ValueError(f"cache.k has shape {tuple(cache.k.shape)}, expected [..., ..., {Hkv}, {D}]")
-    if cache.prefix_len.shape != (B,):
-        raise ValueError(f"cache.prefix_len must be [B={B}]")
-    if cache.block_table is None:
-        if cache.k.shape[0] != B:
-            raise ValueError(f"cache.k has {cache.k.shape[0]} sequences, q has {B}")
-    elif cache.block_table.dim() != 2 or cache.block_table.shape[0] != B:
-        raise ValueError(f"cache.block_table must be [B={B}, max_blocks]")
-    elif cache.k.shape[1] != int(cache.block_size):
-        raise ValueError(f"cache.k has blocks of {cache.k.shape[1]} rows, block_size is {cache.block_size}")
-
-
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _on_device(*tensors):
-    """The context of a call on these tensors' device, which must be one and the same."""
-    dev = tensors[0].device
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one call works on one device")
-    return _NO_SWITCH if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    shape = k.shape
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D or (table is None and shape[0] != B):
+        raise ValueError(f"cache.k has shape {tuple(shape)}, expected [{'B' if table is None else 'blocks'}, rows, "
+                         f"{Hkv}, {D}] (B = {B})")
+    kp, vp = _arg(k, "cache.k", dtype, shape, dev), _arg(cache.v, "cache.v", dtype, shape, dev)
+    lens = _arg(cache.prefix_len, "cache.prefix_len", torch.int32, (B,), dev)
+    if table is None:
+        return _KVCacheC(kp, vp, lens, None, shape[1], 0, 0, 0)
+    if table.dim() != 2 or shape[1] != cache.block_size:
+        raise ValueError(f"blocks of {shape[1]} rows need block_size {shape[1]} and a block_table [B, max_blocks]")
+    return _KVCacheC(kp, vp, lens, _arg(table, "cache.block_table", torch.int32, (B, table.shape[1]), dev), 0,
+                     shape[1], table.shape[1], shape[0])
 
 
 def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], zero: bool = False):
@@ -333,26 +374,29 @@ def sv_window_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, window
     and result as sv_tree_attention.  A node at position P = prefix_len + depth sees a prefix
     position (or a node of its root path) p iff P - p < window or p < sinks."""
     lib = load_library()
-    _dev(q, "q", (torch.bfloat16, torch.float32))
+    dev, dtype = _home(q, "q"), q.dtype
+    dt = _dt(q)
     B, N, Hq, D = q.shape
     Hkv = k_tree.shape[2]
-    _dev(k_tree, "k_tree", q.dtype, (B, N, Hkv, D))
-    _dev(v_tree, "v_tree", q.dtype, (B, N, Hkv, D))
-    _cache_shapes(cache, q, B, Hkv, D)
+    qp = _arg(q, "q", dtype, q.shape, dev)
+    kp = _arg(k_tree, "k_tree", dtype, (B, N, Hkv, D), dev)
+    vp = _arg(v_tree, "v_tree", dtype, (B, N, Hkv, D), dev)
+    cs = _cache_arg(cache, dtype, B, Hkv, D, dev)
     if out is None:
         out = torch.empty_like(q)
-    _dev(out, "out", q.dtype, q.shape)
     window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
-    cs = cache.c_struct()
-    ws_need = int(lib.sv_window_attention_workspace_size(_dt(q), B, N, Hq, Hkv, D, cache.max_prefix, window))
-    # a workspace passed in must have been zero-filled before its first use
-    workspace, ws_bytes = _workspace(ws_need, q.device, workspace, zero=True)
-    par, pstride, _ = _tree_arg(parent, B, N)
-    with _on_device(q, k_tree, v_tree, cache.k, cache.v, cache.prefix_len, cache.block_table, out, workspace,
-                    parent):
-        _check(lib.sv_window_attention(_dt(q), B, N, Hq, Hkv, D, _ptr(q), _ptr(k_tree), _ptr(v_tree), cs, par,
-                                       pstride, float(scale), window, sinks, _ptr(out), _ptr(workspace),
-                                       ws_bytes, _stream(stream)))
+    if workspace is None:
+        need = lib.sv_window_attention_workspace_size(dt, B, N, Hq, Hkv, D, cache.max_prefix, window)
+        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device) if need else None
+    # (a workspace passed in must have been zero-filled before its first use; the library
+    # checks its size)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    keep, par, pstride = _tree_ptr(parent, B, N, dev)
+    _launch(lib.sv_window_attention, dev, stream, dt, B, N, Hq, Hkv, D, qp, kp, vp, cs, par, pstride, scale, window,
+            sinks, _arg(out, "out", dtype, q.shape, dev), ws_ptr, ws_bytes)
     return out
 
 
@@ -364,66 +408,68 @@ def sv_block_tables(length, new_tokens, block_table, free_blocks, block_size, nu
     (``length`` [B] are in it) with pages of ``free_blocks`` from ``free_head`` [1] on, and make
     the new tokens' slot map.  block_table [B,max_blocks] is written in place.  Returns a dict of
     int32 device tensors: token_start [B+1], slots and positions [num_slots] (-1 past the
-    total), free_head [1] (the advanced head, never the one passed in)."""
+    total), free_head [1] (the advanced head, never the one passed in).  ``outs`` may hold those
+    tensors to write into; the ones it lacks are made (as views of one buffer)."""
     lib = load_library()
-    _dev(length, "length", torch.int32)
+    dev, i32 = _home(length, "length"), torch.int32
     if length.dim() != 1:
         raise ValueError("length must be [B]")
     B = length.shape[0]
-    _dev(new_tokens, "new_tokens", torch.int32, (B,))
-    _dev(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [B={B}, max_blocks]")
-    _dev(free_blocks, "free_blocks", torch.int32)
-    if free_head is not None:
-        _dev(free_head, "free_head", torch.int32, (1,))
     T = _int32(num_slots, "num_slots")
     if T < 0:
         raise ValueError(f"num_slots = {T}")
-    outs = {} if outs is None else outs
-    for name, shape in (("token_start", (B + 1,)), ("slots", (T,)), ("positions", (T,)), ("free_head", (1,))):
-        if name not in outs:
-            outs[name] = torch.empty(shape, dtype=torch.int32, device=length.device)
-        _dev(outs[name], name, torch.int32, shape)
-    with _on_device(length, new_tokens, block_table, free_blocks, free_head, *outs.values()):
-        _check(lib.sv_block_tables(B, _ptr(length), _ptr(new_tokens), _int32(block_size, "block_size"),
-                                   block_table.shape[1], _int32(num_blocks, "num_blocks"), _ptr(free_blocks),
-                                   free_blocks.numel(), _ptr(free_head), _ptr(block_table), T,
-                                   _ptr(outs["token_start"]), _ptr(outs["slots"]), _ptr(outs["positions"]),
-                                   _ptr(outs["free_head"]), _stream(stream)))
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be [B={B}, max_blocks]")
+    columns, n_free = block_table.shape[1], free_blocks.numel()
+    if not outs:
+        outs = {} if outs is None else outs
+        pad = -T % 4  # (the maps start on 16-byte boundaries)
+        buf = torch.empty(2 * (T + pad) + B + 2, dtype=i32, device=length.device)
+        outs["slots"] = buf.as_strided((T,), (1,), 0)
+        outs["positions"] = buf.as_strided((T,), (1,), T + pad)
+        outs["token_start"] = buf.as_strided((B + 1,), (1,), 2 * (T + pad))
+        outs["free_head"] = buf.as_strided((1,), (1,), 2 * (T + pad) + B + 1)
+        slots = buf.data_ptr()
+        positions = slots + 4 * (T + pad)
+        start = positions + 4 * (T + pad)
+        head = start + 4 * (B + 1)
+    else:
+        for name, shape in (("token_start", (B + 1,)), ("slots", (T,)), ("positions", (T,)), ("free_head", (1,))):
+            if name not in outs:
+                outs[name] = torch.empty(shape, dtype=i32, device=length.device)
+        slots = _arg(outs["slots"], "slots", i32, (T,), dev)
+        positions = _arg(outs["positions"], "positions", i32, (T,), dev)
+        start = _arg(outs["token_start"], "token_start", i32, (B + 1,), dev)
+        head = _arg(outs["free_head"], "free_head", i32, (1,), dev)
+    _launch(lib.sv_block_tables, dev, stream, B, _arg(length, "length", i32, (B,), dev),
+            _arg(new_tokens, "new_tokens", i32, (B,), dev), _int32(block_size, "block_size"), columns,
+            _int32(num_blocks, "num_blocks"), _arg(free_blocks, "free_blocks", i32, free_blocks.shape, dev), n_free,
+            None if free_head is None else _arg(free_head, "free_head", i32, (1,), dev),
+            _arg(block_table, "block_table", i32, (B, columns), dev), T, start, slots, positions, head)
     return outs
 
 
-def _rope_args(qkv, lead, Hq, Hkv, q_weight, k_weight, inv_freq):
-    """(D, rot, row stride) of a projection qkv [*lead, (Hq + 2 Hkv) * D] with evenly spaced rows."""
-    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
-        raise TypeError("qkv must be a CUDA tensor")
-    if qkv.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"qkv has dtype {qkv.dtype}, expected bfloat16 or float32")
-    _dev(q_weight, "q_weight", torch.float32)
-    D = q_weight.numel()
-    _dev(q_weight, "q_weight", torch.float32, (D,))
-    _dev(k_weight, "k_weight", torch.float32, (D,))
-    _dev(inv_freq, "inv_freq", torch.float64)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot/2]")
+def _rope_args(qkv, lead: int, Hq: int, Hkv: int, q_weight, k_weight, inv_freq):
+    """(device, D, rot, row stride, pointers of the weights and frequencies) of a projection qkv
+    [*lead, (Hq + 2 Hkv) * D] with evenly spaced rows."""
+    dev, f32 = _home(qkv, "qkv"), torch.float32
+    D, half = q_weight.numel(), inv_freq.numel()
     width = (Hq + 2 * Hkv) * D
-    if qkv.dim() != lead + 1 or qkv.shape[-1] != width:
-        raise ValueError(f"qkv has shape {tuple(qkv.shape)}, expected {lead} leading dimensions and rows of {width}")
-    if qkv.numel() == 0:
-        return D, 2 * inv_freq.numel(), width
-    rows, ld = 1, width
-    for n, step in zip(reversed(qkv.shape[:-1]), reversed(qkv.stride()[:-1])):
-        if n == 1:
-            continue
-        if rows == 1:
-            ld = step
-        elif step != rows * ld:
+    shape, step = qkv.shape, qkv.stride()
+    if len(shape) != lead + 1 or shape[lead] != width:
+        raise ValueError(f"qkv has shape {tuple(shape)}, expected {lead} leading dimensions and rows of {width}")
+    if lead == 1:
+        rows, ld = shape[0], step[0]
+    else:
+        rows, ld = shape[0] * shape[1], step[1] if shape[1] != 1 else step[0]
+        if rows and shape[0] != 1 and step[0] != shape[1] * ld:
             raise ValueError("the rows of qkv must be evenly spaced")
-        rows *= n
-    if qkv.stride(-1) != 1 or ld < width:
+    if rows <= 1:
+        ld = width
+    if rows and (step[lead] != 1 or ld < width):
         raise ValueError("the rows of qkv must be contiguous and apart")
-    return D, 2 * inv_freq.numel(), ld
+    return dev, D, 2 * half, ld, (_arg(q_weight, "q_weight", f32, (D,), dev), _arg(k_weight, "k_weight", f32, (D,), dev),
+                                  _arg(inv_freq, "inv_freq", torch.float64, (half,), dev))
 
 
 def sv_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, positions, eps=1e-6, interleaved=False,
@@ -433,29 +479,26 @@ def sv_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, positions, eps=1
     int32 (negative: padding).  Returns (q [T,Hq,D], k, v): k and v are k_out and v_out
     [..., Hkv, D] (a KV cache, paged or not), token t in row slots[t]; without slots row t."""
     lib = load_library()
-    D, rot, ld = _rope_args(qkv, 1, Hq, Hkv, q_weight, k_weight, inv_freq)
-    T = qkv.shape[0]
-    _dev(positions, "positions", torch.int32, (T,))
+    dev, D, rot, ld, (qw, kw, freq) = _rope_args(qkv, 1, Hq, Hkv, q_weight, k_weight, inv_freq)
+    T, dtype, dt = qkv.shape[0], qkv.dtype, _dt(qkv)
+    at = _arg(positions, "positions", torch.int32, (T,), dev)
+    to = None
     if slots is not None:
-        _dev(slots, "slots", torch.int32, (T,))
         if k_out is None or v_out is None:
             raise ValueError("slots need k_out and v_out")
+        to = _arg(slots, "slots", torch.int32, (T,), dev)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=qkv.dtype, device=qkv.device)
+        q_out = torch.empty((T, Hq, D), dtype=dtype, device=qkv.device)
     if k_out is None:
-        k_out = torch.empty((T, Hkv, D), dtype=qkv.dtype, device=qkv.device)
+        k_out = torch.empty((T, Hkv, D), dtype=dtype, device=qkv.device)
     if v_out is None:
-        v_out = torch.empty((T, Hkv, D), dtype=qkv.dtype, device=qkv.device)
-    _dev(q_out, "q_out", qkv.dtype, (T, Hq, D))
-    _dev(k_out, "k_out", qkv.dtype)
-    _dev(v_out, "v_out", qkv.dtype, k_out.shape)
-    if k_out.dim() < 3 or tuple(k_out.shape[-2:]) != (Hkv, D):
-        raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected [..., {Hkv}, {D}]")
-    with _on_device(qkv, q_weight, k_weight, inv_freq, positions, slots, q_out, k_out, v_out):
-        _check(lib.sv_qk_norm_rope(_dt(qkv), T, Hq, Hkv, D, rot, int(bool(interleaved)), _ptr(qkv), ld,
-                                   _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), _ptr(positions),
-                                   _ptr(slots), k_out.numel() // (Hkv * D), _ptr(q_out), _ptr(k_out), _ptr(v_out),
-                                   _stream(stream)))
+        v_out = torch.empty((T, Hkv, D), dtype=dtype, device=qkv.device)
+    shape = k_out.shape
+    if len(shape) < 3 or shape[-2] != Hkv or shape[-1] != D:
+        raise ValueError(f"k_out has shape {tuple(shape)}, expected [..., {Hkv}, {D}]")
+    _launch(lib.sv_qk_norm_rope, dev, stream, dt, T, Hq, Hkv, D, rot, 1 if interleaved else 0, qkv.data_ptr(), ld, qw, kw,
+            eps, freq, at, to, k_out.numel() // (Hkv * D), _arg(q_out, "q_out", dtype, (T, Hq, D), dev),
+            _arg(k_out, "k_out", dtype, shape, dev), _arg(v_out, "v_out", dtype, shape, dev))
     return q_out, k_out, v_out
 
 
@@ -465,21 +508,18 @@ def sv_tree_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, prefix_len,
     sequence b at position prefix_len[b] + depth(n).  Returns (q, k_tree, v_tree), the inputs of
     sv_tree_attention and sv_window_attention (``outs``: those three, to write into)."""
     lib = load_library()
-    D, rot, ld = _rope_args(qkv, 2, Hq, Hkv, q_weight, k_weight, inv_freq)
+    dev, D, rot, ld, (qw, kw, freq) = _rope_args(qkv, 2, Hq, Hkv, q_weight, k_weight, inv_freq)
     B, N = qkv.shape[:2]
-    _dev(prefix_len, "prefix_len", torch.int32, (B,))
+    dtype, dt = qkv.dtype, _dt(qkv)
+    lens = _arg(prefix_len, "prefix_len", torch.int32, (B,), dev)
     if outs is None:
-        outs = tuple(torch.empty((B, N, h, D), dtype=qkv.dtype, device=qkv.device) for h in (Hq, Hkv, Hkv))
+        new = dict(dtype=dtype, device=qkv.device)
+        outs = (torch.empty((B, N, Hq, D), **new), torch.empty((B, N, Hkv, D), **new), torch.empty((B, N, Hkv, D), **new))
     q, k, v = outs
-    _dev(q, "q", qkv.dtype, (B, N, Hq, D))
-    _dev(k, "k_tree", qkv.dtype, (B, N, Hkv, D))
-    _dev(v, "v_tree", qkv.dtype, (B, N, Hkv, D))
-    par, pstride, _ = _tree_arg(parent, B, N)
-    with _on_device(qkv, q_weight, k_weight, inv_freq, prefix_len, q, k, v, parent):
-        _check(lib.sv_tree_qk_norm_rope(_dt(qkv), B, N, Hq, Hkv, D, rot, int(bool(interleaved)), _ptr(qkv), ld,
-                                        _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq),
-                                        _ptr(prefix_len), par, pstride, _ptr(q), _ptr(k), _ptr(v),
-                                        _stream(stream)))
+    keep, par, pstride = _tree_ptr(parent, B, N, dev)
+    _launch(lib.sv_tree_qk_norm_rope, dev, stream, dt, B, N, Hq, Hkv, D, rot, 1 if interleaved else 0, qkv.data_ptr(), ld,
+            qw, kw, eps, freq, lens, par, pstride, _arg(q, "q", dtype, (B, N, Hq, D), dev),
+            _arg(k, "k_tree", dtype, (B, N, Hkv, D), dev), _arg(v, "v_tree", dtype, (B, N, Hkv, D), dev))
     return q, k, v
 
 

@@ -12,11 +12,9 @@
 // and an online softmax.  Splits of the prefix merge in a second kernel by
 // log-sum-exp weights.
 //
-// The WIN instances add a sliding window with sinks: node n at position P = L_b + depth(n)
-// sees a prefix position p (or a tree node at position p on its root path) iff P - p < window
-// or p < sinks.  The prefix tiles then cover [first, L_b), first = L_b - window + 1 being the
-// earliest position in any row's window, and the sinks before `first` are one more tile
-// beside the tree's (no position is read twice, and none outside these ranges at all).
+// fp32 with a sliding window and sinks (the WIN instances): node n at position P = L_b +
+// depth(n) sees a prefix position p (or a tree node at position p on its root path) iff
+// P - p < window or p < sinks.
 #include <atomic>
 #include <cfloat>
 
@@ -55,7 +53,7 @@ __device__ __forceinline__ int clamp_prefix(const AttnParams &p, int b) {
   return L;
 }
 
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) {
   constexpr int LDS = D + 8;  // padded row stride (elements): conflict-free ldmatrix
   constexpr int CH = D / 8;   // 16-byte chunks per row
@@ -77,13 +75,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
   const int kvh = blockIdx.y, b = blockIdx.z;
 
   const int L = clamp_prefix(p, b);
-  const int first = WIN ? window_first(L, p.window) : 0;
-  const int n_sinks = WIN ? min(p.sinks, first) : 0;  // sinks before the window's tiles
-  const int k_begin = first + split * p.chunk;
+  const int k_begin = split * p.chunk;
   const int k_end = min(L, k_begin + p.chunk);
   const int n_pref = k_end > k_begin ? (k_end - k_begin + kTileKeys - 1) / kTileKeys : 0;
-  // split 0 starts with the tree's tile and, when there are any, the sinks' tile
-  const int has_tree = split == 0 ? (n_sinks > 0 ? 2 : 1) : 0;
+  const int has_tree = split == 0 ? 1 : 0;
   const int n_tiles = n_pref + has_tree;
 
   // sequence b's tree (shared, or its own row): ancestor masks of its nodes
@@ -110,9 +105,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
 
   auto load_tile = [&](int t, int stage) {
     const bool tree = has_tree && t == 0;
-    const bool sink = WIN && has_tree == 2 && t == 1;
-    const int base = sink ? 0 : k_begin + (t - has_tree) * kTileKeys;
-    const int end = sink ? n_sinks : k_end;
+    const int base = k_begin + (t - has_tree) * kTileKeys;
     bf16 *dk = sK + stage * kTileKeys * LDS;
     bf16 *dv = sV + stage * kTileKeys * LDS;
     for (int c = tid; c < kTileKeys * CH; c += kThreads) {
@@ -126,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
         sv = gvt + off;
       } else {
         const int pos = base + r;
-        valid = pos < end;
+        valid = pos < k_end;
         long long row = 0;
         if (valid) {
           row = cache_row(p, b, pos);
@@ -166,15 +159,6 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
     const int R = mt * kRowsPerCta + r_lo + 8 * i;
     anc[i] = R < p.M ? sAnc[R / p.G] : 0ull;
   }
-  // the first prefix position in each row's window, and the window's cut of its root path
-  int lo[2] = {0, 0};
-  if constexpr (WIN) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      lo[i] = window_first(L + max(__popcll(anc[i]) - 1, 0), p.window);
-      anc[i] = window_ancestors(anc[i], L, p.window, p.sinks);
-    }
-  }
 
   float o[D / 8][4];
 #pragma unroll
@@ -193,9 +177,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
     const bf16 *tk = sK + stage * kTileKeys * LDS;
     const bf16 *tv = sV + stage * kTileKeys * LDS;
     const bool tree = has_tree && t == 0;
-    const bool sink = WIN && has_tree == 2 && t == 1;
-    const int base = sink ? 0 : k_begin + (t - has_tree) * kTileKeys;
-    const int end = sink ? n_sinks : k_end;
+    const int base = k_begin + (t - has_tree) * kTileKeys;
 
     float sc[kTileKeys / 8][4];
 #pragma unroll
@@ -221,8 +203,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnParams p) 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int kk = nt * 8 + 2 * (lane & 3) + e;
-          bool ok = tree ? ((anc[i] >> kk) & 1ull) != 0 : (base + kk < end);
-          if (WIN && !tree) ok = ok && (base + kk >= lo[i] || base + kk < p.sinks);
+          const bool ok = tree ? ((anc[i] >> kk) & 1ull) != 0 : (base + kk < k_end);
           const float x = ok ? sc[nt][2 * i + e] * p.scale_log2 : -INFINITY;
           sc[nt][2 * i + e] = x;
           mx = fmaxf(mx, x);
@@ -520,20 +501,20 @@ cudaError_t launch_f32(const AttnParams &p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, bool WIN>
+template <int D>
 cudaError_t launch_mma(const AttnParams &p, cudaStream_t s) {
   const size_t smem = attn_smem_bytes<D>();
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<D, WIN>,
+    cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   dim3 grid(p.m_tiles * p.splits, p.Hkv, p.B);
-  attn_mma_kernel<D, WIN><<<grid, kThreads, smem, s>>>(p);
+  attn_mma_kernel<D><<<grid, kThreads, smem, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   attn_combine_kernel<D><<<dim3(p.M, p.Hkv, p.B), D, 0, s>>>(p);
@@ -570,12 +551,9 @@ AttnPlan attn_plan(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, int max_pr
 }
 
 cudaError_t launch_attention(sv_dtype dt, const AttnParams &p, cudaStream_t s) {
-  if (p.window > 0) {
-    if (dt == SV_F32) return p.D == 64 ? launch_f32<64, true>(p, s) : launch_f32<128, true>(p, s);
-    return p.D == 64 ? launch_mma<64, true>(p, s) : launch_mma<128, true>(p, s);
-  }
+  if (dt == SV_F32 && p.window > 0) return p.D == 64 ? launch_f32<64, true>(p, s) : launch_f32<128, true>(p, s);
   if (dt == SV_F32) return p.D == 64 ? launch_f32<64, false>(p, s) : launch_f32<128, false>(p, s);
-  return p.D == 64 ? launch_mma<64, false>(p, s) : launch_mma<128, false>(p, s);
+  return p.D == 64 ? launch_mma<64>(p, s) : launch_mma<128>(p, s);
 }
 
 }  // namespace sv

@@ -58,6 +58,10 @@ bool map5d_pages(CUtensorMap *m, const void *base, int heads, long long rows, in
 
 }  // namespace
 
+bool tma_rows_map(CUtensorMap *m, const void *base, int D, int heads, long long rows, int box_rows) {
+  return map3d(m, base, D, heads, rows, 1, box_rows);
+}
+
 bool tc_eligible(sv_dtype dt, int N, int Hq, int Hkv, int D, int paged_block_size) {
   if (dt != SV_BF16 || (D != 64 && D != 128) || N > 64 || Hkv < 1 || Hq % Hkv != 0) return false;
   const int G = Hq / Hkv;

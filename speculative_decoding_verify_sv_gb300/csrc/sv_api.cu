@@ -42,6 +42,7 @@ sv_status cuda_fail(cudaError_t e, const char *what) {
 }
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxRows = INT32_MAX - 4096;  // rows that 32-bit coordinates reach (tiles may run past the end)
 constexpr int kMaxGridZ = 65535;  // largest y and z extents of a launch grid
 
 // The tensor-core attention kernel's limit on a wait for progress (sv_set_wait_limit_ns).
@@ -169,6 +170,9 @@ sv_status check_cache(const sv_kv_cache &c, bool writable, int B) {
   return SV_OK;
 }
 
+// The most prefix positions that a window holds.
+int window_span(int window, int max_prefix) { return window - 1 < max_prefix ? window - 1 : max_prefix; }
+
 // The general attention kernel keeps its partials behind the words that the tensor-core
 // kernel's calls count in (the workspace's first 256 bytes), so that calls of either kind may
 // share a workspace.
@@ -262,11 +266,13 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
   if (!std::isfinite(scale)) return fail(SV_ERR_INVALID_ARG, "scale is not finite");
   if (B == 0) return SV_OK;
   const int max_prefix = max_prefix_of(cache);
-  const int span = window > 0 && window - 1 < max_prefix ? window - 1 : max_prefix;
-  const sv::AttnPlan plan = sv::attn_plan(dt, B, N, Hq, Hkv, D, span, num_sms());
-  const bool use_tc = sv::tc_eligible(dt, N, Hq, Hkv, D, cache.block_table ? cache.block_size : 0);
+  const sv::AttnPlan plan = sv::attn_plan(dt, B, N, Hq, Hkv, D, max_prefix, num_sms());
+  const int paged = cache.block_table ? cache.block_size : 0;
+  const bool win = window > 0 && dt == SV_BF16;
+  const bool use_tc = sv::tc_eligible(dt, N, Hq, Hkv, D, paged) &&
+                      (!win || sv::window_prefers_tc(B, N, Hq, Hkv, window_span(window, max_prefix), num_sms()));
   const sv::TcPlan tplan = use_tc ? sv::tc_plan(B, N, Hq, Hkv, D, num_sms()) : sv::TcPlan{};
-  const size_t ws_need = use_tc ? tplan.ws_bytes : general_ws_bytes(plan);
+  const size_t ws_need = use_tc ? tplan.ws_bytes : (win ? 0 : general_ws_bytes(plan));
   if (ws_need > 0) {
     if (!workspace || workspace_bytes < ws_need)
       return fail(SV_ERR_WORKSPACE, "attention workspace %zu bytes, need %zu", workspace_bytes,
@@ -313,6 +319,10 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
     e = take_injected_failure() ? cudaErrorLaunchFailure
                                   : sv::launch_attention_tc(p, tplan, workspace, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) sv::count_launches(1);
+  } else if (win) {
+    e = take_injected_failure() ? cudaErrorLaunchFailure
+                                : sv::launch_window_attention(p, num_sms(), static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) sv::count_launches(1);
   } else {
     if (plan.ws_bytes > 0) {
       p.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + kGeneralWsOffset);
@@ -336,9 +346,11 @@ sv_status sv_tree_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, c
 
 size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
                                           int max_prefix, int window) {
-  if (window < 1) return 0;
-  return sv_tree_attention_workspace_size(dt, B, N, Hq, Hkv, D,
-                                          window - 1 < max_prefix ? window - 1 : max_prefix);
+  if (max_prefix < 0 || window < 1 || B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+  if (dt != SV_BF16 || (D != 64 && D != 128) || N > SV_MAX_TREE_NODES || Hq / Hkv > 128 ||
+      !sv::window_prefers_tc(B, N, Hq, Hkv, window_span(window, max_prefix), num_sms()))
+    return 0;
+  return sv::tc_plan(B, N, Hq, Hkv, D, num_sms()).ws_bytes;
 }
 
 sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
@@ -355,9 +367,10 @@ sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
   if (B > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "B = %d (supported up to %d)", B, kMaxGridZ);
   if (Hkv > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "Hkv = %d (supported up to %d)", Hkv, kMaxGridZ);
   const long long cap = cache.block_table ? (long long)cache.max_blocks * cache.block_size : cache.Lmax;
-  if (cap > INT32_MAX - 2 * SV_MAX_TREE_NODES)
-    return fail(SV_ERR_UNSUPPORTED, "the cache holds up to %lld positions (supported %d)", cap,
-                INT32_MAX - 2 * SV_MAX_TREE_NODES);
+  const long long rows = cache.block_table ? (long long)cache.num_blocks * cache.block_size : (long long)B * cache.Lmax;
+  if (cap > kMaxRows || rows > kMaxRows || (long long)B * N > kMaxRows)
+    return fail(SV_ERR_UNSUPPORTED, "a cache of %lld rows, up to %lld of a sequence (supported %d)", rows, cap, kMaxRows);
+  if ((long long)N * Hq > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "%d nodes of %d heads", N, Hq);
   if (cache.block_table && cache.block_size > 0 && cache.block_size % 16 != 0)
     return fail(SV_ERR_UNSUPPORTED, "block_size = %d must be a multiple of 16", cache.block_size);
   return attention_call(dt, B, N, Hq, Hkv, D, q, k_tree, v_tree, cache, parent, parent_stride, scale,

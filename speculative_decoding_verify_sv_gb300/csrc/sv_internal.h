@@ -98,6 +98,29 @@ bool tc_eligible(sv_dtype dt, int N, int Hq, int Hkv, int D, int paged_block_siz
 TcPlan tc_plan(int B, int N, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_attention_tc(const AttnParams &p, const TcPlan &pl, void *ws, cudaStream_t s);
 
+// A bf16 [rows, heads, D] tensor as a 3-D view with boxes of 64 columns of one head and box_rows
+// rows, 128-byte swizzle; false when the driver cannot encode it.
+bool tma_rows_map(CUtensorMap *m, const void *base, int D, int heads, long long rows, int box_rows);
+
+// Windowed attention of units with few query rows (bf16): clusters of CTAs per unit.
+struct WinParams {
+  CUtensorMap tm_kt, tm_vt, tm_kc, tm_vc;  // tree and cache K/V in boxes of 16 rows
+  const void *q;
+  void *out;
+  const int32_t *prefix_len, *block_table;
+  unsigned int *status;
+  int B, N, Hq, Hkv, G, M, m_tiles, cluster;
+  int Lmax, block_size, max_blocks, num_blocks, cap;
+  int window, sinks;
+  float scale_log2;
+  Tree tree;
+  unsigned long long wait_ns;
+};
+cudaError_t launch_window_attention(const AttnParams &p, int num_sms, cudaStream_t s);
+// Whether a windowed bf16 call of these sizes goes to the tensor-core kernel where that takes
+// its shape (span: the most prefix positions that a row's window holds).
+bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms);
+
 // Kernels launched by this library so far (all devices, all threads).
 void count_launches(unsigned n);
 

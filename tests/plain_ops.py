@@ -20,29 +20,32 @@ def window_attention(q, k_tree, v_tree, cache_k, cache_v, prefix_len, parents, s
     spread is sum(p |v|), the size that errors of the weights are relative to."""
     B, N, Hq, D = q.shape
     Hkv = k_tree.shape[2]
-    G = Hq // Hkv
     out = torch.zeros(B, N, Hq, D, dtype=torch.float64)
     spread = torch.zeros_like(out)
     for b in range(B):
         par = parents[b] if isinstance(parents[0], (list, tuple)) else parents
         L = int(prefix_len[b])
-        for n, path in enumerate(paths(par)):
-            P = L + len(path) - 1
-            keep = [p for p in range(L) if P - p < window or p < sinks]
-            nodes = [j for d, j in enumerate(path) if P - (L + d) < window or L + d < sinks]
-            if block_table is None:
-                kp, vp = cache_k[b, keep], cache_v[b, keep]
-            else:
-                rows = [int(block_table[b, p // block_size]) * block_size + p % block_size for p in keep]
-                kp = cache_k.reshape(-1, Hkv, D)[rows]
-                vp = cache_v.reshape(-1, Hkv, D)[rows]
-            k = torch.cat([kp, k_tree[b, nodes]]).double()
-            v = torch.cat([vp, v_tree[b, nodes]]).double()
-            for h in range(Hkv):
-                s = (q[b, n, h * G:(h + 1) * G].double() @ k[:, h].T) * scale
-                p = torch.softmax(s, -1)
-                out[b, n, h * G:(h + 1) * G] = p @ v[:, h]
-                spread[b, n, h * G:(h + 1) * G] = p @ v[:, h].abs()
+        path = paths(par)
+        P = [L + len(x) - 1 for x in path]
+        keep = [p for p in range(L) if p < sinks or min(P) - p < window]
+        see = torch.zeros(N, len(keep) + N, dtype=torch.bool)
+        for n in range(N):
+            see[n, :len(keep)] = torch.tensor([P[n] - p < window or p < sinks for p in keep], dtype=torch.bool)
+            for d, j in enumerate(path[n]):
+                see[n, len(keep) + j] = P[n] - (L + d) < window or L + d < sinks
+        if block_table is None:
+            kp, vp = cache_k[b, keep], cache_v[b, keep]
+        else:
+            rows = [int(block_table[b, p // block_size]) * block_size + p % block_size for p in keep]
+            kp = cache_k.reshape(-1, Hkv, D)[rows]
+            vp = cache_v.reshape(-1, Hkv, D)[rows]
+        k = torch.cat([kp, k_tree[b]]).double().permute(1, 2, 0)  # [Hkv, D, keys]
+        v = torch.cat([vp, v_tree[b]]).double().permute(1, 0, 2)  # [Hkv, keys, D]
+        x = q[b].double().view(N, Hkv, Hq // Hkv, D).permute(1, 0, 2, 3).reshape(Hkv, -1, D)
+        s = (x @ k * scale).view(Hkv, N, Hq // Hkv, -1).masked_fill(~see[None, :, None, :], -math.inf)
+        p = torch.softmax(s, -1).view(Hkv, -1, s.shape[-1])
+        for to, y in ((out, p @ v), (spread, p @ v.abs())):
+            to[b] = y.view(Hkv, N, Hq // Hkv, D).permute(1, 0, 2, 3).reshape(N, Hq, D)
     return out, spread
 
 

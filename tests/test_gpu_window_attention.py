@@ -105,6 +105,26 @@ def test_long_unit_cut_over_many_ctas(cuda_ok, paged):
     _check(inp, wl.TREE_T26, 4096, 4)
 
 
+# (nodes, group heads) -> units with 64, 104, 208 and 512 query rows, where many units with long
+# enough windows go to the 128-row tensor-core kernel: two row copies, one tile, two tiles, two
+# groups of two tiles
+@pytest.mark.parametrize("N,G,B,window", [(16, 4, 72, 1100), (26, 4, 64, 260), (26, 8, 48, 40), (26, 8, 48, 300),
+                                          (64, 8, 24, 17), (64, 8, 24, 200)])
+@pytest.mark.parametrize("D,block_size", [(128, 0), (128, 16), (64, 32), (128, 128), (64, 0)])
+def test_many_units_of_many_rows(cuda_ok, N, G, B, window, D, block_size):
+    Hkv = 8 if B > 24 else 4
+    par = wl.TREE_T26 if N == 26 else (wl.TREE_T64 if N == 64 else wl.chain_parent(N - 1))
+    g = torch.Generator().manual_seed(N + B)
+    lens = torch.randint(0, window + 150, (B,), generator=g).tolist()
+    lens[:4] = [0, 1, window, window + 17]
+    inp = wl.attention_inputs(B, N, G * Hkv, Hkv, D, lens, dtype=BF, paged=block_size > 0,
+                              block_size=block_size or 16, seed=16)
+    limit = inp["cache_k"].shape[1] if not block_size else inp["block_table"].shape[1] * block_size
+    assert sv.sv_window_attention_workspace_size(BF, B, N, G * Hkv, Hkv, D, limit, window) > 0
+    for sinks in (4, 0, 49):
+        _check(inp, par, window, sinks, block_size or 16)
+
+
 def test_whole_prefix_is_tree_attention(cuda_ok):
     """A window beyond every position sees what sv_tree_attention sees."""
     par = wl.TREE_T26
