@@ -219,8 +219,10 @@ struct TableParams {
   int32_t *out_free_head;              // [1]
   unsigned int *status;
   int B, T, block_size, max_blocks, num_blocks, num_free;
+  int cap;                             // positions of a table row (set at the launch, as are the
+  unsigned div_mul, div_shift;         // multiplier and shift of a division by block_size)
 };
-cudaError_t launch_block_tables(const TableParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_block_tables(TableParams p, int num_sms, cudaStream_t s);
 
 struct RopeParams {
   const void *qkv;                     // T rows, ld elements apart

@@ -26,38 +26,33 @@ namespace {
 constexpr int kTableThreads = 512;
 constexpr int kTableTokens = 4;  // neighbouring tokens per thread and step
 
-// a request's sizes, with what is out of range clamped (*bad set)
-__device__ __forceinline__ void request_sizes(const TableParams &p, int b, int *len, int *n, int *have,
-                                              int *need, bool *bad) {
-  const long long cap = (long long)p.max_blocks * p.block_size;
-  long long L = __ldg(p.length + b), x = __ldg(p.new_tokens + b);
-  *bad = L < 0 || L > cap || x < 0 || L + x > cap;
-  L = L < 0 ? 0 : (L > cap ? cap : L);
-  // (tokens past the table get no slot; more of them than the slot map has room for count as
-  // that many, so that a wild number does not make a long loop)
-  x = x < 0 ? 0 : min(x, min(cap - L + p.T, INT32_MAX - L));
-  *len = (int)L;
-  *n = (int)x;
-  *have = (int)((L + p.block_size - 1) / p.block_size);
-  const long long pages = (L + x + p.block_size - 1) / p.block_size;
-  *need = (int)max(0ll, min(pages, (long long)p.max_blocks) - *have);
+// n / block_size for 0 <= n < 2^31 by a multiplication (T. Granlund, P. Montgomery, "Division by
+// invariant integers using multiplication", 1994).
+__device__ __forceinline__ int page_of(const TableParams &p, int n) {
+  return (int)((__umulhi(p.div_mul, (unsigned)n) + (unsigned)n) >> p.div_shift);
 }
+__device__ __forceinline__ int pages_of(const TableParams &p, int n) { return n > 0 ? page_of(p, n - 1) + 1 : 0; }
 
 __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __grid_constant__ TableParams p) {
   extern __shared__ int table_smem[];
-  int *s_start = table_smem;            // [B + 1] first token of each request, at most INT32_MAX
-  int *s_base = table_smem + p.B + 1;   // [B] fresh pages before each request
+  int *s_start = table_smem;             // [B + 1] first token of each request, at most INT32_MAX
+  int *s_base = table_smem + p.B + 1;    // [B] fresh pages before each request
+  int *s_len = table_smem + 2 * p.B + 1; // [B] tokens that it has
   __shared__ long long s_tok[kTableThreads / 32], s_page[kTableThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool report = blockIdx.x == 0;
+  const long long head = p.free_head ? *p.free_head : 0;
 
   for (int b = tid; b < p.B; b += kTableThreads) {
-    int len, n, have, need;
-    bool bad;
-    request_sizes(p, b, &len, &n, &have, &need, &bad);
-    if (bad && report) set_status(p.status, SV_DEV_BAD_PREFIX);
-    s_start[b] = n;
-    s_base[b] = need;
+    int L = __ldg(p.length + b), x = __ldg(p.new_tokens + b);
+    if (report && (L < 0 || L > p.cap || x < 0 || x > p.cap - L)) set_status(p.status, SV_DEV_BAD_PREFIX);
+    L = L < 0 ? 0 : min(L, p.cap);
+    // (tokens past the table get no slot; more of them than the slot map has room for count as
+    // that many, so that a wild number does not make a long loop)
+    x = x < 0 ? 0 : (int)min((long long)x, min((long long)p.cap - L + p.T, (long long)INT32_MAX - L));
+    s_start[b] = x;
+    s_base[b] = max(0, min(pages_of(p, L + x), p.max_blocks) - pages_of(p, L));
+    s_len[b] = L;
   }
   __syncthreads();
   // each thread sums a run of requests (an odd run length: no bank conflicts), then the runs
@@ -104,7 +99,6 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   if (tid == 0) s_start[p.B] = (int)min(total, (long long)INT32_MAX);
   __syncthreads();
 
-  const long long head = p.free_head ? *p.free_head : 0;
   if (report) {
     for (int b = tid; b <= p.B; b += kTableThreads) p.token_start[b] = s_start[b];
     if (tid == 0) {
@@ -120,7 +114,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   const long long step = (long long)gridDim.x * kTableThreads * kTableTokens;
   for (long long t0 = ((long long)blockIdx.x * kTableThreads + tid) * kTableTokens; t0 < end; t0 += step) {
     int slot[kTableTokens], pos[kTableTokens];
-    int b = -1, len = 0, have = 0, pg = -1, off = 0, row = -1, stop = 0;
+    int b = -1, have = 0, pg = -1, off = 0, row = -1, stop = 0;
     long long fresh = 0;
 #pragma unroll
     for (int k = 0; k < kTableTokens; ++k) {
@@ -138,11 +132,10 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
         }
         b = lo;
         stop = s_start[b + 1];
-        int n, need;
-        bool bad;
-        request_sizes(p, b, &len, &n, &have, &need, &bad);
+        const int len = s_len[b];
+        have = pages_of(p, len);
         pos[k] = len + (int)(t - s_start[b]);
-        pg = pos[k] / p.block_size;
+        pg = page_of(p, pos[k]);
         off = pos[k] - pg * p.block_size;
         fresh = head + s_base[b] - have;
         look = true;
@@ -189,14 +182,19 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
 
 }  // namespace
 
-cudaError_t launch_block_tables(const TableParams &p, int num_sms, cudaStream_t s) {
-  const size_t smem = (size_t)(2 * p.B + 1) * sizeof(int);
+cudaError_t launch_block_tables(TableParams p, int num_sms, cudaStream_t s) {
+  const long long cap = (long long)p.max_blocks * p.block_size;
+  p.cap = (int)(cap < INT32_MAX ? cap : INT32_MAX);
+  p.div_shift = 0;
+  while ((1ll << p.div_shift) < p.block_size) ++p.div_shift;
+  p.div_mul = (unsigned)(((1ull << 32) * ((1ull << p.div_shift) - p.block_size)) / p.block_size + 1);
+  const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int);
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
     const cudaError_t e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)((2 * SV_MAX_TABLE_BATCH + 1) * sizeof(int)));
+                                               (int)((3 * SV_MAX_TABLE_BATCH + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
