@@ -8,8 +8,9 @@ kernels; there is no CPU fallback: if the library is missing the calls raise.
 """
 from __future__ import annotations
 
-import array
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -30,6 +31,7 @@ __all__ = [
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libsv.so")
+_BINDING_PATH = os.path.join(_PKG, "_build", "sv_binding.so")
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_WORKSPACE, SV_ERR_CUDA = 0, 1, 2, 3, 4
 SV_F32, SV_BF16 = 0, 1
@@ -58,6 +60,7 @@ class _KVCacheC(ctypes.Structure):
 
 
 _lib = None
+_binding = None
 _lock = threading.Lock()
 
 
@@ -132,6 +135,27 @@ def load_library():
             getattr(lib, fn).restype = ctypes.c_int32
         _lib = lib
         return lib
+
+
+def load_binding():
+    """Load sv_binding.so, the compiled calls of the operators around the KV cache (built beside
+    libsv.so); raise if it is missing."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    load_library()
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(_BINDING_PATH):
+                raise RuntimeError(f"sv_binding.so is not built ({_BINDING_PATH}); run "
+                                   "`python -c 'import __graft_entry__ as g; g.build()'`")
+            loader = importlib.machinery.ExtensionFileLoader("sv_binding", _BINDING_PATH)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("sv_binding", _BINDING_PATH,
+                                                                                       loader=loader))
+            loader.exec_module(m)
+            m.set_error(SVError)
+            _binding = m
+        return _binding
 
 
 def _check(code: int):
@@ -239,82 +263,6 @@ class KVCache:
         return self.block_table.shape[1] * int(self.block_size)
 
 
-def _int32(x, name: str) -> int:
-    x = int(x)
-    if not -2**31 <= x < 2**31:
-        raise ValueError(f"{name} = {x} is not a 32-bit number")
-    return x
-
-
-# The operators around the cache are called once per layer, or for a single token, where the
-# call's host side is what counts: their wrappers check a tensor and take its pointer in one
-# step, take the current stream's handle as it is, and hand plain numbers to the library.
-
-def _arg(t, name: str, dtype, shape, dev: int) -> int:
-    """The pointer of a contiguous CUDA tensor of this type and shape on device ``dev``."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or t.shape != shape \
-            or not t.is_contiguous():
-        _dev(t, name, dtype, shape)
-        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}: one call works on one device")
-    return t.data_ptr()
-
-
-def _home(t, name: str) -> int:
-    """The device index of a call, that of its first tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    return t.get_device()
-
-
-def _launch(fn, dev: int, stream, *args) -> None:
-    """fn(*args, stream) on device ``dev``, on its current stream unless one is given."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch(fn, dev, stream, *args)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    code = fn(*args, int(stream))
-    if code != SV_OK:
-        _check(code)
-
-
-def _tree_ptr(parent, B: int, N: int, dev: int):
-    """(what to keep alive, pointer, parent_stride) of a tree argument, as _tree_arg takes it."""
-    if isinstance(parent, torch.Tensor):
-        if parent.is_cuda:
-            ptr, stride, _ = _tree_arg(parent, B, N)
-            if parent.get_device() != dev:
-                raise ValueError(f"parent is on {parent.device}, the other tensors on cuda:{dev}")
-            return parent, ptr, stride
-        parent = parent.tolist()
-    rows = array.array("i", parent)
-    if len(rows) != N:
-        raise ValueError(f"parent has {len(rows)} entries, the tree has {N} rows")
-    return rows, rows.buffer_info()[0], 0
-
-
-def _cache_arg(cache: KVCache, dtype, B: int, Hkv: int, D: int, dev: int) -> _KVCacheC:
-    """The cache of these sequences and heads: contiguous [B,Lmax,Hkv,D], or pages of block_size
-    rows with a table row per sequence."""
-    k, table = cache.k, cache.block_table
-    if k.dtype is not dtype:
-        raise TypeError("cache dtype differs from q")
-    shape = k.shape
-    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D or (table is None and shape[0] != B):
-        raise ValueError(f"cache.k has shape {tuple(shape)}, expected [{'B' if table is None else 'blocks'}, rows, "
-                         f"{Hkv}, {D}] (B = {B})")
-    kp, vp = _arg(k, "cache.k", dtype, shape, dev), _arg(cache.v, "cache.v", dtype, shape, dev)
-    lens = _arg(cache.prefix_len, "cache.prefix_len", torch.int32, (B,), dev)
-    if table is None:
-        return _KVCacheC(kp, vp, lens, None, shape[1], 0, 0, 0)
-    if table.dim() != 2 or shape[1] != cache.block_size:
-        raise ValueError(f"blocks of {shape[1]} rows need block_size {shape[1]} and a block_table [B, max_blocks]")
-    return _KVCacheC(kp, vp, lens, _arg(table, "cache.block_table", torch.int32, (B, table.shape[1]), dev), 0,
-                     shape[1], table.shape[1], shape[0])
-
-
 def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], zero: bool = False):
     if nbytes == 0:
         return workspace, 0
@@ -373,31 +321,8 @@ def sv_window_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, window
     """Tree attention over the last ``window`` positions and the first ``sinks`` ones; arguments
     and result as sv_tree_attention.  A node at position P = prefix_len + depth sees a prefix
     position (or a node of its root path) p iff P - p < window or p < sinks."""
-    lib = load_library()
-    dev, dtype = _home(q, "q"), q.dtype
-    dt = _dt(q)
-    B, N, Hq, D = q.shape
-    Hkv = k_tree.shape[2]
-    qp = _arg(q, "q", dtype, q.shape, dev)
-    kp = _arg(k_tree, "k_tree", dtype, (B, N, Hkv, D), dev)
-    vp = _arg(v_tree, "v_tree", dtype, (B, N, Hkv, D), dev)
-    cs = _cache_arg(cache, dtype, B, Hkv, D, dev)
-    if out is None:
-        out = torch.empty_like(q)
-    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
-    if workspace is None:
-        need = lib.sv_window_attention_workspace_size(dt, B, N, Hq, Hkv, D, cache.max_prefix, window)
-        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device) if need else None
-    # (a workspace passed in must have been zero-filled before its first use; the library
-    # checks its size)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        ws_ptr = _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    keep, par, pstride = _tree_ptr(parent, B, N, dev)
-    _launch(lib.sv_window_attention, dev, stream, dt, B, N, Hq, Hkv, D, qp, kp, vp, cs, par, pstride, scale, window,
-            sinks, _arg(out, "out", dtype, q.shape, dev), ws_ptr, ws_bytes)
-    return out
+    return load_binding().window_attention(q, k_tree, v_tree, cache.k, cache.v, cache.prefix_len, cache.block_table,
+                                           cache.block_size, parent, scale, window, sinks, out, workspace, stream)
 
 
 # ------------------------------------------------------------- into the KV cache
@@ -409,67 +334,9 @@ def sv_block_tables(length, new_tokens, block_table, free_blocks, block_size, nu
     the new tokens' slot map.  block_table [B,max_blocks] is written in place.  Returns a dict of
     int32 device tensors: token_start [B+1], slots and positions [num_slots] (-1 past the
     total), free_head [1] (the advanced head, never the one passed in).  ``outs`` may hold those
-    tensors to write into; the ones it lacks are made (as views of one buffer)."""
-    lib = load_library()
-    dev, i32 = _home(length, "length"), torch.int32
-    if length.dim() != 1:
-        raise ValueError("length must be [B]")
-    B = length.shape[0]
-    T = _int32(num_slots, "num_slots")
-    if T < 0:
-        raise ValueError(f"num_slots = {T}")
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table must be [B={B}, max_blocks]")
-    columns, n_free = block_table.shape[1], free_blocks.numel()
-    if not outs:
-        outs = {} if outs is None else outs
-        pad = -T % 4  # (the maps start on 16-byte boundaries)
-        buf = torch.empty(2 * (T + pad) + B + 2, dtype=i32, device=length.device)
-        outs["slots"] = buf.as_strided((T,), (1,), 0)
-        outs["positions"] = buf.as_strided((T,), (1,), T + pad)
-        outs["token_start"] = buf.as_strided((B + 1,), (1,), 2 * (T + pad))
-        outs["free_head"] = buf.as_strided((1,), (1,), 2 * (T + pad) + B + 1)
-        slots = buf.data_ptr()
-        positions = slots + 4 * (T + pad)
-        start = positions + 4 * (T + pad)
-        head = start + 4 * (B + 1)
-    else:
-        for name, shape in (("token_start", (B + 1,)), ("slots", (T,)), ("positions", (T,)), ("free_head", (1,))):
-            if name not in outs:
-                outs[name] = torch.empty(shape, dtype=i32, device=length.device)
-        slots = _arg(outs["slots"], "slots", i32, (T,), dev)
-        positions = _arg(outs["positions"], "positions", i32, (T,), dev)
-        start = _arg(outs["token_start"], "token_start", i32, (B + 1,), dev)
-        head = _arg(outs["free_head"], "free_head", i32, (1,), dev)
-    _launch(lib.sv_block_tables, dev, stream, B, _arg(length, "length", i32, (B,), dev),
-            _arg(new_tokens, "new_tokens", i32, (B,), dev), _int32(block_size, "block_size"), columns,
-            _int32(num_blocks, "num_blocks"), _arg(free_blocks, "free_blocks", i32, free_blocks.shape, dev), n_free,
-            None if free_head is None else _arg(free_head, "free_head", i32, (1,), dev),
-            _arg(block_table, "block_table", i32, (B, columns), dev), T, start, slots, positions, head)
-    return outs
-
-
-def _rope_args(qkv, lead: int, Hq: int, Hkv: int, q_weight, k_weight, inv_freq):
-    """(device, D, rot, row stride, pointers of the weights and frequencies) of a projection qkv
-    [*lead, (Hq + 2 Hkv) * D] with evenly spaced rows."""
-    dev, f32 = _home(qkv, "qkv"), torch.float32
-    D, half = q_weight.numel(), inv_freq.numel()
-    width = (Hq + 2 * Hkv) * D
-    shape, step = qkv.shape, qkv.stride()
-    if len(shape) != lead + 1 or shape[lead] != width:
-        raise ValueError(f"qkv has shape {tuple(shape)}, expected {lead} leading dimensions and rows of {width}")
-    if lead == 1:
-        rows, ld = shape[0], step[0]
-    else:
-        rows, ld = shape[0] * shape[1], step[1] if shape[1] != 1 else step[0]
-        if rows and shape[0] != 1 and step[0] != shape[1] * ld:
-            raise ValueError("the rows of qkv must be evenly spaced")
-    if rows <= 1:
-        ld = width
-    if rows and (step[lead] != 1 or ld < width):
-        raise ValueError("the rows of qkv must be contiguous and apart")
-    return dev, D, 2 * half, ld, (_arg(q_weight, "q_weight", f32, (D,), dev), _arg(k_weight, "k_weight", f32, (D,), dev),
-                                  _arg(inv_freq, "inv_freq", torch.float64, (half,), dev))
+    tensors to write into; the ones it lacks are made and put into it."""
+    return load_binding().block_tables(length, new_tokens, block_table, free_blocks, block_size, num_blocks, num_slots,
+                                       free_head, outs, stream)
 
 
 def sv_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, positions, eps=1e-6, interleaved=False,
@@ -478,28 +345,8 @@ def sv_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, positions, eps=1
     slices of a wider projection), weights float32 [D], inv_freq float64 [rot/2], positions [T]
     int32 (negative: padding).  Returns (q [T,Hq,D], k, v): k and v are k_out and v_out
     [..., Hkv, D] (a KV cache, paged or not), token t in row slots[t]; without slots row t."""
-    lib = load_library()
-    dev, D, rot, ld, (qw, kw, freq) = _rope_args(qkv, 1, Hq, Hkv, q_weight, k_weight, inv_freq)
-    T, dtype, dt = qkv.shape[0], qkv.dtype, _dt(qkv)
-    at = _arg(positions, "positions", torch.int32, (T,), dev)
-    to = None
-    if slots is not None:
-        if k_out is None or v_out is None:
-            raise ValueError("slots need k_out and v_out")
-        to = _arg(slots, "slots", torch.int32, (T,), dev)
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dtype, device=qkv.device)
-    if k_out is None:
-        k_out = torch.empty((T, Hkv, D), dtype=dtype, device=qkv.device)
-    if v_out is None:
-        v_out = torch.empty((T, Hkv, D), dtype=dtype, device=qkv.device)
-    shape = k_out.shape
-    if len(shape) < 3 or shape[-2] != Hkv or shape[-1] != D:
-        raise ValueError(f"k_out has shape {tuple(shape)}, expected [..., {Hkv}, {D}]")
-    _launch(lib.sv_qk_norm_rope, dev, stream, dt, T, Hq, Hkv, D, rot, 1 if interleaved else 0, qkv.data_ptr(), ld, qw, kw,
-            eps, freq, at, to, k_out.numel() // (Hkv * D), _arg(q_out, "q_out", dtype, (T, Hq, D), dev),
-            _arg(k_out, "k_out", dtype, shape, dev), _arg(v_out, "v_out", dtype, shape, dev))
-    return q_out, k_out, v_out
+    return load_binding().qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, positions, eps, interleaved, slots,
+                                       q_out, k_out, v_out, stream)
 
 
 def sv_tree_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, prefix_len, parent, eps=1e-6,
@@ -507,20 +354,8 @@ def sv_tree_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, prefix_len,
     """sv_qk_norm_rope for the rows of a candidate tree: qkv [B,N,(Hq+2Hkv)*D], node n of
     sequence b at position prefix_len[b] + depth(n).  Returns (q, k_tree, v_tree), the inputs of
     sv_tree_attention and sv_window_attention (``outs``: those three, to write into)."""
-    lib = load_library()
-    dev, D, rot, ld, (qw, kw, freq) = _rope_args(qkv, 2, Hq, Hkv, q_weight, k_weight, inv_freq)
-    B, N = qkv.shape[:2]
-    dtype, dt = qkv.dtype, _dt(qkv)
-    lens = _arg(prefix_len, "prefix_len", torch.int32, (B,), dev)
-    if outs is None:
-        new = dict(dtype=dtype, device=qkv.device)
-        outs = (torch.empty((B, N, Hq, D), **new), torch.empty((B, N, Hkv, D), **new), torch.empty((B, N, Hkv, D), **new))
-    q, k, v = outs
-    keep, par, pstride = _tree_ptr(parent, B, N, dev)
-    _launch(lib.sv_tree_qk_norm_rope, dev, stream, dt, B, N, Hq, Hkv, D, rot, 1 if interleaved else 0, qkv.data_ptr(), ld,
-            qw, kw, eps, freq, lens, par, pstride, _arg(q, "q", dtype, (B, N, Hq, D), dev),
-            _arg(k, "k_tree", dtype, (B, N, Hkv, D), dev), _arg(v, "v_tree", dtype, (B, N, Hkv, D), dev))
-    return q, k, v
+    return load_binding().tree_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, prefix_len, parent, eps,
+                                            interleaved, outs, stream)
 
 
 # ------------------------------------------------------------------ acceptance
