@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   __shared__ uint64_t sAnc[kMaxNodes];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kvh = blockIdx.y, b = blockIdx.z;
+  if (WIN) wait_previous();
   // sequence b's tree (shared, or its own row): ancestor masks of its nodes
   if (tid < kMaxNodes) sPar[tid] = tid < p.tree.N ? tree_parent(p.tree, b, tid) : -1;
   __syncthreads();
@@ -497,6 +498,7 @@ cudaError_t launch_f32(const AttnParams &p, cudaStream_t s) {
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   dim3 grid((p.M + kThreads / 32 - 1) / (kThreads / 32), p.Hkv, p.B);
+  if (WIN) return launch_close(attn_f32_kernel<D, WIN>, grid, kThreads, smem, s, p);
   attn_f32_kernel<D, WIN><<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }

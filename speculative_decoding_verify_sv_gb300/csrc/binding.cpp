@@ -101,6 +101,15 @@ at::Tensor make(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType ty
   return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
+// n elements of a buffer from element `offset` on, as a tensor of their own.
+at::Tensor part(const at::Tensor &buffer, int64_t offset, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(buffer.storage()),
+                                                          buffer.key_set(), buffer.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(buffer.storage_offset() + offset);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 // The stream of a call on device `dev`: the one given (a torch stream or a handle), else the
 // device's current one.
 void *stream_of(PyObject *o, int dev) {
@@ -270,15 +279,18 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
       Py_INCREF(outs);
     }
     try {
+      // new outputs are parts of one buffer, the slots and positions on 16-byte boundaries
+      const int64_t padded = (T + 3) / 4 * 4, offsets[4] = {2 * padded, 0, padded, 2 * padded + B + 1};
+      at::Tensor buffer;
       int32_t *ptr[4];
       for (int i = 0; i < 4; ++i) {
         PyObject *o = PyDict_GetItemString(outs, names[i]);
         if (o) {
           ptr[i] = tensor(o, names[i], at::kInt, {sizes[i]}, dev).data_ptr<int32_t>();
         } else {
-          at::Tensor t = make({sizes[i]}, len, at::kInt);
-          ptr[i] = t.data_ptr<int32_t>();
-          PyObject *w = THPVariable_Wrap(std::move(t));
+          if (!buffer.defined()) buffer = make({2 * padded + B + 2}, len, at::kInt);
+          ptr[i] = buffer.data_ptr<int32_t>() + offsets[i];
+          PyObject *w = THPVariable_Wrap(part(buffer, offsets[i], sizes[i]));
           if (!w || PyDict_SetItemString(outs, names[i], w) != 0) {
             Py_XDECREF(w);
             throw Refused();

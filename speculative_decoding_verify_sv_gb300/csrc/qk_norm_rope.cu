@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
   const int partner = INTERLEAVED || !turns ? lane : (second ? lane - half / V : lane + half / V);
   const int j0 = (partner % LPH) * V;
   float2 *cs = s_cs[warp];
+  wait_previous();
   if (threadIdx.x < D) {
     s_w[0][threadIdx.x] = p.q_weight[threadIdx.x];
     s_w[1][threadIdx.x] = p.k_weight[threadIdx.x];
@@ -257,9 +258,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
 
 template <typename T, int LPH>
 cudaError_t launch_rope(const RopeParams &p, int grid, cudaStream_t s) {
-  if (p.interleaved) qk_norm_rope_kernel<T, LPH, true><<<grid, kRopeWarps * 32, 0, s>>>(p);
-  else qk_norm_rope_kernel<T, LPH, false><<<grid, kRopeWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_close(p.interleaved ? qk_norm_rope_kernel<T, LPH, true> : qk_norm_rope_kernel<T, LPH, false>, dim3(grid),
+                      kRopeWarps * 32, 0, s, p);
 }
 
 }  // namespace

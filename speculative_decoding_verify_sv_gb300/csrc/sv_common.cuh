@@ -18,6 +18,35 @@ __device__ __forceinline__ void set_status(unsigned int *status, unsigned int bi
   if (status) atomicOr(status, bits);
 }
 
+// ------------------------------------------------- launches close to the previous kernel
+
+// Kernels that a call with this attribute launches begin with wait_previous(): the launch may then
+// be set up while the stream's previous kernel still runs, and nothing is read or written before
+// that kernel has completed.  Back to back an empty kernel costs 1.4 us launched this way and 2.05
+// us the plain way, and kernels of a few us are spared the rounding up to that step.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+inline cudaLaunchAttribute close_launch() {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
+// kernel<<<grid, threads, smem, s>>>(p) that way.
+template <typename P>
+cudaError_t launch_close(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1] = {close_launch()};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // ------------------------------------------------------------------ trees
 
 // Parent of node c (< N) of sequence b: the shared tree's, or the sequence's own row.

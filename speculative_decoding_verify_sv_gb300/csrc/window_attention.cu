@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   const int mt = unit % p.m_tiles, kvh = (unit / p.m_tiles) % p.Hkv, b = unit / p.m_tiles / p.Hkv;
   const bool reports = kvh == 0 && mt == 0 && rank == 0;
 
+  wait_previous();
   int L = p.prefix_len[b];
   if (L < 0 || L > p.cap) {
     if (reports && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
@@ -539,13 +540,14 @@ cudaError_t launch_window_typed(const WinParams &p, long long ctas, cudaStream_t
   cfg.blockDim = dim3(kWinThreads);
   cfg.dynamicSmemBytes = Lay::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0] = close_launch();
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)p.cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
