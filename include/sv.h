@@ -174,7 +174,7 @@ size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int H
  * they can be freed and used again.  Every other argument, the layouts, the kernels' shapes
  * and the workspace's rules (zero-filled before its first use; stream-ordered sharing, also
  * with sv_tree_attention) as sv_tree_attention; a paged block_size that is not a multiple of
- * 16 and B or Hkv above 65535 are SV_ERR_UNSUPPORTED.
+ * 16, and caches or batches of more rows than 32-bit coordinates reach, are SV_ERR_UNSUPPORTED.
  * A NaN or infinity in the V row of a key that some rows of a sequence see can also reach
  * its other rows of the same KV head (0 * NaN).
  * Workspace: sv_window_attention_workspace_size() bytes (max_prefix as there; 0 for float32, for up

@@ -11,10 +11,6 @@
 // cp.async pipeline and both products run on bf16 tensor cores with fp32 accumulators
 // and an online softmax.  Splits of the prefix merge in a second kernel by
 // log-sum-exp weights.
-//
-// fp32 with a sliding window and sinks (the WIN instances): node n at position P = L_b +
-// depth(n) sees a prefix position p (or a tree node at position p on its root path) iff
-// P - p < window or p < sinks.
 #include <atomic>
 #include <cfloat>
 
@@ -325,7 +321,7 @@ __host__ __device__ constexpr int f32_stages() { return D == 64 ? 8 : 6; }
 template <int D>
 __host__ __device__ constexpr size_t f32_stage_floats() { return (size_t)kF32Keys * (D + 4) + (size_t)kF32Keys * D; }
 
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) {
   constexpr int KC = kF32Keys, ST = f32_stages<D>();
   constexpr int KS = D + 4;                 // K row stride in shared memory (floats)
@@ -341,7 +337,6 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   __shared__ uint64_t sAnc[kMaxNodes];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kvh = blockIdx.y, b = blockIdx.z;
-  if (WIN) wait_previous();
   // sequence b's tree (shared, or its own row): ancestor masks of its nodes
   if (tid < kMaxNodes) sPar[tid] = tid < p.tree.N ? tree_parent(p.tree, b, tid) : -1;
   __syncthreads();
@@ -363,14 +358,8 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   const bool live = R < p.M;
   const int n = live ? R / p.G : 0, hq = kvh * p.G + (live ? R % p.G : 0);
 
-  // chunk c: prefix positions [32c, 32c + 32) for c < nP, then tree nodes from 32 (c - nP).
-  // With a window the prefix chunks start at `first`, after nS chunks of the sinks before it.
-  const int first = WIN ? window_first(L, p.window) : 0;
-  const int n_sinks = WIN ? min(p.sinks, first) : 0, nS = (n_sinks + KC - 1) / KC;
-  const int nP = nS + (L - first + KC - 1) / KC, nT = (p.N + KC - 1) / KC, nC = nP + nT;
-  // the prefix position of key `key` of chunk c < nP, and where the chunk's range ends
-  auto chunk_pos = [&](int c, int key) { return c < nS ? c * KC + key : first + (c - nS) * KC + key; };
-  auto chunk_end = [&](int c) { return c < nS ? n_sinks : L; };
+  // chunk c: prefix positions [32c, 32c + 32) for c < nP, then tree nodes from 32 (c - nP)
+  const int nP = (L + KC - 1) / KC, nT = (p.N + KC - 1) / KC, nC = nP + nT;
   auto stage_k = [&](int st) { return f32_ring + (size_t)st * f32_stage_floats<D>(); };
   auto stage_v = [&](int st) { return f32_ring + (size_t)st * f32_stage_floats<D>() + KC * KS; };
   auto issue = [&](int c, int st) {
@@ -381,8 +370,8 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
       const float *srck = gkc, *srcv = gvc;  // any valid address when nothing is read
       bool ok = false;
       if (c < nP) {
-        const int pos = chunk_pos(c, key);
-        if (pos < chunk_end(c)) {
+        const int pos = c * KC + key;
+        if (pos < L) {
           const long long row = cache_row(p, b, pos);
           if (row >= 0) {
             const size_t off = ((size_t)row * p.Hkv + kvh) * D + 4 * d4;
@@ -417,12 +406,7 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   for (int i = lane; i < D; i += 32)
     sQ[warp][i] = live ? gq[(((size_t)b * p.N + n) * p.Hq + hq) * D + i] : 0.f;
   __syncthreads();  // sQ, sAnc
-  uint64_t anc = sAnc[n];
-  int lo = 0;  // the first prefix position in this row's window
-  if constexpr (WIN) {
-    lo = window_first(L + max(__popcll(anc) - 1, 0), p.window);
-    anc = window_ancestors(anc, L, p.window, p.sinks);
-  }
+  const uint64_t anc = sAnc[n];
   float m = -INFINITY, l = 0.f, o[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) o[i] = 0.f;
@@ -435,10 +419,9 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
       const float *sk = stage_k(st), *sv = stage_v(st);
       // lane j scores key j of the chunk
       const bool tree_chunk = c >= nP;
-      const int j = tree_chunk ? (c - nP) * KC + lane : chunk_pos(c, lane);
+      const int j = tree_chunk ? (c - nP) * KC + lane : c * KC + lane;
       bool vis = sValid[st][lane] != 0;
       if (tree_chunk) vis = vis && ((anc >> j) & 1ull);
-      else if (WIN) vis = vis && (j >= lo || j < p.sinks);
       const float4 *kr = reinterpret_cast<const float4 *>(sk + lane * KS);
       const float4 *qr = reinterpret_cast<const float4 *>(sQ[warp]);
       float dot = 0.f;
@@ -485,21 +468,20 @@ __global__ void __launch_bounds__(kThreads) attn_f32_kernel(const AttnParams p) 
   for (int i = 0; i < PL; ++i) dst[lane + 32 * i] = o[i] * inv;
 }
 
-template <int D, bool WIN>
+template <int D>
 cudaError_t launch_f32(const AttnParams &p, cudaStream_t s) {
   const size_t smem = (size_t)f32_stages<D>() * f32_stage_floats<D>() * sizeof(float);
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D, WIN>,
+    const cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true);
   }
   dim3 grid((p.M + kThreads / 32 - 1) / (kThreads / 32), p.Hkv, p.B);
-  if (WIN) return launch_close(attn_f32_kernel<D, WIN>, grid, kThreads, smem, s, p);
-  attn_f32_kernel<D, WIN><<<grid, kThreads, smem, s>>>(p);
+  attn_f32_kernel<D><<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -553,8 +535,7 @@ AttnPlan attn_plan(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, int max_pr
 }
 
 cudaError_t launch_attention(sv_dtype dt, const AttnParams &p, cudaStream_t s) {
-  if (dt == SV_F32 && p.window > 0) return p.D == 64 ? launch_f32<64, true>(p, s) : launch_f32<128, true>(p, s);
-  if (dt == SV_F32) return p.D == 64 ? launch_f32<64, false>(p, s) : launch_f32<128, false>(p, s);
+  if (dt == SV_F32) return p.D == 64 ? launch_f32<64>(p, s) : launch_f32<128>(p, s);
   return p.D == 64 ? launch_mma<64>(p, s) : launch_mma<128>(p, s);
 }
 

@@ -43,7 +43,6 @@ sv_status cuda_fail(cudaError_t e, const char *what) {
 
 constexpr int kMaxDevices = 64;
 constexpr int kMaxRows = INT32_MAX - 4096;  // rows that 32-bit coordinates reach (tiles may run past the end)
-constexpr int kMaxGridZ = 65535;  // largest y and z extents of a launch grid
 
 // The tensor-core attention kernel's limit on a wait for progress (sv_set_wait_limit_ns).
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;
@@ -268,7 +267,7 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
   const int max_prefix = max_prefix_of(cache);
   const sv::AttnPlan plan = sv::attn_plan(dt, B, N, Hq, Hkv, D, max_prefix, num_sms());
   const int paged = cache.block_table ? cache.block_size : 0;
-  const bool win = window > 0 && dt == SV_BF16;
+  const bool win = window > 0;
   const bool use_tc = sv::tc_eligible(dt, N, Hq, Hkv, D, paged) &&
                       (!win || sv::window_prefers_tc(B, N, Hq, Hkv, window_span(window, max_prefix), num_sms()));
   const sv::TcPlan tplan = use_tc ? sv::tc_plan(B, N, Hq, Hkv, D, num_sms()) : sv::TcPlan{};
@@ -321,7 +320,8 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
     if (e == cudaSuccess) sv::count_launches(1);
   } else if (win) {
     e = take_injected_failure() ? cudaErrorLaunchFailure
-                                : sv::launch_window_attention(p, num_sms(), static_cast<cudaStream_t>(stream));
+        : dt == SV_F32 ? sv::launch_window_attention_f32(p, num_sms(), static_cast<cudaStream_t>(stream))
+                       : sv::launch_window_attention(p, num_sms(), static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) sv::count_launches(1);
   } else {
     if (plan.ws_bytes > 0) {
@@ -364,13 +364,11 @@ sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
   if (sinks > SV_MAX_SINKS)
     return fail(SV_ERR_UNSUPPORTED, "sinks = %d (supported 0..%d)", sinks, SV_MAX_SINKS);
   if (!(scale > 0.f)) return fail(SV_ERR_INVALID_ARG, "scale must be positive");
-  if (B > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "B = %d (supported up to %d)", B, kMaxGridZ);
-  if (Hkv > kMaxGridZ) return fail(SV_ERR_UNSUPPORTED, "Hkv = %d (supported up to %d)", Hkv, kMaxGridZ);
   const long long cap = cache.block_table ? (long long)cache.max_blocks * cache.block_size : cache.Lmax;
   const long long rows = cache.block_table ? (long long)cache.num_blocks * cache.block_size : (long long)B * cache.Lmax;
   if (cap > kMaxRows || rows > kMaxRows || (long long)B * N > kMaxRows)
     return fail(SV_ERR_UNSUPPORTED, "a cache of %lld rows, up to %lld of a sequence (supported %d)", rows, cap, kMaxRows);
-  if ((long long)N * Hq > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "%d nodes of %d heads", N, Hq);
+  if ((long long)B * N * Hq > kMaxRows || (long long)B * Hkv * 64 > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "B = %d, N = %d, Hq = %d: too many query rows", B, N, Hq);
   if (cache.block_table && cache.block_size > 0 && cache.block_size % 16 != 0)
     return fail(SV_ERR_UNSUPPORTED, "block_size = %d must be a multiple of 16", cache.block_size);
   return attention_call(dt, B, N, Hq, Hkv, D, q, k_tree, v_tree, cache, parent, parent_stride, scale,

@@ -42,8 +42,7 @@ struct AttnParams {
   int M, m_tiles, Mpad;  // query rows per (b, kv head) = N*G, tiles of 64 rows
   int splits, chunk;     // prefix split: split s covers [s*chunk, (s+1)*chunk)
   // sliding window (0 = the whole prefix) and the first `sinks` positions that stay visible
-  // outside it; with a window the splits cover [first + s*chunk, ...), first the earliest
-  // position in the root's window
+  // outside it
   int window, sinks;
   float scale_log2;      // softmax scale * log2(e)
   float scale;
@@ -117,6 +116,8 @@ struct WinParams {
   unsigned long long wait_ns;
 };
 cudaError_t launch_window_attention(const AttnParams &p, int num_sms, cudaStream_t s);
+// The same in fp32 (any number of rows; p.splits is set at the launch: the CTAs per unit).
+cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t s);
 // Whether a windowed bf16 call of these sizes goes to the tensor-core kernel where that takes
 // its shape (span: the most prefix positions that a row's window holds).
 bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms);

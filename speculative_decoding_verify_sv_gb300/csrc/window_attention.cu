@@ -29,6 +29,7 @@
 #include <atomic>
 #include <cfloat>
 
+#include "cluster.cuh"
 #include "sv_common.cuh"
 #include "sv_internal.h"
 #include "tc_primitives.cuh"
@@ -73,33 +74,6 @@ struct WinLayout {
   static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
 };
 
-__device__ __forceinline__ unsigned win_cluster_rank() {
-  unsigned r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void win_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n"
-               "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ uint32_t win_remote(const void *local, unsigned rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float win_remote_f32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 win_remote_f32x4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -147,7 +121,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   volatile int *s_bad = reinterpret_cast<volatile int *>(sm + Lay::OFF_BAD) + slice * ST;
   uint8_t *ring = sm + slice * ST * Lay::G_BYTES;
 
-  const unsigned C = p.cluster, rank = C > 1 ? win_cluster_rank() : 0;
+  const unsigned C = p.cluster, rank = C > 1 ? cluster_rank() : 0;
   const int unit = blockIdx.x / C;
   const int mt = unit % p.m_tiles, kvh = (unit / p.m_tiles) % p.Hkv, b = unit / p.m_tiles / p.Hkv;
   const bool reports = kvh == 0 && mt == 0 && rank == 0;
@@ -494,28 +468,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     if (C > 1) *reinterpret_cast<float4 *>(acc + (size_t)r * OS + 4 * d4) = x;
     else store(r, d4, x, s_cl[r] > 0.f ? 1.f / s_cl[r] : 0.f);
   }
-  if (C > 1) {
-    // the cluster's CTAs share the rows out: each reads all of its share's partial results
-    win_cluster_sync();
-    for (int u = (int)rank * kWinThreads + tid; u < RB * (D / 4); u += (int)C * kWinThreads) {
-      const int r = u / (D / 4), d4 = u % (D / 4);
-      float top = kWinNone;
-      for (unsigned c = 0; c < C; ++c) top = fmaxf(top, win_remote_f32(win_remote(s_cm + r, c)));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-      for (unsigned c = 0; c < C; ++c) {
-        const float w = ex2_approx(win_remote_f32(win_remote(s_cm + r, c)) - top);
-        const float4 y = win_remote_f32x4(win_remote(acc + (size_t)r * OS + 4 * d4, c));
-        sum += w * win_remote_f32(win_remote(s_cl + r, c));
-        x.x += w * y.x;
-        x.y += w * y.y;
-        x.z += w * y.z;
-        x.w += w * y.w;
-      }
-      store(r, d4, x, sum > 0.f ? 1.f / sum : 0.f);
-    }
-    win_cluster_sync();  // no CTA leaves while its shared memory is read
-  }
+  if (C > 1) cluster_merge<D>(acc, OS, s_cm, s_cl, RB, C, rank, kWinNone, store);
   if (tid == 0) {
     if (!layout_ok) set_status(p.status, SV_DEV_LAYOUT);
     else if (*abort_flag) set_status(p.status, SV_DEV_TIMEOUT);
