@@ -24,7 +24,7 @@
 // weight; the sum is of the unrounded ones); scores, weights, sums and outputs are fp32.
 //
 // The slices merge in shared memory by weights 2^(m_slice - m).  Few long units: a cluster of
-// up to 16 CTAs shares a unit's groups and merges through distributed shared memory, without a
+// up to 8 CTAs shares a unit's groups and merges through distributed shared memory, without a
 // workspace or a second launch.
 #include <atomic>
 #include <cfloat>
@@ -483,8 +483,7 @@ cudaError_t launch_window_typed(const WinParams &p, long long ctas, cudaStream_t
   cudaGetDevice(&dev);
   auto kern = window_attn_kernel<D, NT, RG>;
   if (dev < 0 || dev >= 64 || !attr[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev].store(true);
   }
@@ -578,15 +577,15 @@ cudaError_t launch_window_attention(const AttnParams &a, int num_sms, cudaStream
   const int nt = rows_plan.nt, rg = rows_plan.rg;
   p.m_tiles = rows_plan.m_tiles;
   // CTAs per unit: waves of resident CTAs times the length of one, which costs about 12 groups
-  // (its start and merge) beside its share of the window's groups.  Clusters of 16 find room for
-  // fewer CTAs at a time (16 of them, 256 CTAs, took two waves: 25 us against 13)
-  const long long units = (long long)a.B * a.Hkv * p.m_tiles;
+  // (its start and merge) beside its share of the window's groups.  (Clusters of 16 gain little on
+  // the longest windows and start later: 8 units of 4 rows, window 1024, 7.2 us against 6.6; 16
+  // such clusters find no room together, 25 us against 13.)
+  const long long units = (long long)a.B * a.Hkv * p.m_tiles, slots = 2ll * num_sms;
   const int span = a.window - 1 < a.cap ? a.window - 1 : a.cap;
   const int groups = span / kWinGroup + (a.N + a.sinks) / kWinGroup + 2;
   long long best = 0;
   p.cluster = 1;
-  for (int c = 1; c <= 16; c *= 2) {
-    const long long slots = c == 16 ? num_sms : 2ll * num_sms;
+  for (int c = 1; c <= 8; c *= 2) {
     const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 12);
     if (c == 1 || cost < best) {
       best = cost;

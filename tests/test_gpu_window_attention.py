@@ -247,7 +247,52 @@ def test_refusals_and_empty_batch(cuda_ok):
         _call(inp, par, 2 ** 31, 0)
     with pytest.raises(ValueError):
         _call(dict(inp, cache_k=inp["cache_k"][:1], cache_v=inp["cache_v"][:1]), par, 4, 0)
+    big = _cuda(wl.attention_inputs(64, 26, 32, 4, 64, [300] * 64, dtype=BF, seed=17))
+    need = sv.sv_window_attention_workspace_size(BF, 64, 26, 32, 4, 64, big["cache_k"].shape[1], 300)
+    with pytest.raises(sv.SVError) as e:
+        _call(big, wl.TREE_T26, 300, 0, workspace=torch.zeros(need - 1, dtype=torch.uint8, device="cuda"))
+    assert need > 0 and e.value.code == sv.SV_ERR_WORKSPACE
     n0 = sv.sv_kernel_launches()
     empty = dict(inp, **{k: inp[k][:0] for k in ("q", "k_tree", "v_tree", "cache_k", "cache_v", "prefix_len")})
     assert _call(empty, par, 4, 0).shape == (0, 5, 8, 128)
     assert sv.sv_kernel_launches() == n0 and sv.sv_read_device_status() == 0
+
+
+def test_injected_launch_failure_writes_nothing(cuda_ok):
+    """Each kernel's call reports the failure, launches nothing and works at the next try."""
+    for dtype, B, N, Hq, Hkv, D in ((BF, 3, 5, 8, 2, 128), (F32, 3, 5, 8, 2, 64), (BF, 64, 26, 32, 4, 64)):
+        par = wl.TREE_T26 if N == 26 else wl.chain_parent(4)
+        inp = _cuda(wl.attention_inputs(B, N, Hq, Hkv, D, [300] * B, dtype=dtype, seed=18))
+        want = _call(inp, par, 300, 4)
+        out = torch.full_like(want, 7.0)
+        n0 = sv.sv_kernel_launches()
+        sv.sv_inject_launch_failures(1)
+        try:
+            with pytest.raises(sv.SVError) as e:
+                _call(inp, par, 300, 4, out=out)
+        finally:
+            sv.sv_inject_launch_failures(0)
+        assert e.value.code == sv.SV_ERR_CUDA and sv.sv_kernel_launches() == n0
+        torch.cuda.synchronize()
+        assert (out == 7.0).all()
+        assert torch.equal(_call(inp, par, 300, 4, out=out), want)
+
+
+def test_waits_that_run_out_return(cuda_ok):
+    """With the wait limit far below a copy's time the call returns and reports it; the next one is
+    right.  (Nothing hangs: the waits are bounded, the test shortens their bound.)"""
+    for N, Hq in ((1, 8), (16, 64)):
+        inp = wl.attention_inputs(2, N, Hq, 2, 128, [1500, 900], dtype=BF, seed=19)
+        g, par = _cuda(inp), wl.chain_parent(N - 1)
+        want = _call(g, par, 1024, 4)
+        sv.sv_read_device_status()
+        try:
+            sv.sv_set_wait_limit_ns(100)
+            _call(g, par, 1024, 4)
+            torch.cuda.synchronize()
+            st = sv.sv_read_device_status()
+        finally:
+            sv.sv_set_wait_limit_ns(0)
+        assert st & ~sv.SV_DEV_TIMEOUT == 0
+        assert torch.equal(_call(g, par, 1024, 4), want)
+        assert sv.sv_read_device_status() == 0
