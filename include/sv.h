@@ -234,7 +234,7 @@ sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_token
  * slots[t] (int32 [T], as sv_block_tables makes them: a paged pool seen as num_blocks *
  * block_size rows; a negative slot writes no K/V; slots of one call must differ), or with
  * slots NULL in row t (num_rows >= T).  A slot >= num_rows is skipped and sets
- * SV_DEV_BAD_BLOCK.  Outputs must not overlap qkv (SV_ERR_INVALID_ARG).
+ * SV_DEV_BAD_BLOCK.  Outputs must overlap neither qkv nor one another (SV_ERR_INVALID_ARG).
  * dt: SV_BF16 or SV_F32.  D in {64, 128}; rot a multiple of 16 up to D; qkv, the outputs and
  * the rows of qkv 16-byte aligned.  No workspace. */
 sv_status sv_qk_norm_rope(sv_dtype dt, int T, int Hq, int Hkv, int D, int rot, int interleaved,

@@ -101,12 +101,13 @@ at::Tensor make(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType ty
   return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
-// n elements of a buffer from element `offset` on, as a tensor of their own.
-at::Tensor part(const at::Tensor &buffer, int64_t offset, int64_t n) {
+// A part of a new buffer, from element `offset` on, as a tensor of its own (one allocation for a
+// call's outputs).
+at::Tensor part(const at::Tensor &buffer, int64_t offset, at::IntArrayRef shape) {
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(buffer.storage()),
                                                           buffer.key_set(), buffer.dtype());
   t.unsafeGetTensorImpl()->set_storage_offset(buffer.storage_offset() + offset);
-  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
   return t;
 }
 
@@ -290,7 +291,7 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         } else {
           if (!buffer.defined()) buffer = make({2 * padded + B + 2}, len, at::kInt);
           ptr[i] = buffer.data_ptr<int32_t>() + offsets[i];
-          PyObject *w = THPVariable_Wrap(part(buffer, offsets[i], sizes[i]));
+          PyObject *w = THPVariable_Wrap(part(buffer, offsets[i], {sizes[i]}));
           if (!w || PyDict_SetItemString(outs, names[i], w) != 0) {
             Py_XDECREF(w);
             throw Refused();
@@ -408,9 +409,11 @@ PyObject *tree_qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       k = tensor(o[1], "k_tree", type, {B, N, p.Hkv, p.D}, p.dev);
       v = tensor(o[2], "v_tree", type, {B, N, p.Hkv, p.D}, p.dev);
     } else {
-      q = make({B, N, p.Hq, p.D}, p.qkv, type);
-      k = make({B, N, p.Hkv, p.D}, p.qkv, type);
-      v = make({B, N, p.Hkv, p.D}, p.qkv, type);
+      const int64_t head = B * N * p.D;
+      const at::Tensor buffer = make({head * (p.Hq + 2 * p.Hkv)}, p.qkv, type);
+      q = part(buffer, 0, {B, N, p.Hq, p.D});
+      k = part(buffer, head * p.Hq, {B, N, p.Hkv, p.D});
+      v = part(buffer, head * (p.Hq + p.Hkv), {B, N, p.Hkv, p.D});
     }
     check(sv_tree_qk_norm_rope(p.dt, (int)B, (int)N, (int)p.Hq, (int)p.Hkv, (int)p.D, 2 * (int)p.freq.numel(), interleaved,
                                p.qkv.data_ptr(), p.ld, p.qw.const_data_ptr<float>(), p.kw.const_data_ptr<float>(),

@@ -792,6 +792,7 @@ static sv_status rope_call(sv_dtype dt, int D, sv::RopeParams &p, long long T, v
   if (p.rot < 16 || p.rot > D || p.rot % 16 != 0)
     return fail(SV_ERR_UNSUPPORTED, "rotary dim %d (supported: multiples of 16 up to the head dim %d)", p.rot, D);
   if (T > INT32_MAX) return fail(SV_ERR_UNSUPPORTED, "%lld tokens", T);
+  if (p.num_rows > (1ll << 40)) return fail(SV_ERR_UNSUPPORTED, "%lld rows", p.num_rows);
   const long long width = ((long long)p.Hq + 2ll * p.Hkv) * D, esize = dt == SV_BF16 ? 2 : 4;
   if (width > INT32_MAX) return fail(SV_ERR_UNSUPPORTED, "a token's row of %lld elements", width);
   if (p.ld < width) return fail(SV_ERR_INVALID_ARG, "ld = %lld is below the row's %lld elements", p.ld, width);
@@ -809,8 +810,16 @@ static sv_status rope_call(sv_dtype dt, int D, sv::RopeParams &p, long long T, v
     return o0 < in1 && in0 < o0 + bytes;
   };
   const long long kv_bytes = p.num_rows * p.Hkv * D * esize;
-  if (overlaps(p.q_out, T * p.Hq * D * esize) || overlaps(p.k_out, kv_bytes) || overlaps(p.v_out, kv_bytes))
+  const long long q_bytes = T * p.Hq * D * esize;
+  if (overlaps(p.q_out, q_bytes) || overlaps(p.k_out, kv_bytes) || overlaps(p.v_out, kv_bytes))
     return fail(SV_ERR_INVALID_ARG, "an output overlaps qkv");
+  auto meet = [](const void *a, long long na, const void *b, long long nb) {
+    const char *a0 = static_cast<const char *>(a), *b0 = static_cast<const char *>(b);
+    return na > 0 && nb > 0 && a0 < b0 + nb && b0 < a0 + na;
+  };
+  if (meet(p.q_out, q_bytes, p.k_out, kv_bytes) || meet(p.q_out, q_bytes, p.v_out, kv_bytes) ||
+      meet(p.k_out, kv_bytes, p.v_out, kv_bytes))
+    return fail(SV_ERR_INVALID_ARG, "two outputs overlap");
   p.T = (int)T;
   p.status = status_word();
   if (!p.status) return fail(SV_ERR_CUDA, "no CUDA device");

@@ -9,7 +9,7 @@ import speculative_decoding_verify_sv_gb300 as sv
 from speculative_decoding_verify_sv_gb300 import build as svbuild
 
 P = ctypes.c_void_p(1 << 20)
-FAR = ctypes.c_void_p(1 << 40)
+FAR, FAR2, FAR3 = (ctypes.c_void_p(k << 40) for k in (1, 2, 3))
 
 
 @pytest.fixture(scope="module")
@@ -77,7 +77,7 @@ def test_block_tables_rejects_before_launch(lib):
 
 
 def _rope(lib, dt=1, T=4, Hq=8, Hkv=2, D=128, rot=128, qkv=P, ld=1536, qw=P, kw=P, eps=1e-6, freq=P, positions=P,
-          slots=None, rows=4, q=FAR, k=FAR, v=FAR):
+          slots=None, rows=4, q=FAR, k=FAR2, v=FAR3):
     return lib.sv_qk_norm_rope(dt, T, Hq, Hkv, D, rot, 0, qkv, ld, qw, kw, eps, freq, positions, slots, rows, q, k, v, None)
 
 
@@ -90,13 +90,13 @@ def test_qk_norm_rope_rejects_before_launch(lib):
                      (bad, dict(qw=None)), (bad, dict(kw=None)), (bad, dict(freq=None)), (bad, dict(positions=None)),
                      (bad, dict(q=None)), (bad, dict(k=None)), (bad, dict(v=None)), (bad, dict(q=ctypes.c_void_p(8))),
                      (bad, dict(rows=3)), (bad, dict(rows=-1)), (bad, dict(q=inside)), (bad, dict(k=inside)),
-                     (bad, dict(v=P)), (no, dict(Hq=2 ** 25, ld=2 ** 40))):
+                     (bad, dict(v=P)), (bad, dict(k=FAR)), (bad, dict(v=FAR2)), (no, dict(rows=2 ** 41)), (no, dict(Hq=2 ** 25, ld=2 ** 40))):
         assert _rope(lib, **kw) == code, kw
     assert _rope(lib, T=0, qkv=None, qw=None, kw=None, freq=None, positions=None, q=None, k=None, v=None, rows=0) == sv.SV_OK
     par = (ctypes.c_int32 * 3)(-1, 0, 0)
 
     def tree(B=2, N=3, parent=par, prefix=P, rot=64):
-        return lib.sv_tree_qk_norm_rope(1, B, N, 8, 2, 128, rot, 0, P, 1536, P, P, 1e-6, P, prefix, parent, 0, FAR, FAR, FAR,
+        return lib.sv_tree_qk_norm_rope(1, B, N, 8, 2, 128, rot, 0, P, 1536, P, P, 1e-6, P, prefix, parent, 0, FAR, FAR2, FAR3,
                                         None)
     assert tree(B=-1) == bad and tree(N=0) == bad and tree(N=65) == no and tree(prefix=None) == bad
     assert tree(parent=(ctypes.c_int32 * 3)(-1, 2, 0)) == bad and tree(parent=None) == bad and tree(rot=12) == no

@@ -135,13 +135,19 @@ def test_whole_prefix_is_tree_attention(cuda_ok):
     assert (full - win).abs().max().item() <= 2.0 ** -7 * full.abs().max().item()
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dtype,B,N,Hq,Hkv,D", [(BF, 5, 7, 8, 2, 128), (F32, 5, 7, 8, 2, 128), (BF, 5, 26, 8, 4, 64),
+                                                (BF, 64, 26, 64, 8, 128), (BF, 72, 26, 32, 8, 64)])
 @pytest.mark.parametrize("paged", [False, True])
-def test_nothing_leaks_from_what_no_row_sees(cuda_ok, dtype, paged):
+def test_nothing_leaks_from_what_no_row_sees(cuda_ok, dtype, B, N, Hq, Hkv, D, paged):
     """NaN and infinity in every cache position outside the window and the sinks, in the room
-    behind the prefixes and in the neighbours' rows change no bit; freed pages may hold any id."""
-    lens, window, sinks, par = [300, 40, 129, 33, 0], 37, 5, wl.TREE_EXAMPLE7
-    inp = wl.attention_inputs(5, 7, 8, 2, 128, lens, dtype=dtype, paged=paged, seed=11)
+    behind the prefixes and in the neighbours' rows change no bit; freed pages may hold any id.
+    (The last two shapes go to the 128-row kernel.)"""
+    par = wl.TREE_EXAMPLE7 if N == 7 else wl.TREE_T26
+    window, sinks = (37, 5) if B == 5 else (150, 21)
+    lens = ([300, 40, 129, 33, 0] * 15)[:B]
+    inp = wl.attention_inputs(B, N, Hq, Hkv, D, lens, dtype=dtype, paged=paged, seed=11)
+    if B > 5:
+        assert sv.sv_window_attention_workspace_size(dtype, B, N, Hq, Hkv, D, 300, window) > 0
     clean = _check(inp, par, window, sinks)
     seen = torch.zeros(inp["cache_k"].shape[:2], dtype=torch.bool)
     table = inp["block_table"]
@@ -168,7 +174,7 @@ def test_nothing_leaks_from_what_no_row_sees(cuda_ok, dtype, paged):
     for k in ("k_tree", "v_tree"):
         g[k][1] = float("nan")
     out = _call(g, par, window, sinks)
-    keep = [0, 2, 3, 4]
+    keep = [0] + list(range(2, B))
     assert torch.equal(out[keep], clean[keep])
     torch.cuda.synchronize()
     assert sv.sv_read_device_status() == 0
