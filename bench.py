@@ -591,7 +591,7 @@ def run_ours(args, dist: Dist):
     value = units / (dev_ms / 1e3)
     emitted_total = dist.sum(r["emitted"])
     a_ms, c_ms, achieved, c_gbs = _kernel_figures(r)
-    kernel_file = "attention_tc.cu" if r["tc"] else "attention.cu"
+    kernel_file = "attention_tc_kernel.cuh" if r["tc"] else "attention.cu"
     kernel_name = ("attn_tc_kernel (the one kernel of a sv_tree_attention call)" if r["tc"] else
                    "attn_mma_kernel / attn_f32_kernel + split merge")
     name = r["name"] if args.batch is None else f"{r['name']} with B={c['B']}"
