@@ -23,6 +23,10 @@
 // operand layout by an 8x8 transpose in registers, rounded to bf16 (off by at most 2^-8 of each
 // weight; the sum is of the unrounded ones); scores, weights, sums and outputs are fp32.
 //
+// Bound by HBM for many units: 256 ragged requests of 5 nodes, 32:8 heads of 128, window 1024 in pages
+// of 16, 177 us, 6.1 TB/s, 90 % of the measured copy rate (the 128-row kernel 268 us); by latency
+// for few: one token of one request, window 1024, 6.6 us (49).
+//
 // The slices merge in shared memory by weights 2^(m_slice - m).  Few long units: a cluster of
 // up to 8 CTAs shares a unit's groups and merges through distributed shared memory, without a
 // workspace or a second launch.
