@@ -1546,7 +1546,8 @@ cudaError_t launch_tc_typed(const TcParams &p, int grid, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, MT, CP, BN, STAGES, QBUF, PBUF, WIN>, p);
 }
 
-// The instance for a plan: D, M tiles MT and row copies CP.
+// The instance for a plan: D, M tiles MT and row copies CP.  (Windowed calls of up to 32 rows per
+// KV head, four row copies, go to the kernel of window_attention.cu.)
 template <bool WIN>
 cudaError_t launch_tc_plan(const TcParams &p, int D, const TcPlan &pl, cudaStream_t s) {
   if (D == 128) {
@@ -1556,12 +1557,14 @@ cudaError_t launch_tc_plan(const TcParams &p, int D, const TcPlan &pl, cudaStrea
     // us against 68.2 with the third V stage; ragged-paged, four row copies, 774 against
     // 764 the other way round).
     if (pl.MT == 2) return launch_tc_typed<128, 2, 1, 128, 2, 1, 1, WIN>(p, pl.grid, s);
-    if (pl.CP == 4) return launch_tc_typed<128, 1, 4, 128, 2, 1, 1, WIN>(p, pl.grid, s);
+    if constexpr (!WIN)
+      if (pl.CP == 4) return launch_tc_typed<128, 1, 4, 128, 2, 1, 1, WIN>(p, pl.grid, s);
     if (pl.CP == 2) return launch_tc_typed<128, 1, 2, 128, 2, 2, 1, WIN>(p, pl.grid, s);
     return launch_tc_typed<128, 1, 1, 128, 2, 1, 1, WIN>(p, pl.grid, s);
   }
   if (pl.MT == 2) return launch_tc_typed<64, 2, 1, 128, 4, 2, 1, WIN>(p, pl.grid, s);
-  if (pl.CP == 4) return launch_tc_typed<64, 1, 4, 128, 3, 2, 2, WIN>(p, pl.grid, s);
+  if constexpr (!WIN)
+    if (pl.CP == 4) return launch_tc_typed<64, 1, 4, 128, 3, 2, 2, WIN>(p, pl.grid, s);
   if (pl.CP == 2) return launch_tc_typed<64, 1, 2, 128, 3, 2, 2, WIN>(p, pl.grid, s);
   return launch_tc_typed<64, 1, 1, 128, 3, 2, 2, WIN>(p, pl.grid, s);
 }

@@ -347,7 +347,7 @@ sv_status sv_tree_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, c
 size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
                                           int max_prefix, int window) {
   if (max_prefix < 0 || window < 1 || B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
-  if (dt != SV_BF16 || (D != 64 && D != 128) || N > SV_MAX_TREE_NODES || Hq / Hkv > 128 ||
+  if (dt != SV_BF16 || (D != 64 && D != 128) || N > SV_MAX_TREE_NODES || 128 % (Hq / Hkv) != 0 ||
       !sv::window_prefers_tc(B, N, Hq, Hkv, window_span(window, max_prefix), num_sms()))
     return 0;
   return sv::tc_plan(B, N, Hq, Hkv, D, num_sms()).ws_bytes;
