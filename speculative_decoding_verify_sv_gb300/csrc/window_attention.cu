@@ -32,6 +32,7 @@
 // workspace or a second launch.
 #include <atomic>
 #include <cfloat>
+#include <type_traits>
 
 #include "cluster.cuh"
 #include "sv_common.cuh"
@@ -238,19 +239,6 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   }
   cp_async_wait<0>();
   __syncthreads();
-  uint32_t qf[NT][DT][2];  // this warp's rows as B operands, two 16-column steps per load
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int k = 0; k < DT; k += 2) {
-      uint32_t x[4];
-      const int r = rg * 8 * NT + 8 * j + (lane & 7), c = 2 * k + (lane >> 3);
-      ldmatrix_x4(x, s_q + (c >> 3) * (RB * 128) + sw128_offset(r, c & 7));
-      qf[j][k][0] = x[0];
-      qf[j][k][1] = x[1];
-      qf[j][k + 1][0] = x[2];
-      qf[j][k + 1][1] = x[3];
-    }
   const int lo_last = window_first(L + p.N - 1, p.window);  // no row's window starts later
 
   float o[DT][NT][4];
@@ -270,135 +258,208 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   // the four offsets differ by constants in bits 5 and 6
   const uint32_t k_off = sw128_offset(k_row, k_chunk), v_off = sw128_offset(v_row, v_chunk);
   const uint32_t ring_addr = smem_u32(ring);
+  // query rows as B operands: 8 rows of 8-column step j, 16-byte chunks 2k + 0..3 (two 16-column
+  // steps in one load), the same exclusive-or swizzle
+  const uint32_t q_row = (uint32_t)(rg * 8 * NT + (lane & 7)), q_addr = smem_u32(s_q) + q_row * 128u;
+  const uint32_t q_chunk = (uint32_t)(lane >> 3);
+  auto load_q = [&](int k, uint32_t (&q)[NT][4]) {
+    const uint32_t c = 2 * k + q_chunk;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      ldsm_x4(q[j], q_addr + (c >> 3) * (RB * 128) + j * 1024 + (((c & 7) ^ (q_row & 7)) << 4));
+  };
+  // held for good with one group at a time, loaded for each pair of groups
+  constexpr bool kHold = RG == 1 || NT < 4;
+  uint32_t held[kHold ? DT / 2 : 1][NT][4];
+  if constexpr (kHold) {
+#pragma unroll
+    for (int k = 0; k < DT; k += 2) load_q(k, held[k / 2]);
+  }
   int done = 0, issued = min(ST, n);
-  int st = -1, phase = 0;  // the stage of group i and the parity of its use
-  for (int i = 0; layout_ok && i < n; ++i) {
-    if (++st == ST) st = 0, phase ^= 1;
-    // the stage of group i - RG is filled again: two warps that share a slice need not be done
-    // with the previous group at the same time
-    if (i >= RG && i - RG + ST < n) {
-      const int prev = st >= RG ? st - RG : st - RG + ST;
-      issue(i - RG + ST, prev, st >= RG ? phase : phase ^ 1);
+  int st = 0, phase = 0;  // the stage of group i and the parity of its use
+  // One group at a time, the stage of group i - RG is filled again at the start of group i: two
+  // warps that share a slice need not be done with the previous group at the same time.  Two at a
+  // time, the stages of the last ones are filled again between the products of the next ones.
+  int before = 0;  // groups before i whose stages are not yet filled again
+  auto refill = [&](int i) {
+    for (; before > 0; --before) {
+      if (i - before + ST >= n) continue;
+      issue(i - before + ST, st >= before ? st - before : st - before + ST, st >= before ? phase : phase ^ 1);
       ++issued;
     }
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], phase, abort_flag, p.wait_ns))) break;
-    done = i + 1;
-    if (s_bad[st] == 0) {
-      const uint32_t stage = ring_addr + st * Lay::G_BYTES;
-      uint8_t *sv = ring + st * Lay::G_BYTES + Lay::K_BYTES;
-      uint32_t k_at[4], v_at[4];
+  };
+
+  // NG groups from group i on: scores, exponents, weights, outputs.  Two at a time where rows fill
+  // the operands (64 of them), so that the matrix instructions of one group hide the operand loads
+  // and latencies of the other: 512 units of 64 rows, window 4097, 299 us against 317 one at a
+  // time, while 40 rows would take 250 against 233: fewer copies are in flight meanwhile.
+  auto work = [&](auto ng, int i) {
+    constexpr int NG = decltype(ng)::value;
+    uint32_t stage[NG];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        k_at[q] = stage + (k_off ^ (q << 5));
-        v_at[q] = stage + Lay::K_BYTES + (v_off ^ (q << 5));
-      }
-      const int gi = g0 + slice + KS * i;
+    for (int g = 0; g < NG; ++g) stage[g] = ring_addr + (st + g >= ST ? st + g - ST : st + g) * Lay::G_BYTES;
+    auto load_k = [&](int k, uint32_t (&a)[NG][4]) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) ldsm_x4(a[g], stage[g] + (k_off ^ ((k & 3) << 5)) + (k >> 2) * (kWinGroup * 128));
+    };
+    auto load_v = [&](int d, uint32_t (&a)[NG][4]) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        ldsm_x4_trans(a[g], stage[g] + Lay::K_BYTES + (v_off ^ ((d & 3) << 5)) + (d >> 2) * (kWinGroup * 128));
+    };
+    float s[NG][NT][4];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) s[g][j][0] = s[g][j][1] = s[g][j][2] = s[g][j][3] = 0.f;
+    // each step's operands are loaded a step ahead of its products
+    uint32_t a[2][NG][4], q[2][NT][4];
+    if constexpr (!kHold) load_q(0, q[0]);
+    load_k(0, a[0]);
+#pragma unroll
+    for (int k = 0; k < DT; ++k) {
+      if (k + 1 < DT) load_k(k + 1, a[(k + 1) & 1]);
+      if (!kHold && k % 2 == 0 && k + 2 < DT) load_q(k + 2, q[(k / 2 + 1) & 1]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint32_t *b = kHold ? held[kHold ? k / 2 : 0][j] : q[(k / 2) & 1][j];
+          mma_bf16_16816(s[g][j], a[k & 1][g], b[2 * (k & 1)], b[2 * (k & 1) + 1]);
+        }
+    }
+    if (!kHold) refill(i);  // (by now the other warp of the slice is done with those stages too)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int gi = g0 + slice + KS * (i + g);
       const int base = gi < gs ? kWinGroup * (gi < gt ? gi : gi - gt) : first + kWinGroup * (gi - gs);
       // every row sees every key: inside the window of all rows, before the prefix's end
-      const bool plain = gi >= gs && base >= lo_last && base + kWinGroup <= L;
-
-      float s[NT][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      // each step's operand is loaded a step ahead of its products
-      auto load_k = [&](int k, uint32_t (&a)[4]) { ldsm_x4(a, k_at[k & 3] + (k >> 2) * (kWinGroup * 128)); };
-      auto load_v = [&](int d, uint32_t (&a)[4]) { ldsm_x4_trans(a, v_at[d & 3] + (d >> 2) * (kWinGroup * 128)); };
-      uint32_t a[2][4];
-      load_k(0, a[0]);
-#pragma unroll
-      for (int k = 0; k < DT; ++k) {
-        if (k + 1 < DT) load_k(k + 1, a[(k + 1) & 1]);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mma_bf16_16816(s[j], a[k & 1], qf[j][k][0], qf[j][k][1]);
-      }
-      if (!plain) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = rg * 8 * NT + 8 * j + 2 * ft + (e & 1), key = base + fg + (e >> 1) * 8;
-            bool see;
-            if (gi < gt) see = (s_anc[r] >> key) & 1ull;
-            else if (gi < gs) see = key < n_sinks;
-            else see = key < L && (key >= s_lo[r] || key < p.sinks);
-            if (!see) s[j][e] = -INFINITY;
-          }
-        }
-        // V rows that no row sees may hold anything: zero them, so that 0 * V stays 0
-        const int key = base + k_row;
-        const bool live = gi < gt ? key < p.N
-                                  : (gi < gs ? key < n_sinks : key < L && (key >= lo_root || key < p.sinks));
-        if (!live) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const int ch = k_chunk * (D / 16) + c;
-            *reinterpret_cast<uint4 *>(sv + (ch >> 3) * (kWinGroup * 128) + sw128_offset(k_row, ch & 7)) =
-                make_uint4(0, 0, 0, 0);
-          }
-        }
-        fence_proxy_async_smem();  // before the next copy into this stage
-        __syncwarp();
-      }
-
-      // The weights are taken against a maximum of each row that need not be the latest: only
-      // when a score passes it by more than 2^8 (or there is none yet) is it brought up to date
-      // over the warp's keys, and the sums and outputs with it.  Then no exchange between
-      // lanes is needed but one vote.
-      float x[NT][4], top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[j][e] = fmaf(s[j][e], sc, -m[j][e & 1]);
-          top = fmaxf(top, x[j][e]);
-        }
-      if (__any_sync(0xFFFFFFFFu, top > kWinRescale)) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          float a[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = fmaxf(s[j][e], s[j][e + 2]);
-            y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
-            y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
-            y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
-            y = fmaxf(y * sc, m[j][e]);
-            a[e] = ex2_approx(m[j][e] - y);
-            m[j][e] = y;
-            l[j][e] *= a[e];
-            x[j][e] = fmaf(s[j][e], sc, -y);
-            x[j][e + 2] = fmaf(s[j][e + 2], sc, -y);
-          }
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            o[d][j][0] *= a[0];
-            o[d][j][1] *= a[1];
-            o[d][j][2] *= a[0];
-            o[d][j][3] *= a[1];
-          }
-        }
-      }
-      load_v(0, a[0]);
-      uint32_t pb[NT][2];
+      if (gi >= gs && base >= lo_last && base + kWinGroup <= L) continue;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[j][e] = ex2_approx(x[j][e]);
-          l[j][e & 1] += x[j][e];
+          const int r = rg * 8 * NT + 8 * j + 2 * ft + (e & 1), key = base + fg + (e >> 1) * 8;
+          bool see;
+          if (gi < gt) see = (s_anc[r] >> key) & 1ull;
+          else if (gi < gs) see = key < n_sinks;
+          else see = key < L && (key >= s_lo[r] || key < p.sinks);
+          if (!see) s[g][j][e] = -INFINITY;
         }
-        pb[j][0] = transpose_8x8(pack_bf16x2(x[j][0], x[j][1]));
-        pb[j][1] = transpose_8x8(pack_bf16x2(x[j][2], x[j][3]));
       }
+      // V rows that no row sees may hold anything: zero them, so that 0 * V stays 0
+      const int key = base + k_row;
+      const bool live = gi < gt ? key < p.N
+                                : (gi < gs ? key < n_sinks : key < L && (key >= lo_root || key < p.sinks));
+      if (!live) {
+        uint8_t *sv = ring + (stage[g] - ring_addr) + Lay::K_BYTES;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        if (d + 1 < DT) load_v(d + 1, a[(d + 1) & 1]);
+        for (int c = 0; c < D / 16; ++c) {
+          const int ch = k_chunk * (D / 16) + c;
+          *reinterpret_cast<uint4 *>(sv + (ch >> 3) * (kWinGroup * 128) + sw128_offset(k_row, ch & 7)) =
+              make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();  // before the next copy into this stage
+      __syncwarp();
+    }
+
+    // The weights are taken against a maximum of each row that need not be the latest: only
+    // when a score passes it by more than 2^8 (or there is none yet) is it brought up to date
+    // over the warp's keys, and the sums and outputs with it.  Then no exchange between
+    // lanes is needed but one vote.  (The exponents take the scores' place.)
+    float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_bf16_16816(o[d][j], a[d & 1], pb[j][0], pb[j][1]);
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaf(s[g][j][e], sc, -m[j][e & 1]));
+    if (__any_sync(0xFFFFFFFFu, top > kWinRescale)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = fmaxf(s[0][j][e], s[0][j][e + 2]);
+          if (NG > 1) y = fmaxf(y, fmaxf(s[NG - 1][j][e], s[NG - 1][j][e + 2]));
+          y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
+          y = fmaxf(y * sc, m[j][e]);
+          w[e] = ex2_approx(m[j][e] - y);
+          m[j][e] = y;
+          l[j][e] *= w[e];
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          o[d][j][0] *= w[0];
+          o[d][j][1] *= w[1];
+          o[d][j][2] *= w[0];
+          o[d][j][3] *= w[1];
+        }
       }
     }
-    __syncwarp();  // every lane is done with the stage
-    if (RG > 1 && lane == 0) mbar_arrive(&empty[st]);
+    load_v(0, a[0]);
+    uint32_t pb[NG][NT][2];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = ex2_approx(fmaf(s[g][j][e], sc, -m[j][e & 1]));
+          l[j][e & 1] += x[e];
+        }
+        pb[g][j][0] = transpose_8x8(pack_bf16x2(x[0], x[1]));
+        pb[g][j][1] = transpose_8x8(pack_bf16x2(x[2], x[3]));
+      }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      if (d + 1 < DT) load_v(d + 1, a[(d + 1) & 1]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma_bf16_16816(o[d][j], a[d & 1][g], pb[g][j][0], pb[g][j][1]);
+    }
+  };
+  auto arrived = [&](int at, int par) -> bool {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(&full[at], par, abort_flag, p.wait_ns));
+  };
+  auto step = [&](int count) {  // done with `count` groups
+    __syncwarp();               // every lane is
+    for (int k = 0; k < count; ++k) {
+      if (RG > 1 && lane == 0) mbar_arrive(&empty[st]);
+      if (++st == ST) st = 0, phase ^= 1;
+    }
+    before += count;
+  };
+  for (int i = 0; layout_ok && i < n;) {
+    if constexpr (kHold) {
+      if (i >= RG && i - RG + ST < n) {
+        issue(i - RG + ST, st >= RG ? st - RG : st - RG + ST, st >= RG ? phase : phase ^ 1);
+        ++issued;
+      }
+    } else if (issued < min(n, i + 2)) {
+      refill(i);  // what this step waits for has to be on its way
+    }
+    if (!arrived(st, phase)) break;
+    const int st1 = st + 1 == ST ? 0 : st + 1;
+    const bool two = !kHold && i + 1 < n;
+    if (two && !arrived(st1, st1 == 0 ? phase ^ 1 : phase)) break;
+    done = i + (two ? 2 : 1);
+    if constexpr (!kHold) {
+      if (two && s_bad[st] == 0 && s_bad[st1] == 0) {
+        work(std::integral_constant<int, 2>(), i);
+        step(2);
+        i += 2;
+        continue;
+      }
+    }
+    if (s_bad[st] == 0) work(std::integral_constant<int, 1>(), i);
+    step(1);
+    ++i;
   }
   if (done < n && layout_ok) {
     // a wait gave up: let the copies in flight land before the shared memory is used again
@@ -531,10 +592,10 @@ WinRows window_rows(int M) {
 // The tensor-core kernel pads a unit's rows to 128 or 256 and pays more for a unit's start and
 // for the launch, but takes long windows of many rows at twice the rate.  Both sides as fitted
 // to measurements (us on 152 SMs, D = 128; 8 to 2048 units, 32 to 512 rows, windows 17 to 4097):
-//   here:  10 + units tiles / SMs (3 + 0.32 groups)      (0.2 per group of up to 48 rows)
+//   here:  10 + units tiles / SMs (3 + 0.28 groups)      (0.2 per group of up to 48 rows)
 //   there: 11 + units tiles / SMs (6 + 1.45 key tiles) + 2 SMs / units   (2.55 for 256 rows)
-// e.g. 128 units of 104 rows: window 129 16 us against 20, window 1025 46 against 32; 512 units of
-// 64 rows: 28 against 39, 88 against 86; 8 units of 208 rows, window 4097: 31 against 85.
+// e.g. 128 units of 104 rows: window 129 16 us against 20, window 1025 43 against 32; 512 units of
+// 64 rows: 27 against 39, 82 against 86; 8 units of 208 rows, window 4097: 30 against 85.
 // Up to 32 rows this kernel runs at the memory's rate: 2048 units, window 1025: 180 against 270.
 bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms) {
   const int M = N * (Hq / Hkv);
@@ -542,7 +603,7 @@ bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms) {
   if (r.rg == 1) return false;
   const double units = (double)B * Hkv, sms = num_sms;
   const double groups = span / kWinGroup + 2 + N / kWinGroup, tiles = span / 128 + 2;
-  const double here = 10 + units * r.m_tiles / sms * (3 + (r.nt == 3 ? 0.2 : 0.32) * groups);
+  const double here = 10 + units * r.m_tiles / sms * (3 + (r.nt == 3 ? 0.2 : 0.28) * groups);
   const double there = 11 + units * ((M + 255) / 256) / sms * (6 + (M > 128 ? 2.55 : 1.45) * tiles) + 2 * sms / units;
   return there < here;
 }
