@@ -175,6 +175,7 @@ size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int H
  * and the workspace's rules (zero-filled before its first use; stream-ordered sharing, also
  * with sv_tree_attention) as sv_tree_attention; a paged block_size that is not a multiple of
  * 16, and caches or batches of more rows than 32-bit coordinates reach, are SV_ERR_UNSUPPORTED.
+ * out overlapping q, the tree's or the cache's K/V is SV_ERR_INVALID_ARG.
  * A NaN or infinity in the V row of a key that some rows of a sequence see can also reach
  * its other rows of the same KV head (0 * NaN).
  * Workspace: sv_window_attention_workspace_size() bytes (max_prefix as there; 0 for float32, for up
@@ -207,7 +208,8 @@ size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
  * new_tokens, the last one the total), out_slots and out_positions [T] (entries past the
  * total are -1; 16-byte aligned; NULL when T = 0), out_free_head [1] = free_head + pages
  * added (may pass num_free: the shortage is the difference).  out_free_head must not be
- * free_head itself.  length is not advanced: calling again with the same inputs gives the
+ * free_head itself.  B = 0 writes none of them (the Python call fills them: no tokens, the head
+ * as it was).  length is not advanced: calling again with the same inputs gives the
  * same tables.  B <= SV_MAX_TABLE_BATCH, num_blocks * block_size < 2^31.
  * Device status: SV_DEV_BAD_BLOCK when free ids run out or an id (held or free) lies outside
  * the pool (table entry and slots -1), SV_DEV_BAD_PREFIX for a length or total outside

@@ -15,6 +15,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
+#include <optional>
 
 #include "sv.h"
 
@@ -112,16 +113,31 @@ at::Tensor part(const at::Tensor &buffer, int64_t offset, at::IntArrayRef shape)
 }
 
 // The stream of a call on device `dev`: the one given (a torch stream or a handle), else the
-// device's current one.
-void *stream_of(PyObject *o, int dev) {
-  if (!given(o)) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  PyObject *h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
-  if (!h) throw Refused();
-  void *s = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (!s && PyErr_Occurred()) throw Refused();
-  return s;
-}
+// device's current one.  While it stands it is the current one, so that what the call makes
+// (outputs, a zero-filled workspace) belongs to it and is not in use on another stream.
+class Stream {
+  std::optional<c10::cuda::CUDAGuard> device_;
+  std::optional<c10::cuda::CUDAStreamGuard> given_;
+  c10::cuda::CUDAStream stream_;
+
+  static c10::cuda::CUDAStream of(PyObject *o, int dev) {
+    if (!given(o)) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev);
+    PyObject *h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
+    if (!h) throw Refused();
+    void *s = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (!s && PyErr_Occurred()) throw Refused();
+    return s ? c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), (c10::DeviceIndex)dev)
+             : c10::cuda::getDefaultCUDAStream((c10::DeviceIndex)dev);
+  }
+
+ public:
+  Stream(PyObject *o, int dev) : stream_(of(o, dev)) {
+    if (given(o)) given_.emplace(stream_);
+    else device_.emplace((c10::DeviceIndex)dev);
+  }
+  operator void *() const { return stream_.stream(); }
+};
 
 // A tree argument: a host sequence [N] shared by the batch (stride 0), or a CUDA int32 tensor
 // [B, >= N] with one tree per sequence.
@@ -230,7 +246,7 @@ PyObject *window_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const float scale = real(a[9]);
     const int window = number(a[10], "window"), sinks = number(a[11], "sinks");
     const Tree tree(a[8], B, N, dev);
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Stream stream(a[14], dev);
     at::Tensor out = given(a[12]) ? tensor(a[12], "out", type, q.sizes(), dev) : make(q.sizes(), q, type);
     // (a workspace passed in must have been zero-filled before its first use; the library checks
     // its size)
@@ -245,9 +261,20 @@ PyObject *window_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     check(sv_window_attention(dt, (int)B, (int)N, (int)Hq, (int)Hkv, (int)D, q.data_ptr(), kt.data_ptr(), vt.data_ptr(), c,
                               tree.ptr, tree.stride, scale, window, sinks, out.data_ptr(),
-                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream_of(a[14], dev)));
+                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream));
     return THPVariable_Wrap(std::move(out));
   });
+}
+
+// The outputs of a batch without requests (no kernel runs for it): no tokens, the head as it was.
+void empty_tables(PyObject *outs, const char *const *names, PyObject *head) {
+  at::Tensor t[4];
+  for (int i = 0; i < 4; ++i) t[i] = THPVariable_Unpack(PyDict_GetItemString(outs, names[i]));
+  t[0].zero_();
+  t[1].fill_(-1);
+  t[2].fill_(-1);
+  if (given(head)) t[3].copy_(THPVariable_Unpack(head));
+  else t[3].zero_();
 }
 
 // (length, new_tokens, block_table, free_blocks, block_size, num_blocks, num_slots, free_head, outs,
@@ -270,7 +297,7 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
       refuse(PyExc_ValueError, "a size is not a 32-bit number");
     const int block_size = number(a[4], "block_size"), num_blocks = number(a[5], "num_blocks");
     const int32_t *head = given(a[7]) ? tensor(a[7], "free_head", at::kInt, {1}, dev).const_data_ptr<int32_t>() : nullptr;
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Stream stream(a[9], dev);
     static const char *names[4] = {"token_start", "slots", "positions", "free_head"};
     const int64_t sizes[4] = {B + 1, T, T, 1};
     PyObject *outs = given(a[8]) ? a[8] : PyDict_New();
@@ -299,9 +326,10 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
           Py_DECREF(w);
         }
       }
+      if (B == 0) empty_tables(outs, names, a[7]);
       check(sv_block_tables((int)B, len.const_data_ptr<int32_t>(), add.const_data_ptr<int32_t>(), block_size,
                             (int)bt.size(1), num_blocks, free.const_data_ptr<int32_t>(), (int)free.numel(), head,
-                            bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], stream_of(a[9], dev)));
+                            bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], stream));
     } catch (...) {
       Py_DECREF(outs);
       throw;
@@ -364,7 +392,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const int interleaved = PyObject_IsTrue(a[8]);
     if (interleaved < 0) throw Refused();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);
+    const Stream stream(a[13], p.dev);
     at::Tensor q = given(a[10]) ? tensor(a[10], "q_out", type, {T, p.Hq, p.D}, p.dev) : make({T, p.Hq, p.D}, p.qkv, type);
     at::Tensor k = given(a[11]) ? tensor(a[11], "k_out", type, p.dev) : make({T, p.Hkv, p.D}, p.qkv, type);
     if (k.dim() < 3 || k.size(-2) != p.Hkv || k.size(-1) != p.D) {
@@ -377,7 +405,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check(sv_qk_norm_rope(p.dt, (int)T, (int)p.Hq, (int)p.Hkv, (int)p.D, 2 * (int)p.freq.numel(), interleaved,
                           p.qkv.data_ptr(), p.ld, p.qw.const_data_ptr<float>(), p.kw.const_data_ptr<float>(), real(a[7]),
                           p.freq.const_data_ptr<double>(), at_pos.const_data_ptr<int32_t>(), slots,
-                          k.numel() / (p.Hkv * p.D), q.data_ptr(), k.data_ptr(), v.data_ptr(), stream_of(a[13], p.dev)));
+                          k.numel() / (p.Hkv * p.D), q.data_ptr(), k.data_ptr(), v.data_ptr(), stream));
     return Py_BuildValue("NNN", THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(k)),
                          THPVariable_Wrap(std::move(v)));
   });
@@ -395,7 +423,7 @@ PyObject *tree_qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tree tree(a[7], B, N, p.dev);
     const int interleaved = PyObject_IsTrue(a[9]);
     if (interleaved < 0) throw Refused();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);
+    const Stream stream(a[11], p.dev);
     at::Tensor q, k, v;
     if (given(a[10])) {
       PyObject *f = PySequence_Fast(a[10], "outs must be (q, k_tree, v_tree)");
@@ -418,7 +446,7 @@ PyObject *tree_qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check(sv_tree_qk_norm_rope(p.dt, (int)B, (int)N, (int)p.Hq, (int)p.Hkv, (int)p.D, 2 * (int)p.freq.numel(), interleaved,
                                p.qkv.data_ptr(), p.ld, p.qw.const_data_ptr<float>(), p.kw.const_data_ptr<float>(),
                                real(a[8]), p.freq.const_data_ptr<double>(), len.const_data_ptr<int32_t>(), tree.ptr,
-                               tree.stride, q.data_ptr(), k.data_ptr(), v.data_ptr(), stream_of(a[11], p.dev)));
+                               tree.stride, q.data_ptr(), k.data_ptr(), v.data_ptr(), stream));
     return Py_BuildValue("NNN", THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(k)),
                          THPVariable_Wrap(std::move(v)));
   });

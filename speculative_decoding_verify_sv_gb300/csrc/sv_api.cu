@@ -169,6 +169,12 @@ sv_status check_cache(const sv_kv_cache &c, bool writable, int B) {
   return SV_OK;
 }
 
+// True if two ranges of bytes share one.
+bool meet(const void *a, long long na, const void *b, long long nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && a0 < b0 + (uintptr_t)nb && b0 < a0 + (uintptr_t)na;
+}
+
 // The most prefix positions that a window holds.
 int window_span(int window, int max_prefix) { return window - 1 < max_prefix ? window - 1 : max_prefix; }
 
@@ -268,6 +274,14 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
   const sv::AttnPlan plan = sv::attn_plan(dt, B, N, Hq, Hkv, D, max_prefix, num_sms());
   const int paged = cache.block_table ? cache.block_size : 0;
   const bool win = window > 0;
+  if (win) {
+    const long long row = (long long)D * (dt == SV_BF16 ? 2 : 4), q_bytes = (long long)B * N * Hq * row;
+    const long long tree_bytes = (long long)B * N * Hkv * row;
+    const long long cache_bytes = (paged ? (long long)cache.num_blocks * paged : (long long)B * cache.Lmax) * Hkv * row;
+    if (meet(out, q_bytes, q, q_bytes) || meet(out, q_bytes, k_tree, tree_bytes) || meet(out, q_bytes, v_tree, tree_bytes) ||
+        meet(out, q_bytes, cache.k, cache_bytes) || meet(out, q_bytes, cache.v, cache_bytes))
+      return fail(SV_ERR_INVALID_ARG, "out overlaps an input");
+  }
   const bool use_tc = sv::tc_eligible(dt, N, Hq, Hkv, D, paged) &&
                       (!win || sv::window_prefers_tc(B, N, Hq, Hkv, window_span(window, max_prefix), num_sms()));
   const sv::TcPlan tplan = use_tc ? sv::tc_plan(B, N, Hq, Hkv, D, num_sms()) : sv::TcPlan{};
@@ -792,10 +806,12 @@ static sv_status rope_call(sv_dtype dt, int D, sv::RopeParams &p, long long T, v
   if (p.rot < 16 || p.rot > D || p.rot % 16 != 0)
     return fail(SV_ERR_UNSUPPORTED, "rotary dim %d (supported: multiples of 16 up to the head dim %d)", p.rot, D);
   if (T > INT32_MAX) return fail(SV_ERR_UNSUPPORTED, "%lld tokens", T);
-  if (p.num_rows > (1ll << 40)) return fail(SV_ERR_UNSUPPORTED, "%lld rows", p.num_rows);
   const long long width = ((long long)p.Hq + 2ll * p.Hkv) * D, esize = dt == SV_BF16 ? 2 : 4;
   if (width > INT32_MAX) return fail(SV_ERR_UNSUPPORTED, "a token's row of %lld elements", width);
   if (p.ld < width) return fail(SV_ERR_INVALID_ARG, "ld = %lld is below the row's %lld elements", p.ld, width);
+  // (byte offsets fit 62 bits)
+  if (p.ld > (1ll << 60) / (T > 0 ? T : 1) || p.num_rows > (1ll << 40) || p.num_rows > (1ll << 60) / ((long long)p.Hkv * D))
+    return fail(SV_ERR_UNSUPPORTED, "rows %lld elements apart, %lld rows", p.ld, p.num_rows);
   if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return fail(SV_ERR_INVALID_ARG, "eps must be finite and >= 0");
   if (p.ld * esize % 16 != 0)
     return fail(SV_ERR_INVALID_ARG, "ld = %lld: rows must be 16-byte aligned", p.ld);
@@ -804,19 +820,11 @@ static sv_status rope_call(sv_dtype dt, int D, sv::RopeParams &p, long long T, v
   if (!aligned16(p.qkv) || !aligned16(p.q_out) || !aligned16(p.k_out) || !aligned16(p.v_out))
     return fail(SV_ERR_INVALID_ARG, "qkv, q_out, k_out and v_out must be 16-byte aligned");
   if (T == 0) return SV_OK;  // no tokens: nothing to launch, no device needed
-  const char *in0 = static_cast<const char *>(p.qkv), *in1 = in0 + ((T - 1) * p.ld + width) * esize;
-  auto overlaps = [&](const void *o, long long bytes) {
-    const char *o0 = static_cast<const char *>(o);
-    return o0 < in1 && in0 < o0 + bytes;
-  };
-  const long long kv_bytes = p.num_rows * p.Hkv * D * esize;
-  const long long q_bytes = T * p.Hq * D * esize;
-  if (overlaps(p.q_out, q_bytes) || overlaps(p.k_out, kv_bytes) || overlaps(p.v_out, kv_bytes))
+  const long long qkv_bytes = ((T - 1) * p.ld + width) * esize;
+  const long long kv_bytes = p.num_rows * p.Hkv * D * esize, q_bytes = T * p.Hq * D * esize;
+  if (meet(p.q_out, q_bytes, p.qkv, qkv_bytes) || meet(p.k_out, kv_bytes, p.qkv, qkv_bytes) ||
+      meet(p.v_out, kv_bytes, p.qkv, qkv_bytes))
     return fail(SV_ERR_INVALID_ARG, "an output overlaps qkv");
-  auto meet = [](const void *a, long long na, const void *b, long long nb) {
-    const char *a0 = static_cast<const char *>(a), *b0 = static_cast<const char *>(b);
-    return na > 0 && nb > 0 && a0 < b0 + nb && b0 < a0 + na;
-  };
   if (meet(p.q_out, q_bytes, p.k_out, kv_bytes) || meet(p.q_out, q_bytes, p.v_out, kv_bytes) ||
       meet(p.k_out, kv_bytes, p.v_out, kv_bytes))
     return fail(SV_ERR_INVALID_ARG, "two outputs overlap");

@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
 
   // up to the batch's last token (its pages are given out even where the slot map is too short)
   // and on to the end of the slot map
-  const long long end = max(total, (long long)p.T);
+  // (tokens that a 32-bit place does not reach are not looked at: wild numbers make no long loop)
+  const long long end = min(max(total, (long long)p.T), (long long)INT32_MAX);
   constexpr int U = RUN == 1 ? 2 : RUN;
   const long long step = (long long)gridDim.x * kTableThreads * U;
   const int top = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;  // the search's first stride

@@ -47,6 +47,10 @@ def test_window_attention_rejects_before_launch(lib):
                      (no, dict(cache=_cache(**dict(paged, num_blocks=2 ** 28))))):
         assert _window(lib, **kw) == code, kw
         assert lib.sv_last_error() != b""
+    # an output on top of an input
+    far = dict(cache=_cache(k=1 << 40, v=1 << 41), q=FAR3)
+    for out in (3 << 40, (3 << 40) + 1008, 1 << 20, (1 << 40) + 1024, (1 << 41) + 128 * 4 * 128 * 2 - 16):
+        assert _window(lib, out=ctypes.c_void_p(out), **far) == bad and b"overlaps" in lib.sv_last_error(), out
     # a workspace for the 128-row kernel; sizes that need none, and sizes that are none
     assert lib.sv_window_attention_workspace_size(1, 64, 26, 64, 8, 128, 4096, 2048) > 0
     assert lib.sv_window_attention_workspace_size(1, 256, 5, 32, 8, 128, 8192, 1024) == 0
@@ -92,6 +96,9 @@ def test_qk_norm_rope_rejects_before_launch(lib):
                      (bad, dict(rows=3)), (bad, dict(rows=-1)), (bad, dict(q=inside)), (bad, dict(k=inside)),
                      (bad, dict(v=P)), (bad, dict(k=FAR)), (bad, dict(v=FAR2)), (no, dict(rows=2 ** 41)), (no, dict(Hq=2 ** 25, ld=2 ** 40))):
         assert _rope(lib, **kw) == code, kw
+    # row distances and row counts whose bytes pass 64 bits
+    assert _rope(lib, T=2 ** 31 - 1, ld=2 ** 45, rows=2 ** 31) == no and _rope(lib, ld=2 ** 62) == no
+    assert _rope(lib, Hkv=2 ** 23, ld=2 ** 33, Hq=1, D=64, rot=64, rows=2 ** 33) == no
     assert _rope(lib, T=0, qkv=None, qw=None, kw=None, freq=None, positions=None, q=None, k=None, v=None, rows=0) == sv.SV_OK
     par = (ctypes.c_int32 * 3)(-1, 0, 0)
 

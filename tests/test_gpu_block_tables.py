@@ -175,3 +175,24 @@ def test_refusals_and_empty_batch(cuda_ok):
     n0 = sv.sv_kernel_launches()
     call(length=t["length"][:0], new_tokens=t["new"][:0], block_table=t["table"][:0])
     assert sv.sv_kernel_launches() == n0 and sv.sv_read_device_status() == 0
+    # the Python call fills the outputs of a batch without requests: no tokens, the head as it was
+    for head, want in ((None, 0), (_dev([7]), 7)):
+        r = call(length=t["length"][:0], new_tokens=t["new"][:0], block_table=t["table"][:0], num_slots=6, free_head=head)
+        assert r["token_start"].tolist() == [0] and r["free_head"].tolist() == [want]
+        assert r["slots"].tolist() == [-1] * 6 and r["positions"].tolist() == [-1] * 6
+
+
+def test_totals_past_32_bits_end_and_are_reported(cuda_ok):
+    """8192 requests of 2^30 new tokens: what the slot map holds is right, the call ends soon."""
+    B, bs, columns = sv.SV_MAX_TABLE_BATCH, 2 ** 20, 1024
+    table = torch.full((B, columns), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(1000, -1, -1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for T in (100, 2 ** 21):
+        r = sv.sv_block_tables(zero, zero + 2 ** 30, table, free, bs, 1001, T)
+        torch.cuda.synchronize()
+        assert sv.sv_read_device_status() == sv.SV_DEV_BAD_PREFIX | sv.SV_DEV_BAD_BLOCK
+        at = torch.arange(T, dtype=torch.int64, device="cuda")
+        assert torch.equal(r["positions"].long(), at)
+        assert torch.equal(r["slots"].long(), (1000 - at // bs) * bs + at % bs)
+        assert r["token_start"][:4].tolist() == [0, 2 ** 30, 2 ** 31 - 1, 2 ** 31 - 1]

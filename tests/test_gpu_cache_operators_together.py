@@ -166,3 +166,44 @@ def test_window_of_the_step_is_the_operator(cuda_ok):
     assert torch.equal(got, want)
     with pytest.raises(ValueError):
         VerifyStep(wl.chain_parent(4), 2, 8, 2, 64, 512, cache, sinks=2)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_calls_on_another_stream_keep_their_memory_apart(cuda_ok, handle):
+    """What a call on a given stream makes is not memory that the current stream still writes."""
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if handle else side
+    b, n, hq, hkv, d = 16, 26, 64, 8, 128
+    inp = wl.attention_inputs(b, n, hq, hkv, d, [2100] * b, dtype=BF, seed=3)
+    g = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in inp.items()}
+    cache = sv.KVCache(g["cache_k"], g["cache_v"], g["prefix_len"])
+    assert sv.sv_window_attention_workspace_size(BF, b, n, hq, hkv, d, cache.max_prefix, 2048) > 0
+    qkv = torch.randn(b, n, (hq + 2 * hkv) * d, generator=_gen(6)).to(BF).cuda()
+    w = torch.ones(d, device="cuda")
+    freq = torch.tensor([10000.0 ** (-i / 64) for i in range(64)], dtype=torch.float64, device="cuda")
+    pos = torch.arange(b * n, dtype=torch.int32, device="cuda")
+    new = torch.arange(300, dtype=torch.int32, device="cuda")
+    length, table = torch.zeros_like(new), torch.full((300, 40), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(9000, dtype=torch.int32, device="cuda")
+
+    def table_call(**kw):
+        r = sv.sv_block_tables(length, new, table, free, 16, 9000, 50000, **kw)
+        return r["slots"], r["positions"], r["token_start"], r["free_head"]
+    par = wl.chain_parent(n - 1)
+    calls = (lambda **kw: (sv.sv_window_attention(g["q"], g["k_tree"], g["v_tree"], cache, par, d ** -0.5, 2048, **kw),),
+             lambda **kw: (sv.sv_window_attention(g["q"], g["k_tree"], g["v_tree"], cache, par, d ** -0.5, 17, **kw),),
+             lambda **kw: sv.sv_qk_norm_rope(qkv.view(b * n, -1), hq, hkv, w, w, freq, pos, **kw),
+             lambda **kw: sv.sv_tree_qk_norm_rope(qkv, hq, hkv, w, w, freq, g["prefix_len"], par, **kw), table_call)
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        sizes = [x.untyped_storage().nbytes() for x in want]
+        for size in sizes:
+            old = torch.empty(size, dtype=torch.uint8, device="cuda")
+            torch.cuda._sleep(20_000_000)
+            old.fill_(255)
+            del old  # free for the current stream, which has yet to write it
+        got = call(stream=given)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert sv.sv_read_device_status() == 0
