@@ -58,8 +58,18 @@ bool map5d_pages(CUtensorMap *m, const void *base, int heads, long long rows, in
 
 }  // namespace
 
+// 4-D bf16 view (64 columns, rows, column blocks, heads) with a (64, box_rows, D / 64, 1) box,
+// 128-byte swizzle: one copy brings box_rows rows of a head, a 64-column block after the other.
 bool tma_rows_map(CUtensorMap *m, const void *base, int D, int heads, long long rows, int box_rows) {
-  return map3d(m, base, D, heads, rows, 1, box_rows);
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(D / 64), (cuuint64_t)heads};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2 * heads, 128, (cuuint64_t)D * 2};
+  cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, (cuuint32_t)(D / 64), 1u};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool tc_eligible(sv_dtype dt, int N, int Hq, int Hkv, int D, int paged_block_size) {

@@ -12,8 +12,8 @@
 // flight and that units, which a window keeps short, begin and end without gaps.  So nothing
 // in the main loop waits for another warp: each slice of a CTA (one warp; two with more than
 // 32 rows, which then share a slice's rows) takes every KS-th group, has a ring of its own
-// in shared memory, issues its own TMA copies (16 rows per box, several groups ahead) and
-// keeps its own running maximum, sum and output in registers.  Two CTAs share an SM, so one
+// in shared memory, issues its own TMA copies (16 rows of a head per box, several groups ahead)
+// and keeps its own running maximum, sum and output in registers.  Two CTAs share an SM, so one
 // streams while the other starts or ends.
 //
 // The products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys and head
@@ -23,13 +23,18 @@
 // operand layout by an 8x8 transpose in registers, rounded to bf16 (off by at most 2^-8 of each
 // weight; the sum is of the unrounded ones); scores, weights, sums and outputs are fp32.
 //
-// Bound by HBM for many units: 256 ragged requests of 5 nodes, 32:8 heads of 128, window 1024 in pages
-// of 16, 177 us, 6.1 TB/s, 90 % of the measured copy rate (the 128-row kernel 268 us); by latency
-// for few: one token of one request, window 1024, 6.6 us (49).
+// Bound by HBM for many units of up to 48 rows: 256 ragged requests of 5 nodes, 32:8 heads of 128,
+// window 1024 in pages of 16, 174 us, 6.2 TB/s, 91 % of the measured copy rate (the 128-row kernel
+// 268 us); by the warps' chains of products and exponents for 64 rows (256 units, window 513: 24.5 us,
+// of which 2 start, 17 loop, 2.5 merge; the matrix pipe is half busy); by latency for few units: one
+// token of one request, window 1024, 5.5 us (the 128-row kernel 49).
 //
-// The slices merge in shared memory by weights 2^(m_slice - m).  Few long units: a cluster of
-// up to 8 CTAs shares a unit's groups and merges through distributed shared memory, without a
-// workspace or a second launch.
+// The slices merge in shared memory by weights 2^(m_slice - m), each taking some dimensions of all
+// rows, as they stand in registers, and the results leave as 32-byte sectors by a transpose and an
+// exchange between neighbours (5.3 thousand cycles -> 3.5 for 64 rows against rows of floats in shared
+// memory).  Few long units: a cluster of up to 8 CTAs shares a unit's groups, without a workspace or
+// a second launch; each CTA takes part of the unit's outputs, which the others write into its shared
+// memory (reading them from there instead: 6.6 us against 5.5 for one token).
 #include <atomic>
 #include <cfloat>
 #include <type_traits>
@@ -60,22 +65,26 @@ struct WinLayout {
   static constexpr int RING = (RG == 2 ? 80 : 96) * 1024;
   static constexpr int ST = RING / (KS * G_BYTES);  // stages of a slice's ring
   static constexpr int RB = 8 * NT * RG;        // query rows of a CTA
-  static constexpr int OS = D + 4;              // row stride of the merged outputs (floats): no bank conflicts
+  static constexpr int DO = D / 16 / KS;        // 16-dimension tiles of the outputs that a slice merges
+  static constexpr int UNITS = RG * D / 16 * NT;  // of the merge: 16 dimensions of 8 rows
   static constexpr int OFF_Q = RING;            // query rows [RB][D], 128-byte swizzle per 64 columns
+  // in the ring's room, after the slices' parts: what the CTAs of a cluster hand over, outputs
+  // [units], maxima and sums [8][RB]
+  static constexpr int OFF_JOIN = (KS - 1) * UNITS * 512;
+  static constexpr int JOIN = (UNITS + 8) * 512 + 2 * 8 * RB * 4;
   static constexpr int OFF_FULL = OFF_Q + RB * D * 2;
   static constexpr int OFF_EMPTY = OFF_FULL + KS * ST * 8;
   static constexpr int OFF_ANC = OFF_EMPTY + KS * ST * 8;
   static constexpr int OFF_M = OFF_ANC + RB * 8;        // [KS][RB]
   static constexpr int OFF_L = OFF_M + KS * RB * 4;     // [KS][RB]
-  static constexpr int OFF_CM = OFF_L + KS * RB * 4;    // [RB] the CTA's maximum and sum
-  static constexpr int OFF_CL = OFF_CM + RB * 4;
-  static constexpr int OFF_LO = OFF_CL + RB * 4;        // [RB]
+  static constexpr int OFF_INV = OFF_L + KS * RB * 4;   // [RB] 1 / sum
+  static constexpr int OFF_LO = OFF_INV + RB * 4;       // [RB]
   static constexpr int OFF_ROW = OFF_LO + RB * 4;       // [RB]
   static constexpr int OFF_PAR = OFF_ROW + RB * 4;      // [64]
   static constexpr int OFF_BAD = OFF_PAR + kMaxNodes * 4;  // [KS][ST]
   static constexpr int OFF_ABORT = OFF_BAD + KS * ST * 4;
   static constexpr int SMEM = OFF_ABORT + 16;
-  static_assert(KS * RB * OS * 4 <= RING, "the slices' outputs merge in the ring's room");
+  static_assert(OFF_JOIN + JOIN <= RING, "the merge goes on in the ring's room");
   static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -104,15 +113,22 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr));
 }
 
+// A product that starts a sum.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <int D, int NT, int RG>
 __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __grid_constant__ WinParams p) {
   using Lay = WinLayout<D, NT, RG>;
-  constexpr int KS = Lay::KS, KB = Lay::KB, ST = Lay::ST, RB = Lay::RB, OS = Lay::OS, DT = D / 16;
+  constexpr int KS = Lay::KS, KB = Lay::KB, ST = Lay::ST, RB = Lay::RB, DT = D / 16;
   extern __shared__ __align__(1024) uint8_t win_smem[];
   uint8_t *sm = win_smem;
   uint64_t *s_anc = reinterpret_cast<uint64_t *>(sm + Lay::OFF_ANC);
   float *s_m = reinterpret_cast<float *>(sm + Lay::OFF_M), *s_l = reinterpret_cast<float *>(sm + Lay::OFF_L);
-  float *s_cm = reinterpret_cast<float *>(sm + Lay::OFF_CM), *s_cl = reinterpret_cast<float *>(sm + Lay::OFF_CL);
+  float *s_inv = reinterpret_cast<float *>(sm + Lay::OFF_INV);
   int *s_lo = reinterpret_cast<int *>(sm + Lay::OFF_LO), *s_par = reinterpret_cast<int *>(sm + Lay::OFF_PAR);
   int *s_row = reinterpret_cast<int *>(sm + Lay::OFF_ROW);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Lay::OFF_ABORT);
@@ -131,8 +147,33 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   const int mt = unit % p.m_tiles, kvh = (unit / p.m_tiles) % p.Hkv, b = unit / p.m_tiles / p.Hkv;
   const bool reports = kvh == 0 && mt == 0 && rank == 0;
 
+  const bool layout_ok = (smem_u32(sm) & 1023u) == 0;  // 128-byte-swizzled boxes
+  if (lane == 0 && rg == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], RG);
+      mbar_init(&empty[i], RG);
+    }
+    fence_barrier_init();
+  }
+  // the place of each of the CTA's rows in q and out, in heads (-1: past the unit's rows)
+  if (tid < RB) {
+    const int R = mt * RB + tid, node = R / p.G;
+    s_row[tid] = R < p.M ? (b * p.N + node) * p.Hq + kvh * p.G + R - node * p.G : -1;
+  }
+  if (tid == 0) *abort_flag = 0;
   wait_previous();
   int L = p.prefix_len[b];
+  if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
+  __syncthreads();
+  // query rows as B operands, on their way before the first keys
+  uint8_t *s_q = sm + Lay::OFF_Q;
+#pragma unroll
+  for (int u = tid; u < RB * (D / 8); u += kWinThreads) {
+    const int r = u / (D / 8), c = u % (D / 8), row = s_row[r];
+    cp_async_16(s_q + (c >> 3) * (RB * 128) + sw128_offset(r, c & 7),
+                static_cast<const bf16 *>(p.q) + (size_t)max(row, 0) * D + 8 * c, row >= 0);
+  }
+  cp_async_commit();
   if (L < 0 || L > p.cap) {
     if (reports && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
     L = L < 0 ? 0 : p.cap;
@@ -147,19 +188,10 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   const int g0 = min((int)rank * per, groups), g1 = min(g0 + per, groups);
   const int n = g1 - g0 > slice ? (g1 - g0 - slice + KS - 1) / KS : 0;  // this slice's groups
 
-  // the place of each of the CTA's rows in q and out, in heads (-1: past the unit's rows)
-  if (tid < RB) {
-    const int R = mt * RB + tid, node = R / p.G;
-    s_row[tid] = R < p.M ? (b * p.N + node) * p.Hq + kvh * p.G + R - node * p.G : -1;
-  }
-  if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
-  if (tid == 0) *abort_flag = 0;
-
   // ---- copies: a slice's warp issues its groups' K and V; two warps share that out
   constexpr bool kBoth = RG == 1;
   constexpr uint32_t kTx = kBoth ? Lay::G_BYTES : Lay::K_BYTES;
-  const CUtensorMap *map_tree = rg == 0 ? &p.tm_kt : &p.tm_vt, *map_cache = rg == 0 ? &p.tm_kc : &p.tm_vc;
-  const uint64_t stream_policy = l2_policy_evict_first();
+  const uint64_t stream_policy = l2_policy_evict_first(), tree_policy = l2_policy_evict_normal();
   int desc = -1;  // lane i: row of group (32 k + i) of this slice, k the batch being issued
   auto locate = [&](int i) -> int {
     const int gi = g0 + slice + KS * i;
@@ -174,56 +206,44 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     }
     return blk * p.block_size + pos % p.block_size;
   };
+  // (one lane) a group whose rows start at `row` into stage st; none if the page is bad
+  auto copy = [&](int row, bool tree, int st) {
+    s_bad[st] = row < 0;
+    if (row < 0) {
+      mbar_arrive(&full[st]);
+      return;
+    }
+    uint8_t *dst = ring + st * Lay::G_BYTES;
+    const uint64_t policy = tree ? tree_policy : stream_policy;
+    mbar_expect_tx(&full[st], kTx);
+    if (kBoth || rg == 0) tma_load_4d_hint(dst, tree ? &p.tm_kt : &p.tm_kc, 0, row, 0, kvh, &full[st], policy);
+    if (kBoth || rg == 1)
+      tma_load_4d_hint(dst + Lay::K_BYTES, tree ? &p.tm_vt : &p.tm_vc, 0, row, 0, kvh, &full[st], policy);
+  };
   // group i of the slice into stage st, which is free once its last group's barrier `empty` has
-  // passed the parity (-1: no group was there)
+  // passed the parity
   auto issue = [&](int i, int st, int parity) {
     if ((i & 31) == 0) desc = locate(i + lane);
     const int row = __shfl_sync(0xFFFFFFFFu, desc, i & 31);
     const bool tree = g0 + slice + KS * i < gt;
-    if (elect_one() && (kBoth || parity < 0 || mbar_wait(&empty[st], parity, abort_flag, p.wait_ns))) {
-      s_bad[st] = row < 0;
-      if (row < 0) {
-        mbar_arrive(&full[st]);
-      } else {
-        uint8_t *dst = ring + st * Lay::G_BYTES + (kBoth ? 0 : rg * Lay::K_BYTES);
-        mbar_expect_tx(&full[st], kTx);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb, dst += kWinGroup * 128) {
-          if (tree) {
-            tma_load_3d(dst, map_tree, kb * 64, kvh, row, &full[st]);
-            if (kBoth) tma_load_3d(dst + Lay::K_BYTES, &p.tm_vt, kb * 64, kvh, row, &full[st]);
-          } else {
-            tma_load_3d_hint(dst, map_cache, kb * 64, kvh, row, &full[st], stream_policy);
-            if (kBoth) tma_load_3d_hint(dst + Lay::K_BYTES, &p.tm_vc, kb * 64, kvh, row, &full[st], stream_policy);
-          }
-        }
-      }
-    }
+    if (elect_one() && (kBoth || mbar_wait(&empty[st], parity, abort_flag, p.wait_ns))) copy(row, tree, st);
     __syncwarp();
   };
-  const bool layout_ok = (smem_u32(sm) & 1023u) == 0;  // 128-byte-swizzled boxes
-  if (lane == 0 && rg == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], RG);
-      mbar_init(&empty[i], RG);
+  // The first groups.  A warp that brings both K and V takes them one after another, so that the first
+  // one is whole soon (2048 units of 32 rows, window 1025, 169 us against 176 with a lane each); of
+  // two warps each lane takes one (24.4 us against 25.5 for 256 units of 64 rows, window 513).
+  static_assert(ST <= 32, "a lane each");
+  if (layout_ok) {
+    if (kBoth) {
+      for (int i = 0; i < min(ST, n); ++i) issue(i, i, 0);
+    } else {
+      desc = locate(lane);
+      if (lane < min(ST, n)) copy(desc, g0 + slice + KS * lane < gt, lane);
+      __syncwarp();
     }
-    fence_barrier_init();
   }
-  if (kBoth) __syncwarp();
-  else __syncthreads();
-  if (layout_ok)
-    for (int i = 0; i < min(ST, n); ++i) issue(i, i, -1);
 
-  // ---- query rows as B operands, and what each row sees
-  __syncthreads();
-  uint8_t *s_q = sm + Lay::OFF_Q;
-#pragma unroll
-  for (int u = tid; u < RB * (D / 8); u += kWinThreads) {
-    const int r = u / (D / 8), c = u % (D / 8), row = s_row[r];
-    cp_async_16(s_q + (c >> 3) * (RB * 128) + sw128_offset(r, c & 7),
-                static_cast<const bf16 *>(p.q) + (size_t)max(row, 0) * D + 8 * c, row >= 0);
-  }
-  cp_async_commit();
+  // ---- what each row sees
   if (tid < RB) {
     const int R = mt * RB + tid;
     uint64_t anc = 0;
@@ -239,7 +259,11 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   }
   cp_async_wait<0>();
   __syncthreads();
-  const int lo_last = window_first(L + p.N - 1, p.window);  // no row's window starts later
+  // Every row sees every key of the groups [plain0, plain1) of this slice: inside the window of all
+  // rows (none starts later than the deepest possible node's), before the prefix's end.
+  const int lo_last = window_first(L + p.N - 1, p.window);
+  const int plain0 = max(0, gs + (lo_last - first + kWinGroup - 1) / kWinGroup - g0 - slice + KS - 1) / KS;
+  const int plain1 = max(0, gs + (L - first) / kWinGroup - g0 - slice + KS - 1) / KS;
 
   float o[DT][NT][4];
 #pragma unroll
@@ -260,15 +284,13 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   const uint32_t ring_addr = smem_u32(ring);
   // query rows as B operands: 8 rows of 8-column step j, 16-byte chunks 2k + 0..3 (two 16-column
   // steps in one load), the same exclusive-or swizzle
-  const uint32_t q_row = (uint32_t)(rg * 8 * NT + (lane & 7)), q_addr = smem_u32(s_q) + q_row * 128u;
-  const uint32_t q_chunk = (uint32_t)(lane >> 3);
+  const uint32_t q_row = (uint32_t)(rg * 8 * NT + (lane & 7));
+  const uint32_t q_addr = smem_u32(s_q) + q_row * 128u + ((((uint32_t)lane >> 3) ^ (q_row & 7)) << 4);
   auto load_q = [&](int k, uint32_t (&q)[NT][4]) {
-    const uint32_t c = 2 * k + q_chunk;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      ldsm_x4(q[j], q_addr + (c >> 3) * (RB * 128) + j * 1024 + (((c & 7) ^ (q_row & 7)) << 4));
+    for (int j = 0; j < NT; ++j) ldsm_x4(q[j], (q_addr ^ ((k & 2) << 5)) + (k >> 2) * (RB * 128) + j * 1024);
   };
-  // held for good with one group at a time, loaded for each pair of groups
+  // held in registers where there is room for them, else loaded for each group
   constexpr bool kHold = RG == 1 || NT < 4;
   uint32_t held[kHold ? DT / 2 : 1][NT][4];
   if constexpr (kHold) {
@@ -277,43 +299,25 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   }
   int done = 0, issued = min(ST, n);
   int st = 0, phase = 0;  // the stage of group i and the parity of its use
-  // One group at a time, the stage of group i - RG is filled again at the start of group i: two
-  // warps that share a slice need not be done with the previous group at the same time.  Two at a
-  // time, the stages of the last ones are filled again between the products of the next ones.
-  int before = 0;  // groups before i whose stages are not yet filled again
-  auto refill = [&](int i) {
-    for (; before > 0; --before) {
-      if (i - before + ST >= n) continue;
-      issue(i - before + ST, st >= before ? st - before : st - before + ST, st >= before ? phase : phase ^ 1);
-      ++issued;
-    }
-  };
 
-  // NG groups from group i on: scores, exponents, weights, outputs.  Two at a time where rows fill
-  // the operands (64 of them), so that the matrix instructions of one group hide the operand loads
-  // and latencies of the other: 512 units of 64 rows, window 4097, 299 us against 317 one at a
-  // time, while 40 rows would take 250 against 233: fewer copies are in flight meanwhile.
-  auto work = [&](auto ng, int i) {
-    constexpr int NG = decltype(ng)::value;
-    uint32_t stage[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) stage[g] = ring_addr + (st + g >= ST ? st + g - ST : st + g) * Lay::G_BYTES;
-    auto load_k = [&](int k, uint32_t (&a)[NG][4]) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) ldsm_x4(a[g], stage[g] + (k_off ^ ((k & 3) << 5)) + (k >> 2) * (kWinGroup * 128));
+  float s[NT][4];      // the scores of the group whose weights come next, then their exponents
+  uint32_t pb[NT][2];  // its weights
+  // half h of the weights of 8-column step j
+  auto weigh = [&](int j, int h) {
+    const float x0 = ex2_approx(s[j][2 * h]), x1 = ex2_approx(s[j][2 * h + 1]);
+    l[j][0] += x0;
+    l[j][1] += x1;
+    pb[j][h] = transpose_8x8(pack_bf16x2(x0, x1));
+  };
+  // Products of a group's keys with the query rows, each step's operands loaded a step ahead; with
+  // WEIGH the weights of the group before, between the products.  (512 units of 104 rows, window 4097:
+  // 566 us with one group after another, 525 with two groups side by side, 481 this way.)
+  auto scores = [&](auto weigh_too, uint32_t stage, float (&t)[NT][4]) {
+    constexpr bool WEIGH = decltype(weigh_too)::value;
+    auto load_k = [&](int k, uint32_t (&a)[4]) {
+      ldsm_x4(a, stage + (k_off ^ ((k & 3) << 5)) + (k >> 2) * (kWinGroup * 128));
     };
-    auto load_v = [&](int d, uint32_t (&a)[NG][4]) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-        ldsm_x4_trans(a[g], stage[g] + Lay::K_BYTES + (v_off ^ ((d & 3) << 5)) + (d >> 2) * (kWinGroup * 128));
-    };
-    float s[NG][NT][4];
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) s[g][j][0] = s[g][j][1] = s[g][j][2] = s[g][j][3] = 0.f;
-    // each step's operands are loaded a step ahead of its products
-    uint32_t a[2][NG][4], q[2][NT][4];
+    uint32_t a[2][4], q[2][NT][4];
     if constexpr (!kHold) load_q(0, q[0]);
     load_k(0, a[0]);
 #pragma unroll
@@ -321,145 +325,179 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
       if (k + 1 < DT) load_k(k + 1, a[(k + 1) & 1]);
       if (!kHold && k % 2 == 0 && k + 2 < DT) load_q(k + 2, q[(k / 2 + 1) & 1]);
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint32_t *b = kHold ? held[kHold ? k / 2 : 0][j] : q[(k / 2) & 1][j];
-          mma_bf16_16816(s[g][j], a[k & 1][g], b[2 * (k & 1)], b[2 * (k & 1) + 1]);
-        }
-    }
-    if (!kHold) refill(i);  // (by now the other warp of the slice is done with those stages too)
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int gi = g0 + slice + KS * (i + g);
-      const int base = gi < gs ? kWinGroup * (gi < gt ? gi : gi - gt) : first + kWinGroup * (gi - gs);
-      // every row sees every key: inside the window of all rows, before the prefix's end
-      if (gi >= gs && base >= lo_last && base + kWinGroup <= L) continue;
-#pragma unroll
       for (int j = 0; j < NT; ++j) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = rg * 8 * NT + 8 * j + 2 * ft + (e & 1), key = base + fg + (e >> 1) * 8;
-          bool see;
-          if (gi < gt) see = (s_anc[r] >> key) & 1ull;
-          else if (gi < gs) see = key < n_sinks;
-          else see = key < L && (key >= s_lo[r] || key < p.sinks);
-          if (!see) s[g][j][e] = -INFINITY;
-        }
+        const uint32_t *b = kHold ? held[kHold ? k / 2 : 0][j] : q[(k / 2) & 1][j];
+        if (k == 0) mma_first(t[j], a[0], b[0], b[1]);
+        else mma_bf16_16816(t[j], a[k & 1], b[2 * (k & 1)], b[2 * (k & 1) + 1]);
       }
-      // V rows that no row sees may hold anything: zero them, so that 0 * V stays 0
-      const int key = base + k_row;
-      const bool live = gi < gt ? key < p.N
-                                : (gi < gs ? key < n_sinks : key < L && (key >= lo_root || key < p.sinks));
-      if (!live) {
-        uint8_t *sv = ring + (stage[g] - ring_addr) + Lay::K_BYTES;
+      if constexpr (WEIGH) {
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const int ch = k_chunk * (D / 16) + c;
-          *reinterpret_cast<uint4 *>(sv + (ch >> 3) * (kWinGroup * 128) + sw128_offset(k_row, ch & 7)) =
-              make_uint4(0, 0, 0, 0);
-        }
-      }
-      fence_proxy_async_smem();  // before the next copy into this stage
-      __syncwarp();
-    }
-
-    // The weights are taken against a maximum of each row that need not be the latest: only
-    // when a score passes it by more than 2^8 (or there is none yet) is it brought up to date
-    // over the warp's keys, and the sums and outputs with it.  Then no exchange between
-    // lanes is needed but one vote.  (The exponents take the scores' place.)
-    float top = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaf(s[g][j][e], sc, -m[j][e & 1]));
-    if (__any_sync(0xFFFFFFFFu, top > kWinRescale)) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float w[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y = fmaxf(s[0][j][e], s[0][j][e + 2]);
-          if (NG > 1) y = fmaxf(y, fmaxf(s[NG - 1][j][e], s[NG - 1][j][e + 2]));
-          y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
-          y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
-          y = fmaxf(y * sc, m[j][e]);
-          w[e] = ex2_approx(m[j][e] - y);
-          m[j][e] = y;
-          l[j][e] *= w[e];
-        }
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          o[d][j][0] *= w[0];
-          o[d][j][1] *= w[1];
-          o[d][j][2] *= w[0];
-          o[d][j][3] *= w[1];
-        }
+        for (int u = k * 2 * NT / DT; u < (k + 1) * 2 * NT / DT; ++u) weigh(u >> 1, u & 1);
       }
     }
+  };
+  // Products of the weights with the group's V.
+  auto outputs = [&](uint32_t stage) {
+    auto load_v = [&](int d, uint32_t (&a)[4]) {
+      ldsm_x4_trans(a, stage + Lay::K_BYTES + (v_off ^ ((d & 3) << 5)) + (d >> 2) * (kWinGroup * 128));
+    };
+    uint32_t a[2][4];
     load_v(0, a[0]);
-    uint32_t pb[NG][NT][2];
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = ex2_approx(fmaf(s[g][j][e], sc, -m[j][e & 1]));
-          l[j][e & 1] += x[e];
-        }
-        pb[g][j][0] = transpose_8x8(pack_bf16x2(x[0], x[1]));
-        pb[g][j][1] = transpose_8x8(pack_bf16x2(x[2], x[3]));
-      }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       if (d + 1 < DT) load_v(d + 1, a[(d + 1) & 1]);
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int j = 0; j < NT; ++j) mma_bf16_16816(o[d][j], a[d & 1], pb[j][0], pb[j][1]);
+    }
+  };
+  // What the rows do not see of group i goes from its scores (all of it if its page is bad).
+  auto mask = [&](int i, uint32_t stage, bool bad) {
+    if (!bad && i >= plain0 && i < plain1) return;
+    const int gi = g0 + slice + KS * i;
+    const int base = gi < gs ? kWinGroup * (gi < gt ? gi : gi - gt) : first + kWinGroup * (gi - gs);
+    const bool tree = gi < gt;
+    const int end = bad ? 0 : (tree ? p.N : (gi < gs ? n_sinks : L));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_bf16_16816(o[d][j], a[d & 1][g], pb[g][j][0], pb[g][j][1]);
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = rg * 8 * NT + 8 * j + 2 * ft + e, key = base + fg;
+        bool see0, see1;
+        if (tree) {
+          const uint32_t seen = (uint32_t)(s_anc[r] >> base) >> fg;
+          see0 = seen & 1u;
+          see1 = seen & 256u;
+        } else {
+          const int lo = s_lo[r];
+          see0 = key < end && (key >= lo || key < p.sinks);
+          see1 = key + 8 < end && (key + 8 >= lo || key + 8 < p.sinks);
+        }
+        if (!see0) s[j][e] = -INFINITY;
+        if (!see1) s[j][e + 2] = -INFINITY;
+      }
+    // V rows that no row sees may hold anything: zero them, so that 0 * V stays 0
+    const int key = base + k_row;
+    const bool live = key < end && (tree || key >= lo_root || key < p.sinks);
+    if (__all_sync(0xFFFFFFFFu, live)) return;
+    if (!live) {
+      uint8_t *sv = ring + (stage - ring_addr) + Lay::K_BYTES;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int ch = k_chunk * (D / 16) + c;
+        *reinterpret_cast<uint4 *>(sv + (ch >> 3) * (kWinGroup * 128) + sw128_offset(k_row, ch & 7)) =
+            make_uint4(0, 0, 0, 0);
+      }
+    }
+    fence_proxy_async_smem();  // before the next copy into this stage
+    __syncwarp();
+  };
+  // The weights are taken against a maximum of each row that need not be the latest: only
+  // when a score passes it by more than 2^8 (or there is none yet) is it brought up to date
+  // over the warp's keys, and the sums and outputs with it.  Then no exchange between
+  // lanes is needed but one vote.
+  auto limits = [&]() {
+    float x[NT][4], top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[j][e] = fmaf(s[j][e], sc, -m[j][e & 1]);
+        top = fmaxf(top, x[j][e]);
+      }
+    if (!__any_sync(0xFFFFFFFFu, top > kWinRescale)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = x[j][e];
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y = fmaxf(s[j][e], s[j][e + 2]);
+        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
+        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
+        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
+        y = fmaxf(y * sc, m[j][e]);
+        w[e] = ex2_approx(m[j][e] - y);
+        m[j][e] = y;
+        l[j][e] *= w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = fmaf(s[j][e], sc, -m[j][e & 1]);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        o[d][j][0] *= w[0];
+        o[d][j][1] *= w[1];
+        o[d][j][2] *= w[0];
+        o[d][j][3] *= w[1];
+      }
     }
   };
   auto arrived = [&](int at, int par) -> bool {
     return __all_sync(0xFFFFFFFFu, mbar_wait(&full[at], par, abort_flag, p.wait_ns));
   };
-  auto step = [&](int count) {  // done with `count` groups
-    __syncwarp();               // every lane is
-    for (int k = 0; k < count; ++k) {
-      if (RG > 1 && lane == 0) mbar_arrive(&empty[st]);
-      if (++st == ST) st = 0, phase ^= 1;
-    }
-    before += count;
+  // the stage of group i - back is filled again with group i - back + ST
+  auto refill = [&](int i, int back) {
+    if (i < back || i - back + ST >= n) return;
+    issue(i - back + ST, st >= back ? st - back : st - back + ST, st >= back ? phase : phase ^ 1);
+    ++issued;
   };
-  for (int i = 0; layout_ok && i < n;) {
-    if constexpr (kHold) {
-      if (i >= RG && i - RG + ST < n) {
-        issue(i - RG + ST, st >= RG ? st - RG : st - RG + ST, st >= RG ? phase : phase ^ 1);
-        ++issued;
+  auto next_stage = [&]() {  // done with the stage
+    __syncwarp();            // every lane is
+    if (RG > 1 && lane == 0) mbar_arrive(&empty[st]);
+    if (++st == ST) st = 0, phase ^= 1;
+  };
+  if constexpr (kHold) {
+    for (int i = 0; layout_ok && i < n; ++i) {
+      // (two warps that share a slice need not be done with the previous group at the same time)
+      refill(i, RG);
+      if (!arrived(st, phase)) break;
+      done = i + 1;
+      if (s_bad[st] == 0) {
+        const uint32_t stage = ring_addr + st * Lay::G_BYTES;
+        scores(std::false_type{}, stage, s);
+        mask(i, stage, false);
+        limits();
+#pragma unroll
+        for (int u = 0; u < 2 * NT; ++u) weigh(u >> 1, u & 1);
+        outputs(stage);
       }
-    } else if (issued < min(n, i + 2)) {
-      refill(i);  // what this step waits for has to be on its way
+      next_stage();
     }
-    if (!arrived(st, phase)) break;
-    const int st1 = st + 1 == ST ? 0 : st + 1;
-    const bool two = !kHold && i + 1 < n;
-    if (two && !arrived(st1, st1 == 0 ? phase ^ 1 : phase)) break;
-    done = i + (two ? 2 : 1);
-    if constexpr (!kHold) {
-      if (two && s_bad[st] == 0 && s_bad[st1] == 0) {
-        work(std::integral_constant<int, 2>(), i);
-        step(2);
-        i += 2;
-        continue;
+  } else if (layout_ok && n > 0 && arrived(0, 0)) {
+    // the scores of a group are computed between the weights of the one before
+    done = 1;
+    scores(std::false_type{}, ring_addr, s);
+    mask(0, ring_addr, s_bad[0] != 0);
+    limits();
+    for (int i = 0; i < n; ++i) {
+      const uint32_t stage = ring_addr + st * Lay::G_BYTES;
+      const int st1 = st + 1 == ST ? 0 : st + 1;
+      const uint32_t stage1 = ring_addr + st1 * Lay::G_BYTES;
+      if (i + 1 == n) {
+#pragma unroll
+        for (int u = 0; u < 2 * NT; ++u) weigh(u >> 1, u & 1);
+        outputs(stage);
+        break;
       }
+      if (!arrived(st1, st1 == 0 ? phase ^ 1 : phase)) break;
+      done = i + 2;
+      const bool bad = s_bad[st1] != 0;
+      float t[NT][4];
+      scores(std::true_type{}, stage1, t);
+      outputs(stage);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = t[j][e];
+      refill(i, 1);  // (by now the other warp of the slice is done with that stage too)
+      next_stage();
+      mask(i + 1, stage1, bad);
+      limits();
     }
-    if (s_bad[st] == 0) work(std::integral_constant<int, 1>(), i);
-    step(1);
-    ++i;
   }
   if (done < n && layout_ok) {
     // a wait gave up: let the copies in flight land before the shared memory is used again
@@ -470,7 +508,18 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
       }
   }
 
-  // ---- merge the slices: outputs scaled to the CTA's maximum, rows of OS floats
+  // ---- merge, in units of 16 dimensions of 8 rows as they stand in a warp's registers (one float4
+  // per lane).  A slice takes DT / KS of the 16-dimension tiles and gets them from the others.
+  constexpr int DO = Lay::DO, U = Lay::UNITS;
+  float4 *part = reinterpret_cast<float4 *>(sm);      // [KS taker][KS - 1][RG][DO][NT][32]
+  float4 *joined = reinterpret_cast<float4 *>(sm + Lay::OFF_JOIN);  // [C][units of this CTA][32]
+  float *c_m = reinterpret_cast<float *>(joined + (U + 8) * 32), *c_l = c_m + 8 * RB;  // [C][RB]
+  if (C > 1) {
+    __syncwarp();
+    // done with the ring.  (Room of its own for what the others write and an arrival at the start: one
+    // unit of 4 rows 6.0 us against 5.6.)
+    cluster_arrive();
+  }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -485,7 +534,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
       }
     }
   __syncthreads();  // (and every slice is done with its ring)
-  float *acc = reinterpret_cast<float *>(sm);
+  float w[NT][2];   // this slice's weights against the CTA's maximum
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -494,46 +543,146 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
       float top = kWinNone;
 #pragma unroll
       for (int k = 0; k < KS; ++k) top = fmaxf(top, s_m[k * RB + r]);
-      const float w = ex2_approx(m[j][e] - top);
-      float *dst = acc + (size_t)(slice * RB + r) * OS + fg;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        dst[16 * d] = o[d][j][e] * w;
-        dst[16 * d + 8] = o[d][j][e + 2] * w;
-      }
+      w[j][e] = ex2_approx(m[j][e] - top);
     }
+  auto scaled = [&](int d, int j) {
+    return make_float4(o[d][j][0] * w[j][0], o[d][j][1] * w[j][1], o[d][j][2] * w[j][0], o[d][j][3] * w[j][1]);
+  };
+  auto place = [&](int taker, int k, int d, int j) {
+    return part + ((((taker * (KS - 1) + k) * RG + rg) * DO + d % DO) * NT + j) * 32 + lane;
+  };
+#pragma unroll
+  for (int d = 0; d < DT; ++d) {
+    const int taker = d / DO;
+    if (taker != slice) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) *place(taker, slice < taker ? slice : slice - 1, d, j) = scaled(d, j);
+    }
+  }
+  float top = kWinNone, sum = 0.f;
   if (tid < RB) {
-    float top = kWinNone, sum = 0.f;
 #pragma unroll
     for (int k = 0; k < KS; ++k) top = fmaxf(top, s_m[k * RB + tid]);
 #pragma unroll
     for (int k = 0; k < KS; ++k) sum += ex2_approx(s_m[k * RB + tid] - top) * s_l[k * RB + tid];
-    s_cm[tid] = top;
-    s_cl[tid] = sum;
+    if (C == 1) s_inv[tid] = sum > 0.f ? 1.f / sum : 0.f;
   }
   __syncthreads();
-  auto store = [&](int r, int d4, float4 x, float inv) {
-    const int row = s_row[r];
-    if (row < 0) return;
-    *reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + (size_t)row * D + 4 * d4) =
-        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+  // a unit's final values to memory: rows 2 ft and 2 ft + 1 of dimensions fg and fg + 8 become, by
+  // a transpose and an exchange of neighbours, four dimensions of row fg
+  auto emit = [&](int d, int row, float4 v) {
+    const uint32_t a = transpose_8x8(pack_bf16x2(v.x, v.y)), c = transpose_8x8(pack_bf16x2(v.z, v.w));
+    const bool odd = lane & 1;
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : c, 1);
+    if (row >= 0)
+      *reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + (size_t)row * D + 16 * d + (odd ? 6 + 2 * ft : 2 * ft)) =
+          odd ? make_uint2(other, c) : make_uint2(a, other);
   };
-#pragma unroll 4
-  for (int u = tid; u < RB * (D / 4); u += kWinThreads) {
-    const int r = u / (D / 4), d4 = u % (D / 4);
-    float4 x = *reinterpret_cast<const float4 *>(acc + (size_t)r * OS + 4 * d4);
-#pragma unroll
-    for (int k = 1; k < KS; ++k) {
-      const float4 y = *reinterpret_cast<const float4 *>(acc + (size_t)(k * RB + r) * OS + 4 * d4);
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
-    }
-    if (C > 1) *reinterpret_cast<float4 *>(acc + (size_t)r * OS + 4 * d4) = x;
-    else store(r, d4, x, s_cl[r] > 0.f ? 1.f / s_cl[r] : 0.f);
+  const int shift = 31 - __clz((int)C), local = (U + (int)C - 1) >> shift;  // units of a CTA
+  if (C > 1) {
+    cluster_wait();  // every CTA of the cluster is done with its ring
+    if (tid < RB)
+      for (unsigned c = 0; c < C; ++c) {
+        remote_store(remote_address(c_m + rank * RB + tid, c), top);
+        remote_store(remote_address(c_l + rank * RB + tid, c), sum);
+      }
   }
-  if (C > 1) cluster_merge<D>(acc, OS, s_cm, s_cl, RB, C, rank, kWinNone, store);
+  float inv[NT][2];
+  int rows[NT];
+  if (C == 1) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r0 = rg * 8 * NT + 8 * j;
+      rows[j] = s_row[r0 + fg];
+      inv[j][0] = s_inv[r0 + 2 * ft];
+      inv[j][1] = s_inv[r0 + 2 * ft + 1];
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < DT; ++d) {
+    if (d / DO != slice) continue;
+    float4 x[NT][KS - 1];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < KS - 1; ++k) x[j][k] = *place(d / DO, k, d, j);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float4 v = scaled(d, j);
+#pragma unroll
+      for (int k = 0; k < KS - 1; ++k) {
+        v.x += x[j][k].x;
+        v.y += x[j][k].y;
+        v.z += x[j][k].z;
+        v.w += x[j][k].w;
+      }
+      if (C == 1) {
+        emit(d, rows[j], make_float4(v.x * inv[j][0], v.y * inv[j][1], v.z * inv[j][0], v.w * inv[j][1]));
+      } else {
+        const int u = (rg * DT + d) * NT + j;
+        remote_store(remote_address(joined + ((int)rank * local + (u >> shift)) * 32 + lane, u & (C - 1)), v);
+      }
+    }
+  }
+  if (C > 1) {
+    // each CTA joins its units of the whole cluster; nobody looks into another CTA any more
+    cluster_sync();
+    // the CTAs' weights of a row, for all rows first where a warp joins more than one unit
+    constexpr bool kTable = U > 16;
+    auto weights_of = [&](int r, float2 (&wc)[8]) {  // of rows r and r + 1
+      float2 sums[8], top = make_float2(kWinNone, kWinNone), total = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        wc[c] = top;
+        sums[c] = total;
+        if (c < (int)C) {
+          wc[c] = *reinterpret_cast<const float2 *>(c_m + c * RB + r);
+          sums[c] = *reinterpret_cast<const float2 *>(c_l + c * RB + r);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) top = make_float2(fmaxf(top.x, wc[c].x), fmaxf(top.y, wc[c].y));
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        wc[c] = make_float2(ex2_approx(wc[c].x - top.x), ex2_approx(wc[c].y - top.y));
+        total = make_float2(fmaf(wc[c].x, sums[c].x, total.x), fmaf(wc[c].y, sums[c].y, total.y));
+      }
+      const float i0 = total.x > 0.f ? 1.f / total.x : 0.f, i1 = total.y > 0.f ? 1.f / total.y : 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) wc[c] = make_float2(wc[c].x * i0, wc[c].y * i1);
+    };
+    float2 wc[8];
+    if (kTable) {
+      if (tid < RB / 2) {
+        weights_of(2 * tid, wc);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < (int)C) *reinterpret_cast<float2 *>(c_m + c * RB + 2 * tid) = wc[c];
+      }
+      __syncthreads();
+    }
+    for (int i = warp; i < local; i += kWinThreads / 32) {
+      const int u = (i << shift) + (int)rank;
+      if (u >= U) break;
+      const int j = u % NT, d = u / NT % DT, r0 = u / NT / DT * 8 * NT + 8 * j;
+      float4 y[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < (int)C) y[c] = joined[(c * local + i) * 32 + lane];
+      if (!kTable) weights_of(r0 + 2 * ft, wc);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (c >= (int)C) break;
+        if (kTable) wc[c] = *reinterpret_cast<const float2 *>(c_m + c * RB + r0 + 2 * ft);
+        v.x = fmaf(wc[c].x, y[c].x, v.x);
+        v.y = fmaf(wc[c].y, y[c].y, v.y);
+        v.z = fmaf(wc[c].x, y[c].z, v.z);
+        v.w = fmaf(wc[c].y, y[c].w, v.w);
+      }
+      emit(d, s_row[r0 + fg], v);
+    }
+  }
   if (tid == 0) {
     if (!layout_ok) set_status(p.status, SV_DEV_LAYOUT);
     else if (*abort_flag) set_status(p.status, SV_DEV_TIMEOUT);
@@ -592,18 +741,18 @@ WinRows window_rows(int M) {
 // The tensor-core kernel pads a unit's rows to 128 or 256 and pays more for a unit's start and
 // for the launch, but takes long windows of many rows at twice the rate.  Both sides as fitted
 // to measurements (us on 152 SMs, D = 128; 8 to 2048 units, 32 to 512 rows, windows 17 to 4097):
-//   here:  10 + units tiles / SMs (3 + 0.28 groups)      (0.2 per group of up to 48 rows)
+//   here:  8 + units tiles / SMs (3 + 0.245 groups)      (0.17 per group of up to 48 rows)
 //   there: 11 + units tiles / SMs (6 + 1.45 key tiles) + 2 SMs / units   (2.55 for 256 rows)
-// e.g. 128 units of 104 rows: window 129 16 us against 20, window 1025 43 against 32; 512 units of
-// 64 rows: 27 against 39, 82 against 86; 8 units of 208 rows, window 4097: 30 against 85.
-// Up to 32 rows this kernel runs at the memory's rate: 2048 units, window 1025: 180 against 270.
+// e.g. 128 units of 104 rows: window 129 13 us against 20, window 1025 39 against 32; 512 units of
+// 64 rows: 23 against 39, 71 against 86; 8 units of 208 rows, window 4097: 26 against 85.
+// Up to 32 rows this kernel runs at the memory's rate: 2048 units, window 1025: 172 against 270.
 bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms) {
   const int M = N * (Hq / Hkv);
   const WinRows r = window_rows(M);
   if (r.rg == 1) return false;
   const double units = (double)B * Hkv, sms = num_sms;
   const double groups = span / kWinGroup + 2 + N / kWinGroup, tiles = span / 128 + 2;
-  const double here = 10 + units * r.m_tiles / sms * (3 + (r.nt == 3 ? 0.2 : 0.28) * groups);
+  const double here = 8 + units * r.m_tiles / sms * (3 + (r.nt == 3 ? 0.17 : 0.245) * groups);
   const double there = 11 + units * ((M + 255) / 256) / sms * (6 + (M > 128 ? 2.55 : 1.45) * tiles) + 2 * sms / units;
   return there < here;
 }
@@ -643,8 +792,8 @@ cudaError_t launch_window_attention(const AttnParams &a, int num_sms, cudaStream
   p.m_tiles = rows_plan.m_tiles;
   // CTAs per unit: waves of resident CTAs times the length of one, which costs about 12 groups
   // (its start and merge) beside its share of the window's groups.  (Clusters of 16 gain little on
-  // the longest windows and start later: 8 units of 4 rows, window 1024, 7.2 us against 6.6; 16
-  // such clusters find no room together, 25 us against 13.)
+  // the longest windows and start later: 8 units of 4 rows, window 1024, 0.6 us more; 16 such
+  // clusters find no room together, 25 us against 13.)
   const long long units = (long long)a.B * a.Hkv * p.m_tiles, slots = 2ll * num_sms;
   const int span = a.window - 1 < a.cap ? a.window - 1 : a.cap;
   const int groups = span / kWinGroup + (a.N + a.sinks) / kWinGroup + 2;

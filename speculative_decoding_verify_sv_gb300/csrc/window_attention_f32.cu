@@ -246,11 +246,9 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
     s_cl[tid] = sum;
   }
   __syncthreads();
-  auto store = [&](int r, int d4, float4 x, float inv) {
+  auto store = [&](int r, int d4, float4 x) {
     const int row = s_row[r];
-    if (row < 0) return;
-    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + (size_t)row * D + 4 * d4) =
-        make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (row >= 0) *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + (size_t)row * D + 4 * d4) = x;
   };
   for (int u = tid; u < R * (D / 4); u += NW * 32) {
     const int r = u / (D / 4), d4 = u % (D / 4);
@@ -263,10 +261,14 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
       x.z += y.z;
       x.w += y.w;
     }
-    if (C > 1) *reinterpret_cast<float4 *>(sm + r * D + 4 * d4) = x;
-    else store(r, d4, x, s_cl[r] > 0.f ? 1.f / s_cl[r] : 0.f);
+    if (C > 1) {
+      *reinterpret_cast<float4 *>(sm + r * D + 4 * d4) = x;
+    } else {
+      const float inv = s_cl[r] > 0.f ? 1.f / s_cl[r] : 0.f;
+      store(r, d4, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    }
   }
-  if (C > 1) cluster_merge<D>(sm, D, s_cm, s_cl, R, C, rank, kF32None, store);
+  if (C > 1) cluster_merge<D>(sm, D, s_cm, s_cl, R, C, rank, kF32None, sm + Lay::CHUNK, store);
 }
 
 template <int D, int R>
