@@ -790,8 +790,9 @@ cudaError_t launch_window_attention(const AttnParams &a, int num_sms, cudaStream
   const WinRows rows_plan = window_rows(a.M);
   const int nt = rows_plan.nt, rg = rows_plan.rg;
   p.m_tiles = rows_plan.m_tiles;
-  // CTAs per unit: waves of resident CTAs times the length of one, which costs about 12 groups
-  // (its start and merge) beside its share of the window's groups.  (Clusters of 16 gain little on
+  // CTAs per unit: waves of resident CTAs times the length of one, which costs about 16 groups
+  // (its start and merge) beside its share of the window's groups: 512 units of 32 rows, window
+  // 4097, go without clusters, 156 us against 181 with clusters of four.  (Clusters of 16 gain little on
   // the longest windows and start later: 8 units of 4 rows, window 1024, 0.6 us more; 16 such
   // clusters find no room together, 25 us against 13.)
   const long long units = (long long)a.B * a.Hkv * p.m_tiles, slots = 2ll * num_sms;
@@ -800,7 +801,7 @@ cudaError_t launch_window_attention(const AttnParams &a, int num_sms, cudaStream
   long long best = 0;
   p.cluster = 1;
   for (int c = 1; c <= 8; c *= 2) {
-    const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 12);
+    const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 16);
     if (c == 1 || cost < best) {
       best = cost;
       p.cluster = c;

@@ -24,6 +24,13 @@ namespace {
 constexpr int kF32Keys = 32;   // keys of a chunk: one per lane
 constexpr float kF32None = -3e38f;  // a row's maximum before its first key
 
+// The maximum over a warp.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // R floats of shared memory, in as few accesses as they take.
 template <int R>
 __device__ __forceinline__ void put(float *p, const float (&v)[R]) {
@@ -83,8 +90,22 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   const unsigned C = p.splits, rank = C > 1 ? cluster_rank() : 0;
   const int blocks = (p.M + R - 1) / R, unit = blockIdx.x / C;
   const int mb = unit % blocks, kvh = (unit / blocks) % p.Hkv, b = unit / blocks / p.Hkv;
+  if (tid < R) {
+    const int at = mb * R + tid, node = at / p.G;
+    s_row[tid] = at < p.M ? (b * p.N + node) * p.Hq + kvh * p.G + at - node * p.G : -1;
+  }
+  __syncthreads();
   wait_previous();
   int L = p.prefix_len[b];
+  // rows and tree, on their way before the first chunks
+  constexpr int QL = (R * D + NW * 32 - 1) / (NW * 32);
+  float qv[QL];
+#pragma unroll
+  for (int k = 0; k < QL; ++k) {
+    const int i = tid + k * NW * 32, row = i < R * D ? s_row[i / D] : -1;
+    qv[k] = row >= 0 ? static_cast<const float *>(p.q)[(size_t)row * D + i % D] : 0.f;
+  }
+  const int parent = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
   if (L < 0 || L > p.cap) {
     if (unit % (blocks * p.Hkv) == 0 && rank == 0 && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
     L = L < 0 ? 0 : p.cap;
@@ -130,16 +151,11 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   if (c0 < chunks) there = fetch(c0);
 
   // the rows and what each of them sees, while the first chunks are on their way
-  if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
-  if (tid < R) {
-    const int at = mb * R + tid, node = at / p.G;
-    s_row[tid] = at < p.M ? (b * p.N + node) * p.Hq + kvh * p.G + at - node * p.G : -1;
-  }
+  if (tid < kMaxNodes) s_par[tid] = parent;
+#pragma unroll
+  for (int k = 0; k < QL; ++k)
+    if (tid + k * NW * 32 < R * D) s_q[tid + k * NW * 32] = qv[k];
   __syncthreads();
-  for (int i = tid; i < R * D; i += NW * 32) {
-    const int row = s_row[i / D];
-    s_q[i] = row >= 0 ? static_cast<const float *>(p.q)[(size_t)row * D + i % D] : 0.f;
-  }
   if (tid < R) {
     const int at = mb * R + tid;
     uint64_t anc = 0;
@@ -188,10 +204,7 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
       const bool see = there && (c < ct ? ((s_anc[r] >> (key & 63)) & 1ull) != 0
                                         : (c < cs || key >= s_lo[r] || key < p.sinks));
       const float x = see ? s[r] * p.scale_log2 : -INFINITY;
-      float top = x;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-      top = fmaxf(top, m[r]);
+      const float top = fmaxf(warp_max(x), m[r]);
       const float a = exp2f(m[r] - top);
       m[r] = top;
       w[r] = see ? exp2f(x - top) : 0.f;

@@ -108,7 +108,7 @@ def test_long_unit_cut_over_many_ctas(cuda_ok, paged):
 # (nodes, group heads) -> units with 64, 104, 208 and 512 query rows, where many units with long
 # enough windows go to the 128-row tensor-core kernel: two row copies, one tile, two tiles, two
 # groups of two tiles
-@pytest.mark.parametrize("N,G,B,window", [(16, 4, 72, 1100), (26, 4, 64, 260), (26, 8, 48, 40), (26, 8, 48, 300),
+@pytest.mark.parametrize("N,G,B,window", [(16, 4, 48, 2000), (26, 4, 64, 260), (26, 8, 48, 40), (26, 8, 48, 300),
                                           (64, 8, 24, 17), (64, 8, 24, 200)])
 @pytest.mark.parametrize("D,block_size", [(128, 0), (128, 16), (64, 32), (128, 128), (64, 0)])
 def test_many_units_of_many_rows(cuda_ok, N, G, B, window, D, block_size):
