@@ -25,8 +25,8 @@
 //
 // Bound by HBM for many units of up to 48 rows: 256 ragged requests of 5 nodes, 32:8 heads of 128,
 // window 1024 in pages of 16, 174 us, 6.2 TB/s, 91 % of the measured copy rate (the 128-row kernel
-// 268 us); by the warps' chains of products and exponents for 64 rows (256 units, window 513: 24.5 us,
-// of which 2 start, 17 loop, 2.5 merge; the matrix pipe is half busy); by latency for few units: one
+// 268 us); by the warps' chains of products and exponents for 64 rows (256 units, window 513: 23.8 us,
+// of which 2 start, 16 loop, 2.5 merge; the matrix pipe is half busy); by latency for few units: one
 // token of one request, window 1024, 5.5 us (the 128-row kernel 49).
 //
 // The slices merge in shared memory by weights 2^(m_slice - m), each taking some dimensions of all
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   const bool layout_ok = (smem_u32(sm) & 1023u) == 0;  // 128-byte-swizzled boxes
   if (lane == 0 && rg == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], RG);
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], RG);
     }
     fence_barrier_init();
@@ -188,9 +188,8 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   const int g0 = min((int)rank * per, groups), g1 = min(g0 + per, groups);
   const int n = g1 - g0 > slice ? (g1 - g0 - slice + KS - 1) / KS : 0;  // this slice's groups
 
-  // ---- copies: a slice's warp issues its groups' K and V; two warps share that out
-  constexpr bool kBoth = RG == 1;
-  constexpr uint32_t kTx = kBoth ? Lay::G_BYTES : Lay::K_BYTES;
+  // ---- copies: a slice's warp issues its groups' K and V; of two warps each does so for every other
+  // group
   const uint64_t stream_policy = l2_policy_evict_first(), tree_policy = l2_policy_evict_normal();
   int desc = -1;  // lane i: row of group (32 k + i) of this slice, k the batch being issued
   auto locate = [&](int i) -> int {
@@ -215,31 +214,32 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     }
     uint8_t *dst = ring + st * Lay::G_BYTES;
     const uint64_t policy = tree ? tree_policy : stream_policy;
-    mbar_expect_tx(&full[st], kTx);
-    if (kBoth || rg == 0) tma_load_4d_hint(dst, tree ? &p.tm_kt : &p.tm_kc, 0, row, 0, kvh, &full[st], policy);
-    if (kBoth || rg == 1)
-      tma_load_4d_hint(dst + Lay::K_BYTES, tree ? &p.tm_vt : &p.tm_vc, 0, row, 0, kvh, &full[st], policy);
+    mbar_expect_tx(&full[st], Lay::G_BYTES);
+    tma_load_4d_hint(dst, tree ? &p.tm_kt : &p.tm_kc, 0, row, 0, kvh, &full[st], policy);
+    tma_load_4d_hint(dst + Lay::K_BYTES, tree ? &p.tm_vt : &p.tm_vc, 0, row, 0, kvh, &full[st], policy);
   };
+  auto mine = [&](int i) { return RG == 1 || (i & 1) == rg; };
   // group i of the slice into stage st, which is free once its last group's barrier `empty` has
   // passed the parity
   auto issue = [&](int i, int st, int parity) {
     if ((i & 31) == 0) desc = locate(i + lane);
+    if (!mine(i)) return;
     const int row = __shfl_sync(0xFFFFFFFFu, desc, i & 31);
     const bool tree = g0 + slice + KS * i < gt;
-    if (elect_one() && (kBoth || mbar_wait(&empty[st], parity, abort_flag, p.wait_ns))) copy(row, tree, st);
+    if (elect_one() && (RG == 1 || parity < 0 || mbar_wait(&empty[st], parity, abort_flag, p.wait_ns))) copy(row, tree, st);
     __syncwarp();
   };
-  // The first groups.  A warp that brings both K and V takes them one after another, so that the first
-  // one is whole soon (2048 units of 32 rows, window 1025, 169 us against 176 with a lane each); of
-  // two warps each lane takes one (24.4 us against 25.5 for 256 units of 64 rows, window 513).
-  static_assert(ST <= 32, "a lane each");
+  // The first groups, one after another so that the first one is whole soon (2048 units of 32 rows,
+  // window 1025, 169 us against 176 with a lane each); with a lane each only for 33 to 48 rows (512
+  // units, window 4097, 179 us against 185; 256 units of 64 rows, window 513, 23.8 against 24.9).
+  static_assert(ST <= 32, "the first groups are one batch");
   if (layout_ok) {
-    if (kBoth) {
-      for (int i = 0; i < min(ST, n); ++i) issue(i, i, 0);
-    } else {
+    if (RG == 2 && NT < 4) {
       desc = locate(lane);
-      if (lane < min(ST, n)) copy(desc, g0 + slice + KS * lane < gt, lane);
+      if (lane < min(ST, n) && mine(lane)) copy(desc, g0 + slice + KS * lane < gt, lane);
       __syncwarp();
+    } else {
+      for (int i = 0; i < min(ST, n); ++i) issue(i, i, -1);
     }
   }
 
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     *abort_flag = 1;
     const unsigned long long t0 = global_ns();
     for (int i = done; i < issued; ++i)
-      while (!mbar_try_wait(&full[i % ST], (i / ST) & 1) && global_ns() - t0 < kWaitLimitNs) {
+      while (mine(i) && !mbar_try_wait(&full[i % ST], (i / ST) & 1) && global_ns() - t0 < kWaitLimitNs) {
       }
   }
 
@@ -741,10 +741,10 @@ WinRows window_rows(int M) {
 // The tensor-core kernel pads a unit's rows to 128 or 256 and pays more for a unit's start and
 // for the launch, but takes long windows of many rows at twice the rate.  Both sides as fitted
 // to measurements (us on 152 SMs, D = 128; 8 to 2048 units, 32 to 512 rows, windows 17 to 4097):
-//   here:  8 + units tiles / SMs (3 + 0.245 groups)      (0.17 per group of up to 48 rows)
-//   there: 11 + units tiles / SMs (6 + 1.45 key tiles) + 2 SMs / units   (2.55 for 256 rows)
-// e.g. 128 units of 104 rows: window 129 13 us against 20, window 1025 39 against 32; 512 units of
-// 64 rows: 23 against 39, 71 against 86; 8 units of 208 rows, window 4097: 26 against 85.
+//   here:  8 + units tiles / SMs (3 + 0.23 groups)       (0.17 per group of up to 48 rows)
+//   there: 13 + units tiles / SMs (6 + 1.45 key tiles) + 2 SMs / units   (2.55 for 256 rows)
+// e.g. 128 units of 104 rows: window 129 14 us against 21, window 1025 37 against 33; 512 units of
+// 64 rows: 24 against 39, 69 against 87; 8 units of 208 rows, window 4097: 25 against 85.
 // Up to 32 rows this kernel runs at the memory's rate: 2048 units, window 1025: 172 against 270.
 bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms) {
   const int M = N * (Hq / Hkv);
@@ -752,8 +752,8 @@ bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms) {
   if (r.rg == 1) return false;
   const double units = (double)B * Hkv, sms = num_sms;
   const double groups = span / kWinGroup + 2 + N / kWinGroup, tiles = span / 128 + 2;
-  const double here = 8 + units * r.m_tiles / sms * (3 + (r.nt == 3 ? 0.17 : 0.245) * groups);
-  const double there = 11 + units * ((M + 255) / 256) / sms * (6 + (M > 128 ? 2.55 : 1.45) * tiles) + 2 * sms / units;
+  const double here = 8 + units * r.m_tiles / sms * (3 + (r.nt == 3 ? 0.17 : 0.23) * groups);
+  const double there = 13 + units * ((M + 255) / 256) / sms * (6 + (M > 128 ? 2.55 : 1.45) * tiles) + 2 * sms / units;
   return there < here;
 }
 

@@ -108,7 +108,7 @@ def test_long_unit_cut_over_many_ctas(cuda_ok, paged):
 # (nodes, group heads) -> units with 64, 104, 208 and 512 query rows, where many units with long
 # enough windows go to the 128-row tensor-core kernel: two row copies, one tile, two tiles, two
 # groups of two tiles
-@pytest.mark.parametrize("N,G,B,window", [(16, 4, 48, 2000), (26, 4, 64, 260), (26, 8, 48, 40), (26, 8, 48, 300),
+@pytest.mark.parametrize("N,G,B,window", [(16, 4, 40, 3500), (26, 4, 64, 260), (26, 8, 48, 40), (26, 8, 48, 300),
                                           (64, 8, 24, 17), (64, 8, 24, 200)])
 @pytest.mark.parametrize("D,block_size", [(128, 0), (128, 16), (64, 32), (128, 128), (64, 0)])
 def test_many_units_of_many_rows(cuda_ok, N, G, B, window, D, block_size):
@@ -136,7 +136,7 @@ def test_whole_prefix_is_tree_attention(cuda_ok):
 
 
 @pytest.mark.parametrize("dtype,B,N,Hq,Hkv,D", [(BF, 5, 7, 8, 2, 128), (F32, 5, 7, 8, 2, 128), (BF, 5, 26, 8, 4, 64),
-                                                (BF, 64, 26, 64, 8, 128), (BF, 72, 26, 32, 8, 64)])
+                                                (BF, 64, 26, 64, 8, 128), (BF, 64, 26, 64, 8, 64)])
 @pytest.mark.parametrize("paged", [False, True])
 def test_nothing_leaks_from_what_no_row_sees(cuda_ok, dtype, B, N, Hq, Hkv, D, paged):
     """NaN and infinity in every cache position outside the window and the sinks, in the room
