@@ -298,7 +298,9 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int block_size = number(a[4], "block_size"), num_blocks = number(a[5], "num_blocks");
     const int32_t *head = given(a[7]) ? tensor(a[7], "free_head", at::kInt, {1}, dev).const_data_ptr<int32_t>() : nullptr;
     const Stream stream(a[9], dev);
-    static const char *names[4] = {"token_start", "slots", "positions", "free_head"};
+    static const char *const names[4] = {"token_start", "slots", "positions", "free_head"};
+    static PyObject *const keys[4] = {PyUnicode_InternFromString(names[0]), PyUnicode_InternFromString(names[1]),
+                                      PyUnicode_InternFromString(names[2]), PyUnicode_InternFromString(names[3])};
     const int64_t sizes[4] = {B + 1, T, T, 1};
     PyObject *outs = given(a[8]) ? a[8] : PyDict_New();
     if (!outs) throw Refused();
@@ -312,14 +314,15 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
       at::Tensor buffer;
       int32_t *ptr[4];
       for (int i = 0; i < 4; ++i) {
-        PyObject *o = PyDict_GetItemString(outs, names[i]);
+        PyObject *o = given(a[8]) ? PyDict_GetItemWithError(outs, keys[i]) : nullptr;
+        if (!o && PyErr_Occurred()) throw Refused();
         if (o) {
           ptr[i] = tensor(o, names[i], at::kInt, {sizes[i]}, dev).data_ptr<int32_t>();
         } else {
           if (!buffer.defined()) buffer = make({2 * padded + B + 2}, len, at::kInt);
           ptr[i] = buffer.data_ptr<int32_t>() + offsets[i];
           PyObject *w = THPVariable_Wrap(part(buffer, offsets[i], {sizes[i]}));
-          if (!w || PyDict_SetItemString(outs, names[i], w) != 0) {
+          if (!w || PyDict_SetItem(outs, keys[i], w) != 0) {
             Py_XDECREF(w);
             throw Refused();
           }

@@ -11,12 +11,12 @@
 // request from L2, one block-wide scan) and then fills its share of the slot map, so nothing is
 // handed from CTA to CTA.  A thread finds the requests of its tokens by a search of a fixed number
 // of steps, several tokens side by side, so that neither the searches nor the reads of the page
-// ids wait for one another.  Where requests bring many tokens (256 places
-// of the map per request and more) a thread takes four neighbouring tokens, which mostly share
-// their request and page: 256 prompts of 512 to 8192 tokens 8.8 us against 16.4 with single tokens;
-// 4096 requests of up to 64 tokens 7.3 us with single tokens against 9.9 with four, whose
-// crossings of requests diverge; 256 requests of 5 tokens 5.0 us.  A fresh page starts with a new token (its first position is not
-// below length_b), so the thread that holds this token writes the page's table entry.
+// ids wait for one another.  Where requests bring many tokens (256 places of the map per request
+// and more) a thread takes four neighbouring tokens, which mostly share their request and page: 256
+// prompts of 512 to 8192 tokens 9.0 us against 16.4 with single tokens; 4096 requests of up to 64
+// tokens 7.4 us with single tokens against 9.9 with four, whose crossings of requests diverge.
+// A fresh page starts with a new token (its first position is not below length_b), so the thread
+// that holds this token writes the page's table entry.
 // What bounds it: 8 bytes written per token (slot and position); small batches are a chain of
 // three dependent memory round trips (lengths, page ids, stores) and two block barriers.
 #include <atomic>
@@ -250,23 +250,32 @@ cudaError_t launch_block_tables(TableParams p, int num_sms, cudaStream_t s) {
   p.div_shift = 0;
   while ((1ll << p.div_shift) < p.block_size) ++p.div_shift;
   p.div_mul = (unsigned)(((1ull << 32) * ((1ull << p.div_shift) - p.block_size)) / p.block_size + 1);
-  const int run = p.T / p.B >= 256 ? 4 : 1;
-  const int threads = run == 4 ? 512 : 1024;
-  auto kernel = run == 4 ? block_tables_kernel<4, 512> : block_tables_kernel<1, 1024>;
+  // Many tokens per request: four neighbouring ones per thread.  Else CTAs of 256 threads with two
+  // tokens each, so that few tokens go over many SMs, while the sums over the batch that every CTA
+  // makes are short; beyond 2048 requests 1024 threads (256 requests of 5 tokens 3.7 us against 5.2,
+  // 2048 of 5 5.6 against 6.6; 4096 of 32 9.1 against 7.4; device time).
+  struct Form {
+    void (*kernel)(TableParams);
+    int threads, tokens;  // tokens that a CTA takes in a step
+  };
+  static const Form forms[3] = {{block_tables_kernel<4, 512>, 512, 2048},
+                                {block_tables_kernel<1, 256>, 256, 512},
+                                {block_tables_kernel<1, 1024>, 1024, 2048}};
+  const int form = p.T / p.B >= 256 ? 0 : (p.B <= 2048 ? 1 : 2);
+  const Form &f = forms[form];
   const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int);
-  static std::atomic<bool> attr_set[2][64];
+  static std::atomic<bool> attr_set[3][64];
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !attr_set[run == 4][dev].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (dev < 0 || dev >= 64 || !attr_set[form][dev].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)((3 * SV_MAX_TABLE_BATCH + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[run == 4][dev].store(true);
+    if (dev >= 0 && dev < 64) attr_set[form][dev].store(true);
   }
-  const long long per_cta = 2048;  // tokens per step
-  long long ctas = (p.T + per_cta - 1) / per_cta;
+  long long ctas = (p.T + f.tokens - 1) / f.tokens;
   ctas = ctas < 1 ? 1 : (ctas > 2ll * num_sms ? 2ll * num_sms : ctas);
-  return launch_close(kernel, dim3((unsigned)ctas), threads, smem, s, p);
+  return launch_close(f.kernel, dim3((unsigned)ctas), f.threads, smem, s, p);
 }
 
 }  // namespace sv
