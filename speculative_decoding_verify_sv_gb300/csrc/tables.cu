@@ -13,8 +13,9 @@
 // of steps, several tokens side by side, so that neither the searches nor the reads of the page
 // ids wait for one another.  Where requests bring many tokens (256 places of the map per request
 // and more) a thread takes four neighbouring tokens, which mostly share their request and page: 256
-// prompts of 512 to 8192 tokens 9.0 us against 16.4 with single tokens; 4096 requests of up to 64
-// tokens 7.4 us with single tokens against 9.9 with four, whose crossings of requests diverge.
+// prompts of 512 to 8192 tokens 7.9 us (8.9 with 64-bit places) against 16.4 with single tokens; 4096
+// requests of up to 64 tokens 7.2 us with single tokens against 9.9 with four, whose crossings of
+// requests diverge.
 // A fresh page starts with a new token (its first position is not below length_b), so the thread
 // that holds this token writes the page's table entry.
 // What bounds it: 8 bytes written per token (slot and position); small batches are a chain of
@@ -122,50 +123,54 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   if (tid == 0) s_start[p.B] = (int)min(total, (long long)INT32_MAX);
   __syncthreads();
 
-  // up to the batch's last token (its pages are given out even where the slot map is too short)
-  // and on to the end of the slot map
-  // (tokens that a 32-bit place does not reach are not looked at: wild numbers make no long loop)
-  const long long end = min(max(total, (long long)p.T), (long long)INT32_MAX);
+  // Up to the batch's last token (its pages are given out even where the slot map is too short) and
+  // on to the end of the slot map.  Tokens that a 32-bit place does not reach are not looked at: wild
+  // numbers make no long loop, and places are 32-bit numbers in it.
+  const unsigned tokens = (unsigned)min(total, (long long)INT32_MAX), end = max(tokens, (unsigned)p.T);
   constexpr int U = RUN == 1 ? 2 : RUN;
-  const long long step = (long long)gridDim.x * kTableThreads * U;
+  const unsigned step = gridDim.x * kTableThreads * U;
   const int top = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;  // the search's first stride
   // where the id of page pg of request b is: held (in the table) or fresh (NULL: none is left)
+  const unsigned left = head >= 0 && head < p.num_free ? (unsigned)(p.num_free - head) : 0u;
+  const int32_t *fresh = p.free_blocks + (left ? head : 0);
   auto page_source = [&](int b, int pg, int have) -> const int32_t * {
-    const long long i = head + s_base[b] + pg - have;
     if (pg >= p.max_blocks) return nullptr;
     if (pg < have) return p.block_table + (size_t)b * p.max_blocks + pg;
-    return head >= 0 && i < p.num_free ? p.free_blocks + i : nullptr;
+    const unsigned i = (unsigned)s_base[b] + (unsigned)(pg - have);
+    return i < left ? fresh + i : nullptr;
   };
+  bool bad = false;  // an id outside the pool, or none left
   // the id as it was read, checked; the entry of a fresh page is written with its first token
   auto checked = [&](int row, int b, int pg, bool entry) -> int {
     if (pg >= p.max_blocks) return -1;
-    if (row < 0 || row >= p.num_blocks) {
-      set_status(p.status, SV_DEV_BAD_BLOCK);
+    if ((unsigned)row >= (unsigned)p.num_blocks) {
+      bad = true;
       row = -1;
     }
     if (entry) p.block_table[(size_t)b * p.max_blocks + pg] = row;
     return row;
   };
-  for (long long t0 = (long long)blockIdx.x * kTableThreads * U + tid * RUN; t0 < end; t0 += step) {
+  for (unsigned t0 = blockIdx.x * kTableThreads * U + tid * RUN; t0 < end; t0 += step) {
     if constexpr (RUN == 1) {
-      int b[U], t[U], pos[U], row[U];
+      int b[U], pos[U], row[U];
+      unsigned t[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        t[k] = (int)min(t0 + k * kTableThreads, (long long)INT32_MAX);
+        t[k] = t0 + k * kTableThreads;
         b[k] = 0;
       }
       // the last request that starts at or before the token (those without tokens are passed over)
       for (int d = top; d > 0; d >>= 1)
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if (b[k] + d < p.B && s_start[b[k] + d] <= t[k]) b[k] += d;
+          if (b[k] + d < p.B && (unsigned)s_start[b[k] + d] <= t[k]) b[k] += d;
       const int32_t *src[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         pos[k] = -1;
         src[k] = nullptr;
-        if (t[k] >= total || t[k] == INT32_MAX) continue;
-        pos[k] = s_len[b[k]] + t[k] - s_start[b[k]];
+        if (t[k] >= tokens) continue;
+        pos[k] = s_len[b[k]] + ((int)t[k] - s_start[b[k]]);
         src[k] = page_source(b[k], page_of(p, pos[k]), pages_of(p, s_len[b[k]]));
       }
 #pragma unroll
@@ -178,29 +183,28 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
           row[k] = checked(row[k], b[k], pg, off == 0 && pos[k] >= s_len[b[k]]);
           if (row[k] >= 0) slot = row[k] * p.block_size + off;
         }
-        const long long at = t0 + k * kTableThreads;
-        if (at < p.T) {
-          p.slots[at] = slot;
-          p.positions[at] = pos[k];
+        if (t[k] < (unsigned)p.T) {
+          p.slots[t[k]] = slot;
+          p.positions[t[k]] = pos[k];
         }
       }
     } else {
       int slot[U], pos[U];
       int b = 0, have = 0, pg = 0, off = 0, row = -1, last = -1;
-      long long stop = -1;  // the first token of the next request
+      unsigned stop = 0;  // the first token of the next request
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const long long t = t0 + k;
         slot[k] = pos[k] = -1;
-        if (t >= total || t >= INT32_MAX) continue;
+        const unsigned t = t0 + k;
+        if (t >= tokens) continue;
         bool look = false;  // the page's id has to be read
         if (t >= stop) {
           for (int d = top; d > 0; d >>= 1)
-            if (b + d < p.B && s_start[b + d] <= t) b += d;
-          stop = s_start[b + 1];
+            if (b + d < p.B && (unsigned)s_start[b + d] <= t) b += d;
+          stop = (unsigned)s_start[b + 1];
           const int len = s_len[b];
           have = pages_of(p, len);
-          pos[k] = len + (int)(t - s_start[b]);
+          pos[k] = len + ((int)t - s_start[b]);
           pg = page_of(p, pos[k]);
           off = pos[k] - pg * p.block_size;
           look = true;
@@ -219,19 +223,20 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
         }
         if (row >= 0) slot[k] = row * p.block_size + off;
       }
-      if (t0 + U <= p.T) {
+      if (t0 + U <= (unsigned)p.T) {
         *reinterpret_cast<int4 *>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
         *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       } else {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if (t0 + k < p.T) {
+          if (t0 + k < (unsigned)p.T) {
             p.slots[t0 + k] = slot[k];
             p.positions[t0 + k] = pos[k];
           }
       }
     }
   }
+  if (bad) set_status(p.status, SV_DEV_BAD_BLOCK);
   if (report) {
     for (int b = tid; b <= p.B; b += kTableThreads) p.token_start[b] = s_start[b];
     if (tid == 0) {
