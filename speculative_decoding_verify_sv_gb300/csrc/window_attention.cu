@@ -514,12 +514,9 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   float4 *part = reinterpret_cast<float4 *>(sm);      // [KS taker][KS - 1][RG][DO][NT][32]
   float4 *joined = reinterpret_cast<float4 *>(sm + Lay::OFF_JOIN);  // [C][units of this CTA][32]
   float *c_m = reinterpret_cast<float *>(joined + (U + 8) * 32), *c_l = c_m + 8 * RB;  // [C][RB]
-  if (C > 1) {
-    __syncwarp();
-    // done with the ring.  (Room of its own for what the others write and an arrival at the start: one
-    // unit of 4 rows 6.0 us against 5.6.)
-    cluster_arrive();
-  }
+  // Done with the ring.  (Room of its own for what the others write and an arrival at the start gain
+  // nothing.)
+  if (C > 1) cluster_arrive();
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
