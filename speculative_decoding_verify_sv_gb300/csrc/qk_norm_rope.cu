@@ -10,8 +10,8 @@
 //
 // Angles: a position is a whole number, so only the fraction of a turn per position matters.
 // It is held as a 64-bit fixed-point fraction (of 2^64), which the 64-bit product with the
-// position wraps exactly: no argument reduction and no loss at far positions (the error is
-// that of the frequency, 2^-53 of it per position).  The nearest quarter turn comes off in
+// position wraps exactly: no argument reduction and no loss at far positions (off by less than
+// 2^-64 of a turn per position).  The nearest quarter turn comes off in
 // integers, so that the sine and cosine are taken of at most an eighth of a turn.
 //
 // A warp takes a token (or, when there are few tokens, a part of its heads) and reads whole
@@ -21,7 +21,7 @@
 //   out_i = r (x_i A_i + x_j B_i),  j the other element of i's pair, r = 1 / sqrt(mean + eps),
 // and the other lane's x_j comes as the raw 16 bits it was loaded as.  It is bound by HBM:
 // each element is read once and written once.  32768 tokens of 32:8 heads of 128 in bf16 take
-// 129 us, 6.25 TB/s, 92 % of the measured copy rate; 171 us before the loads ran ahead of the
+// 127 us, 6.32 TB/s, 93 % of the measured copy rate; 171 us before the loads ran ahead of the
 // work and the factors were made per token; 135 us with 16 instead of 20 warps per SM; 140 us
 // with stores that stay in L2 (the outputs of a prompt exceed it).
 #include "sv_common.cuh"
@@ -46,10 +46,22 @@ __device__ __forceinline__ uint4 pack_vec<float>(const float *f) {
   return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
-// The fraction of a turn per position, of 2^64.
-__device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
-  const double turns = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  return __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+// The fraction of a turn per position, of 2^64: f / (2 pi) mod 1 with f = m 2^e, m a 53-bit integer, as
+// the 117-bit product of m and 2^66 / (2 pi), shifted by e - 2 places (off by less than 2^-64 and
+// 2^-64 f).  In integers, once per CTA: products and roundings in double take 16 cycles of the SM per
+// warp each.  With that, and the first token requested before the weights: 384 tokens 5.8 -> 5.1 us,
+// 4096 21.7 -> 21.0, 32768 129 -> 127.4.
+__device__ __forceinline__ uint64_t turn_fraction(double f) {
+  constexpr uint64_t kPerTurn = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi)
+  const uint64_t bits = (uint64_t)__double_as_longlong(f);
+  const int field = (int)(bits >> 52) & 2047, shift = 1077 - (field ? field : 1);
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (field ? 1ull << 52 : 0ull);
+  const uint64_t lo = m * kPerTurn, hi = __umul64hi(m, kPerTurn);
+  uint64_t x;
+  if (shift <= 0) x = shift > -64 ? lo << -shift : 0ull;
+  else if (shift < 64) x = lo >> shift | hi << (64 - shift);
+  else x = shift < 128 ? hi >> (shift - 64) : 0ull;
+  return bits >> 63 ? 0ull - x : x;
 }
 
 // (cos, sin) of position * frequency.
@@ -104,6 +116,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
   constexpr int U = kRopeBatch;
   __shared__ __align__(16) float2 s_cs[kRopeWarps][64];
   __shared__ __align__(16) float s_w[2][128];
+  __shared__ uint64_t s_turn[64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LPH, sub = lane / LPH, e0 = l * V;
   const int half = p.rot >> 1;
@@ -113,14 +126,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
   const int j0 = (partner % LPH) * V;
   float2 *cs = s_cs[warp];
   wait_previous();
-  if (threadIdx.x < D) {
-    s_w[0][threadIdx.x] = p.q_weight[threadIdx.x];
-    s_w[1][threadIdx.x] = p.k_weight[threadIdx.x];
-  }
-  uint64_t freq[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) freq[i] = lane + 32 * i < half ? turn_fraction(p.inv_freq[lane + 32 * i]) : 0ull;
-  __syncthreads();
+  // (requested before the first token, used behind its loads)
+  const bool holds = threadIdx.x < D;
+  const float qw = holds ? p.q_weight[threadIdx.x] : 0.f, kw = holds ? p.k_weight[threadIdx.x] : 0.f;
+  const double turn = threadIdx.x < 64 && (int)threadIdx.x < half ? p.inv_freq[threadIdx.x] : 0.0;
 
   // a token's batches: query heads, key heads, value heads (none mixes two kinds)
   const int nq = (p.Hq + HPW * U - 1) / (HPW * U), nk = (p.Hkv + HPW * U - 1) / (HPW * U), nb = nq + 2 * nk;
@@ -167,11 +176,18 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (lane + 32 * i < half) cs[lane + 32 * i] = turn_cos_sin(freq[i], position);
+      if (lane + 32 * i < half) cs[lane + 32 * i] = turn_cos_sin(s_turn[lane + 32 * i], position);
     __syncwarp();
   };
-  if (!begin()) return;
-  load(raw[0], t, bi);
+  const bool any = begin();
+  if (any) load(raw[0], t, bi);
+  if (holds) {
+    s_w[0][threadIdx.x] = qw;
+    s_w[1][threadIdx.x] = kw;
+  }
+  if (threadIdx.x < 64) s_turn[threadIdx.x] = turn_fraction(turn);
+  __syncthreads();
+  if (!any) return;
   angles();
   int kind = -1;
   float2 A[V / 2], B[V / 2];
