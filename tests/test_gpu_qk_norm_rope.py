@@ -55,6 +55,21 @@ def test_many_tokens(cuda_ok, T):
     _compare(got, inp, positions, 8, 2, 1e-6, False)
 
 
+def test_frequencies_of_all_sizes_and_signs(cuda_ok):
+    """Turns per position from double frequencies: zero, subnormal, whole turns, negative, and up to
+    2^30 (the positions are powers of two, so that the definition's products are exact)."""
+    inp = _inputs(4, 3, 2, 64, 64, F32, seed=21)
+    special = [0.0, -0.0, 5e-324, 1e-310, 2.0 ** -1022, 1e-20, -1e-20, 2.0 ** -64, -2.0 ** -63, -1e-3, 0.5, -0.5, 1.0, -1.0,
+               6.283185307179586, -6.283185307179586, 0.7853981633974483, 1.5707963267948966, 3.0, 100.25, -1234.5678,
+               2.0 ** 20 + 0.1, 2.0 ** 30 + 0.3, -2.0 ** 30 - 0.7]
+    inp["inv"] = torch.tensor(special + [0.1 * (i + 1) for i in range(32 - len(special))], dtype=torch.float64)
+    positions = torch.tensor([0, 1, 2, 4], dtype=torch.int32)
+    dev = {k: v.cuda() for k, v in inp.items()}
+    for interleaved in (False, True):
+        got = sv.sv_qk_norm_rope(dev["qkv"], 3, 2, dev["qw"], dev["kw"], dev["inv"], positions.cuda(), interleaved=interleaved)
+        _compare(got, inp, positions, 3, 2, 1e-6, interleaved)
+
+
 def test_slots_and_padding(cuda_ok):
     """K/V go to their slots and nowhere else; padding tokens and negative slots write nothing."""
     T, Hq, Hkv, D, rows = 12, 8, 2, 128, 64
