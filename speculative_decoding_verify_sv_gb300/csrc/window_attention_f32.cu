@@ -9,8 +9,8 @@
 // D + 4 floats: conflict-free 16-byte reads, each read once for all rows); for P V lane i holds the
 // dimensions i, i + 32, ... and reads the weights of a key as two broadcast vectors.
 //
-// Bound by latency for few units (5 sequences of 4 heads of 64, window 129: 8.7 us; with chunks
-// walked by the whole CTA, a barrier each, 11.9), by the FFMA rate for many.
+// Bound by latency for few units (5 sequences of 4 heads of 64, 5 rows, window 129: 4.3 us; 7.5 with
+// the 5 rows in one CTA), by the FFMA rate for many.
 #include <atomic>
 
 #include "cluster.cuh"
@@ -316,13 +316,30 @@ cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t s) {
-  // CTAs per unit (splits): more while the CTAs still find an SM each and have chunks for their warps
-  const int rows = p.M >= 5 ? 8 : (p.M >= 3 ? 4 : p.M);
-  const long long units = (long long)p.B * p.Hkv * ((p.M + rows - 1) / rows);
+  // Rows of a CTA and CTAs per unit (splits): few rows are done sooner, many read K and V fewer
+  // times.  As fitted to measurements (us, 4 to 128 KV heads of 1 to 64 rows, windows 17 to 2049; one
+  // CTA per SM): a wave of CTAs takes 3.4 + 0.45 rows and 2.3 + 0.25 rows for every further chunk of
+  // its warps, a cluster 2 more.  20 KV heads of 5 rows of 64, window 129: 4.7 us with a row each
+  // against 7.8 with eight; 32 of 20 rows of 128, window 2049, 98 with eight (two take 128).
   const int span = p.window - 1 < p.cap ? p.window - 1 : p.cap, warps = p.D == 64 ? 8 : 4;
   const int chunks = span / kF32Keys + (p.N + p.sinks) / kF32Keys + 2;
-  p.splits = 1;
-  while (p.splits < 8 && units * p.splits * 2 <= num_sms && p.splits * warps < chunks) p.splits *= 2;
+  int rows = 1;
+  long long units = 0;
+  double best = 0;
+  for (int r = 1; r <= 8 && (r == 1 || r < 2 * p.M); r *= 2)
+    for (int c = 1; c <= 8; c *= 2) {
+      const long long u = (long long)p.B * p.Hkv * ((p.M + r - 1) / r);
+      if (c == 8 && u * c > num_sms * 2 / 3) break;  // 16 clusters of 8 do not find room together
+      const double waves = (double)((u * c + num_sms - 1) / num_sms);
+      const int further = (chunks + c * warps - 1) / (c * warps) - 1;
+      const double cost = waves * (3.4 + 0.45 * r + further * (2.3 + 0.25 * r) + (c > 1 ? 2 : 0));
+      if (units == 0 || cost < best) {
+        best = cost;
+        rows = r;
+        units = u;
+        p.splits = c;
+      }
+    }
   const long long ctas = units * p.splits;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   switch (rows * 1000 + p.D) {
