@@ -2,7 +2,7 @@
 //
 // Node n of sequence b stands at P = L_b + depth(n); its keys are the prefix positions p with
 // P - p < window or p < sinks, and the nodes of its root path by the same rule.  A unit is a
-// sequence and KV head: its M = N * G query rows (tree nodes x group heads) against
+// sequence and KV head: its M = N * G query rows (tree nodes x group heads), in tiles of up to 64, against
 //   the tree's N nodes, the sinks before the window, and [first, L_b),
 // first = L_b - window + 1 being the earliest position that a row's window reaches (rounded
 // down to 16 in a paged cache).  These keys are cut into groups of 16, none of which crosses a
@@ -11,7 +11,7 @@
 // With few rows the work is a stream of K and V: what counts is that loads are always in
 // flight and that units, which a window keeps short, begin and end without gaps.  So nothing
 // in the main loop waits for another warp: each slice of a CTA (one warp; two with more than
-// 32 rows, which then share a slice's rows) takes every KS-th group, has a ring of its own
+// 32 rows in it, which then share a slice's rows) takes every KS-th group, has a ring of its own
 // in shared memory, issues its own TMA copies (16 rows of a head per box, several groups ahead)
 // and keeps its own running maximum, sum and output in registers.  Two CTAs share an SM, so one
 // streams while the other starts or ends.
@@ -35,8 +35,10 @@
 // memory).  Few long units: a cluster of up to 8 CTAs shares a unit's groups, without a workspace or
 // a second launch; each CTA takes part of the unit's outputs, which the others write into its shared
 // memory (reading them from there instead: 6.6 us against 5.5 for one token).
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
+#include <cmath>
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -722,34 +724,73 @@ cudaError_t launch_window_d(const WinParams &p, int nt, int rg, long long ctas, 
   return nt == 3 ? launch_window_typed<D, 3, 1>(p, ctas, s) : launch_window_typed<D, 4, 1>(p, ctas, s);
 }
 
-// 8-column steps of rows per warp, warps per slice and CTAs' worth of rows of a unit: up to four
-// steps per warp, two warps per slice beyond 32 rows; more than 64 rows go 64 at a time.
-struct WinRows {
-  int nt, rg, m_tiles;
+// Rows of a CTA: up to four 8-column steps per warp, or up to four per each of a slice's two warps.
+// Few rows per CTA make short chains and many CTAs, which read the same K and V from L2; many rows
+// read them once.  Fitted to measurements (8 to 128 units of 32 to 512 rows, windows 17 to 4097, root
+// mean square error 5 %): a CTA takes `start` us and `group` us for each of its groups, 1.16 times
+// that with two CTAs per SM.  8 units of 64 rows, window 4097, in tiles of 16 rows 12.1 us against
+// 18.3 in one; 128 units of 208 rows, window 4097, in tiles of 32 rows 177 against 223 in tiles of
+// 64; 512 rows, window 513, 114 against 90.
+struct WinForm {
+  int nt, rg;
+  double start, group;
 };
-WinRows window_rows(int M) {
-  const int steps = (M + 7) / 8, rg = steps > 4 ? 2 : 1;
-  const int nt = rg == 2 ? (steps <= 6 ? 3 : 4) : steps;
-  return {nt, rg, (M + 8 * nt * rg - 1) / (8 * nt * rg)};
+constexpr WinForm kWinForms[] = {{4, 2, 5.9, 0.363}, {3, 2, 4.8, 0.281}, {4, 1, 5.5, 0.179},
+                                 {3, 1, 4.6, 0.145}, {2, 1, 3.7, 0.126}, {1, 1, 2.7, 0.112}};
+struct WinPlan {
+  int nt, rg, m_tiles, cluster;
+  double us;
+};
+
+// M rows against `groups` groups of keys for each of `kv_units` sequences and KV heads.
+WinPlan window_plan(long long kv_units, int M, int groups, int num_sms) {
+  WinPlan plan{};
+  const double sms = num_sms, moved = (double)kv_units * groups * kWinGroup * 512 * 1e-6;  // K and V, MB
+  for (const WinForm &f : kWinForms) {
+    const int rows = 8 * f.nt * f.rg;
+    // no more rows than the unit's, in whole steps (three or four for two warps)
+    if (f.rg == 2 ? M <= (f.nt == 4 ? 48 : 32) : rows >= M + 8) continue;
+    const int tiles = (M + rows - 1) / rows;
+    const long long units = kv_units * tiles, slots = 2ll * num_sms;
+    // CTAs per unit: waves of resident CTAs times the length of one, which costs about 16 groups
+    // (its start and merge) beside its share of the window's groups: 512 units of 32 rows, window
+    // 4097, go without clusters, 156 us against 181 with clusters of four.  (Clusters of 16 gain
+    // little on the longest windows and start later: 8 units of 4 rows, window 1024, 0.6 us more; 16
+    // such clusters find no room together, 25 us against 13.)
+    long long best = 0;
+    int cluster = 1;
+    for (int c = 1; c <= 8; c *= 2) {
+      const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 16);
+      if (c == 1 || cost < best) {
+        best = cost;
+        cluster = c;
+      }
+    }
+    const double load = (double)units * cluster / (2 * sms);
+    const double waves = load <= 0.5 ? 1 : 1.16 * (load <= 3 ? std::ceil(load) : load + 0.5);
+    const double chains = waves * (f.start + f.group * ((groups + cluster - 1) / cluster));
+    const double us = 1.6 + (cluster > 1 ? 1.3 : 0) + std::max(chains, std::max(moved / 5.8, moved * tiles / 18.2));
+    // (more tiles have to be worth it)
+    if (plan.us == 0 || us < 0.97 * plan.us) plan = {f.nt, f.rg, tiles, cluster, us};
+  }
+  return plan;
 }
 
 }  // namespace
 
 // The tensor-core kernel pads a unit's rows to 128 or 256 and pays more for a unit's start and
-// for the launch, but takes long windows of many rows at twice the rate.  Both sides as fitted
-// to measurements (us on 152 SMs, D = 128; 8 to 2048 units, 32 to 512 rows, windows 17 to 4097):
-//   here:  8 + units tiles / SMs (3 + 0.23 groups)       (0.17 per group of up to 48 rows)
-//   there: 13 + units tiles / SMs (6 + 1.45 key tiles) + 2 SMs / units   (2.55 for 256 rows)
-// e.g. 128 units of 104 rows: window 129 14 us against 21, window 1025 37 against 33; 512 units of
-// 64 rows: 24 against 39, 69 against 87; 8 units of 208 rows, window 4097: 25 against 85.
+// for the launch, but takes long windows of many rows at twice the rate.  As fitted to measurements
+// (us; 128 to 2048 units, 40 to 512 rows, windows 17 to 4097):
+//   13 + units tiles / SMs (6 + 1.45 key tiles) + 2 SMs / units      (2.55 for 256 rows)
+// e.g. 128 units of 104 rows: window 129 13 us here against 21, window 1025 36 against 33; 512 units
+// of 64 rows: 24 against 39, 69 against 87; 8 units of 208 rows, window 4097: 20 against 85.
 // Up to 32 rows this kernel runs at the memory's rate: 2048 units, window 1025: 172 against 270.
 bool window_prefers_tc(int B, int N, int Hq, int Hkv, int span, int num_sms) {
   const int M = N * (Hq / Hkv);
-  const WinRows r = window_rows(M);
-  if (r.rg == 1) return false;
+  if (M <= 32) return false;
   const double units = (double)B * Hkv, sms = num_sms;
-  const double groups = span / kWinGroup + 2 + N / kWinGroup, tiles = span / 128 + 2;
-  const double here = 8 + units * r.m_tiles / sms * (3 + (r.nt == 3 ? 0.17 : 0.23) * groups);
+  const double here = window_plan((long long)B * Hkv, M, span / kWinGroup + N / kWinGroup + 2, num_sms).us;
+  const double tiles = span / 128 + 2;
   const double there = 13 + units * ((M + 255) / 256) / sms * (6 + (M > 128 ? 2.55 : 1.45) * tiles) + 2 * sms / units;
   return there < here;
 }
@@ -784,29 +825,14 @@ cudaError_t launch_window_attention(const AttnParams &a, int num_sms, cudaStream
   p.scale_log2 = a.scale_log2;
   p.tree = a.tree;
   p.wait_ns = a.wait_ns;
-  const WinRows rows_plan = window_rows(a.M);
-  const int nt = rows_plan.nt, rg = rows_plan.rg;
-  p.m_tiles = rows_plan.m_tiles;
-  // CTAs per unit: waves of resident CTAs times the length of one, which costs about 16 groups
-  // (its start and merge) beside its share of the window's groups: 512 units of 32 rows, window
-  // 4097, go without clusters, 156 us against 181 with clusters of four.  (Clusters of 16 gain little on
-  // the longest windows and start later: 8 units of 4 rows, window 1024, 0.6 us more; 16 such
-  // clusters find no room together, 25 us against 13.)
-  const long long units = (long long)a.B * a.Hkv * p.m_tiles, slots = 2ll * num_sms;
   const int span = a.window - 1 < a.cap ? a.window - 1 : a.cap;
-  const int groups = span / kWinGroup + (a.N + a.sinks) / kWinGroup + 2;
-  long long best = 0;
-  p.cluster = 1;
-  for (int c = 1; c <= 8; c *= 2) {
-    const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 16);
-    if (c == 1 || cost < best) {
-      best = cost;
-      p.cluster = c;
-    }
-  }
+  const WinPlan plan = window_plan((long long)a.B * a.Hkv, a.M, span / kWinGroup + (a.N + a.sinks) / kWinGroup + 2, num_sms);
+  p.m_tiles = plan.m_tiles;
+  p.cluster = plan.cluster;
+  const long long units = (long long)a.B * a.Hkv * p.m_tiles;
   const long long ctas = units * p.cluster;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  return a.D == 128 ? launch_window_d<128>(p, nt, rg, ctas, s) : launch_window_d<64>(p, nt, rg, ctas, s);
+  return a.D == 128 ? launch_window_d<128>(p, plan.nt, plan.rg, ctas, s) : launch_window_d<64>(p, plan.nt, plan.rg, ctas, s);
 }
 
 }  // namespace sv
