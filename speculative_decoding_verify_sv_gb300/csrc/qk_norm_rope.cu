@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) qk_norm_rope_kerne
                    (size_t)(h0 + (kind == 0 ? 0 : (kind == 1 ? p.Hq : p.Hq + p.Hkv))) * D;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      raw[u] = h0 + u * HPW < heads ? __ldcs(reinterpret_cast<const uint4 *>(src + u * HPW * D)) : make_uint4(0, 0, 0, 0);
+      raw[u] = h0 + u * HPW < heads ? load_streamed(reinterpret_cast<const uint4 *>(src + u * HPW * D)) : make_uint4(0, 0, 0, 0);
   };
 
   // the task at hand (a token, or a part of its batches), its place in the cache, its position

@@ -24,7 +24,18 @@ __device__ __forceinline__ void set_status(unsigned int *status, unsigned int bi
 // be set up while the stream's previous kernel still runs, and nothing is read or written before
 // that kernel has completed.  Back to back an empty kernel costs 1.4 us launched this way and 2.05
 // us the plain way, and kernels of a few us are spared the rounding up to that step.
+// Such a grid may be resident while the previous kernel still writes, so that nothing of it is
+// read-only for the grid's lifetime: what it reads behind the wait it reads with ordinary loads, never
+// with non-coherent ones (__ldg), which may also be moved ahead of the wait.
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// 16 bytes that are read once, from behind wait_previous(): like the wait it is volatile, which keeps
+// the two in order.
+__device__ __forceinline__ uint4 load_streamed(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 inline cudaLaunchAttribute close_launch() {
   cudaLaunchAttribute a;
@@ -51,7 +62,7 @@ cudaError_t launch_close(void (*kernel)(P), dim3 grid, int threads, size_t smem,
 
 // Parent of node c (< N) of sequence b: the shared tree's, or the sequence's own row.
 __device__ __forceinline__ int tree_parent(const Tree &t, int b, int c) {
-  return t.rows ? __ldg(t.rows + (size_t)b * t.stride + c) : (int)t.parent[c];
+  return t.rows ? t.rows[(size_t)b * t.stride + c] : (int)t.parent[c];
 }
 
 // Walk from node c to the root over a parent array par[] (BFS order): the ancestor mask

@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < kTableLoads; ++k) {
       const int b = c + k * kTableThreads + tid;
-      len[k] = b < p.B ? __ldg(p.length + b) : 0;
-      add[k] = b < p.B ? __ldg(p.new_tokens + b) : 0;
+      len[k] = b < p.B ? p.length[b] : 0;
+      add[k] = b < p.B ? p.new_tokens[b] : 0;
     }
 #pragma unroll
     for (int k = 0; k < kTableLoads; ++k) {

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     if (gi < gt) return b * p.N + kWinGroup * gi;
     const int pos = gi < gs ? kWinGroup * (gi - gt) : first + kWinGroup * (gi - gs);
     if (!p.block_table) return b * p.Lmax + pos;
-    const int blk = __ldg(p.block_table + (size_t)b * p.max_blocks + pos / p.block_size);
+    const int blk = p.block_table[(size_t)b * p.max_blocks + pos / p.block_size];
     if (blk < 0 || blk >= p.num_blocks) {
       set_status(p.status, SV_DEV_BAD_BLOCK);
       return -1;

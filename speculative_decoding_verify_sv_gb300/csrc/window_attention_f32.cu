@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
       if (c < ct) {
         row = (long long)b * p.N + key;
       } else if (p.block_table) {
-        const int blk = __ldg(p.block_table + (size_t)b * p.max_blocks + key / p.block_size);
+        const int blk = p.block_table[(size_t)b * p.max_blocks + key / p.block_size];
         if (blk >= 0 && blk < p.num_blocks) row = (long long)blk * p.block_size + key % p.block_size;
         else set_status(p.status, SV_DEV_BAD_BLOCK);
       } else {
