@@ -180,7 +180,13 @@ size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int H
  * its other rows of the same KV head (0 * NaN).
  * Workspace: sv_window_attention_workspace_size() bytes (max_prefix as there; 0 for float32, for up
  * to 32 query rows per KV head, and where few or short windows make the kernel without one
- * the faster). */
+ * the faster).  It serves the faster of two kernels, and which one that is changes back and forth
+ * with the batch, the prefixes and the window: a smaller call may ask for one where a larger one asks
+ * for none.  So a call given less than 256 bytes (or none) is not refused but runs without one, by
+ * the other kernel; a larger workspace than it asks for always serves it.  Calls of several shapes
+ * take the largest of their sizes to run each the faster way.  The two kernels' results differ by
+ * their roundings.  A workspace from 256 bytes up to less than the call's size is
+ * SV_ERR_WORKSPACE. */
 #define SV_MAX_SINKS 64
 sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
                               const void *k_tree, const void *v_tree, sv_kv_cache cache,

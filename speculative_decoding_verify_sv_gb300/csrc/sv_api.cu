@@ -182,6 +182,8 @@ int window_span(int window, int max_prefix) { return window - 1 < max_prefix ? w
 // kernel's calls count in (the workspace's first 256 bytes), so that calls of either kind may
 // share a workspace.
 constexpr size_t kGeneralWsOffset = 256;
+// No workspace that a call asks for is smaller than those first bytes.
+constexpr size_t kLeastWorkspace = kGeneralWsOffset;
 size_t general_ws_bytes(const sv::AttnPlan &pl) { return pl.ws_bytes > 0 ? kGeneralWsOffset + pl.ws_bytes : 0; }
 
 }  // namespace
@@ -282,8 +284,12 @@ static sv_status attention_call(sv_dtype dt, int B, int N, int Hq, int Hkv, int 
         meet(out, q_bytes, cache.k, cache_bytes) || meet(out, q_bytes, cache.v, cache_bytes))
       return fail(SV_ERR_INVALID_ARG, "out overlaps an input");
   }
+  // A windowed call without a workspace takes the kernel that needs none: which kernel is the faster
+  // does not go one way with the batch, so that a caller may have been told 0 bytes for its largest
+  // one and come with a smaller one.
   const bool use_tc = sv::tc_eligible(dt, N, Hq, Hkv, D, paged) &&
-                      (!win || sv::window_prefers_tc(B, N, Hq, Hkv, window_span(window, max_prefix), num_sms()));
+                      (!win || (workspace_bytes >= kLeastWorkspace &&
+                                sv::window_prefers_tc(B, N, Hq, Hkv, window_span(window, max_prefix), num_sms())));
   const sv::TcPlan tplan = use_tc ? sv::tc_plan(B, N, Hq, Hkv, D, num_sms()) : sv::TcPlan{};
   const size_t ws_need = use_tc ? tplan.ws_bytes : (win ? 0 : general_ws_bytes(plan));
   if (ws_need > 0) {
