@@ -20,6 +20,7 @@
 // that holds this token writes the page's table entry.
 // What bounds it: 8 bytes written per token (slot and position); small batches are a chain of
 // three dependent memory round trips (lengths, page ids, stores) and two block barriers.
+#include <algorithm>
 #include <atomic>
 
 #include "sv_common.cuh"
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
       if (report && (L < 0 || L > p.cap || x < 0 || x > p.cap - L)) set_status(p.status, SV_DEV_BAD_PREFIX);
       L = L < 0 ? 0 : min(L, p.cap);
       // (tokens past the table get no slot; more of them than the slot map has room for count
-      // as that many, so that a wild number does not make a long loop)
+      // as that many)
       x = x < 0 ? 0 : (int)min((long long)x, min((long long)p.cap - L + p.T, (long long)INT32_MAX - L));
       s_start[b] = x;
       s_base[b] = max(0, min(pages_of(p, L + x), p.max_blocks) - pages_of(p, L));
@@ -123,10 +124,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   if (tid == 0) s_start[p.B] = (int)min(total, (long long)INT32_MAX);
   __syncthreads();
 
-  // Up to the batch's last token (its pages are given out even where the slot map is too short) and
-  // on to the end of the slot map.  Tokens that a 32-bit place does not reach are not looked at: wild
-  // numbers make no long loop, and places are 32-bit numbers in it.
-  const unsigned tokens = (unsigned)min(total, (long long)INT32_MAX), end = max(tokens, (unsigned)p.T);
+  // The slot map's places, 32-bit numbers; the pages of tokens past its end follow below.
+  const unsigned tokens = (unsigned)min(total, (long long)p.T), end = (unsigned)p.T;
   constexpr int U = RUN == 1 ? 2 : RUN;
   const unsigned step = gridDim.x * kTableThreads * U;
   const int top = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;  // the search's first stride
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
           row[k] = checked(row[k], b[k], pg, off == 0 && pos[k] >= s_len[b[k]]);
           if (row[k] >= 0) slot = row[k] * p.block_size + off;
         }
-        if (t[k] < (unsigned)p.T) {
+        if (t[k] < end) {
           p.slots[t[k]] = slot;
           p.positions[t[k]] = pos[k];
         }
@@ -223,17 +222,37 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
         }
         if (row >= 0) slot[k] = row * p.block_size + off;
       }
-      if (t0 + U <= (unsigned)p.T) {
+      if (t0 + U <= end) {
         *reinterpret_cast<int4 *>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
         *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       } else {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-          if (t0 + k < (unsigned)p.T) {
+          if (t0 + k < end) {
             p.slots[t0 + k] = slot[k];
             p.positions[t0 + k] = pos[k];
           }
       }
+    }
+  }
+  if (total > p.T) {
+    // More tokens than the slot map has room for: the pages whose first token lies past its end are
+    // given out page by page (of a batch of 2^31 fresh pages and more the first 2^31 - 1), so that the
+    // time goes by the table's entries and not by the number of tokens, however wild.
+    unsigned from = 0;
+    if (p.T > 0) {  // behind the pages up to the last token with a place
+      int b = 0;
+      for (int d = top; d > 0; d >>= 1)
+        if (b + d < p.B && s_start[b + d] < p.T) b += d;
+      const int len = s_len[b];
+      from = (unsigned)s_base[b] + (unsigned)max(0, min(pages_of(p, len + (p.T - s_start[b])), p.max_blocks) - pages_of(p, len));
+    }
+    const unsigned last = (unsigned)min(pages, (long long)INT32_MAX);
+    for (unsigned i = from + blockIdx.x * kTableThreads + tid; i < last; i += gridDim.x * kTableThreads) {
+      int b = 0;  // the last request whose fresh pages begin at or before page i
+      for (int d = top; d > 0; d >>= 1)
+        if (b + d < p.B && (unsigned)s_base[b + d] <= i) b += d;
+      checked(i < left ? fresh[i] : -1, b, pages_of(p, s_len[b]) + (int)(i - (unsigned)s_base[b]), true);
     }
   }
   if (bad) set_status(p.status, SV_DEV_BAD_BLOCK);
@@ -278,7 +297,9 @@ cudaError_t launch_block_tables(TableParams p, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[form][dev].store(true);
   }
-  long long ctas = (p.T + f.tokens - 1) / f.tokens;
+  // (and, should there be more new tokens than places, CTAs for the table's entries: at most 64 a thread
+  // as long as two CTAs per SM are enough for that)
+  long long ctas = std::max(((long long)p.T + f.tokens - 1) / f.tokens, (long long)p.B * p.max_blocks / (64 * f.threads));
   ctas = ctas < 1 ? 1 : (ctas > 2ll * num_sms ? 2ll * num_sms : ctas);
   return launch_close(f.kernel, dim3((unsigned)ctas), f.threads, smem, s, p);
 }
