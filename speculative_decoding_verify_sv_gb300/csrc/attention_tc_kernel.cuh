@@ -41,7 +41,8 @@
 // sinks, loaded in boxes of 16 rows.  A separate tile for a handful of sinks would cost a
 // unit of a short window another of its few tiles.  P V of that tile issues only the 16-key
 // steps that hold keys, and V rows in those steps that no row sees are zeroed, as are the
-// rows of the first window tile before the root's window.
+// rows of the first window tile before the root's window.  A page whose id lies outside the pool
+// is loaded as zeros (from past the pool's end) and its columns are hidden from every row.
 #pragma once
 
 #include <atomic>
@@ -566,17 +567,17 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
       if (WIN && src.kind == 0) {
         // tree rows in one box of 64, sinks behind them in boxes of 16 (lane i the i-th)
         const bool mine = lane < src.npg;
-        const bool valid = mine && (!p.paged || (src.blk >= 0 && src.blk < p.num_blocks));
-        if (mine && !valid && !is_v) set_status(p.status, SV_DEV_BAD_BLOCK);
-        const unsigned nvalid = __popc(__ballot_sync(0xFFFFFFFFu, valid));
+        const bool there = !p.paged || (unsigned)src.blk < (unsigned)p.num_blocks;
+        if (mine && !there && !is_v) set_status(p.status, SV_DEV_BAD_BLOCK);
         if (lane == 0) {
-          mbar_expect_tx(full, (64u + 16u * nvalid) * (uint32_t)Lay::KB * 128u);
+          mbar_expect_tx(full, (64u + 16u * src.npg) * (uint32_t)Lay::KB * 128u);
           for (int kb = 0; kb < Lay::KB; ++kb)
             tma_load_3d(dst + kb * Lay::KV_BLOCK, map, kb * 64, src.kvh, src.row, full);
         }
         __syncwarp();
-        if (valid) {
-          const int prow = p.paged ? src.blk * p.block_size + (16 * lane) % p.block_size : src.pos0 + 16 * lane;
+        if (mine) {
+          const int prow = !p.paged ? src.pos0 + 16 * lane
+                                    : (there ? src.blk * p.block_size + (16 * lane) % p.block_size : p.num_blocks * p.block_size);
           for (int kb = 0; kb < Lay::KB; ++kb)
             tma_load_3d(dst + kb * Lay::KV_BLOCK + (64 + 16 * lane) * 128, is_v ? &p.tm_vs : &p.tm_ks, kb * 64,
                         src.kvh, prow, full);
@@ -594,15 +595,16 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
         }
       } else {
         const bool mine = lane < src.npg;
-        const bool valid = mine && src.blk >= 0 && src.blk < p.num_blocks;
-        if (mine && !valid && !is_v) set_status(p.status, SV_DEV_BAD_BLOCK);
-        const unsigned nvalid = __popc(__ballot_sync(0xFFFFFFFFu, valid));
+        const bool there = src.blk >= 0 && src.blk < p.num_blocks;
+        const bool loads = mine && (WIN || there);
+        if (mine && !there && !is_v) set_status(p.status, SV_DEV_BAD_BLOCK);
+        const unsigned pages = __popc(__ballot_sync(0xFFFFFFFFu, loads));
         if (lane == 0)
-          mbar_expect_tx(full, nvalid * (uint32_t)Lay::KB * (uint32_t)p.page_rows * 128u);
+          mbar_expect_tx(full, pages * (uint32_t)Lay::KB * (uint32_t)p.page_rows * 128u);
         __syncwarp();
-        if (valid) {
+        if (loads) {
           const int pos = src.pos0 + lane * p.page_rows;
-          const int prow = src.blk * p.block_size + pos % p.block_size;
+          const int prow = WIN && !there ? p.num_blocks * p.block_size : src.blk * p.block_size + pos % p.block_size;
           if (p.pg_grouped) {
             // both halves of the page in one copy: rows prow .. prow + page_rows (a multiple
             // of 8) land as page_rows / 8 groups of 2 KB
@@ -1062,6 +1064,15 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
         const int gk = g + k, j = gk & 1, s = gk % VST, t = pc.t0 + k, pb = gk % PBUF;
         const bool tree = t == 0;
         const int nvalid = tree ? p.N : min(BN, L - first - (t - 1) * BN);
+        // WIN: lane i looks at the id of the tile's page i (a tree tile's box i of sinks), read while
+        // S is waited for
+        const int page_keys = tree ? 16 : p.page_rows;
+        int page_id = 0;
+        if constexpr (WIN) {
+          if (p.paged && lane * page_keys < (tree ? n_sinks : nvalid))
+            page_id = __ldg(p.block_table + (size_t)pc.b * p.max_blocks +
+                            ((tree ? 0 : first + (t - 1) * BN) + lane * page_keys) / p.block_size);
+        }
         // S of this tile: buffer j, or (P in TMEM) this M tile's region, one phase per tile
         if (!(Lay::PT ? mbar_wait(&s_full[mt], gk & 1, abort_flag, wlim)
                       : mbar_wait(&s_full[j], (gk >> 1) & 1, abort_flag, wlim))) {
@@ -1093,6 +1104,8 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
           }
           return true;
         };
+        // pages outside the pool, a bit each
+        const uint32_t bad_pages = WIN && p.paged ? __ballot_sync(0xFFFFFFFFu, (unsigned)page_id >= (unsigned)p.num_blocks) : 0u;
         // visible columns of this warp's slice: tree tile -> ancestor bits, prefix
         // tile -> columns before the prefix end
         const uint64_t anc_s = (tree && valid_row && col0 < 64) ? (anc >> col0) : 0ull;
@@ -1100,7 +1113,7 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
         // WIN: columns of this warp's slice before the row's window, and those that are sinks
         const int base = WIN ? first + (t - 1) * BN + col0 : 0;
         const int lo_rel = WIN ? lo - base : 0, sk_rel = WIN ? p.sinks - base : 0;
-        const bool full = !tree && valid_row && nv_rel >= CW && (!WIN || lo_rel <= 0);
+        const bool full = !tree && valid_row && nv_rel >= CW && (!WIN || (lo_rel <= 0 && bad_pages == 0));
         const uint32_t ta0 = t_lane + (uint32_t)(((Lay::PT ? 0 : j * MT) + mt) * BN + col0);
 
         // bit c of visible(h) <=> column h*CH + c of this warp's slice is a key the row sees.
@@ -1112,11 +1125,16 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
           const int sh = h * CH;
           if constexpr (WIN) {
             auto below = [&](int x) -> uint32_t { return x <= 0 ? 0u : (x >= CH ? kAll : (1u << x) - 1u); };
-            if (tree) {
-              const int c = col0 + sh;
-              return c < 64 ? (uint32_t)(anc >> c) & kAll : below(n_sinks - (c - 64));
+            const int c = col0 + sh;
+            if (tree && c < 64) return (uint32_t)(anc >> c) & kAll;
+            uint32_t hidden = 0;
+            if (bad_pages) {
+#pragma unroll
+              for (int u = 0; u < CH; u += 16)
+                if ((bad_pages >> ((tree ? c - 64 + u : c + u) / page_keys)) & 1u) hidden |= 0xFFFFu << u;
             }
-            return below(nv_rel - sh) & (~below(lo_rel - sh) | below(sk_rel - sh));
+            if (tree) return below(n_sinks - (c - 64)) & ~hidden;
+            return below(nv_rel - sh) & (~below(lo_rel - sh) | below(sk_rel - sh)) & ~hidden;
           }
           if (tree) return sh < 64 ? (uint32_t)(anc_s >> sh) & kAll : 0u;
           const int r = nv_rel - sh;
