@@ -228,6 +228,23 @@ sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_token
                           int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
                           int32_t *out_free_head, void *stream);
 
+/* The same where requests may hold more pages than their lengths reach: a verify round asks for the
+ * longest path's tokens and commits those of the accepted one, so that pages stay in the row which
+ * its length does not reach.  sv_block_tables does not know of them and puts fresh ids in their
+ * place, which loses the old ones (a caller of it gives such pages back before the next call).  Here
+ * held [B] (int32, device) is the number of pages in each row, 0 for a new request, and
+ *   pages held:   max(ceil(length[b] / block_size), held[b])
+ *   out_held[b]:  pages held + pages added, the next call's held[b] (in an array that does not
+ *                 overlap held)
+ * so that none is taken twice: the ids of a finished request are block_table[b][0 .. held[b]).  A
+ * held[b] outside [0, max_blocks] is clamped and sets SV_DEV_BAD_PREFIX.  After SV_DEV_BAD_BLOCK for
+ * want of free ids, repeat the call with the same length, held and free_head. */
+sv_status sv_block_tables_held(int B, const int32_t *length, const int32_t *new_tokens, int block_size,
+                               int max_blocks, int num_blocks, const int32_t *free_blocks, int num_free,
+                               const int32_t *free_head, const int32_t *held, int32_t *block_table, int T,
+                               int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
+                               int32_t *out_free_head, int32_t *out_held, void *stream);
+
 /* Per-head norms of queries and keys with the position rotation, in one pass.  Row t of qkv
  * (rows ld elements apart, ld >= (Hq + 2 Hkv) * D) is a token's projection: Hq query heads,
  * Hkv key heads, Hkv value heads of D elements.  Each query and key head x becomes

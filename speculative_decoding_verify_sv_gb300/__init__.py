@@ -122,6 +122,7 @@ def load_library():
         lib.sv_window_attention_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
         lib.sv_window_attention_workspace_size.restype = SZ
         lib.sv_block_tables.argtypes = [I, P, P, I, I, I, P, I, P, P, I, P, P, P, P, P]
+        lib.sv_block_tables_held.argtypes = [I, P, P, I, I, I, P, I, P, P, P, I, P, P, P, P, P, P]
         lib.sv_qk_norm_rope.argtypes = [I, I, I, I, I, I, I, P, I64, P, P, F, P, P, P, I64, P, P, P, P]
         lib.sv_tree_qk_norm_rope.argtypes = [I, I, I, I, I, I, I, I, P, I64, P, P, F, P, P, P, I, P, P, P, P]
         lib.sv_last_error.restype = ctypes.c_char_p
@@ -130,7 +131,7 @@ def load_library():
         for fn in ("sv_tree_attention", "sv_accept_chain", "sv_accept_tree", "sv_commit_kv",
                    "sv_tree_prepare", "sv_read_device_status", "sv_accept_tree_noalloc",
                    "sv_accept_tree_commit", "sv_accept_chain_commit", "sv_ngram_draft",
-                   "sv_accept_tree_recursive", "sv_window_attention", "sv_block_tables",
+                   "sv_accept_tree_recursive", "sv_window_attention", "sv_block_tables", "sv_block_tables_held",
                    "sv_qk_norm_rope", "sv_tree_qk_norm_rope"):
             getattr(lib, fn).restype = ctypes.c_int32
         _lib = lib
@@ -328,15 +329,19 @@ def sv_window_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, window
 # ------------------------------------------------------------- into the KV cache
 
 def sv_block_tables(length, new_tokens, block_table, free_blocks, block_size, num_blocks, num_slots,
-                    free_head=None, outs=None, stream=None) -> dict:
+                    free_head=None, outs=None, stream=None, held=None) -> dict:
     """Extend a paged cache's block tables for ``new_tokens`` [B] more tokens per request
     (``length`` [B] are in it) with pages of ``free_blocks`` from ``free_head`` [1] on, and make
     the new tokens' slot map.  block_table [B,max_blocks] is written in place.  Returns a dict of
     int32 device tensors: token_start [B+1], slots and positions [num_slots] (-1 past the
     total), free_head [1] (the advanced head, never the one passed in).  ``outs`` may hold those
-    tensors to write into; the ones it lacks are made and put into it."""
+    tensors to write into; the ones it lacks are made and put into it.
+
+    ``held`` [B]: the pages in each row of block_table, which may be more than ``length`` reaches
+    (rounds that asked for more tokens than they kept); the dict then has "held" [B] too, the next
+    call's.  Without it a row holds the pages of its length, and others are lost unless given back."""
     return load_binding().block_tables(length, new_tokens, block_table, free_blocks, block_size, num_blocks, num_slots,
-                                       free_head, outs, stream)
+                                       free_head, outs, stream, held)
 
 
 def sv_qk_norm_rope(qkv, Hq, Hkv, q_weight, k_weight, inv_freq, positions, eps=1e-6, interleaved=False,

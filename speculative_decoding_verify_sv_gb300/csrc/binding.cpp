@@ -278,10 +278,10 @@ void empty_tables(PyObject *outs, const char *const *names, PyObject *head) {
 }
 
 // (length, new_tokens, block_table, free_blocks, block_size, num_blocks, num_slots, free_head, outs,
-//  stream) -> outs, a dict, filled up with the outputs it lacks
+//  stream, held) -> outs, a dict, filled up with the outputs it lacks
 PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    expect(n, 10);
+    expect(n, 11);
     const at::Tensor &len0 = cuda_tensor(a[0], "length");
     const int dev = len0.get_device();
     if (len0.dim() != 1) refuse(PyExc_ValueError, "length must be [B]");
@@ -297,11 +297,14 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
       refuse(PyExc_ValueError, "a size is not a 32-bit number");
     const int block_size = number(a[4], "block_size"), num_blocks = number(a[5], "num_blocks");
     const int32_t *head = given(a[7]) ? tensor(a[7], "free_head", at::kInt, {1}, dev).const_data_ptr<int32_t>() : nullptr;
+    const int32_t *held = given(a[10]) ? tensor(a[10], "held", at::kInt, {B}, dev).const_data_ptr<int32_t>() : nullptr;
     const Stream stream(a[9], dev);
-    static const char *const names[4] = {"token_start", "slots", "positions", "free_head"};
-    static PyObject *const keys[4] = {PyUnicode_InternFromString(names[0]), PyUnicode_InternFromString(names[1]),
-                                      PyUnicode_InternFromString(names[2]), PyUnicode_InternFromString(names[3])};
-    const int64_t sizes[4] = {B + 1, T, T, 1};
+    static const char *const names[5] = {"token_start", "slots", "positions", "free_head", "held"};
+    static PyObject *const keys[5] = {PyUnicode_InternFromString(names[0]), PyUnicode_InternFromString(names[1]),
+                                      PyUnicode_InternFromString(names[2]), PyUnicode_InternFromString(names[3]),
+                                      PyUnicode_InternFromString(names[4])};
+    const int64_t sizes[5] = {B + 1, T, T, 1, B};
+    const int made = given(a[10]) ? 5 : 4;  // outputs
     PyObject *outs = given(a[8]) ? a[8] : PyDict_New();
     if (!outs) throw Refused();
     if (given(a[8])) {
@@ -310,16 +313,16 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     try {
       // new outputs are parts of one buffer, the slots and positions on 16-byte boundaries
-      const int64_t padded = (T + 3) / 4 * 4, offsets[4] = {2 * padded, 0, padded, 2 * padded + B + 1};
+      const int64_t padded = (T + 3) / 4 * 4, offsets[5] = {2 * padded, 0, padded, 2 * padded + B + 1, 2 * padded + B + 2};
       at::Tensor buffer;
-      int32_t *ptr[4];
-      for (int i = 0; i < 4; ++i) {
+      int32_t *ptr[5];
+      for (int i = 0; i < made; ++i) {
         PyObject *o = given(a[8]) ? PyDict_GetItemWithError(outs, keys[i]) : nullptr;
         if (!o && PyErr_Occurred()) throw Refused();
         if (o) {
           ptr[i] = tensor(o, names[i], at::kInt, {sizes[i]}, dev).data_ptr<int32_t>();
         } else {
-          if (!buffer.defined()) buffer = make({2 * padded + B + 2}, len, at::kInt);
+          if (!buffer.defined()) buffer = make({2 * padded + B + 2 + (made == 5 ? B : 0)}, len, at::kInt);
           ptr[i] = buffer.data_ptr<int32_t>() + offsets[i];
           PyObject *w = THPVariable_Wrap(part(buffer, offsets[i], {sizes[i]}));
           if (!w || PyDict_SetItem(outs, keys[i], w) != 0) {
@@ -330,9 +333,14 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
       }
       if (B == 0) empty_tables(outs, names, a[7]);
-      check(sv_block_tables((int)B, len.const_data_ptr<int32_t>(), add.const_data_ptr<int32_t>(), block_size,
-                            (int)bt.size(1), num_blocks, free.const_data_ptr<int32_t>(), (int)free.numel(), head,
-                            bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], stream));
+      const int32_t *lengths = len.const_data_ptr<int32_t>(), *added = add.const_data_ptr<int32_t>(), *ids = free.const_data_ptr<int32_t>();
+      const int columns = (int)bt.size(1), num_free = (int)free.numel();
+      if (made == 5)
+        check(sv_block_tables_held((int)B, lengths, added, block_size, columns, num_blocks, ids, num_free, head, held,
+                                   bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], ptr[4], stream));
+      else
+        check(sv_block_tables((int)B, lengths, added, block_size, columns, num_blocks, ids, num_free, head,
+                              bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], stream));
     } catch (...) {
       Py_DECREF(outs);
       throw;

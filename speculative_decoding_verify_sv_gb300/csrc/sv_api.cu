@@ -769,12 +769,11 @@ sv_status sv_ngram_draft(int B, int Lmax, const int32_t *history, const int32_t 
 
 // --------------------------------------------------------------- block tables
 
-sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_tokens, int block_size,
-                          int max_blocks, int num_blocks, const int32_t *free_blocks, int num_free,
-                          const int32_t *free_head, int32_t *block_table, int T,
-                          int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
-                          int32_t *out_free_head, void *stream) {
-  const CallRange range("sv_block_tables");
+static sv_status tables_call(int B, const int32_t *length, const int32_t *new_tokens, int block_size,
+                             int max_blocks, int num_blocks, const int32_t *free_blocks, int num_free,
+                             const int32_t *free_head, const int32_t *held, int32_t *block_table, int T,
+                             int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
+                             int32_t *out_free_head, int32_t *out_held, void *stream) {
   if (B < 0 || T < 0 || num_free < 0)
     return fail(SV_ERR_INVALID_ARG, "B = %d, T = %d, num_free = %d", B, T, num_free);
   if (B > SV_MAX_TABLE_BATCH)
@@ -791,8 +790,8 @@ sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_token
   if (free_head && free_head == out_free_head)
     return fail(SV_ERR_INVALID_ARG, "out_free_head must not be free_head (every part of the call reads it)");
   if (B == 0) return SV_OK;  // an empty batch: nothing to launch, no device needed
-  sv::TableParams p{length, new_tokens, free_blocks, free_head, block_table, out_token_start, out_slots,
-                    out_positions, out_free_head, status_word(), B, T, block_size, max_blocks, num_blocks, num_free};
+  sv::TableParams p{length, new_tokens, free_blocks, free_head, held, block_table, out_token_start, out_slots,
+                    out_positions, out_free_head, out_held, status_word(), B, T, block_size, max_blocks, num_blocks, num_free};
   if (!p.status) return fail(SV_ERR_CUDA, "no CUDA device");
   const cudaError_t e = take_injected_failure()
                             ? cudaErrorLaunchFailure
@@ -800,6 +799,29 @@ sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_token
   if (e != cudaSuccess) return cuda_fail(e, "block table launch");
   sv::count_launches(1);
   return SV_OK;
+}
+
+sv_status sv_block_tables(int B, const int32_t *length, const int32_t *new_tokens, int block_size,
+                          int max_blocks, int num_blocks, const int32_t *free_blocks, int num_free,
+                          const int32_t *free_head, int32_t *block_table, int T,
+                          int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
+                          int32_t *out_free_head, void *stream) {
+  const CallRange range("sv_block_tables");
+  return tables_call(B, length, new_tokens, block_size, max_blocks, num_blocks, free_blocks, num_free, free_head, nullptr,
+                     block_table, T, out_token_start, out_slots, out_positions, out_free_head, nullptr, stream);
+}
+
+sv_status sv_block_tables_held(int B, const int32_t *length, const int32_t *new_tokens, int block_size,
+                               int max_blocks, int num_blocks, const int32_t *free_blocks, int num_free,
+                               const int32_t *free_head, const int32_t *held, int32_t *block_table, int T,
+                               int32_t *out_token_start, int32_t *out_slots, int32_t *out_positions,
+                               int32_t *out_free_head, int32_t *out_held, void *stream) {
+  const CallRange range("sv_block_tables_held");
+  if (B > 0 && (!held || !out_held)) return fail(SV_ERR_INVALID_ARG, "held or out_held is NULL");
+  if (held && meet(held, 4ll * B, out_held, 4ll * B))
+    return fail(SV_ERR_INVALID_ARG, "out_held overlaps held (every part of the call reads it)");
+  return tables_call(B, length, new_tokens, block_size, max_blocks, num_blocks, free_blocks, num_free, free_head, held,
+                     block_table, T, out_token_start, out_slots, out_positions, out_free_head, out_held, stream);
 }
 
 // --------------------------------------------------- Q/K norms and the rotation

@@ -214,10 +214,12 @@ struct TableParams {
   const int32_t *length, *new_tokens;  // [B]
   const int32_t *free_blocks;          // [num_free]
   const int32_t *free_head;            // [1] or NULL (0)
+  const int32_t *held;                 // [B] pages in each row, or NULL: those of the length
   int32_t *block_table;                // [B,max_blocks]
   int32_t *token_start;                // [B+1]
   int32_t *slots, *positions;          // [T]
   int32_t *out_free_head;              // [1]
+  int32_t *out_held;                   // [B] (with held)
   unsigned int *status;
   int B, T, block_size, max_blocks, num_blocks, num_free;
   int cap;                             // positions of a table row (set at the launch, as are the

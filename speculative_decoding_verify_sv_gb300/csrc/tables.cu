@@ -5,7 +5,9 @@
 //   need_b = ceil((length_b + new_b) / bs) - ceil(length_b / bs)
 // fresh pages, taken from the free list in request order (an exclusive sum over need), and its
 // new token i lands in cache row table[b][p / bs] * bs + p % bs, p = length_b + i, at place
-// start_b + i of the flat slot map (an exclusive sum over new).
+// start_b + i of the flat slot map (an exclusive sum over new).  A round that asked for more tokens
+// than it kept leaves pages behind that its length does not reach; where the caller says how many
+// pages a row holds, that number stands in the place of ceil(length_b / bs) if it is the larger.
 //
 // One launch, no workspace: every CTA makes both sums over the whole batch itself (8 bytes per
 // request from L2, one block-wide scan) and then fills its share of the slot map, so nothing is
@@ -46,6 +48,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   int *s_start = table_smem;             // [B + 1] first token of each request, at most INT32_MAX
   int *s_base = table_smem + p.B + 1;    // [B] fresh pages before each request
   int *s_len = table_smem + 2 * p.B + 1; // [B] tokens that it has
+  int *s_have = table_smem + 3 * p.B + 1; // [B] pages that it has (given held; else those of its tokens)
   __shared__ long long s_tok[kTableThreads / 32], s_page[kTableThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool report = blockIdx.x == 0;
@@ -53,12 +56,13 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   const long long head = p.free_head ? *p.free_head : 0;
 
   for (int c = 0; c < p.B; c += kTableThreads * kTableLoads) {
-    int len[kTableLoads], add[kTableLoads];
+    int len[kTableLoads], add[kTableLoads], held[kTableLoads];
 #pragma unroll
     for (int k = 0; k < kTableLoads; ++k) {
       const int b = c + k * kTableThreads + tid;
       len[k] = b < p.B ? p.length[b] : 0;
       add[k] = b < p.B ? p.new_tokens[b] : 0;
+      held[k] = p.held && b < p.B ? p.held[b] : 0;
     }
 #pragma unroll
     for (int k = 0; k < kTableLoads; ++k) {
@@ -70,9 +74,15 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
       // (tokens past the table get no slot; more of them than the slot map has room for count
       // as that many)
       x = x < 0 ? 0 : (int)min((long long)x, min((long long)p.cap - L + p.T, (long long)INT32_MAX - L));
+      int have = pages_of(p, L);
+      if (p.held) {
+        if (report && (held[k] < 0 || held[k] > p.max_blocks)) set_status(p.status, SV_DEV_BAD_PREFIX);
+        s_have[b] = have = max(have, min(held[k], p.max_blocks));
+      }
       s_start[b] = x;
-      s_base[b] = max(0, min(pages_of(p, L + x), p.max_blocks) - pages_of(p, L));
+      s_base[b] = max(0, min(pages_of(p, L + x), p.max_blocks) - have);
       s_len[b] = L;
+      if (report && p.held) p.out_held[b] = have + s_base[b];
     }
   }
   __syncthreads();
@@ -129,6 +139,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   constexpr int U = RUN == 1 ? 2 : RUN;
   const unsigned step = gridDim.x * kTableThreads * U;
   const int top = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;  // the search's first stride
+  auto pages_had = [&](int b) { return p.held ? s_have[b] : pages_of(p, s_len[b]); };
   // where the id of page pg of request b is: held (in the table) or fresh (NULL: none is left)
   const unsigned left = head >= 0 && head < p.num_free ? (unsigned)(p.num_free - head) : 0u;
   const int32_t *fresh = p.free_blocks + (left ? head : 0);
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
         src[k] = nullptr;
         if (t[k] >= tokens) continue;
         pos[k] = s_len[b[k]] + ((int)t[k] - s_start[b[k]]);
-        src[k] = page_source(b[k], page_of(p, pos[k]), pages_of(p, s_len[b[k]]));
+        src[k] = page_source(b[k], page_of(p, pos[k]), pages_had(b[k]));
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) row[k] = src[k] ? *src[k] : -1;
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
         int slot = -1;
         if (pos[k] >= 0) {
           const int pg = page_of(p, pos[k]), off = pos[k] - pg * p.block_size;
-          row[k] = checked(row[k], b[k], pg, off == 0 && pos[k] >= s_len[b[k]]);
+          row[k] = checked(row[k], b[k], pg, off == 0 && pg >= pages_had(b[k]));
           if (row[k] >= 0) slot = row[k] * p.block_size + off;
         }
         if (t[k] < end) {
@@ -202,7 +213,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
             if (b + d < p.B && (unsigned)s_start[b + d] <= t) b += d;
           stop = (unsigned)s_start[b + 1];
           const int len = s_len[b];
-          have = pages_of(p, len);
+          have = pages_had(b);
           pos[k] = len + ((int)t - s_start[b]);
           pg = page_of(p, pos[k]);
           off = pos[k] - pg * p.block_size;
@@ -245,14 +256,14 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
       for (int d = top; d > 0; d >>= 1)
         if (b + d < p.B && s_start[b + d] < p.T) b += d;
       const int len = s_len[b];
-      from = (unsigned)s_base[b] + (unsigned)max(0, min(pages_of(p, len + (p.T - s_start[b])), p.max_blocks) - pages_of(p, len));
+      from = (unsigned)s_base[b] + (unsigned)max(0, min(pages_of(p, len + (p.T - s_start[b])), p.max_blocks) - pages_had(b));
     }
     const unsigned last = (unsigned)min(pages, (long long)INT32_MAX);
     for (unsigned i = from + blockIdx.x * kTableThreads + tid; i < last; i += gridDim.x * kTableThreads) {
       int b = 0;  // the last request whose fresh pages begin at or before page i
       for (int d = top; d > 0; d >>= 1)
         if (b + d < p.B && (unsigned)s_base[b + d] <= i) b += d;
-      checked(i < left ? fresh[i] : -1, b, pages_of(p, s_len[b]) + (int)(i - (unsigned)s_base[b]), true);
+      checked(i < left ? fresh[i] : -1, b, pages_had(b) + (int)(i - (unsigned)s_base[b]), true);
     }
   }
   if (bad) set_status(p.status, SV_DEV_BAD_BLOCK);
@@ -287,13 +298,13 @@ cudaError_t launch_block_tables(TableParams p, int num_sms, cudaStream_t s) {
                                 {block_tables_kernel<1, 1024>, 1024, 2048}};
   const int form = p.T / p.B >= 256 ? 0 : (p.B <= 2048 ? 1 : 2);
   const Form &f = forms[form];
-  const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int);
+  const size_t smem = (size_t)((p.held ? 4 : 3) * p.B + 1) * sizeof(int);
   static std::atomic<bool> attr_set[3][64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[form][dev].load()) {
     const cudaError_t e = cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)((3 * SV_MAX_TABLE_BATCH + 1) * sizeof(int)));
+                                               (int)((4 * SV_MAX_TABLE_BATCH + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[form][dev].store(true);
   }
