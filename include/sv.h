@@ -213,8 +213,8 @@ size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
  * are); all int32 in device memory.  Outputs: out_token_start [B+1] (exclusive sums of
  * new_tokens, the last one the total), out_slots and out_positions [T] (entries past the
  * total are -1; 16-byte aligned; NULL when T = 0), out_free_head [1] = free_head + pages
- * added (may pass num_free: the shortage is the difference).  out_free_head must not be
- * free_head itself.  B = 0 writes none of them (the Python call fills them: no tokens, the head
+ * added (may pass num_free: the shortage is the difference).  Outputs and block_table must overlap
+ * neither one another nor an input (SV_ERR_INVALID_ARG; out_free_head is not free_head).  B = 0 writes none of them (the Python call fills them: no tokens, the head
  * as it was).  length is not advanced: calling again with the same inputs gives the
  * same tables.  B <= SV_MAX_TABLE_BATCH, num_blocks * block_size < 2^31.
  * Device status: SV_DEV_BAD_BLOCK when free ids run out or an id (held or free) lies outside

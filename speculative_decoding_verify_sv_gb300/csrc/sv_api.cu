@@ -790,6 +790,22 @@ static sv_status tables_call(int B, const int32_t *length, const int32_t *new_to
   if (free_head && free_head == out_free_head)
     return fail(SV_ERR_INVALID_ARG, "out_free_head must not be free_head (every part of the call reads it)");
   if (B == 0) return SV_OK;  // an empty batch: nothing to launch, no device needed
+  // every part of the call reads all the inputs and nothing says which part writes first
+  struct Range {
+    const void *at;
+    long long bytes;
+  };
+  const Range written[] = {{out_token_start, 4ll * (B + 1)}, {out_slots, 4ll * T}, {out_positions, 4ll * T}, {out_free_head, 4},
+                           {out_held, out_held ? 4ll * B : 0}, {block_table, 4ll * B * max_blocks}};
+  const Range read[] = {{length, 4ll * B}, {new_tokens, 4ll * B}, {free_blocks, 4ll * num_free},
+                        {free_head, free_head ? 4 : 0}, {held, held ? 4ll * B : 0}};
+  for (const Range &w : written) {
+    for (const Range &r : read)
+      if (meet(w.at, w.bytes, r.at, r.bytes)) return fail(SV_ERR_INVALID_ARG, "an output or block_table overlaps an input");
+    for (const Range &o : written)
+      if (&o < &w && meet(w.at, w.bytes, o.at, o.bytes))
+        return fail(SV_ERR_INVALID_ARG, "outputs and block_table overlap one another");
+  }
   sv::TableParams p{length, new_tokens, free_blocks, free_head, held, block_table, out_token_start, out_slots,
                     out_positions, out_free_head, out_held, status_word(), B, T, block_size, max_blocks, num_blocks, num_free};
   if (!p.status) return fail(SV_ERR_CUDA, "no CUDA device");

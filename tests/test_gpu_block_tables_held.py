@@ -148,3 +148,34 @@ def test_refusals_before_launch():
     assert call(held=None) == bad and call(out=None) == bad and call(out=at(7)) == bad and call(bs=0) == bad
     assert call(out=ctypes.c_void_p((7 << 20) + 4)) == bad and b"out_held" in lib.sv_last_error()
     assert call(B=0, held=None, out=None) == sv.SV_OK
+
+
+def test_overlaps_are_refused():
+    """The table and every output against one another and against every input (host addresses only)."""
+    from speculative_decoding_verify_sv_gb300 import build as svbuild
+    svbuild.build()
+    lib, bad = sv.load_library(), sv.SV_ERR_INVALID_ARG
+    B, mb, T, num_free = 5, 6, 8, 9
+    names = ["length", "new", "free", "head", "held", "table", "start", "slots", "positions", "out_head", "out_held"]
+    words = dict(length=B, new=B, free=num_free, head=1, held=B, table=B * mb, start=B + 1, slots=T, positions=T, out_head=1, out_held=B)
+
+    def call(with_held, **over):
+        at = {n: (i + 1) << 20 for i, n in enumerate(names)}
+        at.update(over)
+        p = {n: ctypes.c_void_p(x) for n, x in at.items()}
+        if with_held:
+            return lib.sv_block_tables_held(B, p["length"], p["new"], 16, mb, 64, p["free"], num_free, p["head"], p["held"], p["table"],
+                                            T, p["start"], p["slots"], p["positions"], p["out_head"], p["out_held"], None)
+        return lib.sv_block_tables(B, p["length"], p["new"], 16, mb, 64, p["free"], num_free, p["head"], p["table"], T, p["start"],
+                                   p["slots"], p["positions"], p["out_head"], None)
+    for with_held in (False, True):
+        for w in names[5:]:
+            for o in names:
+                if o == w or (not with_held and "held" in w + o):
+                    continue
+                base = (names.index(o) + 1) << 20
+                # the first and the last word that they share (slots and positions stay 16-byte aligned)
+                step = 16 if w in ("slots", "positions") else 4
+                for at in (base, base + 4 * (words[o] - 1) // step * step):
+                    assert call(with_held, **{w: at}) == bad, (w, o)
+                    assert b"overlap" in lib.sv_last_error() or {w, o} == {"out_head", "head"}
