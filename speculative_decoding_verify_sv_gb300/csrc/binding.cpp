@@ -332,7 +332,6 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
           Py_DECREF(w);
         }
       }
-      if (B == 0) empty_tables(outs, names, a[7]);
       const int32_t *lengths = len.const_data_ptr<int32_t>(), *added = add.const_data_ptr<int32_t>(), *ids = free.const_data_ptr<int32_t>();
       const int columns = (int)bt.size(1), num_free = (int)free.numel();
       if (made == 5)
@@ -341,6 +340,7 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
       else
         check(sv_block_tables((int)B, lengths, added, block_size, columns, num_blocks, ids, num_free, head,
                               bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], stream));
+      if (B == 0) empty_tables(outs, names, a[7]);  // (the arguments are checked)
     } catch (...) {
       Py_DECREF(outs);
       throw;

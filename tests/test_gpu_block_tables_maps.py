@@ -117,3 +117,15 @@ def test_pages_of_tokens_past_32_bits(cuda_ok):
         assert np.array_equal(t.cpu().numpy().reshape(-1), free)
         assert r["free_head"].tolist() == [3 * columns] and r["slots"].tolist() == list(range(T))
         assert begin.elapsed_time(end) < 20
+
+
+def test_a_refused_empty_batch_writes_nothing(cuda_ok):
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    outs = {k: torch.full((n,), 7, dtype=torch.int32, device="cuda")
+            for k, n in (("token_start", 1), ("slots", 4), ("positions", 4), ("free_head", 1))}
+    for kw in (dict(block_size=0), dict(num_blocks=0), dict(num_blocks=2 ** 30)):
+        with pytest.raises(sv.SVError):
+            sv.sv_block_tables(none, none, none.view(0, 3), _dev([1]), **{**dict(block_size=4, num_blocks=8), **kw}, num_slots=4, outs=outs)
+        assert all((t == 7).all() for t in outs.values())
+    sv.sv_block_tables(none, none, none.view(0, 3), _dev([1]), 4, 8, 4, outs=outs)
+    assert [outs[k].tolist() for k in ("token_start", "slots", "positions", "free_head")] == [[0], [-1] * 4, [-1] * 4, [0]]
