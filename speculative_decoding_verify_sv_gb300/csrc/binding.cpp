@@ -33,7 +33,20 @@ struct Refused {};  // the Python error is set
   throw Refused();
 }
 
-void check(sv_status st) {
+// Runs a call of libsv.so and turns its status into an error.  The interpreter's lock is given up
+// meanwhile: a launch waits while the device's queue of launches is full, and what would empty it may
+// need another thread of this process (a host function of a stream, the feeder of a copy).
+// (The call touches no Python object.)
+template <typename Call>
+void check(Call &&call) {
+  struct Unlocked {
+    PyThreadState *const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  };
+  const sv_status st = [&] {
+    const Unlocked unlocked;
+    return call();
+  }();
   if (st == SV_OK) return;
   PyObject *e = PyObject_CallFunction(g_error, "is", (int)st, sv_last_error());
   if (e) {
@@ -259,9 +272,11 @@ PyObject *window_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                                              (int)std::min<long long>(cap, INT32_MAX), window);
       if (need) ws = at::zeros({(int64_t)need}, q.options().dtype(at::kByte));
     }
-    check(sv_window_attention(dt, (int)B, (int)N, (int)Hq, (int)Hkv, (int)D, q.data_ptr(), kt.data_ptr(), vt.data_ptr(), c,
-                              tree.ptr, tree.stride, scale, window, sinks, out.data_ptr(),
-                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream));
+    check([&] {
+      return sv_window_attention(dt, (int)B, (int)N, (int)Hq, (int)Hkv, (int)D, q.data_ptr(), kt.data_ptr(), vt.data_ptr(), c,
+                                 tree.ptr, tree.stride, scale, window, sinks, out.data_ptr(),
+                                 ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream);
+    });
     return THPVariable_Wrap(std::move(out));
   });
 }
@@ -335,11 +350,15 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
       const int32_t *lengths = len.const_data_ptr<int32_t>(), *added = add.const_data_ptr<int32_t>(), *ids = free.const_data_ptr<int32_t>();
       const int columns = (int)bt.size(1), num_free = (int)free.numel();
       if (made == 5)
-        check(sv_block_tables_held((int)B, lengths, added, block_size, columns, num_blocks, ids, num_free, head, held,
-                                   bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], ptr[4], stream));
+        check([&] {
+          return sv_block_tables_held((int)B, lengths, added, block_size, columns, num_blocks, ids, num_free, head, held,
+                                      bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], ptr[4], stream);
+        });
       else
-        check(sv_block_tables((int)B, lengths, added, block_size, columns, num_blocks, ids, num_free, head,
-                              bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], stream));
+        check([&] {
+          return sv_block_tables((int)B, lengths, added, block_size, columns, num_blocks, ids, num_free, head,
+                                 bt.data_ptr<int32_t>(), (int)T, ptr[0], ptr[1], ptr[2], ptr[3], stream);
+        });
       if (B == 0) empty_tables(outs, names, a[7]);  // (the arguments are checked)
     } catch (...) {
       Py_DECREF(outs);
@@ -403,6 +422,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const int interleaved = PyObject_IsTrue(a[8]);
     if (interleaved < 0) throw Refused();
+    const float eps = real(a[7]);
     const Stream stream(a[13], p.dev);
     at::Tensor q = given(a[10]) ? tensor(a[10], "q_out", type, {T, p.Hq, p.D}, p.dev) : make({T, p.Hq, p.D}, p.qkv, type);
     at::Tensor k = given(a[11]) ? tensor(a[11], "k_out", type, p.dev) : make({T, p.Hkv, p.D}, p.qkv, type);
@@ -413,10 +433,12 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       throw Refused();
     }
     at::Tensor v = given(a[12]) ? tensor(a[12], "v_out", type, k.sizes(), p.dev) : make(k.sizes(), p.qkv, type);
-    check(sv_qk_norm_rope(p.dt, (int)T, (int)p.Hq, (int)p.Hkv, (int)p.D, 2 * (int)p.freq.numel(), interleaved,
-                          p.qkv.data_ptr(), p.ld, p.qw.const_data_ptr<float>(), p.kw.const_data_ptr<float>(), real(a[7]),
-                          p.freq.const_data_ptr<double>(), at_pos.const_data_ptr<int32_t>(), slots,
-                          k.numel() / (p.Hkv * p.D), q.data_ptr(), k.data_ptr(), v.data_ptr(), stream));
+    check([&] {
+      return sv_qk_norm_rope(p.dt, (int)T, (int)p.Hq, (int)p.Hkv, (int)p.D, 2 * (int)p.freq.numel(), interleaved,
+                             p.qkv.data_ptr(), p.ld, p.qw.const_data_ptr<float>(), p.kw.const_data_ptr<float>(), eps,
+                             p.freq.const_data_ptr<double>(), at_pos.const_data_ptr<int32_t>(), slots,
+                             k.numel() / (p.Hkv * p.D), q.data_ptr(), k.data_ptr(), v.data_ptr(), stream);
+    });
     return Py_BuildValue("NNN", THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(k)),
                          THPVariable_Wrap(std::move(v)));
   });
@@ -434,6 +456,7 @@ PyObject *tree_qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tree tree(a[7], B, N, p.dev);
     const int interleaved = PyObject_IsTrue(a[9]);
     if (interleaved < 0) throw Refused();
+    const float eps = real(a[8]);
     const Stream stream(a[11], p.dev);
     at::Tensor q, k, v;
     if (given(a[10])) {
@@ -454,10 +477,12 @@ PyObject *tree_qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
       k = part(buffer, head * p.Hq, {B, N, p.Hkv, p.D});
       v = part(buffer, head * (p.Hq + p.Hkv), {B, N, p.Hkv, p.D});
     }
-    check(sv_tree_qk_norm_rope(p.dt, (int)B, (int)N, (int)p.Hq, (int)p.Hkv, (int)p.D, 2 * (int)p.freq.numel(), interleaved,
-                               p.qkv.data_ptr(), p.ld, p.qw.const_data_ptr<float>(), p.kw.const_data_ptr<float>(),
-                               real(a[8]), p.freq.const_data_ptr<double>(), len.const_data_ptr<int32_t>(), tree.ptr,
-                               tree.stride, q.data_ptr(), k.data_ptr(), v.data_ptr(), stream));
+    check([&] {
+      return sv_tree_qk_norm_rope(p.dt, (int)B, (int)N, (int)p.Hq, (int)p.Hkv, (int)p.D, 2 * (int)p.freq.numel(), interleaved,
+                                  p.qkv.data_ptr(), p.ld, p.qw.const_data_ptr<float>(), p.kw.const_data_ptr<float>(), eps,
+                                  p.freq.const_data_ptr<double>(), len.const_data_ptr<int32_t>(), tree.ptr, tree.stride,
+                                  q.data_ptr(), k.data_ptr(), v.data_ptr(), stream);
+    });
     return Py_BuildValue("NNN", THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(k)),
                          THPVariable_Wrap(std::move(v)));
   });
