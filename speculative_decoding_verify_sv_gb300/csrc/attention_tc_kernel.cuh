@@ -1376,6 +1376,7 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
             if (!fn(j++, pc.unit + c2)) break;
           }
         };
+        bool gave_up = false;
         if (head && valid_row) {
           // wait for the later pieces, then weigh every piece by 2^(m_piece - M)
           float M = m_ref;
@@ -1404,7 +1405,7 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
             np = j + 1;
             return true;
           });
-          if (*abort_flag) break;
+          gave_up = *abort_flag != 0;
           w_own = m_ref == -INFINITY ? 0.f : exp2f(m_ref - M);
           float L = l * w_own;
 #pragma unroll
@@ -1426,6 +1427,9 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
           inv = L > 0.f ? 1.f / L : 0.f;
           m_ref = M;  // the weights below are 2^(m_piece - M)
         }
+        // (the whole warp leaves: lanes of real rows alone would wait for the CTA and those of
+        // padding rows for them)
+        if (__any_sync(0xFFFFFFFFu, gave_up)) break;
         // The first producer's partial rows were staged in shared memory by the producer
         // warp (one M tile only); 16-byte unit i of row r at r * (D / 4) + (i ^ (r % (D / 4))).
         float4 *stage = nullptr;
