@@ -83,13 +83,38 @@ struct WinLayout {
   static constexpr int OFF_LO = OFF_INV + RB * 4;       // [RB]
   static constexpr int OFF_ROW = OFF_LO + RB * 4;       // [RB]
   static constexpr int OFF_PAR = OFF_ROW + RB * 4;      // [64]
-  static constexpr int OFF_BAD = OFF_PAR + kMaxNodes * 4;  // [KS][ST]
-  static constexpr int OFF_ABORT = OFF_BAD + KS * ST * 4;
+  static constexpr int OFF_COPIED = OFF_PAR + kMaxNodes * 4;  // [KS][ST]
+  static constexpr int OFF_ABORT = OFF_COPIED + KS * ST * 4;
   static constexpr int SMEM = OFF_ABORT + 16;
   static_assert(OFF_JOIN + JOIN <= RING, "the merge goes on in the ring's room");
   static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
 };
 
+// Wait for the phase of the given parity; false if it ran past the limit (then *abort is raised) or
+// *abort was raised.  A try suspends the thread until the phase is complete or a time is over, which
+// by itself is far longer than a copy takes: it is given the limit, or a millisecond, so that limits
+// of any length count and an abort is seen soon.
+__device__ __forceinline__ bool try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+               : "memory");
+  return ok != 0;
+}
+constexpr unsigned kWinTryNs = 1000000;
+__device__ __noinline__ bool limited_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit_ns) {
+  const uint32_t ns = (uint32_t)min(limit_ns, (unsigned long long)kWinTryNs);
+  const unsigned long long t0 = global_ns() - ns;  // (the first try took about that)
+  while (!*abort && global_ns() - t0 < limit_ns)
+    if (try_wait_for(bar, parity, ns)) return true;
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool limited_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit_ns) {
+  const uint32_t ns = (uint32_t)min(limit_ns, (unsigned long long)kWinTryNs);
+  return try_wait_for(bar, parity, ns) || limited_wait_slow(bar, parity, abort, limit_ns);
+}
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -141,7 +166,8 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   const int fg = lane >> 2, ft = lane & 3;  // fragment row and column pair
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + Lay::OFF_FULL) + slice * ST;
   uint64_t *empty = reinterpret_cast<uint64_t *>(sm + Lay::OFF_EMPTY) + slice * ST;
-  volatile int *s_bad = reinterpret_cast<volatile int *>(sm + Lay::OFF_BAD) + slice * ST;
+  // the group copied into each stage, twice, and 1 if its page is bad
+  volatile int *s_copied = reinterpret_cast<volatile int *>(sm + Lay::OFF_COPIED) + slice * ST;
   uint8_t *ring = sm + slice * ST * Lay::G_BYTES;
 
   const unsigned C = p.cluster, rank = C > 1 ? cluster_rank() : 0;
@@ -154,6 +180,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], RG);
+      s_copied[i] = -2;
     }
     fence_barrier_init();
   }
@@ -207,9 +234,9 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     }
     return blk * p.block_size + pos % p.block_size;
   };
-  // (one lane) a group whose rows start at `row` into stage st; none if the page is bad
-  auto copy = [&](int row, bool tree, int st) {
-    s_bad[st] = row < 0;
+  // (one lane) group i, whose rows start at `row`, into stage st; none if the page is bad
+  auto copy = [&](int i, int row, bool tree, int st) {
+    s_copied[st] = 2 * i + (row < 0);
     if (row < 0) {
       mbar_arrive(&full[st]);
       return;
@@ -228,7 +255,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     if (!mine(i)) return;
     const int row = __shfl_sync(0xFFFFFFFFu, desc, i & 31);
     const bool tree = g0 + slice + KS * i < gt;
-    if (elect_one() && (RG == 1 || parity < 0 || mbar_wait(&empty[st], parity, abort_flag, p.wait_ns))) copy(row, tree, st);
+    if (elect_one() && (RG == 1 || parity < 0 || limited_wait(&empty[st], parity, abort_flag, p.wait_ns))) copy(i, row, tree, st);
     __syncwarp();
   };
   // The first groups, one after another so that the first one is whole soon (2048 units of 32 rows,
@@ -238,7 +265,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
   if (layout_ok) {
     if (RG == 2 && NT < 4) {
       desc = locate(lane);
-      if (lane < min(ST, n) && mine(lane)) copy(desc, g0 + slice + KS * lane < gt, lane);
+      if (lane < min(ST, n) && mine(lane)) copy(lane, desc, g0 + slice + KS * lane < gt, lane);
       __syncwarp();
     } else {
       for (int i = 0; i < min(ST, n); ++i) issue(i, i, -1);
@@ -299,7 +326,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < DT; k += 2) load_q(k, held[k / 2]);
   }
-  int done = 0, issued = min(ST, n);
+  int done = 0;
   int st = 0, phase = 0;  // the stage of group i and the parity of its use
 
   float s[NT][4];      // the scores of the group whose weights come next, then their exponents
@@ -439,13 +466,12 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     }
   };
   auto arrived = [&](int at, int par) -> bool {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(&full[at], par, abort_flag, p.wait_ns));
+    return __all_sync(0xFFFFFFFFu, limited_wait(&full[at], par, abort_flag, p.wait_ns));
   };
   // the stage of group i - back is filled again with group i - back + ST
   auto refill = [&](int i, int back) {
     if (i < back || i - back + ST >= n) return;
     issue(i - back + ST, st >= back ? st - back : st - back + ST, st >= back ? phase : phase ^ 1);
-    ++issued;
   };
   auto next_stage = [&]() {  // done with the stage
     __syncwarp();            // every lane is
@@ -458,7 +484,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
       refill(i, RG);
       if (!arrived(st, phase)) break;
       done = i + 1;
-      if (s_bad[st] == 0) {
+      if ((s_copied[st] & 1) == 0) {
         const uint32_t stage = ring_addr + st * Lay::G_BYTES;
         scores(std::false_type{}, stage, s);
         mask(i, stage, false);
@@ -473,7 +499,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     // the scores of a group are computed between the weights of the one before
     done = 1;
     scores(std::false_type{}, ring_addr, s);
-    mask(0, ring_addr, s_bad[0] != 0);
+    mask(0, ring_addr, (s_copied[0] & 1) != 0);
     limits();
     for (int i = 0; i < n; ++i) {
       const uint32_t stage = ring_addr + st * Lay::G_BYTES;
@@ -487,7 +513,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
       }
       if (!arrived(st1, st1 == 0 ? phase ^ 1 : phase)) break;
       done = i + 2;
-      const bool bad = s_bad[st1] != 0;
+      const bool bad = (s_copied[st1] & 1) != 0;
       float t[NT][4];
       scores(std::true_type{}, stage1, t);
       outputs(stage);
@@ -502,12 +528,15 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     }
   }
   if (done < n && layout_ok) {
-    // a wait gave up: let the copies in flight land before the shared memory is used again
+    // a wait gave up: let this warp's copies in flight (those that were made) land before the shared
+    // memory is used again
     *abort_flag = 1;
     const unsigned long long t0 = global_ns();
-    for (int i = done; i < issued; ++i)
-      while (mine(i) && !mbar_try_wait(&full[i % ST], (i / ST) & 1) && global_ns() - t0 < kWaitLimitNs) {
+    for (int k = 0; k < ST; ++k) {
+      const int i = s_copied[k] >> 1;
+      while (i >= done && mine(i) && !mbar_try_wait(&full[k], (i / ST) & 1) && global_ns() - t0 < kWaitLimitNs) {
       }
+    }
   }
 
   // ---- merge, in units of 16 dimensions of 8 rows as they stand in a warp's registers (one float4
