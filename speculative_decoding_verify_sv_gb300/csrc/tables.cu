@@ -41,14 +41,47 @@ __device__ __forceinline__ int page_of(const TableParams &p, int n) {
 }
 __device__ __forceinline__ int pages_of(const TableParams &p, int n) { return n > 0 ? page_of(p, n - 1) + 1 : 0; }
 
-// RUN: neighbouring tokens per thread (1: two tokens a block apart)
-template <int RUN, int kTableThreads>
+// More tokens than the slot map has room for: the pages whose first token lies past its end are given
+// out page by page (of a batch of 2^31 fresh pages and more the first 2^31 - 1), so that the time goes by
+// the table's entries and not by the number of tokens, however wild.  Out of line: in the kernel's own
+// code, where it is hardly ever reached, it costs every call 0.3 us.
+template <bool HELD>
+__device__ __noinline__ void pages_past_the_map(const TableParams &p, const int *sums, long long head, long long pages) {
+  const int *s_start = sums, *s_base = sums + p.B + 1, *s_len = sums + 2 * p.B + 1, *s_have = sums + 3 * p.B + 1;
+  auto pages_had = [&](int b) { return HELD ? s_have[b] : pages_of(p, s_len[b]); };
+  const int top = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;
+  const unsigned left = head >= 0 && head < p.num_free ? (unsigned)(p.num_free - head) : 0u;
+  unsigned from = 0;
+  if (p.T > 0) {  // behind the pages up to the last token with a place
+    int b = 0;
+    for (int d = top; d > 0; d >>= 1)
+      if (b + d < p.B && s_start[b + d] < p.T) b += d;
+    from = (unsigned)s_base[b] +
+           (unsigned)max(0, min(pages_of(p, s_len[b] + (p.T - s_start[b])), p.max_blocks) - pages_had(b));
+  }
+  const unsigned last = (unsigned)min(pages, (long long)INT32_MAX);
+  bool bad = false;
+  for (unsigned i = from + blockIdx.x * blockDim.x + threadIdx.x; i < last; i += gridDim.x * blockDim.x) {
+    int b = 0;  // the last request whose fresh pages begin at or before page i
+    for (int d = top; d > 0; d >>= 1)
+      if (b + d < p.B && (unsigned)s_base[b + d] <= i) b += d;
+    const int id = i < left ? p.free_blocks[head + i] : -1;
+    const bool there = (unsigned)id < (unsigned)p.num_blocks;
+    p.block_table[(size_t)b * p.max_blocks + pages_had(b) + (int)(i - (unsigned)s_base[b])] = there ? id : -1;
+    if (!there) bad = true;
+  }
+  if (bad) set_status(p.status, SV_DEV_BAD_BLOCK);
+}
+
+// RUN: neighbouring tokens per thread (1: two tokens a block apart).  HELD: rows may hold more pages
+// than those of their tokens (an instance of its own: one more array to read and keep costs 0.3 to 0.6 us).
+template <int RUN, int kTableThreads, bool HELD>
 __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __grid_constant__ TableParams p) {
   extern __shared__ int table_smem[];
   int *s_start = table_smem;             // [B + 1] first token of each request, at most INT32_MAX
   int *s_base = table_smem + p.B + 1;    // [B] fresh pages before each request
   int *s_len = table_smem + 2 * p.B + 1; // [B] tokens that it has
-  int *s_have = table_smem + 3 * p.B + 1; // [B] pages that it has (given held; else those of its tokens)
+  int *s_have = table_smem + 3 * p.B + 1; // [B] pages that it has (HELD; else those of its tokens)
   __shared__ long long s_tok[kTableThreads / 32], s_page[kTableThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool report = blockIdx.x == 0;
@@ -62,7 +95,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
       const int b = c + k * kTableThreads + tid;
       len[k] = b < p.B ? p.length[b] : 0;
       add[k] = b < p.B ? p.new_tokens[b] : 0;
-      held[k] = p.held && b < p.B ? p.held[b] : 0;
+      held[k] = HELD && b < p.B ? p.held[b] : 0;
     }
 #pragma unroll
     for (int k = 0; k < kTableLoads; ++k) {
@@ -75,14 +108,14 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
       // as that many)
       x = x < 0 ? 0 : (int)min((long long)x, min((long long)p.cap - L + p.T, (long long)INT32_MAX - L));
       int have = pages_of(p, L);
-      if (p.held) {
+      if constexpr (HELD) {
         if (report && (held[k] < 0 || held[k] > p.max_blocks)) set_status(p.status, SV_DEV_BAD_PREFIX);
         s_have[b] = have = max(have, min(held[k], p.max_blocks));
       }
       s_start[b] = x;
       s_base[b] = max(0, min(pages_of(p, L + x), p.max_blocks) - have);
       s_len[b] = L;
-      if (report && p.held) p.out_held[b] = have + s_base[b];
+      if (HELD && report) p.out_held[b] = have + s_base[b];
     }
   }
   __syncthreads();
@@ -139,7 +172,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
   constexpr int U = RUN == 1 ? 2 : RUN;
   const unsigned step = gridDim.x * kTableThreads * U;
   const int top = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;  // the search's first stride
-  auto pages_had = [&](int b) { return p.held ? s_have[b] : pages_of(p, s_len[b]); };
+  auto pages_had = [&](int b) { return HELD ? s_have[b] : pages_of(p, s_len[b]); };
   // where the id of page pg of request b is: held (in the table) or fresh (NULL: none is left)
   const unsigned left = head >= 0 && head < p.num_free ? (unsigned)(p.num_free - head) : 0u;
   const int32_t *fresh = p.free_blocks + (left ? head : 0);
@@ -246,26 +279,6 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
       }
     }
   }
-  if (total > p.T) {
-    // More tokens than the slot map has room for: the pages whose first token lies past its end are
-    // given out page by page (of a batch of 2^31 fresh pages and more the first 2^31 - 1), so that the
-    // time goes by the table's entries and not by the number of tokens, however wild.
-    unsigned from = 0;
-    if (p.T > 0) {  // behind the pages up to the last token with a place
-      int b = 0;
-      for (int d = top; d > 0; d >>= 1)
-        if (b + d < p.B && s_start[b + d] < p.T) b += d;
-      const int len = s_len[b];
-      from = (unsigned)s_base[b] + (unsigned)max(0, min(pages_of(p, len + (p.T - s_start[b])), p.max_blocks) - pages_had(b));
-    }
-    const unsigned last = (unsigned)min(pages, (long long)INT32_MAX);
-    for (unsigned i = from + blockIdx.x * kTableThreads + tid; i < last; i += gridDim.x * kTableThreads) {
-      int b = 0;  // the last request whose fresh pages begin at or before page i
-      for (int d = top; d > 0; d >>= 1)
-        if (b + d < p.B && (unsigned)s_base[b + d] <= i) b += d;
-      checked(i < left ? fresh[i] : -1, b, pages_had(b) + (int)(i - (unsigned)s_base[b]), true);
-    }
-  }
   if (bad) set_status(p.status, SV_DEV_BAD_BLOCK);
   if (report) {
     for (int b = tid; b <= p.B; b += kTableThreads) p.token_start[b] = s_start[b];
@@ -275,6 +288,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __gri
       if (head < 0 || (pages > 0 && head + pages > p.num_free)) set_status(p.status, SV_DEV_BAD_BLOCK);
     }
   }
+  if (total > p.T) pages_past_the_map<HELD>(p, table_smem, head, pages);
 }
 
 }  // namespace
@@ -293,13 +307,16 @@ cudaError_t launch_block_tables(TableParams p, int num_sms, cudaStream_t s) {
     void (*kernel)(TableParams);
     int threads, tokens;  // tokens that a CTA takes in a step
   };
-  static const Form forms[3] = {{block_tables_kernel<4, 512>, 512, 2048},
-                                {block_tables_kernel<1, 256>, 256, 512},
-                                {block_tables_kernel<1, 1024>, 1024, 2048}};
-  const int form = p.T / p.B >= 256 ? 0 : (p.B <= 2048 ? 1 : 2);
+  static const Form forms[6] = {{block_tables_kernel<4, 512, false>, 512, 2048},
+                                {block_tables_kernel<1, 256, false>, 256, 512},
+                                {block_tables_kernel<1, 1024, false>, 1024, 2048},
+                                {block_tables_kernel<4, 512, true>, 512, 2048},
+                                {block_tables_kernel<1, 256, true>, 256, 512},
+                                {block_tables_kernel<1, 1024, true>, 1024, 2048}};
+  const int form = (p.T / p.B >= 256 ? 0 : (p.B <= 2048 ? 1 : 2)) + (p.held ? 3 : 0);
   const Form &f = forms[form];
   const size_t smem = (size_t)((p.held ? 4 : 3) * p.B + 1) * sizeof(int);
-  static std::atomic<bool> attr_set[3][64];
+  static std::atomic<bool> attr_set[6][64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[form][dev].load()) {
