@@ -85,6 +85,7 @@ struct TcParams {
   // two that a unit's first tile starts at a multiple of
   CUtensorMap tm_ks, tm_vs;
   int window, sinks, win_align;
+  int block_shift;  // block_size is 2 to this power; -1 if it is none
 };
 
 struct TcPlan {
@@ -113,7 +114,8 @@ struct WinParams {
   int window, sinks;
   float scale_log2;
   Tree tree;
-  unsigned long long wait_ns;
+  unsigned long long wait_ns;  // the limit of a wait, and of a single try
+  unsigned try_ns;
 };
 cudaError_t launch_window_attention(const AttnParams &p, int num_sms, cudaStream_t s);
 // The same in fp32 (any number of rows; p.splits is set at the launch: the CTAs per unit).

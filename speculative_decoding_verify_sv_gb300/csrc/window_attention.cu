@@ -91,9 +91,9 @@ struct WinLayout {
 };
 
 // Wait for the phase of the given parity; false if it ran past the limit (then *abort is raised) or
-// *abort was raised.  A try suspends the thread until the phase is complete or a time is over, which
-// by itself is far longer than a copy takes: it is given the limit, or a millisecond, so that limits
-// of any length count and an abort is seen soon.
+// *abort was raised.  A try suspends the thread for a time of the hardware's choice, or for a given one:
+// behind the first try it is the limit, or a millisecond, so that short limits count (those up to a
+// millisecond with the first try) and an abort is seen soon.  (A time given to the first try too costs 2 %.)
 __device__ __forceinline__ bool try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -103,17 +103,16 @@ __device__ __forceinline__ bool try_wait_for(uint64_t *bar, uint32_t parity, uin
   return ok != 0;
 }
 constexpr unsigned kWinTryNs = 1000000;
-__device__ __noinline__ bool limited_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit_ns) {
-  const uint32_t ns = (uint32_t)min(limit_ns, (unsigned long long)kWinTryNs);
-  const unsigned long long t0 = global_ns() - ns;  // (the first try took about that)
+__device__ __noinline__ bool limited_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t ns,
+                                               unsigned long long limit_ns) {
+  const unsigned long long t0 = global_ns() - ns;  // (the first try)
   while (!*abort && global_ns() - t0 < limit_ns)
     if (try_wait_for(bar, parity, ns)) return true;
   *abort = 1;
   return false;
 }
-__device__ __forceinline__ bool limited_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit_ns) {
-  const uint32_t ns = (uint32_t)min(limit_ns, (unsigned long long)kWinTryNs);
-  return try_wait_for(bar, parity, ns) || limited_wait_slow(bar, parity, abort, limit_ns);
+__device__ __forceinline__ bool limited_wait(uint64_t *bar, uint32_t parity, volatile int *abort, const WinParams &p) {
+  return mbar_try_wait(bar, parity) || limited_wait_slow(bar, parity, abort, p.try_ns, p.wait_ns);
 }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     if (!mine(i)) return;
     const int row = __shfl_sync(0xFFFFFFFFu, desc, i & 31);
     const bool tree = g0 + slice + KS * i < gt;
-    if (elect_one() && (RG == 1 || parity < 0 || limited_wait(&empty[st], parity, abort_flag, p.wait_ns))) copy(i, row, tree, st);
+    if (elect_one() && (RG == 1 || parity < 0 || limited_wait(&empty[st], parity, abort_flag, p))) copy(i, row, tree, st);
     __syncwarp();
   };
   // The first groups, one after another so that the first one is whole soon (2048 units of 32 rows,
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) window_attn_kernel(const __gri
     }
   };
   auto arrived = [&](int at, int par) -> bool {
-    return __all_sync(0xFFFFFFFFu, limited_wait(&full[at], par, abort_flag, p.wait_ns));
+    return __all_sync(0xFFFFFFFFu, limited_wait(&full[at], par, abort_flag, p));
   };
   // the stage of group i - back is filled again with group i - back + ST
   auto refill = [&](int i, int back) {
@@ -854,6 +853,7 @@ cudaError_t launch_window_attention(const AttnParams &a, int num_sms, cudaStream
   p.scale_log2 = a.scale_log2;
   p.tree = a.tree;
   p.wait_ns = a.wait_ns;
+  p.try_ns = (unsigned)std::min<unsigned long long>(a.wait_ns, kWinTryNs);
   const int span = a.window - 1 < a.cap ? a.window - 1 : a.cap;
   const WinPlan plan = window_plan((long long)a.B * a.Hkv, a.M, span / kWinGroup + (a.N + a.sinks) / kWinGroup + 2, num_sms);
   p.m_tiles = plan.m_tiles;
