@@ -23,7 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsv.so")
 BINDING = os.path.join(BUILD, "sv_binding.so")
 
-SOURCES = ["sv_api.cu", "attention.cu", "attention_tc.cu", "attention_tc_window.cu", "window_attention.cu", "window_attention_f32.cu",
+SOURCES = ["sv_api.cu", "attention.cu", "attention_tc.cu", "attention_tc_window.cu", "attention_tc_window_paged.cu", "window_attention.cu", "window_attention_f32.cu",
            "accept.cu", "accept_recursive.cu", "commit.cu", "ngram.cu", "lm_head.cu", "tables.cu", "qk_norm_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -7,6 +7,7 @@
 namespace sv {
 
 cudaError_t launch_tc_window(const TcParams &p, int D, const TcPlan &pl, cudaStream_t s);
+cudaError_t launch_tc_window_paged(const TcParams &p, int D, const TcPlan &pl, cudaStream_t s);
 
 namespace {
 
@@ -147,6 +148,9 @@ cudaError_t launch_attention_tc(const AttnParams &a, const TcPlan &pl, void *ws,
     p.sinks = a.sinks;
     // a paged tile starts with a page (or, in longer pages, at a multiple of the tile)
     p.win_align = a.block_table ? p.page_rows : 1;
+    p.block_shift = -1;
+    for (int k = 4; k < 31; ++k)
+      if (a.block_size == 1 << k) p.block_shift = k;
   }
   uint8_t *w = static_cast<uint8_t *>(ws);
   p.hdr = reinterpret_cast<unsigned long long *>(w + pl.off_hdr);
@@ -175,7 +179,8 @@ cudaError_t launch_attention_tc(const AttnParams &a, const TcPlan &pl, void *ws,
   p.scale_log2 = a.scale_log2;
   p.tree = a.tree;
   p.wait_ns = a.wait_ns;
-  return a.window > 0 ? launch_tc_window(p, a.D, pl, s) : launch_tc_plan<false>(p, a.D, pl, s);
+  if (!win) return launch_tc_plan<false, false>(p, a.D, pl, s);
+  return p.paged ? launch_tc_window_paged(p, a.D, pl, s) : launch_tc_window(p, a.D, pl, s);
 }
 
 }  // namespace sv

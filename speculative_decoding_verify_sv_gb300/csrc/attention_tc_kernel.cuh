@@ -42,7 +42,7 @@
 // unit of a short window another of its few tiles.  P V of that tile issues only the 16-key
 // steps that hold keys, and V rows in those steps that no row sees are zeroed, as are the
 // rows of the first window tile before the root's window.  A page whose id lies outside the pool
-// is loaded as zeros (from past the pool's end) and its columns are hidden from every row.
+// is loaded as zeros (from past the pool's end) and its scores become -inf (the PAGES instances).
 #pragma once
 
 #include <atomic>
@@ -166,6 +166,11 @@ __device__ __forceinline__ int unit_first(const TcParams &p, int L) {
   return WIN ? window_first(L, p.window) & -p.win_align : 0;
 }
 
+// the block that holds a position
+__device__ __forceinline__ int block_of(const TcParams &p, int pos) {
+  return p.block_shift >= 0 ? pos >> p.block_shift : pos / p.block_size;
+}
+
 // sinks that stand in the tree tile: those before the unit's other tiles
 __device__ __forceinline__ int tile_sinks(const TcParams &p, int first) { return min(p.sinks, first); }
 
@@ -182,6 +187,22 @@ __device__ __forceinline__ int unit_tiles(const TcParams &p, int b) {
 // 16-key steps of the tree tile that hold keys (WIN): the tree's rows, then the sinks' from 64
 __device__ __forceinline__ uint32_t tree_tile_steps(int N, int n_sinks) {
   return ((1u << ((N + 15) >> 4)) - 1u) | (((1u << ((n_sinks + 15) >> 4)) - 1u) << 4);
+}
+
+// Hides the keys of the pages marked in `bad`, each of page_keys columns from column 0 on, from this
+// warp's slice of S (`columns` TMEM columns at ta, the first one column `c` of the tile): their scores
+// become -inf.  Out of line and ahead of the row loop, which knows nothing of them, since hardly any
+// tile has one; even so the test costs windows of many rows 1.5 to 3 %, so that contiguous caches have
+// instances without it.
+__device__ __noinline__ void hide_pages(uint32_t ta, int c, int columns, uint32_t bad, int page_keys) {
+  for (int k = 0; k < columns; k += 16) {
+    if (c + k < 0 || !((bad >> ((c + k) / page_keys)) & 1u)) continue;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = -INFINITY;
+    tmem_st16(ta + k, v);
+  }
+  tmem_wait_st();
 }
 
 template <int BN>
@@ -333,7 +354,7 @@ __device__ __noinline__ bool idle_piece(const TcParams &p, int N, int t0, int n,
   return true;
 }
 
-template <int D, int MT, int CP, int BN, int STAGES, int QBUF, int PBUF, bool WIN>
+template <int D, int MT, int CP, int BN, int STAGES, int QBUF, int PBUF, bool WIN, bool PAGES>
 __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::THREADS, 1)
     attn_tc_kernel(const __grid_constant__ TcParams p) {
   static_assert(CP == 1 || MT == 1, "row copies need a single M tile");
@@ -1064,14 +1085,14 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
         const int gk = g + k, j = gk & 1, s = gk % VST, t = pc.t0 + k, pb = gk % PBUF;
         const bool tree = t == 0;
         const int nvalid = tree ? p.N : min(BN, L - first - (t - 1) * BN);
-        // WIN: lane i looks at the id of the tile's page i (a tree tile's box i of sinks), read while
+        // PAGES: lane i looks at the id of the tile's page i (a tree tile's box i of sinks), read while
         // S is waited for
         const int page_keys = tree ? 16 : p.page_rows;
         int page_id = 0;
-        if constexpr (WIN) {
-          if (p.paged && lane * page_keys < (tree ? n_sinks : nvalid))
+        if constexpr (PAGES) {
+          if (lane * page_keys < (tree ? n_sinks : nvalid))
             page_id = __ldg(p.block_table + (size_t)pc.b * p.max_blocks +
-                            ((tree ? 0 : first + (t - 1) * BN) + lane * page_keys) / p.block_size);
+                            block_of(p, (tree ? 0 : first + (t - 1) * BN) + lane * page_keys));
         }
         // S of this tile: buffer j, or (P in TMEM) this M tile's region, one phase per tile
         if (!(Lay::PT ? mbar_wait(&s_full[mt], gk & 1, abort_flag, wlim)
@@ -1104,8 +1125,6 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
           }
           return true;
         };
-        // pages outside the pool, a bit each
-        const uint32_t bad_pages = WIN && p.paged ? __ballot_sync(0xFFFFFFFFu, (unsigned)page_id >= (unsigned)p.num_blocks) : 0u;
         // visible columns of this warp's slice: tree tile -> ancestor bits, prefix
         // tile -> columns before the prefix end
         const uint64_t anc_s = (tree && valid_row && col0 < 64) ? (anc >> col0) : 0ull;
@@ -1113,9 +1132,12 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
         // WIN: columns of this warp's slice before the row's window, and those that are sinks
         const int base = WIN ? first + (t - 1) * BN + col0 : 0;
         const int lo_rel = WIN ? lo - base : 0, sk_rel = WIN ? p.sinks - base : 0;
-        const bool full = !tree && valid_row && nv_rel >= CW && (!WIN || (lo_rel <= 0 && bad_pages == 0));
+        const bool full = !tree && valid_row && nv_rel >= CW && (!WIN || lo_rel <= 0);
         const uint32_t ta0 = t_lane + (uint32_t)(((Lay::PT ? 0 : j * MT) + mt) * BN + col0);
-
+        if constexpr (PAGES) {
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, (unsigned)page_id >= (unsigned)p.num_blocks);
+          if (bad) hide_pages(ta0, tree ? col0 - 64 : col0, CW, bad, page_keys);
+        }
         // bit c of visible(h) <=> column h*CH + c of this warp's slice is a key the row sees.
         // Padding rows (past the unit's rows) see every column: their results are never
         // used, and this keeps a warp that mixes real and padding rows on one code path.
@@ -1125,16 +1147,11 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
           const int sh = h * CH;
           if constexpr (WIN) {
             auto below = [&](int x) -> uint32_t { return x <= 0 ? 0u : (x >= CH ? kAll : (1u << x) - 1u); };
-            const int c = col0 + sh;
-            if (tree && c < 64) return (uint32_t)(anc >> c) & kAll;
-            uint32_t hidden = 0;
-            if (bad_pages) {
-#pragma unroll
-              for (int u = 0; u < CH; u += 16)
-                if ((bad_pages >> ((tree ? c - 64 + u : c + u) / page_keys)) & 1u) hidden |= 0xFFFFu << u;
+            if (tree) {
+              const int c = col0 + sh;
+              return c < 64 ? (uint32_t)(anc >> c) & kAll : below(n_sinks - (c - 64));
             }
-            if (tree) return below(n_sinks - (c - 64)) & ~hidden;
-            return below(nv_rel - sh) & (~below(lo_rel - sh) | below(sk_rel - sh)) & ~hidden;
+            return below(nv_rel - sh) & (~below(lo_rel - sh) | below(sk_rel - sh));
           }
           if (tree) return sh < 64 ? (uint32_t)(anc_s >> sh) & kAll : 0u;
           const int r = nv_rel - sh;
@@ -1541,7 +1558,7 @@ __global__ void __launch_bounds__(TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>::T
   if (MT == 2) finish();
 }
 
-template <int D, int MT, int CP, int BN, int STAGES, int QBUF, int PBUF, bool WIN>
+template <int D, int MT, int CP, int BN, int STAGES, int QBUF, int PBUF, bool WIN, bool PAGES>
 cudaError_t launch_tc_typed(const TcParams &p, int grid, cudaStream_t s) {
   using Lay = TcLayout<D, MT, CP, BN, STAGES, QBUF, PBUF>;
   static_assert(Lay::SMEM <= 232448, "shared memory layout exceeds 227 KB");
@@ -1549,7 +1566,7 @@ cudaError_t launch_tc_typed(const TcParams &p, int grid, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr[dev].load()) {
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, MT, CP, BN, STAGES, QBUF, PBUF, WIN>,
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, MT, CP, BN, STAGES, QBUF, PBUF, WIN, PAGES>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev].store(true);
@@ -1565,12 +1582,12 @@ cudaError_t launch_tc_typed(const TcParams &p, int grid, cudaStream_t s) {
   at[0].val.cooperative = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, MT, CP, BN, STAGES, QBUF, PBUF, WIN>, p);
+  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, MT, CP, BN, STAGES, QBUF, PBUF, WIN, PAGES>, p);
 }
 
 // The instance for a plan: D, M tiles MT and row copies CP.  (Windowed calls of up to 32 rows per
 // KV head, four row copies, go to the kernel of window_attention.cu.)
-template <bool WIN>
+template <bool WIN, bool PAGES>
 cudaError_t launch_tc_plan(const TcParams &p, int D, const TcPlan &pl, cudaStream_t s) {
   if (D == 128) {
     // One M tile: one P buffer, its room spent on a third V stage (ragged-paged 763 us
@@ -1578,17 +1595,17 @@ cudaError_t launch_tc_plan(const TcParams &p, int D, const TcPlan &pl, cudaStrea
     // that the next piece's Q is loaded before the current piece ends (medusa-t64 66.7
     // us against 68.2 with the third V stage; ragged-paged, four row copies, 774 against
     // 764 the other way round).
-    if (pl.MT == 2) return launch_tc_typed<128, 2, 1, 128, 2, 1, 1, WIN>(p, pl.grid, s);
+    if (pl.MT == 2) return launch_tc_typed<128, 2, 1, 128, 2, 1, 1, WIN, PAGES>(p, pl.grid, s);
     if constexpr (!WIN)
-      if (pl.CP == 4) return launch_tc_typed<128, 1, 4, 128, 2, 1, 1, WIN>(p, pl.grid, s);
-    if (pl.CP == 2) return launch_tc_typed<128, 1, 2, 128, 2, 2, 1, WIN>(p, pl.grid, s);
-    return launch_tc_typed<128, 1, 1, 128, 2, 1, 1, WIN>(p, pl.grid, s);
+      if (pl.CP == 4) return launch_tc_typed<128, 1, 4, 128, 2, 1, 1, WIN, PAGES>(p, pl.grid, s);
+    if (pl.CP == 2) return launch_tc_typed<128, 1, 2, 128, 2, 2, 1, WIN, PAGES>(p, pl.grid, s);
+    return launch_tc_typed<128, 1, 1, 128, 2, 1, 1, WIN, PAGES>(p, pl.grid, s);
   }
-  if (pl.MT == 2) return launch_tc_typed<64, 2, 1, 128, 4, 2, 1, WIN>(p, pl.grid, s);
+  if (pl.MT == 2) return launch_tc_typed<64, 2, 1, 128, 4, 2, 1, WIN, PAGES>(p, pl.grid, s);
   if constexpr (!WIN)
-    if (pl.CP == 4) return launch_tc_typed<64, 1, 4, 128, 3, 2, 2, WIN>(p, pl.grid, s);
-  if (pl.CP == 2) return launch_tc_typed<64, 1, 2, 128, 3, 2, 2, WIN>(p, pl.grid, s);
-  return launch_tc_typed<64, 1, 1, 128, 3, 2, 2, WIN>(p, pl.grid, s);
+    if (pl.CP == 4) return launch_tc_typed<64, 1, 4, 128, 3, 2, 2, WIN, PAGES>(p, pl.grid, s);
+  if (pl.CP == 2) return launch_tc_typed<64, 1, 2, 128, 3, 2, 2, WIN, PAGES>(p, pl.grid, s);
+  return launch_tc_typed<64, 1, 1, 128, 3, 2, 2, WIN, PAGES>(p, pl.grid, s);
 }
 
 }  // namespace
