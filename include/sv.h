@@ -137,7 +137,9 @@ typedef struct {
  * [B,N,Hq,D].
  * dt: SV_BF16 (fp32 accumulation, bf16 output) or SV_F32 (fp32 throughout).
  * Supported: D in {64, 128}; Hq % Hkv == 0; 1 <= N <= 64; block_size % 16 == 0 for
- * paged caches.  Workspace: sv_tree_attention_workspace_size() bytes (may be 0).  The
+ * paged caches.  A page id outside the pool sets SV_DEV_BAD_BLOCK: its page is not read and
+ * that sequence's outputs are not meaningful.
+ * Workspace: sv_tree_attention_workspace_size() bytes (may be 0).  The
  * workspace must be zero-filled before its first use with this function (it keeps a
  * generation counter and per-piece completion words that later calls rely on); each call
  * leaves it ready for the next, whatever the shape, including after a call that reported
@@ -176,8 +178,11 @@ size_t sv_tree_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int H
  * with sv_tree_attention) as sv_tree_attention; a paged block_size that is not a multiple of
  * 16, and caches or batches of more rows than 32-bit coordinates reach, are SV_ERR_UNSUPPORTED.
  * out overlapping q, the tree's or the cache's K/V is SV_ERR_INVALID_ARG.
+ * Keys of a page whose id lies outside the pool are left out (SV_DEV_BAD_BLOCK).
  * A NaN or infinity in the V row of a key that some rows of a sequence see can also reach
  * its other rows of the same KV head (0 * NaN).
+ * With SV_BF16 the weights are rounded to bf16 for the product with V (off by at most 2^-8 of each, as
+ * in sv_tree_attention); scores, sums and outputs are fp32 up to the one rounding at the store.
  * Workspace: sv_window_attention_workspace_size() bytes (max_prefix as there; 0 for float32, for up
  * to 32 query rows per KV head, and where few or short windows make the kernel without one
  * the faster).  It serves the faster of two kernels, and which one that is changes back and forth
