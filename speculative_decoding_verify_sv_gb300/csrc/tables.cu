@@ -15,8 +15,8 @@
 // of steps, several tokens side by side, so that neither the searches nor the reads of the page
 // ids wait for one another.  Where requests bring many tokens (256 places of the map per request
 // and more) a thread takes four neighbouring tokens, which mostly share their request and page: 256
-// prompts of 512 to 8192 tokens 7.9 us (8.9 with 64-bit places) against 16.4 with single tokens; 4096
-// requests of up to 64 tokens 7.2 us with single tokens against 9.9 with four, whose crossings of
+// prompts of 512 to 8192 tokens 8.1 us (8.9 with 64-bit places) against 16.4 with single tokens; 4096
+// requests of up to 64 tokens 7.3 us with single tokens against 9.9 with four, whose crossings of
 // requests diverge.
 // A fresh page starts with a new token (its first position is not below length_b), so the thread
 // that holds this token writes the page's table entry.
@@ -74,7 +74,7 @@ __device__ __noinline__ void pages_past_the_map(const TableParams &p, const int 
 }
 
 // RUN: neighbouring tokens per thread (1: two tokens a block apart).  HELD: rows may hold more pages
-// than those of their tokens (an instance of its own: one more array to read and keep costs 0.3 to 0.6 us).
+// than those of their tokens (an instance of its own: one more array to read and keep costs up to 0.3 us, 4096 requests).
 template <int RUN, int kTableThreads, bool HELD>
 __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const __grid_constant__ TableParams p) {
   extern __shared__ int table_smem[];

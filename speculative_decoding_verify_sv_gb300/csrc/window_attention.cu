@@ -754,8 +754,9 @@ cudaError_t launch_window_d(const WinParams &p, int nt, int rg, long long ctas, 
 
 // Rows of a CTA: up to four 8-column steps per warp, or up to four per each of a slice's two warps.
 // Few rows per CTA make short chains and many CTAs, which read the same K and V from L2; many rows
-// read them once.  Fitted to measurements (8 to 128 units of 32 to 512 rows, windows 17 to 4097, root
-// mean square error 5 %): a CTA takes `start` us and `group` us for each of its groups, 1.16 times
+// read them once.  Fitted to measurements (D = 128, contiguous caches, 8 to 128 units of 32 to 512 rows,
+// windows 17 to 4097, root mean square error 5 %; D = 64 goes by the same figures, its bytes counted
+// twice over): a CTA takes `start` us and `group` us for each of its groups, 1.16 times
 // that with two CTAs per SM.  8 units of 64 rows, window 4097, in tiles of 16 rows 12.1 us against
 // 18.3 in one; 128 units of 208 rows, window 4097, in tiles of 32 rows 177 against 223 in tiles of
 // 64; 512 rows, window 513, 114 against 90.
@@ -808,7 +809,7 @@ WinPlan window_plan(long long kv_units, int M, int groups, int num_sms) {
 
 // The tensor-core kernel pads a unit's rows to 128 or 256 and pays more for a unit's start and
 // for the launch, but takes long windows of many rows at twice the rate.  As fitted to measurements
-// (us; 128 to 2048 units, 40 to 512 rows, windows 17 to 4097):
+// (us; D = 128, contiguous caches, 128 to 2048 units, 40 to 512 rows, windows 17 to 4097):
 //   13 + units tiles / SMs (6 + 1.45 key tiles) + 2 SMs / units      (2.55 for 256 rows)
 // e.g. 128 units of 104 rows: window 129 13 us here against 21, window 1025 36 against 33; 512 units
 // of 64 rows: 24 against 39, 69 against 87; 8 units of 208 rows, window 4097: 20 against 85.
