@@ -329,13 +329,14 @@ PyObject *block_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
     try {
       // new outputs are parts of one buffer, the slots and positions on 16-byte boundaries
       const int64_t padded = (T + 3) / 4 * 4, offsets[5] = {2 * padded, 0, padded, 2 * padded + B + 1, 2 * padded + B + 2};
-      at::Tensor buffer;
+      at::Tensor buffer, kept[5];  // (another thread may change the dict while the call is under way)
       int32_t *ptr[5];
       for (int i = 0; i < made; ++i) {
         PyObject *o = given(a[8]) ? PyDict_GetItemWithError(outs, keys[i]) : nullptr;
         if (!o && PyErr_Occurred()) throw Refused();
         if (o) {
-          ptr[i] = tensor(o, names[i], at::kInt, {sizes[i]}, dev).data_ptr<int32_t>();
+          kept[i] = tensor(o, names[i], at::kInt, {sizes[i]}, dev);
+          ptr[i] = kept[i].data_ptr<int32_t>();
         } else {
           if (!buffer.defined()) buffer = make({2 * padded + B + 2 + (made == 5 ? B : 0)}, len, at::kInt);
           ptr[i] = buffer.data_ptr<int32_t>() + offsets[i];
