@@ -14,7 +14,10 @@
  * sv_block_tables extends a paged cache's block tables and makes the slot map of the new
  * tokens, sv_qk_norm_rope / sv_tree_qk_norm_rope turn a projection's rows into the rotated
  * Q, K and V that the cache and the attention take, and sv_window_attention is the tree
- * attention of layers with a sliding window and sinks.
+ * attention of layers with a sliding window and sinks.  For long caches: sv_shared_attention is
+ * the tree attention of sequences that share prefixes, computed once for all of them, and
+ * sv_sparse_attention the one over listed pages, which sv_page_bounds, sv_page_scores and
+ * sv_select_pages choose.
  *
  * Conventions shared by every entry point
  *  - Every tensor argument is caller-owned DEVICE memory, dense row-major in the layout
@@ -85,6 +88,8 @@ typedef int32_t sv_status;
                                       (or, in exact acceptance, deeper than q's Dq rows):
                                       that sequence's outputs are not meaningful (its
                                       acceptance keeps the root alone) */
+#define SV_DEV_BAD_GROUP 0x80u     /* group_start does not ascend within [0, B]: nothing is
+                                      shared in that call */
 
 /* The two counts of a packed near-tie word (see "Near ties" above). */
 #define SV_NEAR_DECISIONS(w) ((uint32_t)(w) & 0xFFFFu)
@@ -200,6 +205,96 @@ sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
                               void *stream);
 size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
                                           int max_prefix, int window);
+
+/* ------------------------------------------- shared prefixes and selected pages */
+
+/* Tree attention of sequences that share prefixes (a system prompt, the samples of one prompt): what
+ * sv_tree_attention computes, with the keys that a group's sequences have in common worked on once
+ * for all of the group's query rows.
+ * Sequences group_start[g] .. group_start[g+1] - 1 are group g, whose cache positions [0,
+ * shared_len[g]) hold the same K and V in every sequence, for example in the same pages; from which
+ * of them they are read is not specified.  Positions from shared_len[g] to prefix_len[b] are the
+ * sequence's own.  group_start [groups + 1] ascends within [0, B] (empty groups are allowed;
+ * sequences before the first and behind the last group share nothing); shared_len [groups] is at
+ * most the prefix_len of each of the group's sequences.  Both are int32 in device memory, so that a
+ * captured call follows them.  1 <= groups <= SV_MAX_SHARED_GROUPS.
+ * Device status: SV_DEV_BAD_GROUP for a group_start that does not ascend within [0, B] (nothing is
+ * shared then), SV_DEV_BAD_PREFIX for a shared_len outside the cache (clamped) or beyond a member's
+ * prefix_len (the outputs of that sequence are not meaningful).
+ * Every other argument, the layouts, the kernels' shapes and the refusals are sv_window_attention's
+ * (without window and sinks); Hq / Hkv <= 128, else SV_ERR_UNSUPPORTED.  Rounding as there.  float32
+ * calls read each sequence's own rows.
+ * Workspace: sv_shared_attention_workspace_size() bytes, 16-byte aligned (0 for float32); it needs no
+ * initial value.  Calls that share one must be stream-ordered.  max_prefix as for
+ * sv_tree_attention. */
+#define SV_MAX_SHARED_GROUPS 256
+sv_status sv_shared_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                              const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                              const int32_t *parent, int parent_stride, float scale,
+                              const int32_t *group_start, const int32_t *shared_len, int groups,
+                              void *out, void *workspace, size_t workspace_bytes, void *stream);
+size_t sv_shared_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
+                                          int max_prefix, int groups);
+
+/* Tree attention over listed pages, for layers that look at a part of a long prefix only.  Page j of
+ * a sequence is its positions [j * page_size, (j + 1) * page_size).  pages [B,sets,Hkv,K] int32
+ * (device) lists pages for each sequence, set of nodes and KV head: with sets = 1 one list for all
+ * nodes, with sets = N one for each.  The keys of node n and query head h are the positions below
+ * prefix_len[b] of the pages in its list and the tree nodes on n's root path:
+ *   out = softmax(scale * q . K^T) V over those keys.
+ * Entries may be in any order; a negative one, or one whose page begins at or behind prefix_len[b], names
+ * no keys; a page that is listed twice counts twice (weights of its keys doubled).
+ * page_size: a multiple of 16, the block_size in a paged cache.  K >= 1.  Pages that no list names
+ * are not read, and their blocks need not exist.  Keys of a page whose id lies outside the pool are
+ * left out (SV_DEV_BAD_BLOCK).
+ * Every other argument, the layouts, the kernels' shapes and the refusals are sv_window_attention's
+ * (without window and sinks); Hq / Hkv <= 128, else SV_ERR_UNSUPPORTED.  Rounding as there.
+ * Workspace: sv_sparse_attention_workspace_size() bytes, 16-byte aligned (0 for float32 and for few
+ * query rows per list); it needs no initial value.  Calls that share one must be stream-ordered. */
+sv_status sv_sparse_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                              const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                              const int32_t *parent, int parent_stride, float scale,
+                              const int32_t *pages, int sets, int K, int page_size, void *out,
+                              void *workspace, size_t workspace_bytes, void *stream);
+size_t sv_sparse_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
+                                          int page_size, int K, int sets);
+
+/* The least and the largest value of each channel of a page's keys, for the pages of sequence b that
+ * hold positions [start[b], prefix_len[b]) (start NULL: all of them): of the page's positions below
+ * prefix_len[b], also those before start[b].  bounds [num_blocks,Hkv,2,D] in a paged cache, by block
+ * (sequences that share a block write the same bounds, where they fill it alike), [B,
+ * ceil(Lmax/page_size),Hkv,2,D] in a contiguous one; in the cache's type; [..,0,:] the least values.
+ * Other rows of bounds are left as they are.  After a commit, start = the prefix lengths before it.
+ * start [B] int32 (device); a negative one counts as 0.  page_size >= 1, the block_size in a paged
+ * cache.  D in {64, 128}; B <= 65535.  A NaN among the values is kept.  bounds (16-byte aligned) must not
+ * overlap the cache.  Only cache.k is read (cache.v may be NULL).  Device status: SV_DEV_BAD_PREFIX
+ * (clamped), SV_DEV_BAD_BLOCK (the page is skipped).  No workspace. */
+sv_status sv_page_bounds(sv_dtype dt, int B, int Hkv, int D, int page_size, sv_kv_cache cache,
+                         const int32_t *start, void *bounds, void *stream);
+
+/* Scores of pages against queries: an upper bound of q . k over a page's keys,
+ *   score = max over the rows of the set of  sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d,
+ * the rows of a set being the query heads of the KV head at all nodes (sets = 1) or at one (sets = N).
+ * q [B,N,Hq,D]; bounds as sv_page_bounds makes them; prefix_len [B]; block_table [B,P] with
+ * bounds [num_blocks,Hkv,2,D], or NULL (num_blocks unused) with bounds [B,P,Hkv,2,D].
+ * out [B,sets,Hkv,P] float32: -infinity for pages that hold no position below prefix_len[b], and for
+ * those whose id lies outside the pool (SV_DEV_BAD_BLOCK).  fp32 accumulation.  A NaN in a row's
+ * product makes the score NaN.  Hq / Hkv <= 128; D in {64, 128}; out must not overlap an input.
+ * A prefix_len outside [0, P * page_size] is clamped (SV_DEV_BAD_PREFIX).  No workspace. */
+sv_status sv_page_scores(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                         const void *bounds, const int32_t *prefix_len, int page_size, int P,
+                         const int32_t *block_table, int num_blocks, int sets, float *out, void *stream);
+
+/* The K pages of each list that sv_sparse_attention should look at: of the ceil(prefix_len[b] /
+ * page_size) pages of sequence b the first `first`, the last `last`, and of the others those with
+ * the highest scores (a NaN ranks highest; of equal ones the lower page first), in ascending order, -1
+ * behind them when there are no more than K pages.
+ * scores [B,lists,P] float32 (sv_page_scores' with lists = sets * Hkv), out [B,lists,K] int32.
+ * first, last >= 0, first + last <= K; 1 <= P <= SV_MAX_SCORE_PAGES.  out must not overlap an input.  A
+ * prefix_len outside [0, P * page_size] is clamped (SV_DEV_BAD_PREFIX).  No workspace. */
+#define SV_MAX_SCORE_PAGES 32768
+sv_status sv_select_pages(int B, int lists, int P, const float *scores, const int32_t *prefix_len,
+                          int page_size, int K, int first, int last, int32_t *out, void *stream);
 
 /* --------------------------------------------------------- into the KV cache */
 

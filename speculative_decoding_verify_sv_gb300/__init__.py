@@ -25,7 +25,8 @@ __all__ = [
     "sv_accept_chain_commit", "sv_accept_tree_recursive", "sv_ngram_draft", "sv_tree_prepare", "sv_read_device_status",
     "sv_lm_head", "sv_accept_lmhead_workspace_size", "sv_accept_chain_lmhead", "sv_accept_tree_lmhead",
     "sv_window_attention", "sv_window_attention_workspace_size", "sv_block_tables", "sv_qk_norm_rope",
-    "sv_tree_qk_norm_rope", "sv_accept_typical", "sv_set_wait_limit_ns", "sv_get_wait_limit_ns", "sv_inject_launch_failures",
+    "sv_tree_qk_norm_rope", "sv_shared_attention", "sv_shared_attention_workspace_size", "sv_sparse_attention",
+    "sv_sparse_attention_workspace_size", "sv_page_bounds", "sv_page_scores", "sv_select_pages", "sv_accept_typical", "sv_set_wait_limit_ns", "sv_get_wait_limit_ns", "sv_inject_launch_failures",
     "sv_version", "sv_kernel_launches", "GREEDY", "EXACT", "Q_PROBS_F32", "Q_LOGITS", "Q_DRAFT_ONEHOT", "SV_MAX_TREE_NODES",
 ]
 
@@ -40,7 +41,8 @@ Q_PROBS_F32, Q_LOGITS, Q_DRAFT_ONEHOT = 0, 1, 2  # q as probabilities, draft log
 SV_MAX_TREE_NODES = 64
 SV_MAX_SINKS, SV_MAX_TABLE_BATCH = 64, 8192
 SV_DEV_BAD_TOKEN, SV_DEV_BAD_BLOCK, SV_DEV_BAD_PREFIX, SV_DEV_ZERO_DRAFT_PROB = 1, 2, 4, 8
-SV_DEV_TIMEOUT, SV_DEV_LAYOUT, SV_DEV_BAD_TREE = 0x10, 0x20, 0x40
+SV_DEV_TIMEOUT, SV_DEV_LAYOUT, SV_DEV_BAD_TREE, SV_DEV_BAD_GROUP = 0x10, 0x20, 0x40, 0x80
+SV_MAX_SHARED_GROUPS, SV_MAX_SCORE_PAGES = 256, 32768
 
 _STATUS_NAMES = {1: "SV_ERR_INVALID_ARG", 2: "SV_ERR_UNSUPPORTED", 3: "SV_ERR_WORKSPACE",
                  4: "SV_ERR_CUDA"}
@@ -121,6 +123,15 @@ def load_library():
         lib.sv_window_attention.argtypes = [I, I, I, I, I, I, P, P, P, _KVCacheC, P, I, F, I, I, P, P, SZ, P]
         lib.sv_window_attention_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
         lib.sv_window_attention_workspace_size.restype = SZ
+        lib.sv_shared_attention.argtypes = [I, I, I, I, I, I, P, P, P, _KVCacheC, P, I, F, P, P, I, P, P, SZ, P]
+        lib.sv_shared_attention_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
+        lib.sv_shared_attention_workspace_size.restype = SZ
+        lib.sv_sparse_attention.argtypes = [I, I, I, I, I, I, P, P, P, _KVCacheC, P, I, F, P, I, I, I, P, P, SZ, P]
+        lib.sv_sparse_attention_workspace_size.argtypes = [I, I, I, I, I, I, I, I, I]
+        lib.sv_sparse_attention_workspace_size.restype = SZ
+        lib.sv_page_bounds.argtypes = [I, I, I, I, I, _KVCacheC, P, P, P]
+        lib.sv_page_scores.argtypes = [I, I, I, I, I, I, P, P, P, I, I, P, I, I, P, P]
+        lib.sv_select_pages.argtypes = [I, I, I, P, P, I, I, I, I, P, P]
         lib.sv_block_tables.argtypes = [I, P, P, I, I, I, P, I, P, P, I, P, P, P, P, P]
         lib.sv_block_tables_held.argtypes = [I, P, P, I, I, I, P, I, P, P, P, I, P, P, P, P, P, P]
         lib.sv_qk_norm_rope.argtypes = [I, I, I, I, I, I, I, P, I64, P, P, F, P, P, P, I64, P, P, P, P]
@@ -132,7 +143,8 @@ def load_library():
                    "sv_tree_prepare", "sv_read_device_status", "sv_accept_tree_noalloc",
                    "sv_accept_tree_commit", "sv_accept_chain_commit", "sv_ngram_draft",
                    "sv_accept_tree_recursive", "sv_window_attention", "sv_block_tables", "sv_block_tables_held",
-                   "sv_qk_norm_rope", "sv_tree_qk_norm_rope"):
+                   "sv_qk_norm_rope", "sv_tree_qk_norm_rope", "sv_shared_attention", "sv_sparse_attention",
+                   "sv_page_bounds", "sv_page_scores", "sv_select_pages"):
             getattr(lib, fn).restype = ctypes.c_int32
         _lib = lib
         return lib
@@ -324,6 +336,63 @@ def sv_window_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, window
     position (or a node of its root path) p iff P - p < window or p < sinks."""
     return load_binding().window_attention(q, k_tree, v_tree, cache.k, cache.v, cache.prefix_len, cache.block_table,
                                            cache.block_size, parent, scale, window, sinks, out, workspace, stream)
+
+
+# -------------------------------------------- shared prefixes and selected pages
+
+def sv_shared_attention_workspace_size(dtype, B, N, Hq, Hkv, D, max_prefix, groups) -> int:
+    dt = SV_BF16 if dtype == torch.bfloat16 else SV_F32
+    return int(load_library().sv_shared_attention_workspace_size(dt, B, N, Hq, Hkv, D, max_prefix, groups))
+
+
+def sv_shared_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, group_start, shared_len, out=None,
+                        workspace=None, stream=None) -> torch.Tensor:
+    """Tree attention of sequences that share prefixes; arguments and result as sv_tree_attention.
+    Sequences group_start[g] .. group_start[g+1] - 1 hold the same K and V at the cache positions
+    [0, shared_len[g]) (the same pages, or copies), which are worked on once for all of them; positions
+    from there to prefix_len are each sequence's own.  group_start [groups+1], shared_len [groups]: CUDA
+    int32 tensors."""
+    return load_binding().shared_attention(q, k_tree, v_tree, cache.k, cache.v, cache.prefix_len, cache.block_table,
+                                           cache.block_size, parent, scale, group_start, shared_len, out, workspace, stream)
+
+
+def sv_sparse_attention_workspace_size(dtype, B, N, Hq, Hkv, D, page_size, count, sets=1) -> int:
+    dt = SV_BF16 if dtype == torch.bfloat16 else SV_F32
+    return int(load_library().sv_sparse_attention_workspace_size(dt, B, N, Hq, Hkv, D, page_size, count, sets))
+
+
+def sv_sparse_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, pages, out=None, workspace=None,
+                        stream=None) -> torch.Tensor:
+    """Tree attention over listed pages of the prefix and the tree; other arguments and result as
+    sv_tree_attention.  pages [B,1,Hkv,K] (a list for all nodes) or [B,N,Hkv,K] (one for each), CUDA
+    int32: page j is positions [j * block_size, (j+1) * block_size) of the sequence (block_size is the
+    cache's, also where it is contiguous); negative entries are none."""
+    return load_binding().sparse_attention(q, k_tree, v_tree, cache.k, cache.v, cache.prefix_len, cache.block_table,
+                                           cache.block_size, parent, scale, pages, out, workspace, stream)
+
+
+def sv_page_bounds(cache: KVCache, bounds=None, start=None, stream=None) -> torch.Tensor:
+    """Least and largest values of the channels of each page's keys, for the pages that hold positions
+    [start, prefix_len) (start: CUDA int32 [B], or None for all).  bounds: [num_blocks,Hkv,2,D] of a
+    paged cache, [B,ceil(Lmax/block_size),Hkv,2,D] of a contiguous one; written there, or to a new
+    tensor, and returned."""
+    return load_binding().page_bounds(cache.k, cache.v, cache.prefix_len, cache.block_table, cache.block_size, bounds, start,
+                                      stream)
+
+
+def sv_page_scores(q, bounds, prefix_len, page_size, block_table=None, per_node=False, out=None,
+                   stream=None) -> torch.Tensor:
+    """Scores [B,sets,Hkv,P] float32 of pages against queries q [B,N,Hq,D]: an upper bound of q . k over
+    the page's keys, the largest over the query heads of a KV head at all nodes (sets = 1), or
+    at each (per_node: sets = N).  bounds [num_blocks,Hkv,2,D] with block_table [B,P], or
+    [B,P,Hkv,2,D].  Pages without a position below prefix_len have -inf."""
+    return load_binding().page_scores(q, bounds, prefix_len, page_size, block_table, per_node, out, stream)
+
+
+def sv_select_pages(scores, prefix_len, page_size, count, first=1, last=1, out=None, stream=None) -> torch.Tensor:
+    """[B,sets,Hkv,count] int32 from scores [B,sets,Hkv,P]: the first ``first`` and last ``last`` pages of
+    the prefix and the best others, ascending, -1 behind them where there are no more."""
+    return load_binding().select_pages(scores, prefix_len, page_size, count, first, last, out, stream)
 
 
 # ------------------------------------------------------------- into the KV cache

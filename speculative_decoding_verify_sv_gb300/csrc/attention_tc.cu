@@ -24,8 +24,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
+}  // namespace
+
 // 3-D bf16 view (D, heads, rows) with a (64, box1, box2) box, 128-byte swizzle.
-bool map3d(CUtensorMap *m, const void *base, int D, int heads, long long rows, int box1,
+bool tma_heads_map(CUtensorMap *m, const void *base, int D, int heads, long long rows, int box1,
            int box2) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
   if (!enc) return false;
@@ -43,7 +45,7 @@ bool map3d(CUtensorMap *m, const void *base, int D, int heads, long long rows, i
 // groups of 8 rows, heads) with a (64, 8, 2, page_rows / 8, 1) box, 128-byte swizzle: one
 // copy brings both 64-column halves of a page, as page_rows / 8 groups of 2 KB (the grouped
 // tile layout).  D = 128 only.  rows must be a multiple of 8.
-bool map5d_pages(CUtensorMap *m, const void *base, int heads, long long rows, int page_rows) {
+bool tma_pages_map(CUtensorMap *m, const void *base, int heads, long long rows, int page_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
   if (!enc || rows % 8 != 0 || page_rows % 8 != 0 || page_rows / 8 > 256) return false;
   const cuuint64_t row_bytes = (cuuint64_t)128 * 2 * heads;  // one position, all heads
@@ -56,8 +58,6 @@ bool map5d_pages(CUtensorMap *m, const void *base, int heads, long long rows, in
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
-
-}  // namespace
 
 // 4-D bf16 view (64 columns, rows, column blocks, heads) with a (64, box_rows, D / 64, 1) box,
 // 128-byte swizzle: one copy brings box_rows rows of a head, a 64-column block after the other.
@@ -116,33 +116,33 @@ cudaError_t launch_attention_tc(const AttnParams &a, const TcPlan &pl, void *ws,
   const int BN = pl.BN;
   const bool win = a.window > 0;
   const int tree_box = win ? SV_MAX_TREE_NODES : BN;  // rows of a tree tile's box
-  if (!map3d(&p.tm_q, a.q, a.D, a.Hq, (long long)a.B * a.N, G, rows_q / G) ||
-      !map3d(&p.tm_kt, a.k_tree, a.D, a.Hkv, (long long)a.B * a.N, 1, tree_box) ||
-      !map3d(&p.tm_vt, a.v_tree, a.D, a.Hkv, (long long)a.B * a.N, 1, tree_box))
+  if (!tma_heads_map(&p.tm_q, a.q, a.D, a.Hq, (long long)a.B * a.N, G, rows_q / G) ||
+      !tma_heads_map(&p.tm_kt, a.k_tree, a.D, a.Hkv, (long long)a.B * a.N, 1, tree_box) ||
+      !tma_heads_map(&p.tm_vt, a.v_tree, a.D, a.Hkv, (long long)a.B * a.N, 1, tree_box))
     return cudaErrorInvalidValue;
   if (a.block_table == nullptr) {
     const long long rows = (long long)a.B * (a.Lmax > 0 ? a.Lmax : 1);
-    if (!map3d(&p.tm_kc, a.cache_k, a.D, a.Hkv, rows, 1, BN) ||
-        !map3d(&p.tm_vc, a.cache_v, a.D, a.Hkv, rows, 1, BN))
+    if (!tma_heads_map(&p.tm_kc, a.cache_k, a.D, a.Hkv, rows, 1, BN) ||
+        !tma_heads_map(&p.tm_vc, a.cache_v, a.D, a.Hkv, rows, 1, BN))
       return cudaErrorInvalidValue;
     p.paged = 0;
     p.page_rows = BN;
   } else {
     p.page_rows = a.block_size < BN ? a.block_size : BN;
     const long long rows = (long long)a.num_blocks * a.block_size;
-    if (!map3d(&p.tm_kc, a.cache_k, a.D, a.Hkv, rows, 1, p.page_rows) ||
-        !map3d(&p.tm_vc, a.cache_v, a.D, a.Hkv, rows, 1, p.page_rows))
+    if (!tma_heads_map(&p.tm_kc, a.cache_k, a.D, a.Hkv, rows, 1, p.page_rows) ||
+        !tma_heads_map(&p.tm_vc, a.cache_v, a.D, a.Hkv, rows, 1, p.page_rows))
       return cudaErrorInvalidValue;
     p.paged = 1;
     // pages shorter than a tile: one copy per page (both column halves) instead of two,
     // into the grouped layout; the plain layout stays when the 5-D view is not available
     p.pg_grouped = a.D == 128 && p.page_rows < BN &&
-                   map5d_pages(&p.tm_kc5, a.cache_k, a.Hkv, rows, p.page_rows) &&
-                   map5d_pages(&p.tm_vc5, a.cache_v, a.Hkv, rows, p.page_rows);
+                   tma_pages_map(&p.tm_kc5, a.cache_k, a.Hkv, rows, p.page_rows) &&
+                   tma_pages_map(&p.tm_vc5, a.cache_v, a.Hkv, rows, p.page_rows);
   }
   if (win) {
     const long long rows = a.block_table ? (long long)a.num_blocks * a.block_size : (long long)a.B * (a.Lmax > 0 ? a.Lmax : 1);
-    if (!map3d(&p.tm_ks, a.cache_k, a.D, a.Hkv, rows, 1, 16) || !map3d(&p.tm_vs, a.cache_v, a.D, a.Hkv, rows, 1, 16))
+    if (!tma_heads_map(&p.tm_ks, a.cache_k, a.D, a.Hkv, rows, 1, 16) || !tma_heads_map(&p.tm_vs, a.cache_v, a.D, a.Hkv, rows, 1, 16))
       return cudaErrorInvalidValue;
     p.window = a.window;
     p.sinks = a.sinks;

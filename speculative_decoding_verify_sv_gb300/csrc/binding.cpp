@@ -14,6 +14,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstring>
 #include <optional>
 
@@ -211,71 +212,252 @@ void expect(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) refuse(PyExc_TypeError, "%zd arguments, expected %zd", n, want);
 }
 
-// (q, k_tree, v_tree, cache k, v, prefix_len, block_table, block_size, parent, scale, window, sinks,
-//  out, workspace, stream) -> out
-PyObject *window_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject * {
-    expect(n, 15);
-    const at::Tensor &q0 = cuda_tensor(a[0], "q");
-    const int dev = q0.get_device();
-    const sv_dtype dt = dtype_of(q0);
-    const at::ScalarType type = q0.scalar_type();
-    if (q0.dim() != 4) refuse(PyExc_ValueError, "q must be [B, N, Hq, D]");
-    const at::Tensor &q = tensor(a[0], "q", type, q0.sizes(), dev);
-    const int64_t B = q.size(0), N = q.size(1), Hq = q.size(2), D = q.size(3);
-    const at::Tensor &kt0 = cuda_tensor(a[1], "k_tree");
-    if (kt0.dim() != 4) refuse(PyExc_ValueError, "k_tree must be [B, N, Hkv, D]");
-    const int64_t Hkv = kt0.size(2);
-    const at::Tensor &kt = tensor(a[1], "k_tree", type, {B, N, Hkv, D}, dev);
-    const at::Tensor &vt = tensor(a[2], "v_tree", type, {B, N, Hkv, D}, dev);
-    const at::Tensor &k0 = cuda_tensor(a[3], "cache.k");
-    const bool paged = given(a[6]);
+// A cache (k, v, prefix_len, block_table, block_size) of B sequences with Hkv heads of D.
+struct Cache {
+  sv_kv_cache c{};
+  Cache(PyObject *const *a, at::ScalarType type, int64_t B, int64_t Hkv, int64_t D, int dev) {
+    const at::Tensor &k0 = cuda_tensor(a[0], "cache.k");
+    const bool paged = given(a[3]);
     if (k0.scalar_type() != type) refuse(PyExc_TypeError, "cache dtype differs from q");
     if (k0.dim() != 4 || k0.size(2) != Hkv || k0.size(3) != D || (!paged && k0.size(0) != B))
       refuse(PyExc_ValueError, "cache.k does not hold %lld heads of %lld%s", (long long)Hkv, (long long)D,
              paged ? " in pages" : " of q's sequences");
-    const at::Tensor &k = tensor(a[3], "cache.k", type, k0.sizes(), dev);
-    const at::Tensor &v = tensor(a[4], "cache.v", type, k0.sizes(), dev);
-    const at::Tensor &len = tensor(a[5], "cache.prefix_len", at::kInt, {B}, dev);
-    if (B > INT32_MAX || N > INT32_MAX || Hq > INT32_MAX || Hkv > INT32_MAX || k.size(0) > INT32_MAX || k.size(1) > INT32_MAX)
+    const at::Tensor &k = tensor(a[0], "cache.k", type, k0.sizes(), dev);
+    const at::Tensor &v = tensor(a[1], "cache.v", type, k0.sizes(), dev);
+    const at::Tensor &len = tensor(a[2], "cache.prefix_len", at::kInt, {B}, dev);
+    if (B > INT32_MAX || Hkv > INT32_MAX || k.size(0) > INT32_MAX || k.size(1) > INT32_MAX)
       refuse(PyExc_ValueError, "a size is not a 32-bit number");
-    sv_kv_cache c{};
     c.k = k.data_ptr();
     c.v = v.data_ptr();
     c.prefix_len = len.data_ptr<int32_t>();
     if (paged) {
-      const int block_size = number(a[7], "block_size");
-      const at::Tensor &bt = cuda_tensor(a[6], "cache.block_table");
+      const int block_size = number(a[4], "block_size");
+      const at::Tensor &bt = cuda_tensor(a[3], "cache.block_table");
       if (bt.dim() != 2 || k.size(1) != block_size || bt.size(1) > INT32_MAX)
         refuse(PyExc_ValueError, "blocks of %lld rows need block_size %lld and a block_table [B, max_blocks]",
                (long long)k.size(1), (long long)k.size(1));
-      c.block_table = tensor(a[6], "cache.block_table", at::kInt, {B, bt.size(1)}, dev).const_data_ptr<int32_t>();
+      c.block_table = tensor(a[3], "cache.block_table", at::kInt, {B, bt.size(1)}, dev).const_data_ptr<int32_t>();
       c.block_size = block_size;
       c.max_blocks = (int)bt.size(1);
       c.num_blocks = (int)k.size(0);
     } else {
       c.Lmax = (int)k.size(1);
     }
-    const float scale = real(a[9]);
+  }
+  int max_prefix() const {
+    const long long cap = c.block_table ? (long long)c.max_blocks * c.block_size : c.Lmax;
+    return (int)std::min<long long>(cap, INT32_MAX);
+  }
+};
+
+// The arguments that the attentions have in common: (q, k_tree, v_tree, cache k, v, prefix_len,
+// block_table, block_size, parent, scale, ...).
+struct Attention {
+  const at::Tensor &q0;
+  const int dev;
+  const sv_dtype dt;
+  const at::ScalarType type;
+  int64_t B, N, Hq, Hkv, D;
+  const at::Tensor *q, *kt, *vt;
+  std::optional<Cache> cache;
+  float scale;
+  std::optional<Tree> tree;
+  explicit Attention(PyObject *const *a)
+      : q0(cuda_tensor(a[0], "q")), dev(q0.get_device()), dt(dtype_of(q0)), type(q0.scalar_type()) {
+    if (q0.dim() != 4) refuse(PyExc_ValueError, "q must be [B, N, Hq, D]");
+    q = &tensor(a[0], "q", type, q0.sizes(), dev);
+    B = q->size(0), N = q->size(1), Hq = q->size(2), D = q->size(3);
+    const at::Tensor &kt0 = cuda_tensor(a[1], "k_tree");
+    if (kt0.dim() != 4) refuse(PyExc_ValueError, "k_tree must be [B, N, Hkv, D]");
+    Hkv = kt0.size(2);
+    kt = &tensor(a[1], "k_tree", type, {B, N, Hkv, D}, dev);
+    vt = &tensor(a[2], "v_tree", type, {B, N, Hkv, D}, dev);
+    cache.emplace(a + 3, type, B, Hkv, D, dev);
+    if (N > INT32_MAX || Hq > INT32_MAX) refuse(PyExc_ValueError, "a size is not a 32-bit number");
+    scale = real(a[9]);
+    tree.emplace(a[8], B, N, dev);
+  }
+  at::Tensor output(PyObject *o) const { return given(o) ? tensor(o, "out", type, q->sizes(), dev) : make(q->sizes(), *q, type); }
+};
+
+// (q, k_tree, v_tree, cache k, v, prefix_len, block_table, block_size, parent, scale, window, sinks,
+//  out, workspace, stream) -> out
+PyObject *window_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    expect(n, 15);
+    const Attention t(a);
     const int window = number(a[10], "window"), sinks = number(a[11], "sinks");
-    const Tree tree(a[8], B, N, dev);
-    const Stream stream(a[14], dev);
-    at::Tensor out = given(a[12]) ? tensor(a[12], "out", type, q.sizes(), dev) : make(q.sizes(), q, type);
+    const Stream stream(a[14], t.dev);
+    at::Tensor out = t.output(a[12]);
     // (a workspace passed in must have been zero-filled before its first use; the library checks
     // its size)
     at::Tensor ws;
     if (given(a[13])) {
-      ws = tensor(a[13], "workspace", cuda_tensor(a[13], "workspace").scalar_type(), dev);
+      ws = tensor(a[13], "workspace", cuda_tensor(a[13], "workspace").scalar_type(), t.dev);
     } else {
-      const long long cap = paged ? (long long)c.max_blocks * c.block_size : c.Lmax;
-      const size_t need = sv_window_attention_workspace_size(dt, (int)B, (int)N, (int)Hq, (int)Hkv, (int)D,
-                                                             (int)std::min<long long>(cap, INT32_MAX), window);
-      if (need) ws = at::zeros({(int64_t)need}, q.options().dtype(at::kByte));
+      const size_t need = sv_window_attention_workspace_size(t.dt, (int)t.B, (int)t.N, (int)t.Hq, (int)t.Hkv, (int)t.D,
+                                                             t.cache->max_prefix(), window);
+      if (need) ws = at::zeros({(int64_t)need}, t.q->options().dtype(at::kByte));
     }
     check([&] {
-      return sv_window_attention(dt, (int)B, (int)N, (int)Hq, (int)Hkv, (int)D, q.data_ptr(), kt.data_ptr(), vt.data_ptr(), c,
-                                 tree.ptr, tree.stride, scale, window, sinks, out.data_ptr(),
+      return sv_window_attention(t.dt, (int)t.B, (int)t.N, (int)t.Hq, (int)t.Hkv, (int)t.D, t.q->data_ptr(), t.kt->data_ptr(),
+                                 t.vt->data_ptr(), t.cache->c, t.tree->ptr, t.tree->stride, t.scale, window, sinks,
+                                 out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream);
+    });
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// The workspace given, or a new one of the size that need() says.
+template <typename Need>
+at::Tensor workspace_of(PyObject *o, const at::Tensor &like, int dev, Need &&need) {
+  if (given(o)) return tensor(o, "workspace", cuda_tensor(o, "workspace").scalar_type(), dev);
+  const size_t bytes = need();
+  return bytes ? make({(int64_t)bytes}, like, at::kByte) : at::Tensor();
+}
+
+// (q, k_tree, v_tree, cache k, v, prefix_len, block_table, block_size, parent, scale, group_start, shared_len,
+//  out, workspace, stream) -> out
+PyObject *shared_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    expect(n, 15);
+    const Attention t(a);
+    const at::Tensor &len = cuda_tensor(a[11], "shared_len");
+    if (len.dim() != 1 || len.size(0) < 1 || len.size(0) > SV_MAX_SHARED_GROUPS)
+      refuse(PyExc_ValueError, "shared_len must be [groups], 1 to %d of them", SV_MAX_SHARED_GROUPS);
+    const int groups = (int)len.size(0);
+    const int32_t *lens = tensor(a[11], "shared_len", at::kInt, {groups}, t.dev).const_data_ptr<int32_t>();
+    const int32_t *starts = tensor(a[10], "group_start", at::kInt, {groups + 1}, t.dev).const_data_ptr<int32_t>();
+    const Stream stream(a[14], t.dev);
+    at::Tensor out = t.output(a[12]);
+    const at::Tensor ws = workspace_of(a[13], *t.q, t.dev, [&] {
+      return sv_shared_attention_workspace_size(t.dt, (int)t.B, (int)t.N, (int)t.Hq, (int)t.Hkv, (int)t.D, t.cache->max_prefix(), groups);
+    });
+    check([&] {
+      return sv_shared_attention(t.dt, (int)t.B, (int)t.N, (int)t.Hq, (int)t.Hkv, (int)t.D, t.q->data_ptr(), t.kt->data_ptr(),
+                                 t.vt->data_ptr(), t.cache->c, t.tree->ptr, t.tree->stride, t.scale, starts, lens, groups,
+                                 out.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream);
+    });
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// (q, k_tree, v_tree, cache k, v, prefix_len, block_table, block_size, parent, scale, pages, out, workspace,
+//  stream) -> out
+PyObject *sparse_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    expect(n, 14);
+    const Attention t(a);
+    const at::Tensor &p0 = cuda_tensor(a[10], "pages");
+    if (p0.dim() != 4 || p0.size(3) > INT32_MAX || (p0.size(1) != 1 && p0.size(1) != t.N))
+      refuse(PyExc_ValueError, "pages must be [B, 1 or N, Hkv, K]");
+    const int64_t sets = p0.size(1), K = p0.size(3);
+    const at::Tensor &pages = tensor(a[10], "pages", at::kInt, {t.B, sets, t.Hkv, K}, t.dev);
+    const int page_size = number(a[7], "block_size");
+    const Stream stream(a[13], t.dev);
+    at::Tensor out = t.output(a[11]);
+    const at::Tensor ws = workspace_of(a[12], *t.q, t.dev, [&] {
+      return sv_sparse_attention_workspace_size(t.dt, (int)t.B, (int)t.N, (int)t.Hq, (int)t.Hkv, (int)t.D, page_size, (int)K, (int)sets);
+    });
+    check([&] {
+      return sv_sparse_attention(t.dt, (int)t.B, (int)t.N, (int)t.Hq, (int)t.Hkv, (int)t.D, t.q->data_ptr(), t.kt->data_ptr(),
+                                 t.vt->data_ptr(), t.cache->c, t.tree->ptr, t.tree->stride, t.scale,
+                                 pages.const_data_ptr<int32_t>(), (int)sets, (int)K, page_size, out.data_ptr(),
                                  ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream);
+    });
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// (cache k, v, prefix_len, block_table, block_size, bounds, start, stream) -> bounds
+PyObject *page_bounds(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    expect(n, 8);
+    const at::Tensor &k = cuda_tensor(a[0], "cache.k"), &len = cuda_tensor(a[2], "cache.prefix_len");
+    const int dev = k.get_device();
+    const sv_dtype dt = dtype_of(k);
+    if (k.dim() != 4 || len.dim() != 1) refuse(PyExc_ValueError, "cache.k must be [.., .., Hkv, D] and cache.prefix_len [B]");
+    const int64_t B = len.size(0), Hkv = k.size(2), D = k.size(3);
+    const Cache cache(a, k.scalar_type(), B, Hkv, D, dev);
+    const int page_size = number(a[4], "block_size");
+    if (page_size < 1) refuse(PyExc_ValueError, "block_size = %d", page_size);
+    const int64_t seq_pages = (cache.c.Lmax + (int64_t)page_size - 1) / page_size;
+    const int32_t *start = given(a[6]) ? tensor(a[6], "start", at::kInt, {B}, dev).const_data_ptr<int32_t>() : nullptr;
+    const Stream stream(a[7], dev);
+    const bool paged = cache.c.block_table != nullptr;
+    at::Tensor bounds;
+    if (given(a[5])) {
+      bounds = paged ? tensor(a[5], "bounds", k.scalar_type(), {k.size(0), Hkv, 2, D}, dev)
+                     : tensor(a[5], "bounds", k.scalar_type(), {B, seq_pages, Hkv, 2, D}, dev);
+    } else {  // (rows of pages that hold nothing yet are not written)
+      bounds = paged ? make({k.size(0), Hkv, 2, D}, k, k.scalar_type()) : make({B, seq_pages, Hkv, 2, D}, k, k.scalar_type());
+    }
+    check([&] { return sv_page_bounds(dt, (int)B, (int)Hkv, (int)D, page_size, cache.c, start, bounds.data_ptr(), stream); });
+    return THPVariable_Wrap(std::move(bounds));
+  });
+}
+
+// (q, bounds, prefix_len, page_size, block_table, per_node, out, stream) -> out
+PyObject *page_scores(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    expect(n, 8);
+    const at::Tensor &q0 = cuda_tensor(a[0], "q"), &b0 = cuda_tensor(a[1], "bounds");
+    const int dev = q0.get_device();
+    const sv_dtype dt = dtype_of(q0);
+    if (q0.dim() != 4) refuse(PyExc_ValueError, "q must be [B, N, Hq, D]");
+    const at::Tensor &q = tensor(a[0], "q", q0.scalar_type(), q0.sizes(), dev);
+    const int64_t B = q.size(0), N = q.size(1), Hq = q.size(2), D = q.size(3);
+    const bool paged = given(a[4]);
+    if (b0.dim() != (paged ? 4 : 5)) refuse(PyExc_ValueError, "bounds must be %s", paged ? "[num_blocks, Hkv, 2, D]" : "[B, P, Hkv, 2, D]");
+    const int64_t Hkv = b0.size(-3);
+    int64_t P, blocks = 0;
+    const int32_t *table = nullptr;
+    const at::Tensor *bounds;
+    if (paged) {
+      const at::Tensor &bt = cuda_tensor(a[4], "block_table");
+      if (bt.dim() != 2) refuse(PyExc_ValueError, "block_table must be [B, max_blocks]");
+      P = bt.size(1), blocks = b0.size(0);
+      table = tensor(a[4], "block_table", at::kInt, {B, P}, dev).const_data_ptr<int32_t>();
+      bounds = &tensor(a[1], "bounds", q.scalar_type(), {blocks, Hkv, 2, D}, dev);
+    } else {
+      P = b0.size(1);
+      bounds = &tensor(a[1], "bounds", q.scalar_type(), {B, P, Hkv, 2, D}, dev);
+    }
+    const int32_t *len = tensor(a[2], "prefix_len", at::kInt, {B}, dev).const_data_ptr<int32_t>();
+    if (B > INT32_MAX || N > INT32_MAX || Hq > INT32_MAX || Hkv > INT32_MAX || P > INT32_MAX || blocks > INT32_MAX)
+      refuse(PyExc_ValueError, "a size is not a 32-bit number");
+    const int page_size = number(a[3], "page_size"), per_node = PyObject_IsTrue(a[5]);
+    if (per_node < 0) throw Refused();
+    const int64_t sets = per_node ? N : 1;
+    const Stream stream(a[7], dev);
+    at::Tensor out = given(a[6]) ? tensor(a[6], "out", at::kFloat, {B, sets, Hkv, P}, dev) : make({B, sets, Hkv, P}, q, at::kFloat);
+    check([&] {
+      return sv_page_scores(dt, (int)B, (int)N, (int)Hq, (int)Hkv, (int)D, q.data_ptr(), bounds->data_ptr(), len, page_size, (int)P,
+                            table, (int)blocks, (int)sets, out.data_ptr<float>(), stream);
+    });
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// (scores, prefix_len, page_size, count, first, last, out, stream) -> out
+PyObject *select_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    expect(n, 8);
+    const at::Tensor &s0 = cuda_tensor(a[0], "scores");
+    const int dev = s0.get_device();
+    if (s0.dim() != 4) refuse(PyExc_ValueError, "scores must be [B, sets, Hkv, P]");
+    const at::Tensor &scores = tensor(a[0], "scores", at::kFloat, s0.sizes(), dev);
+    const int64_t B = scores.size(0), sets = scores.size(1), Hkv = scores.size(2), P = scores.size(3);
+    if (B > INT32_MAX || sets > INT32_MAX || Hkv > INT32_MAX || sets * Hkv > INT32_MAX || P > INT32_MAX)
+      refuse(PyExc_ValueError, "a size is not a 32-bit number");
+    const int32_t *len = tensor(a[1], "prefix_len", at::kInt, {B}, dev).const_data_ptr<int32_t>();
+    const int page_size = number(a[2], "page_size"), K = number(a[3], "count"), first = number(a[4], "first"), last = number(a[5], "last");
+    if (K < 0) refuse(PyExc_ValueError, "count = %d", K);
+    const Stream stream(a[7], dev);
+    at::Tensor out = given(a[6]) ? tensor(a[6], "out", at::kInt, {B, sets, Hkv, K}, dev) : make({B, sets, Hkv, K}, scores, at::kInt);
+    check([&] {
+      return sv_select_pages((int)B, (int)(sets * Hkv), (int)P, scores.const_data_ptr<float>(), len, page_size, K, first, last,
+                             out.data_ptr<int32_t>(), stream);
     });
     return THPVariable_Wrap(std::move(out));
   });
@@ -498,6 +680,11 @@ PyObject *set_error(PyObject *, PyObject *type) {
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef methods[] = {{"window_attention", FAST(window_attention), METH_FASTCALL, nullptr},
+                         {"shared_attention", FAST(shared_attention), METH_FASTCALL, nullptr},
+                         {"sparse_attention", FAST(sparse_attention), METH_FASTCALL, nullptr},
+                         {"page_bounds", FAST(page_bounds), METH_FASTCALL, nullptr},
+                         {"page_scores", FAST(page_scores), METH_FASTCALL, nullptr},
+                         {"select_pages", FAST(select_pages), METH_FASTCALL, nullptr},
                          {"block_tables", FAST(block_tables), METH_FASTCALL, nullptr},
                          {"qk_norm_rope", FAST(qk_norm_rope), METH_FASTCALL, nullptr},
                          {"tree_qk_norm_rope", FAST(tree_qk_norm_rope), METH_FASTCALL, nullptr},

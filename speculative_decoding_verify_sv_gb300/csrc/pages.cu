@@ -1,0 +1,482 @@
+// Pages that a query looks at (sm_103a): bounds of the pages' keys, scores of the pages against queries, and
+// the selection of the best ones, for sv_sparse_attention.
+//
+// Bounds: for a page (16 or more keys of a KV head) the least and the largest value of each of its D
+// channels.  Of any key k of the page, q . k <= sum_d max(q_d lo_d, q_d hi_d) =
+//   sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d,
+// so that a page whose score is low holds no key that matters to q, and the score is two products of
+// matrices.  Read once, K is what bounds the first; the bounds (1/8 of K and less) the second.
+#include <algorithm>
+#include <atomic>
+#include <cfloat>
+#include <climits>
+
+#include "sv_common.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+
+namespace {
+
+// ---------------------------------------------------------------------- bounds
+
+constexpr int kBoundThreads = 128;
+constexpr int kBoundRows = 16;  // rows on their way at a time
+
+// Two elements' least and largest; a NaN is kept.
+__device__ __forceinline__ uint32_t min_bf16x2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+template <bool F32>
+__device__ __forceinline__ uint32_t low_of(uint32_t a, uint32_t b) {
+  if constexpr (F32) return __float_as_uint(min_nan(__uint_as_float(a), __uint_as_float(b)));
+  else return min_bf16x2_nan(a, b);
+}
+template <bool F32>
+__device__ __forceinline__ uint32_t high_of(uint32_t a, uint32_t b) {
+  if constexpr (F32) return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  else return max_bf16x2_nan(a, b);
+}
+
+// A thread per 16 bytes of a page's rows: consecutive threads read consecutive pieces of a row, and each
+// has the page's rows, 16 at a time, on their way together.
+template <bool F32>
+__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundParams p) {
+  wait_previous();
+  const int b = blockIdx.y;
+  int L = p.prefix_len[b];
+  if (L < 0 || L > p.cap) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
+    L = L < 0 ? 0 : p.cap;
+  }
+  const int start = p.start ? max(p.start[b], 0) : 0;
+  if (start >= L) return;
+  const int first = start / p.page_size, pages = (L + p.page_size - 1) / p.page_size - first;
+  const long long items = (long long)pages * p.vecs;
+  for (long long i = (long long)blockIdx.x * kBoundThreads + threadIdx.x; i < items; i += (long long)gridDim.x * kBoundThreads) {
+    const int page = first + (int)(i / p.vecs), v = (int)(i % p.vecs);
+    const int rows = min(p.page_size, L - page * p.page_size);
+    long long row, out;
+    if (p.block_table) {
+      const int blk = p.block_table[(size_t)b * p.max_blocks + page];
+      if (blk < 0 || blk >= p.num_blocks) {
+        if (v == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
+        continue;
+      }
+      row = (long long)blk * p.page_size;
+      out = blk;
+    } else {
+      row = (long long)b * p.Lmax + (long long)page * p.page_size;
+      out = (long long)b * p.seq_pages + page;
+    }
+    const uint4 *src = static_cast<const uint4 *>(p.k) + (size_t)row * p.vecs + v;
+    uint4 lo, hi;
+    for (int r0 = 0; r0 < rows; r0 += kBoundRows) {
+      uint4 x[kBoundRows];
+      // (rows past the last one are the last one again)
+#pragma unroll
+      for (int r = 0; r < kBoundRows; ++r) x[r] = load_streamed(src + (size_t)min(r0 + r, rows - 1) * p.vecs);
+      if (r0 == 0) lo = hi = x[0];
+#pragma unroll
+      for (int r = 0; r < kBoundRows; ++r) {
+        lo = make_uint4(low_of<F32>(lo.x, x[r].x), low_of<F32>(lo.y, x[r].y), low_of<F32>(lo.z, x[r].z), low_of<F32>(lo.w, x[r].w));
+        hi = make_uint4(high_of<F32>(hi.x, x[r].x), high_of<F32>(hi.y, x[r].y), high_of<F32>(hi.z, x[r].z), high_of<F32>(hi.w, x[r].w));
+      }
+    }
+    // head h: D least values, then D largest
+    const int per = p.head_vecs, h = v / per, d = v % per;
+    uint4 *dst = static_cast<uint4 *>(p.bounds) + ((size_t)out * p.vecs + (size_t)h * per) * 2 + d;
+    dst[0] = lo;
+    dst[per] = hi;
+  }
+}
+
+// ---------------------------------------------------------------------- scores
+
+constexpr int kScorePages = 16;  // pages of a warp's tile
+constexpr int kScoreCols = 256;  // query rows in shared memory at a time
+
+// The columns of a product are query rows: those of a set one after another, padded (with the set's last
+// row again, which changes no maximum) so that no step of 8 columns holds parts of two sets, or else a
+// whole number of sets.
+__host__ __device__ inline int score_set_cols(int rows) {
+  if (rows >= 8) return (rows + 7) & ~7;
+  return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
+}
+
+// bf16 on mma.sync: the pages are the 16-row side, query rows the 8-column side.  A product's columns may
+// be summed in any order: lane t of a quad takes 16 neighbouring channels of each 64 of a page (32 bytes,
+// straight from memory to operand registers) and of a query row.
+template <int D>
+__global__ void __launch_bounds__(256) page_scores_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int KB = D / 64, STRIDE = D * 2 + 16;  // (16 more bytes: conflict-free 16-byte reads of 8 rows)
+  extern __shared__ __align__(16) uint8_t score_smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int fg = lane >> 2, ft = lane & 3;
+  const int bh = blockIdx.x / p.splits, part = blockIdx.x % p.splits, h = bh % p.Hkv, b = bh / p.Hkv;
+  wait_previous();
+  int L = p.prefix_len[b];
+  const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
+  if (L < 0 || L > most) {
+    if (h == 0 && part == 0 && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
+    L = L < 0 ? 0 : most;
+  }
+  const int pages = (int)(((long long)L + p.page_size - 1) / p.page_size);
+  const int tiles = (p.P + kScorePages - 1) / kScorePages, per = (tiles + p.splits - 1) / p.splits;
+  const int t0 = part * per, t1 = min(tiles, t0 + per);
+  const int rows = p.set_nodes * p.G, cols = p.sets * p.set_cols;  // rows of a set, columns of all sets
+  float *out = p.out + (size_t)b * p.sets * p.Hkv * p.P + (size_t)h * p.P;  // [sets][.][P]
+  for (int c0 = 0; c0 < cols; c0 += kScoreCols) {
+    const int n = min(kScoreCols, cols - c0), n8 = (n + 7) & ~7;
+    if (c0 > 0) __syncthreads();
+    for (int u = tid; u < n8 * (D / 8); u += blockDim.x) {
+      const int c = u / (D / 8), d = u % (D / 8), col = min(c0 + c, cols - 1);
+      const int set = col / p.set_cols, r = min(col % p.set_cols, rows - 1), node = set * p.set_nodes + r / p.G;
+      const size_t row = ((size_t)b * p.N + node) * p.Hq + h * p.G + r % p.G;
+      cp_async_16(score_smem + c * STRIDE + 16 * d, static_cast<const bf16 *>(p.q) + row * D + 8 * d, true);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    for (int t = t0 + warp; t < t1; t += warps) {
+      const int page = t * kScorePages + fg;
+      // this lane's channels of pages `page` and page + 8: least and largest values
+      uint32_t a[2][2][KB][8];
+      bool there[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = page + 8 * i;
+        long long row = -1;
+        if (at < pages) {
+          if (!p.block_table) {
+            row = (long long)b * p.P + at;
+          } else {
+            const int blk = p.block_table[(size_t)b * p.P + at];
+            if (blk >= 0 && blk < p.num_blocks) row = blk;
+            else if (h == 0 && c0 == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
+          }
+        }
+        there[i] = row >= 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(p.bounds) + ((size_t)max(row, 0ll) * p.Hkv + h) * 2 * D) + 2 * ft;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 v = there[i] ? src[s * (D / 8) + 8 * k + e] : make_uint4(0, 0, 0, 0);
+              a[i][s][k][4 * e] = v.x;
+              a[i][s][k][4 * e + 1] = v.y;
+              a[i][s][k][4 * e + 2] = v.z;
+              a[i][s][k][4 * e + 3] = v.w;
+            }
+      }
+      float best[2] = {-INFINITY, -INFINITY};
+      for (int j = 0; j < n8 / 8; ++j) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint4 *q = reinterpret_cast<const uint4 *>(score_smem + (8 * j + fg) * STRIDE) + 2 * ft;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 v = q[8 * k + e];
+            w[4 * e] = v.x;
+            w[4 * e + 1] = v.y;
+            w[4 * e + 2] = v.z;
+            w[4 * e + 3] = v.w;
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t lo[4] = {a[0][0][k][2 * s], a[1][0][k][2 * s], a[0][0][k][2 * s + 1], a[1][0][k][2 * s + 1]};
+            const uint32_t hi[4] = {a[0][1][k][2 * s], a[1][1][k][2 * s], a[0][1][k][2 * s + 1], a[1][1][k][2 * s + 1]};
+            mma_bf16_16816(acc, hi, max_bf16x2_nan(w[2 * s], 0u), max_bf16x2_nan(w[2 * s + 1], 0u));
+            mma_bf16_16816(acc, lo, min_bf16x2_nan(w[2 * s], 0u), min_bf16x2_nan(w[2 * s + 1], 0u));
+          }
+        }
+        // acc: columns 2 ft, 2 ft + 1 of pages fg and fg + 8
+        const int col = c0 + 8 * j;
+        auto put = [&](int set, float x, float y) {
+          if (set >= p.sets) return;
+          float *to = out + (size_t)set * p.Hkv * p.P;
+          if (page < p.P) to[page] = there[0] ? x : -INFINITY;
+          if (page + 8 < p.P) to[page + 8] = there[1] ? y : -INFINITY;
+        };
+        if (p.set_cols == 1) {
+          put(col + 2 * ft, acc[0], acc[2]);
+          put(col + 2 * ft + 1, acc[1], acc[3]);
+          continue;
+        }
+        float x = max_nan(acc[0], acc[1]), y = max_nan(acc[2], acc[3]);
+        if (p.set_cols == 2) {
+          put(col / 2 + ft, x, y);
+          continue;
+        }
+        x = max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+        y = max_nan(y, __shfl_xor_sync(0xFFFFFFFFu, y, 1));
+        if (p.set_cols == 4) {
+          if ((ft & 1) == 0) put(col / 4 + ft / 2, x, y);
+          continue;
+        }
+        x = max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+        y = max_nan(y, __shfl_xor_sync(0xFFFFFFFFu, y, 2));
+        best[0] = max_nan(best[0], x);
+        best[1] = max_nan(best[1], y);
+        const int set = col / p.set_cols;
+        const bool last = (col + 8) % p.set_cols == 0;
+        if (last || j + 1 == n8 / 8) {
+          if (ft == 0) {
+            // a set whose rows came in parts: the best so far is in memory
+            float *to = out + (size_t)set * p.Hkv * p.P;
+            if (set * p.set_cols < c0) {
+              if (page < p.P) best[0] = max_nan(best[0], to[page]);
+              if (page + 8 < p.P) best[1] = max_nan(best[1], to[page + 8]);
+            }
+            put(set, best[0], best[1]);
+          }
+          best[0] = best[1] = -INFINITY;
+        }
+      }
+    }
+  }
+}
+
+// fp32: a warp per page, lanes over the channels.
+template <int D>
+__global__ void __launch_bounds__(256) page_scores_f32_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int PL = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bh = blockIdx.x / p.splits, part = blockIdx.x % p.splits, h = bh % p.Hkv, b = bh / p.Hkv;
+  wait_previous();
+  int L = p.prefix_len[b];
+  const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
+  if (L < 0 || L > most) {
+    if (h == 0 && part == 0 && threadIdx.x == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
+    L = L < 0 ? 0 : most;
+  }
+  const int pages = (int)(((long long)L + p.page_size - 1) / p.page_size);
+  float *out = p.out + (size_t)b * p.sets * p.Hkv * p.P + (size_t)h * p.P;
+  for (int page = part * 8 + warp; page < p.P; page += p.splits * 8) {
+    long long row = -1;
+    if (page < pages) {
+      if (!p.block_table) {
+        row = (long long)b * p.P + page;
+      } else {
+        const int blk = p.block_table[(size_t)b * p.P + page];
+        if (blk >= 0 && blk < p.num_blocks) row = blk;
+        else if (h == 0 && lane == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
+      }
+    }
+    float lo[PL], hi[PL];
+    const float *src = static_cast<const float *>(p.bounds) + ((size_t)max(row, 0ll) * p.Hkv + h) * 2 * D + lane;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      lo[i] = row >= 0 ? src[32 * i] : 0.f;
+      hi[i] = row >= 0 ? src[D + 32 * i] : 0.f;
+    }
+    for (int set = 0; set < p.sets; ++set) {
+      float best = -INFINITY;
+      for (int r = 0; r < p.set_nodes * p.G && row >= 0; ++r) {
+        const float *q = static_cast<const float *>(p.q) + (((size_t)b * p.N + set * p.set_nodes + r / p.G) * p.Hq + h * p.G + r % p.G) * D + lane;
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          const float y = q[32 * i];
+          x = fmaf(max_nan(y, 0.f), hi[i], x);
+          x = fmaf(min_nan(y, 0.f), lo[i], x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        best = max_nan(best, x);
+      }
+      if (lane == 0) out[(size_t)set * p.Hkv * p.P + page] = best;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- selection
+
+// Order-preserving key of a score: larger for larger scores, the largest for a NaN; the two zeros are one.
+__device__ __forceinline__ uint32_t score_key(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// A CTA per list.  The threshold is found by digits of 8 bits of the keys, from the highest bit in which
+// they differ at all; what is above it and, of those equal to it, the first ones go out in order.
+__global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ uint32_t sel_smem[];
+  uint32_t *keys = sel_smem;                      // [P]
+  __shared__ uint32_t hist[256], red[2][32], s_prefix, s_need;
+  __shared__ int above[32], equal[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
+  const long long list = blockIdx.x;
+  const int b = (int)(list / p.lists);
+  wait_previous();
+  int L = p.prefix_len[b];
+  const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
+  if (L < 0 || L > most) {
+    if (list % p.lists == 0 && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
+    L = L < 0 ? 0 : most;
+  }
+  const int pages = (int)(((long long)L + p.page_size - 1) / p.page_size);
+  int32_t *out = p.out + list * p.K;
+  if (pages <= p.K) {
+    for (int i = tid; i < p.K; i += T) out[i] = i < pages ? i : -1;
+    return;
+  }
+  // pages [m0, m1) compete for `need` places
+  const int m0 = p.first, m1 = pages - p.last, need = p.K - p.first - p.last;
+  const float *x = p.scores + list * p.P;
+  uint32_t any = 0, all = 0xFFFFFFFFu;
+  for (int i = m0 + tid; i < m1; i += T) {
+    const uint32_t k = score_key(x[i]);
+    keys[i] = k;
+    any |= k;
+    all &= k;
+  }
+  any = __reduce_or_sync(0xFFFFFFFFu, any);
+  all = __reduce_and_sync(0xFFFFFFFFu, all);
+  if (lane == 0) red[0][warp] = any, red[1][warp] = all;
+  __syncthreads();
+  any = lane < warps ? red[0][lane] : 0;
+  all = lane < warps ? red[1][lane] : 0xFFFFFFFFu;
+  any = __reduce_or_sync(0xFFFFFFFFu, any);
+  all = __reduce_and_sync(0xFFFFFFFFu, all);
+  int high = 32 - __clz((int)(any ^ all));  // bits below which the keys differ
+  uint32_t prefix = high >= 32 ? 0 : (all >> high) << high;
+  int left = need;  // places for keys that begin with the prefix
+  while (high > 0 && left > 0) {
+    const int low = max(0, high - 8), bins = 1 << (high - low);
+    for (int i = tid; i < bins; i += T) hist[i] = 0;
+    __syncthreads();
+    const uint32_t mask = high >= 32 ? 0 : ~0u << high;
+    for (int i = m0 + tid; i < m1; i += T) {
+      const uint32_t k = keys[i];
+      if (((k ^ prefix) & mask) == 0) atomicAdd(&hist[(k >> low) & (bins - 1)], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // bins from the top: the one in which the last place falls
+      uint32_t n[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int bin = bins - 1 - (8 * lane + e);
+        n[e] = bin >= 0 ? hist[bin] : 0;
+        sum += n[e];
+      }
+      uint32_t before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= sum;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (before < (uint32_t)left && before + n[e] >= (uint32_t)left) {
+          s_prefix = prefix | (uint32_t)(bins - 1 - (8 * lane + e)) << low;
+          s_need = left - before;
+        }
+        before += n[e];
+      }
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = (int)s_need;
+    high = low;
+  }
+  // keys above `prefix`, and the first `left` of those equal to it
+  int base = 0, ties = 0;  // what earlier rounds have put out; ties among the earlier ones
+  for (int i0 = 0; i0 < pages; i0 += T) {
+    const int i = i0 + tid;
+    bool over = false, tie = false;
+    if (i < pages) {
+      if (i < m0 || i >= m1) {
+        over = true;
+      } else if (need > 0) {
+        const uint32_t k = keys[i];
+        over = k > prefix;
+        tie = k == prefix;
+      }
+    }
+    const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bt = __ballot_sync(0xFFFFFFFFu, tie);
+    if (lane == 0) above[warp] = __popc(bo), equal[warp] = __popc(bt);
+    __syncthreads();
+    int o = lane < warps ? above[lane] : 0, e = lane < warps ? equal[lane] : 0;
+    const int o_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? o : 0), e_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? e : 0);
+    o = __reduce_add_sync(0xFFFFFFFFu, o);
+    e = __reduce_add_sync(0xFFFFFFFFu, e);
+    const unsigned lt = (1u << lane) - 1;
+    const int my_over = base + o_before + __popc(bo & lt), my_ties = ties + e_before + __popc(bt & lt);
+    if (over || (tie && my_ties < left)) out[my_over + min(my_ties, left)] = i;
+    base += o;
+    ties += e;
+    __syncthreads();
+  }
+}
+
+cudaError_t allow_smem(const void *kern, size_t smem) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+}  // namespace
+
+cudaError_t launch_page_bounds(sv_dtype dt, BoundParams p, int B, int num_sms, cudaStream_t s) {
+  // enough CTAs for any split of the pages over the sequences; those without a page leave at once
+  const long long most = ((long long)p.cap + p.page_size - 1) / p.page_size * p.vecs;
+  const long long per = std::max(1ll, std::min((most + kBoundThreads - 1) / kBoundThreads, (16ll * num_sms + B - 1) / B));
+  const dim3 grid((unsigned)per, (unsigned)B);
+  return dt == SV_F32 ? launch_close(page_bounds_kernel<true>, grid, kBoundThreads, 0, s, p)
+                      : launch_close(page_bounds_kernel<false>, grid, kBoundThreads, 0, s, p);
+}
+
+cudaError_t launch_page_scores(sv_dtype dt, int D, ScoreParams p, int B, int num_sms, cudaStream_t s) {
+  const int units = B * p.Hkv, tiles = (p.P + kScorePages - 1) / kScorePages;
+  p.set_cols = score_set_cols(p.set_nodes * p.G);
+  if (dt == SV_F32) {
+    p.splits = std::max(1, std::min((p.P + 7) / 8, (8 * num_sms + units - 1) / units));
+    return D == 128 ? launch_close(page_scores_f32_kernel<128>, dim3((unsigned)units * p.splits), 256, 0, s, p)
+                    : launch_close(page_scores_f32_kernel<64>, dim3((unsigned)units * p.splits), 256, 0, s, p);
+  }
+  p.splits = std::max(1, std::min((tiles + 7) / 8, (4 * num_sms + units - 1) / units));
+  const int cols = (int)std::min<long long>(kScoreCols, ((long long)p.sets * p.set_cols + 7) / 8 * 8);
+  const size_t smem = (size_t)cols * (D * 2 + 16);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = D == 128 ? allow_smem((const void *)page_scores_kernel<128>, kScoreCols * (128 * 2 + 16))
+                                   : allow_smem((const void *)page_scores_kernel<64>, kScoreCols * (64 * 2 + 16));
+    if (e != cudaSuccess) return e;
+  }
+  return D == 128 ? launch_close(page_scores_kernel<128>, dim3((unsigned)units * p.splits), 256, smem, s, p)
+                  : launch_close(page_scores_kernel<64>, dim3((unsigned)units * p.splits), 256, smem, s, p);
+}
+
+cudaError_t launch_select_pages(const SelectParams &p, long long lists, int num_sms, cudaStream_t s) {
+  const size_t smem = (size_t)p.P * 4;
+  if (smem > 44 * 1024) {  // (with the kernel's other 1.5 KB more than the default 48)
+    const cudaError_t e = allow_smem((const void *)select_pages_kernel, SV_MAX_SCORE_PAGES * 4);
+    if (e != cudaSuccess) return e;
+  }
+  const int threads = p.P <= 256 ? 128 : lists <= num_sms || p.P > 8192 ? 1024 : 256;
+  return launch_close(select_pages_kernel, dim3((unsigned)lists), threads, smem, s, p);
+}
+
+}  // namespace sv

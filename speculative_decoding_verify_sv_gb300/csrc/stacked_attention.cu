@@ -1,0 +1,614 @@
+// Attention of many query rows over keys that they all see, on the 5th-generation tensor cores (tcgen05,
+// TMEM, TMA; sm_103a, bf16): the shared part of sv_shared_attention and the listed pages of
+// sv_sparse_attention where one list serves many rows.
+//
+// Sequences that share a prefix have, at each of its keys, K and V in common, so that their query rows
+// (tokens x group heads) stack up to one matrix per KV head: S = Q K^T and O = P V over the prefix are
+// matrix products like a prompt's, and K and V are read once for all instead of once per sequence.
+// What differs by row (a sequence's own keys, the tree's mask) is not here: this kernel leaves each
+// row's unnormalised output, maximum and sum over the keys that it has worked on, and the kernel of
+// stacked_units.cu, which takes the own keys and the tree, joins them by softmax's rule
+//   m = max m_i,  l = sum 2^(m_i - m) l_i,  o = sum 2^(m_i - m) o_i / l.
+//
+// Work: a unit is a KV head and up to 256 rows of a group (two MMA tiles A and B of 128), against the
+// group's keys in tiles of 128.  The flattened (unit, key tile) space of W items is split evenly over min(W,
+// SMs) persistent CTAs, so that each has at least one item; a unit that a CTA boundary cuts leaves one piece
+// per CTA.  Piece number = unit + CTA, which is unique, since one of the two grows from piece to piece.
+//
+// Per CTA: a copying warp (TMA: Q per piece, K and V tiles through a ring), an issuing warp (one thread),
+// and two groups of four softmax warps, one thread per row, a group per MMA tile.  P goes back to TMEM
+// over the S it came from.  The issue order is S_A S_B | P_A V, S_A', P_B V, S_B' | ...: one tile's softmax
+// runs beside the other's products.  MMAs of one thread run in the order of their issue, so that S'
+// may be issued over P as soon as P V has been, without waiting for it.
+#include <atomic>
+#include <cfloat>
+
+#include "sv_common.cuh"
+#include "sv_internal.h"
+#include "tc_primitives.cuh"
+
+namespace sv {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;               // rows of an MMA tile
+constexpr int kKeys = 128;               // keys of a tile
+constexpr float kStackRescale = 8.f;     // log2 units by which a row's maximum may lag behind
+constexpr float kStackNone = -3e38f;     // a row's maximum before its first key
+constexpr int kStackThreads = 384;       // two softmax groups; copies, issue and two warps without work
+constexpr unsigned long long kAllKeys = 0x1010101010101010ull;  // 16 keys in each of 8 chunks
+
+template <int D>
+struct StackLayout {
+  static constexpr int KB = D / 64;                 // 64-column blocks
+  static constexpr int Q_TILE = kRows * D * 2;      // rows of an MMA tile
+  static constexpr int KV_BYTES = kKeys * D * 2;    // K or V of a key tile
+  static constexpr int ST = D == 128 ? 4 : 8;       // stages of the ring, K and V in turn
+  static constexpr int OFF_RING = 2 * Q_TILE;
+  static constexpr int OFF_BAR = OFF_RING + ST * KV_BYTES;
+  // full[ST], empty[ST], q_full, q_empty, s_full[2], p_half[2], p_full[2], o_full[2], drain
+  static constexpr int NBAR = 2 * ST + 11;
+  static constexpr int OFF_KEYS = OFF_BAR + NBAR * 8;   // [8] keys of each chunk of a tile
+  static constexpr int OFF_MISC = OFF_KEYS + 8 * 8;     // TMEM address, abort
+  static constexpr int OFF_WORK = OFF_MISC + 16;        // [groups + 1] first work item of a group
+  // [groups] first unit, key tiles, keys, first sequence, sequences
+  static constexpr int OFF_GROUP = OFF_WORK + (SV_MAX_SHARED_GROUPS + 1) * 8;
+  static constexpr int SMEM = OFF_GROUP + SV_MAX_SHARED_GROUPS * 20;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// A piece: key tiles [t0, t1) of a unit.
+struct StackPiece {
+  int head, first, token, tokens, t0, t1, slot, keys, list;
+};
+
+struct StackTables {
+  const long long *work;
+  const int *unit, *tiles, *keys, *start, *members;
+};
+
+// Walks a CTA's share [w, end) of the work, piece by piece.
+struct StackWalk {
+  long long w, end;
+  int g;
+};
+template <bool LIST>
+__device__ __forceinline__ bool next_piece(StackWalk &it, const StackParams &p, const StackTables &t, StackPiece &pc) {
+  if (it.w >= it.end) return false;
+  int kt;
+  if constexpr (LIST) {
+    kt = p.list_tiles;
+    const long long u = it.w / kt;
+    pc.t0 = (int)(it.w - u * kt);
+    const int tile = (int)(u % p.row_tiles), bh = (int)(u / p.row_tiles);
+    pc.list = bh;
+    pc.head = bh % p.Hkv;
+    pc.first = bh / p.Hkv;
+    pc.token = pc.first * p.N + tile * 2 * p.tile_tokens;
+    pc.tokens = min(2 * p.tile_tokens, p.N - tile * 2 * p.tile_tokens);
+    pc.keys = 0;
+    pc.slot = (int)u + (int)blockIdx.x;
+  } else {
+    while (it.w >= t.work[it.g + 1]) ++it.g;
+    const int g = it.g;
+    kt = t.tiles[g];
+    const int u = (int)((it.w - t.work[g]) / kt);
+    pc.t0 = (int)(it.w - t.work[g] - (long long)u * kt);
+    const int total = t.members[g] * p.N, per = (total + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+    const int tile = u % per;
+    pc.head = u / per;
+    pc.first = t.start[g];
+    pc.token = pc.first * p.N + tile * 2 * p.tile_tokens;
+    pc.tokens = min(2 * p.tile_tokens, total - tile * 2 * p.tile_tokens);
+    pc.keys = t.keys[g];
+    pc.list = 0;
+    pc.slot = t.unit[g] + u + (int)blockIdx.x;
+  }
+  pc.t1 = (int)min((long long)kt, pc.t0 + (it.end - it.w));
+  it.w += pc.t1 - pc.t0;
+  return true;
+}
+
+// A lane's chunk of 16 keys of a key tile (lanes 0 to 7).
+struct ChunkRows {
+  int row;    // of the cache, -1: none
+  int count;  // keys
+};
+
+// 32 bytes to global memory.
+__device__ __forceinline__ void store_8(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mov.b64 rc, {%6, %7};\n"
+      " fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// Wait for the phase of the given parity; false if it ran past the limit (then *abort is raised) or *abort
+// was raised.  (Inline: with a function call in it ptxas finds no registers for the split below.)
+__device__ __forceinline__ bool stack_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (global_ns() - t0 > limit) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int D, bool LIST>
+__global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __grid_constant__ StackParams p) {
+  using Lay = StackLayout<D>;
+  constexpr int ST = Lay::ST, KB = Lay::KB;
+  extern __shared__ __align__(1024) uint8_t stack_smem[];
+  uint8_t *sm = stack_smem;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + Lay::OFF_BAR), *empty = full + ST;
+  uint64_t *q_full = empty + ST, *q_empty = q_full + 1, *s_full = q_empty + 1, *p_half = s_full + 2, *p_full = p_half + 2,
+           *o_full = p_full + 2, *drain = o_full + 2;
+  volatile unsigned long long *s_keys = reinterpret_cast<volatile unsigned long long *>(sm + Lay::OFF_KEYS);
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + Lay::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(s_tmem + 1);
+  long long *s_work = reinterpret_cast<long long *>(sm + Lay::OFF_WORK);
+  int *s_unit = reinterpret_cast<int *>(sm + Lay::OFF_GROUP), *s_tiles = s_unit + SV_MAX_SHARED_GROUPS,
+      *s_len = s_tiles + SV_MAX_SHARED_GROUPS, *s_start = s_len + SV_MAX_SHARED_GROUPS,
+      *s_members = s_start + SV_MAX_SHARED_GROUPS;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const unsigned long long limit = p.wait_ns;
+
+  const bool layout_ok = (smem_u32(sm) & 1023u) == 0;  // 128-byte-swizzled tiles
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 4);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  wait_previous();
+  // The kernel behind this one may be set up from here on: it reads what was there before this one, and
+  // waits for this one before it reads the pieces.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- the work: units and key tiles of each group
+  long long total = p.list_work;
+  if constexpr (!LIST) {
+    int bad = 0;
+    for (int g = tid; g < p.groups; g += kStackThreads) {
+      const int a = p.group_start[g], b = p.group_start[g + 1];
+      int len = p.shared_len[g];
+      bad |= a < 0 || b < a || b > p.B;
+      if (len < 0 || len > p.cap) {
+        if (blockIdx.x == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
+        len = len < 0 ? 0 : p.cap;
+      }
+      len &= ~15;
+      s_start[g] = a;
+      s_members[g] = b - a;
+      s_len[g] = len;
+      s_tiles[g] = b > a ? (len + kKeys - 1) / kKeys : 0;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0 && blockIdx.x == 0) set_status(p.status, SV_DEV_BAD_GROUP);
+    if (warp == 0) {
+      long long work = 0;
+      int units = 0;
+      for (int g0 = 0; g0 < p.groups && !bad; g0 += 32) {
+        const int g = g0 + lane;
+        int n = 0;
+        if (g < p.groups && s_tiles[g] > 0) n = (s_members[g] * p.N + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens) * p.Hkv;
+        long long x = g < p.groups ? (long long)n * s_tiles[g] : 0;
+        const long long mine_x = x;
+        const int mine_n = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+          const int k = __shfl_up_sync(0xFFFFFFFFu, n, o);
+          if (lane >= o) x += y, n += k;
+        }
+        if (g < p.groups) {
+          s_work[g] = work + x - mine_x;
+          s_unit[g] = units + n - mine_n;
+        }
+        work += __shfl_sync(0xFFFFFFFFu, x, 31);
+        units += __shfl_sync(0xFFFFFFFFu, n, 31);
+      }
+      if (lane == 0) s_work[p.groups] = work;
+    }
+    __syncthreads();
+    total = s_work[p.groups];
+    // for the kernel that joins the pieces
+    if (blockIdx.x == 0) {
+      if (tid == 0) p.header[0] = total;
+      for (int g = tid; g < p.groups; g += kStackThreads) {
+        p.header[1 + 2 * g] = bad ? 0 : s_work[g];
+        p.header[2 + 2 * g] = bad ? 0 : (long long)s_tiles[g] << 32 | (unsigned)s_unit[g];
+      }
+    }
+  } else {
+    __syncthreads();
+  }
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const StackTables tables{s_work, s_unit, s_tiles, s_len, s_start, s_members};
+  // every CTA that takes part has work, so that a unit's pieces are those of neighbouring CTAs
+  const long long ctas = min((long long)gridDim.x, total);
+  StackWalk walk{0, 0, 0};
+  if (blockIdx.x < ctas && layout_ok) walk = {total * blockIdx.x / ctas, total * (blockIdx.x + 1) / ctas, 0};
+  uint8_t *ring = sm + Lay::OFF_RING;
+  int copied = 0, q_copied = 0;  // (the copying warp) stages filled, pieces begun
+
+  if (warp >= 8) {
+    // 168 registers per thread at the launch, 64512 in all: 128 threads keep 88, 256 take 208
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ---------------------------------------------------------------- copies
+      const uint64_t policy = l2_policy_evict_normal();
+      int tiles = 0;  // key tiles
+      // this lane's chunk of key tile t
+      auto locate = [&](const StackPiece &pc, int t) -> ChunkRows {
+        ChunkRows c{-1, 0};
+        if (lane >= 8) return c;
+        const int at = t * kKeys + 16 * lane;
+        int page = 0, off, pos, count = 16;
+        if constexpr (LIST) {
+          const int k = at / p.page_size;
+          if (k >= p.list_len) return c;
+          page = p.pages[(size_t)pc.list * p.list_len + k];
+          off = at - k * p.page_size;
+          const long long far = (long long)page * p.page_size + off;
+          const int L = min(max(p.prefix_len[pc.first], 0), p.cap);
+          if (page < 0 || far >= L) return c;
+          pos = (int)far;
+          count = min(16, L - pos);
+        } else {
+          if (at >= pc.keys) return c;
+          pos = at;
+          if (p.block_table) page = pos / p.block_size;
+          off = pos - page * p.block_size;
+        }
+        if (!p.block_table) return ChunkRows{pc.first * p.Lmax + pos, count};
+        const int blk = p.block_table[(size_t)pc.first * p.max_blocks + page];
+        if (blk < 0 || blk >= p.num_blocks) {
+          set_status(p.status, SV_DEV_BAD_BLOCK);
+          return c;
+        }
+        return ChunkRows{blk * p.block_size + off, count};
+      };
+      const int per_box = p.box_rows / 16;  // chunks of a box
+      // the next stage: K or V of the tile whose rows the lanes hold
+      auto load = [&](const StackPiece &pc, const ChunkRows &c, bool is_v) -> bool {
+        const int st = copied % ST;
+        int ok = 1;
+        if (copied >= ST && lane == 0) ok = stack_wait(&empty[st], (copied / ST - 1) & 1, abort_flag, limit);
+        if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return false;
+        const bool box = lane < 8 && lane % per_box == 0 && c.row >= 0;
+        const unsigned boxes = __popc(__ballot_sync(0xFFFFFFFFu, box));
+        if (!is_v) {
+          const unsigned lo = __reduce_or_sync(0xFFFFFFFFu, lane < 4 ? (unsigned)c.count << (8 * lane) : 0u);
+          const unsigned hi = __reduce_or_sync(0xFFFFFFFFu, lane >= 4 && lane < 8 ? (unsigned)c.count << (8 * (lane - 4)) : 0u);
+          if (lane == 0) s_keys[tiles & 7] = (unsigned long long)hi << 32 | lo;
+        }
+        if (lane == 0) mbar_expect_tx(&full[st], boxes * (unsigned)p.box_rows * D * 2u);
+        __syncwarp();
+        uint8_t *dst = ring + st * Lay::KV_BYTES;
+        const CUtensorMap *map = is_v ? &p.tm_v : &p.tm_k;
+        if (box) {
+          if (p.grouped) {
+            tma_load_5d_hint(dst + lane * 16 * (D * 2), map, 0, 0, 0, c.row >> 3, pc.head, &full[st], policy);
+          } else {
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+              tma_load_3d_hint(dst + k * (kKeys * 128) + lane * 16 * 128, map, 64 * k, pc.head, c.row, &full[st], policy);
+          }
+        }
+        ++copied;
+        return true;
+      };
+      StackPiece pc;
+      bool ok = true;
+      while (ok && next_piece<LIST>(walk, p, tables, pc)) {
+        ChunkRows cur = locate(pc, pc.t0);
+        for (int t = pc.t0; ok && t < pc.t1; ++t) {
+          ok = load(pc, cur, false);
+          if (ok && t == pc.t0) {
+            int free = 1;
+            if (q_copied > 0 && lane == 0) free = stack_wait(q_empty, (q_copied - 1) & 1, abort_flag, limit);
+            ok = __shfl_sync(0xFFFFFFFFu, free, 0);
+            if (ok && lane == 0) {
+              const int n = pc.tokens > p.tile_tokens ? 2 : 1;
+              mbar_expect_tx(q_full, (unsigned)(n * p.tile_tokens * p.G) * D * 2u);
+              for (int i = 0; i < n; ++i)
+                for (int k = 0; k < KB; ++k)
+                  tma_load_3d(sm + i * Lay::Q_TILE + k * (kRows * 128), &p.tm_q, 64 * k, pc.head * p.G,
+                              pc.token + i * p.tile_tokens, q_full);
+            }
+            if (ok) ++q_copied;
+          }
+          const ChunkRows mine = cur;
+          if (t + 1 < pc.t1) cur = locate(pc, t + 1);
+          if (ok) ok = load(pc, mine, true);
+          ++tiles;
+        }
+      }
+    } else if (warp == 9 && lane == 0) {
+      // ----------------------------------------------------------------- issue
+      constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0, 0), id_o = idesc_bf16(kRows, D, 0, 1);
+      const int block = p.grouped ? 1024 : kKeys * 128, step8 = p.grouped ? KB * 1024 : 1024;
+      const uint64_t dq = sdesc_sw128(smem_u32(sm), 16, 1024);
+      const uint64_t dk = sdesc_sw128(smem_u32(ring), 16, step8), dv = sdesc_sw128(smem_u32(ring), block, step8);
+      int r = 0, pieces = 0, na = 0, nb = 0;  // stages used, pieces, key tiles of A and of B
+      auto scores = [&](int x, int st) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t a = dq + (uint64_t)((x * Lay::Q_TILE + (k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4);
+          const uint64_t b = dk + (uint64_t)((st * Lay::KV_BYTES + (k >> 2) * block + (k & 3) * 32) >> 4);
+          umma_bf16(tmem + x * kKeys, a, b, id_s, k > 0);
+        }
+        umma_commit(&s_full[x]);
+      };
+      auto outputs = [&](int x, int st, bool first, int n) -> bool {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!stack_wait(h ? &p_full[x] : &p_half[x], n & 1, abort_flag, limit)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4 * h; k < 4 * h + 4; ++k)
+            umma_bf16_ts(tmem + 256 + x * D, tmem + x * kKeys + k * 8, dv + (uint64_t)((st * Lay::KV_BYTES + k * 2 * step8) >> 4),
+                         id_o, (!first || k > 0) ? 1u : 0u);
+        }
+        return true;
+      };
+      StackPiece pc;
+      bool ok = true;
+      while (ok && next_piece<LIST>(walk, p, tables, pc)) {
+        const bool two = pc.tokens > p.tile_tokens;
+        const int n = pc.t1 - pc.t0;
+        ok = stack_wait(q_full, pieces & 1, abort_flag, limit) && stack_wait(&full[r % ST], (r / ST) & 1, abort_flag, limit);
+        if (!ok) break;
+        tc_fence_after();
+        scores(0, r % ST);
+        if (two) scores(1, r % ST);
+        umma_commit(&empty[r % ST]);
+        if (n == 1) umma_commit(q_empty);
+        ++r;
+        for (int i = 0; i < n; ++i) {
+          const int sv = r % ST, sk = (r + 1) % ST;
+          const bool more = i + 1 < n;
+          ok = stack_wait(&full[sv], (r / ST) & 1, abort_flag, limit) &&
+               (!more || stack_wait(&full[sk], ((r + 1) / ST) & 1, abort_flag, limit)) && outputs(0, sv, i == 0, na);
+          if (!ok) break;
+          ++na;
+          if (more) scores(0, sk);
+          else umma_commit(&o_full[0]);
+          if (two) {
+            ok = outputs(1, sv, i == 0, nb);
+            if (!ok) break;
+            ++nb;
+          }
+          umma_commit(&empty[sv]);
+          if (more) {
+            if (two) scores(1, sk);
+            umma_commit(&empty[sk]);
+            if (i + 2 == n) umma_commit(q_empty);
+          } else if (two) {
+            umma_commit(&o_full[1]);
+          }
+          r += more ? 2 : 1;
+        }
+        ++pieces;
+      }
+      // every MMA has completed before TMEM is given up
+      umma_commit(drain);
+      const unsigned long long t0 = global_ns();
+      while (!mbar_try_wait(drain, 0) && global_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int x = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t ts = tmem + lanes + x * kKeys, to = tmem + lanes + 256 + x * D;
+    const float sc = p.scale_log2;
+    int r = 0, tiles = 0, n = 0, done = 0;  // stages, key tiles of the CTA, of this MMA tile, pieces of this MMA tile
+    StackPiece pc;
+    bool ok = true;
+    while (ok && next_piece<LIST>(walk, p, tables, pc)) {
+      const int rows = min(p.tile_tokens, pc.tokens - x * p.tile_tokens) * p.G;  // of this MMA tile
+      if (rows <= 0) {
+        r += 2 * (pc.t1 - pc.t0);
+        tiles += pc.t1 - pc.t0;
+        continue;
+      }
+      const bool idle = wq * 32 >= rows;  // padding: the barriers only
+      float m = kStackNone, l = 0.f;
+      for (int t = pc.t0; t < pc.t1; ++t, ++tiles, ++n, r += 2) {
+        if (!stack_wait(&s_full[x], n & 1, abort_flag, limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const unsigned long long keys = s_keys[tiles & 7];
+        if (keys != kAllKeys && x == 0) {
+          // V rows that are no keys may hold anything: zero, so that 0 * V stays 0
+          const int sv = (r + 1) % ST;
+          if (!stack_wait(&full[sv], ((r + 1) / ST) & 1, abort_flag, limit)) {
+            ok = false;
+            break;
+          }
+          uint8_t *v = ring + sv * Lay::KV_BYTES;
+          for (int i = tid; i < kKeys * (D / 8); i += 128) {
+            const int k = i / (D / 8), c = i % (D / 8);
+            if ((k & 15) < (int)(keys >> (8 * (k >> 4)) & 31)) continue;
+            uint8_t *at = p.grouped ? v + (k >> 3) * (KB * 1024) + (c >> 3) * 1024 + (k & 7) * 128 + (c & 7) * 16
+                                    : v + (c >> 3) * (kKeys * 128) + k * 128 + (c & 7) * 16;
+            // (whole rows are zeroed, so that the swizzle of their 16-byte chunks does not matter)
+            *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!idle) {
+          float s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+          tmem_wait_ld();
+          if (keys != kAllKeys) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int count = (int)(keys >> (8 * c) & 31);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i >= count) s[c >> 1][16 * (c & 1) + i] = -INFINITY;
+            }
+          }
+          float top[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            top[c] = fmaxf(s[c][0], s[c][1]);
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) top[c] = fmax3(top[c], s[c][i], s[c][i + 1]);
+          }
+          const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+          const bool moves = best > m + kStackRescale;
+          if (__any_sync(0xFFFFFFFFu, moves)) {
+            const float to_m = fmaxf(best, m), w = ex2_approx(m - to_m);
+            m = to_m;
+            l *= w;
+            if (t > pc.t0) {  // (S of this tile is there, so P V of the tile before is done)
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= w;
+                tmem_st16(to + c, o);
+              }
+            }
+          }
+          const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 e = fma2(make_float2(s[c][2 * i], s[c][2 * i + 1]), sc2, m2);
+              e.x = ex2_approx(e.x);
+              e.y = ex2_approx(e.y);
+              sum[i & 1] = add2(sum[i & 1], e);
+              // (rounded to bf16 for the product with V, at most 2^-8 of each; the sum is of the unrounded)
+              w[i] = __uint_as_float(pack_bf16x2(e.x, e.y));
+            }
+            tmem_st16(ts + 16 * c, w);
+            if (c == 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_half[x]);
+            }
+          }
+          const float2 both = add2(sum[0], sum[1]);
+          l += both.x + both.y;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&p_half[x]);
+            mbar_arrive(&p_full[x]);
+          }
+        }
+      }
+      if (!ok) break;
+      if (!stack_wait(&o_full[x], done & 1, abort_flag, limit)) break;
+      ++done;
+      tc_fence_after();
+      if (!idle) {
+        const size_t at = (size_t)pc.slot * kStackRows + x * kRows + row;
+        if (row < rows) p.part_ml[at] = make_float2(m, l);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(to + c, o);
+          tmem_wait_ld();
+          if (row < rows) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) store_8(p.part_o + at * D + c + i, &o[i]);
+          }
+        }
+        tc_fence_before();  // (the next piece's first P V comes behind this warp's next arrival)
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 8 && lane == 0 && *abort_flag) {
+    // a wait gave up: let the copies in flight land before the CTA's shared memory is given up
+    const unsigned long long t0 = global_ns();
+    for (int i = max(0, copied - ST); i < copied; ++i)
+      while (!mbar_try_wait(&full[i % ST], (i / ST) & 1) && global_ns() - t0 < kWaitLimitNs) {
+      }
+    while (q_copied > 0 && !mbar_try_wait(q_full, (q_copied - 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
+    }
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0) {
+    if (!layout_ok) set_status(p.status, SV_DEV_LAYOUT);
+    else if (*abort_flag) set_status(p.status, SV_DEV_TIMEOUT);
+  }
+}
+
+template <int D, bool LIST>
+cudaError_t launch_stacked_typed(const StackParams &p, int grid, cudaStream_t s) {
+  using Lay = StackLayout<D>;
+  static std::atomic<bool> attr[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  auto kern = stacked_attn_kernel<D, LIST>;
+  if (dev < 0 || dev >= 64 || !attr[dev].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr[dev].store(true);
+  }
+  return launch_close(kern, dim3((unsigned)grid), kStackThreads, (size_t)Lay::SMEM, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_stacked(const StackParams &p, int D, bool listed, int grid, cudaStream_t s) {
+  if (D == 128) return listed ? launch_stacked_typed<128, true>(p, grid, s) : launch_stacked_typed<128, false>(p, grid, s);
+  return listed ? launch_stacked_typed<64, true>(p, grid, s) : launch_stacked_typed<64, false>(p, grid, s);
+}
+
+}  // namespace sv

@@ -395,6 +395,282 @@ sv_status sv_window_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
                         window, sinks, out, workspace, workspace_bytes, stream);
 }
 
+// ------------------------------------------- shared prefixes and selected pages
+
+// What the attentions of this section have in common: the checks, and the launch's parameters.
+static sv_status page_attention_args(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                                     const void *k_tree, const void *v_tree, const sv_kv_cache &cache,
+                                     const int32_t *parent, int parent_stride, float scale, void *out,
+                                     sv::AttnParams *p) {
+  if (dt != SV_F32 && dt != SV_BF16) return fail(SV_ERR_UNSUPPORTED, "dtype %d not supported", (int)dt);
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
+    return fail(SV_ERR_INVALID_ARG, "bad sizes B=%d Hq=%d Hkv=%d", B, Hq, Hkv);
+  if (D != 64 && D != 128) return fail(SV_ERR_UNSUPPORTED, "head dim %d (supported 64, 128)", D);
+  if (Hq / Hkv > 128) return fail(SV_ERR_UNSUPPORTED, "%d query heads per KV head (supported 128)", Hq / Hkv);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(SV_ERR_INVALID_ARG, "scale must be positive");
+  sv_status st = tree_arg(N, parent, parent_stride, &p->tree);
+  if (st != SV_OK) return st;
+  if (B > 0 && (!q || !k_tree || !v_tree || !out))
+    return fail(SV_ERR_INVALID_ARG, "q, k_tree, v_tree or out is NULL");
+  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(out))
+    return fail(SV_ERR_INVALID_ARG, "q, k_tree, v_tree and out must be 16-byte aligned");
+  if ((st = check_cache(cache, false, B)) != SV_OK) return st;
+  const int paged = cache.block_table ? cache.block_size : 0;
+  if (paged % 16 != 0) return fail(SV_ERR_UNSUPPORTED, "block_size = %d must be a multiple of 16", paged);
+  const long long cap = paged ? (long long)cache.max_blocks * paged : cache.Lmax;
+  const long long rows = paged ? (long long)cache.num_blocks * paged : (long long)B * cache.Lmax;
+  if (cap > kMaxRows || rows > kMaxRows || (long long)B * N > kMaxRows)
+    return fail(SV_ERR_UNSUPPORTED, "a cache of %lld rows, up to %lld of a sequence (supported %d)", rows, cap, kMaxRows);
+  if ((long long)B * N * Hq > kMaxRows || (long long)B * Hkv * 64 > kMaxRows || (long long)Hkv * D > kMaxRows)
+    return fail(SV_ERR_UNSUPPORTED, "B = %d, N = %d, Hq = %d: too many query rows", B, N, Hq);
+  const long long row = (long long)D * (dt == SV_BF16 ? 2 : 4), q_bytes = (long long)B * N * Hq * row;
+  const long long tree_bytes = (long long)B * N * Hkv * row, cache_bytes = rows * Hkv * row;
+  if (meet(out, q_bytes, q, q_bytes) || meet(out, q_bytes, k_tree, tree_bytes) || meet(out, q_bytes, v_tree, tree_bytes) ||
+      meet(out, q_bytes, cache.k, cache_bytes) || meet(out, q_bytes, cache.v, cache_bytes))
+    return fail(SV_ERR_INVALID_ARG, "out overlaps an input");
+  p->q = q;
+  p->k_tree = k_tree;
+  p->v_tree = v_tree;
+  p->cache_k = cache.k;
+  p->cache_v = cache.v;
+  p->prefix_len = cache.prefix_len;
+  p->block_table = cache.block_table;
+  p->out = out;
+  p->B = B;
+  p->N = N;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->G = Hq / Hkv;
+  p->D = D;
+  p->Lmax = cache.Lmax;
+  p->block_size = cache.block_size;
+  p->max_blocks = cache.max_blocks;
+  p->num_blocks = cache.num_blocks;
+  p->cap = max_prefix_of(cache);
+  p->M = N * p->G;
+  p->window = INT32_MAX;  // (the whole prefix, where a window's kernel runs)
+  p->sinks = 0;
+  p->scale = scale;
+  p->scale_log2 = scale * sv::kLog2e;
+  p->wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return SV_OK;
+}
+
+static sv_status check_plan(const sv::StackPlan &plan, const void *workspace, size_t bytes) {
+  if (plan.pieces * sv::kStackRows > INT32_MAX) return fail(SV_ERR_UNSUPPORTED, "too many query rows");
+  if (plan.ws_bytes == 0) return SV_OK;
+  if (!workspace || bytes < plan.ws_bytes)
+    return fail(SV_ERR_WORKSPACE, "attention workspace %zu bytes, need %zu", bytes, plan.ws_bytes);
+  if (!aligned16(workspace)) return fail(SV_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+  return SV_OK;
+}
+
+size_t sv_shared_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, int max_prefix, int groups) {
+  if (dt != SV_BF16 || B <= 0 || N <= 0 || N > SV_MAX_TREE_NODES || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
+      Hq / Hkv > 128 || (D != 64 && D != 128) || max_prefix < 0 || groups < 1 || groups > SV_MAX_SHARED_GROUPS)
+    return 0;
+  return sv::shared_plan(B, N, Hq, Hkv, D, groups, num_sms()).ws_bytes;
+}
+
+sv_status sv_shared_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                              const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                              const int32_t *parent, int parent_stride, float scale,
+                              const int32_t *group_start, const int32_t *shared_len, int groups,
+                              void *out, void *workspace, size_t workspace_bytes, void *stream) {
+  const CallRange range("sv_shared_attention");
+  sv::AttnParams p{};
+  sv_status st = page_attention_args(dt, B, N, Hq, Hkv, D, q, k_tree, v_tree, cache, parent, parent_stride, scale, out, &p);
+  if (st != SV_OK) return st;
+  if (groups < 1) return fail(SV_ERR_INVALID_ARG, "groups = %d", groups);
+  if (groups > SV_MAX_SHARED_GROUPS) return fail(SV_ERR_UNSUPPORTED, "%d groups (supported %d)", groups, SV_MAX_SHARED_GROUPS);
+  if (B == 0) return SV_OK;
+  if (!group_start || !shared_len) return fail(SV_ERR_INVALID_ARG, "group_start or shared_len is NULL");
+  const sv::StackPlan plan = dt == SV_BF16 ? sv::shared_plan(B, N, Hq, Hkv, D, groups, num_sms()) : sv::StackPlan{};
+  if ((st = check_plan(plan, workspace, workspace_bytes)) != SV_OK) return st;
+  if (!(p.status = status_word())) return fail(SV_ERR_CUDA, "no CUDA device");
+  const sv::ListArgs l{group_start, shared_len, groups, nullptr, 0, 0, 0};
+  unsigned launches = 0;
+  cudaError_t e = cudaErrorLaunchFailure;
+  if (dt == SV_F32) {
+    if (!take_injected_failure() && (e = sv::launch_window_attention_f32(p, num_sms(), static_cast<cudaStream_t>(stream))) == cudaSuccess)
+      ++launches;
+  } else {
+    e = sv::launch_shared_attention(p, l, plan, workspace, static_cast<cudaStream_t>(stream), take_injected_failure, &launches);
+  }
+  sv::count_launches(launches);
+  return e == cudaSuccess ? SV_OK : cuda_fail(e, "shared attention launch");
+}
+
+size_t sv_sparse_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, int page_size, int K, int sets) {
+  if (dt != SV_BF16 || B <= 0 || N <= 0 || N > SV_MAX_TREE_NODES || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
+      Hq / Hkv > 128 || (D != 64 && D != 128) || page_size < 16 || K < 1 || (sets != 1 && sets != N))
+    return 0;
+  return sv::sparse_plan(B, N, Hq, Hkv, D, page_size, K, sets, num_sms()).ws_bytes;
+}
+
+sv_status sv_sparse_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                              const void *k_tree, const void *v_tree, sv_kv_cache cache,
+                              const int32_t *parent, int parent_stride, float scale,
+                              const int32_t *pages, int sets, int K, int page_size, void *out,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+  const CallRange range("sv_sparse_attention");
+  sv::AttnParams p{};
+  sv_status st = page_attention_args(dt, B, N, Hq, Hkv, D, q, k_tree, v_tree, cache, parent, parent_stride, scale, out, &p);
+  if (st != SV_OK) return st;
+  if (K < 1) return fail(SV_ERR_INVALID_ARG, "K = %d pages in a list", K);
+  if (sets != 1 && sets != N) return fail(SV_ERR_INVALID_ARG, "sets = %d (1, or N = %d)", sets, N);
+  if (page_size < 1) return fail(SV_ERR_INVALID_ARG, "page_size = %d", page_size);
+  if (page_size % 16 != 0) return fail(SV_ERR_UNSUPPORTED, "page_size = %d must be a multiple of 16", page_size);
+  if (cache.block_table && page_size != cache.block_size)
+    return fail(SV_ERR_INVALID_ARG, "page_size = %d in a cache of blocks of %d", page_size, cache.block_size);
+  if ((long long)K * page_size > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "lists of %d pages of %d keys", K, page_size);
+  if ((long long)B * sets * Hkv * 64 > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "B = %d, sets = %d, Hkv = %d: too many lists", B, sets, Hkv);
+  if (B == 0) return SV_OK;
+  if (!pages) return fail(SV_ERR_INVALID_ARG, "pages is NULL");
+  if (meet(out, (long long)B * N * Hq * D * (dt == SV_BF16 ? 2 : 4), pages, (long long)B * sets * Hkv * K * 4))
+    return fail(SV_ERR_INVALID_ARG, "out overlaps an input");
+  const sv::StackPlan plan = dt == SV_BF16 ? sv::sparse_plan(B, N, Hq, Hkv, D, page_size, K, sets, num_sms()) : sv::StackPlan{};
+  if ((st = check_plan(plan, workspace, workspace_bytes)) != SV_OK) return st;
+  if (!(p.status = status_word())) return fail(SV_ERR_CUDA, "no CUDA device");
+  const sv::ListArgs l{nullptr, nullptr, 0, pages, K, sets, page_size};
+  unsigned launches = 0;
+  cudaError_t e = cudaErrorLaunchFailure;
+  if (dt == SV_F32) {
+    if (!take_injected_failure() && (e = sv::launch_sparse_attention_f32(p, l, num_sms(), static_cast<cudaStream_t>(stream))) == cudaSuccess)
+      ++launches;
+  } else {
+    e = sv::launch_sparse_attention(p, l, plan, workspace, num_sms(), static_cast<cudaStream_t>(stream), take_injected_failure, &launches);
+  }
+  sv::count_launches(launches);
+  return e == cudaSuccess ? SV_OK : cuda_fail(e, "sparse attention launch");
+}
+
+sv_status sv_page_bounds(sv_dtype dt, int B, int Hkv, int D, int page_size, sv_kv_cache cache,
+                         const int32_t *start, void *bounds, void *stream) {
+  const CallRange range("sv_page_bounds");
+  if (dt != SV_F32 && dt != SV_BF16) return fail(SV_ERR_UNSUPPORTED, "dtype %d not supported", (int)dt);
+  if (B < 0 || Hkv < 1) return fail(SV_ERR_INVALID_ARG, "bad sizes B=%d Hkv=%d", B, Hkv);
+  if (D != 64 && D != 128) return fail(SV_ERR_UNSUPPORTED, "head dim %d (supported 64, 128)", D);
+  if (page_size < 1) return fail(SV_ERR_INVALID_ARG, "page_size = %d", page_size);
+  sv_kv_cache c = cache;
+  c.v = c.k;  // (only K is read)
+  sv_status st = check_cache(c, false, B);
+  if (st != SV_OK) return st;
+  if (c.block_table && page_size != c.block_size)
+    return fail(SV_ERR_INVALID_ARG, "page_size = %d in a cache of blocks of %d", page_size, c.block_size);
+  if (B > 65535) return fail(SV_ERR_UNSUPPORTED, "B = %d (supported 65535)", B);
+  const long long cap = c.block_table ? (long long)c.max_blocks * c.block_size : c.Lmax;
+  const long long rows = c.block_table ? (long long)c.num_blocks * c.block_size : (long long)B * c.Lmax;
+  if (cap > kMaxRows || rows > kMaxRows || (long long)Hkv * D > kMaxRows / 4)
+    return fail(SV_ERR_UNSUPPORTED, "a cache of %lld rows, up to %lld of a sequence (supported %d)", rows, cap, kMaxRows);
+  if (B == 0) return SV_OK;
+  if (!bounds) return fail(SV_ERR_INVALID_ARG, "bounds is NULL");
+  if (!aligned16(bounds)) return fail(SV_ERR_INVALID_ARG, "bounds not 16-byte aligned");
+  const int seq_pages = (int)((cap + page_size - 1) / page_size);
+  const long long row = (long long)Hkv * D * (dt == SV_BF16 ? 2 : 4);
+  if (meet(bounds, 2 * row * (c.block_table ? c.num_blocks : (long long)B * seq_pages), c.k, rows * row) ||
+      meet(bounds, 2 * row * (c.block_table ? c.num_blocks : (long long)B * seq_pages), cache.v, rows * row))
+    return fail(SV_ERR_INVALID_ARG, "bounds overlap the cache");
+  sv::BoundParams p{};
+  if (!(p.status = status_word())) return fail(SV_ERR_CUDA, "no CUDA device");
+  p.k = c.k;
+  p.prefix_len = c.prefix_len;
+  p.start = start;
+  p.block_table = c.block_table;
+  p.bounds = bounds;
+  p.Lmax = c.Lmax;
+  p.page_size = page_size;
+  p.max_blocks = c.max_blocks;
+  p.num_blocks = c.num_blocks;
+  p.cap = (int)cap;
+  p.seq_pages = seq_pages;
+  p.vecs = (int)(row / 16);
+  p.head_vecs = p.vecs / Hkv;
+  const cudaError_t e = take_injected_failure() ? cudaErrorLaunchFailure
+                                                : sv::launch_page_bounds(dt, p, B, num_sms(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page bounds launch");
+  sv::count_launches(1);
+  return SV_OK;
+}
+
+sv_status sv_page_scores(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
+                         const void *bounds, const int32_t *prefix_len, int page_size, int P,
+                         const int32_t *block_table, int num_blocks, int sets, float *out, void *stream) {
+  const CallRange range("sv_page_scores");
+  if (dt != SV_F32 && dt != SV_BF16) return fail(SV_ERR_UNSUPPORTED, "dtype %d not supported", (int)dt);
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0)
+    return fail(SV_ERR_INVALID_ARG, "bad sizes B=%d Hq=%d Hkv=%d", B, Hq, Hkv);
+  if (D != 64 && D != 128) return fail(SV_ERR_UNSUPPORTED, "head dim %d (supported 64, 128)", D);
+  if (Hq / Hkv > 128) return fail(SV_ERR_UNSUPPORTED, "%d query heads per KV head (supported 128)", Hq / Hkv);
+  if (N < 1) return fail(SV_ERR_INVALID_ARG, "N = %d", N);
+  if (N > SV_MAX_TREE_NODES) return fail(SV_ERR_UNSUPPORTED, "%d nodes (supported %d)", N, SV_MAX_TREE_NODES);
+  if (page_size < 1 || P < 1) return fail(SV_ERR_INVALID_ARG, "P = %d pages of %d", P, page_size);
+  if (sets != 1 && sets != N) return fail(SV_ERR_INVALID_ARG, "sets = %d (1, or N = %d)", sets, N);
+  if (block_table && num_blocks < 1) return fail(SV_ERR_INVALID_ARG, "num_blocks = %d", num_blocks);
+  if ((long long)B * N * Hq > kMaxRows || (long long)B * Hkv * ((long long)P / 8 + 2) > kMaxRows || (long long)Hkv * D > kMaxRows / 8)
+    return fail(SV_ERR_UNSUPPORTED, "B = %d, N = %d, Hq = %d, P = %d: too many rows", B, N, Hq, P);
+  if (B == 0) return SV_OK;
+  if (!q || !bounds || !prefix_len || !out) return fail(SV_ERR_INVALID_ARG, "q, bounds, prefix_len or out is NULL");
+  if (!aligned16(q) || !aligned16(bounds) || !aligned16(out)) return fail(SV_ERR_INVALID_ARG, "q, bounds and out must be 16-byte aligned");
+  const long long row = (long long)D * (dt == SV_BF16 ? 2 : 4), out_bytes = (long long)B * sets * Hkv * P * 4;
+  if (meet(out, out_bytes, q, (long long)B * N * Hq * row) ||
+      meet(out, out_bytes, bounds, 2 * row * Hkv * (block_table ? num_blocks : (long long)B * P)) ||
+      meet(out, out_bytes, prefix_len, 4ll * B) || (block_table && meet(out, out_bytes, block_table, 4ll * B * P)))
+    return fail(SV_ERR_INVALID_ARG, "out overlaps an input");
+  sv::ScoreParams p{};
+  if (!(p.status = status_word())) return fail(SV_ERR_CUDA, "no CUDA device");
+  p.q = q;
+  p.bounds = bounds;
+  p.prefix_len = prefix_len;
+  p.block_table = block_table;
+  p.out = out;
+  p.N = N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.P = P;
+  p.page_size = page_size;
+  p.num_blocks = num_blocks;
+  p.sets = sets;
+  p.set_nodes = N / sets;
+  const cudaError_t e = take_injected_failure() ? cudaErrorLaunchFailure
+                                                : sv::launch_page_scores(dt, D, p, B, num_sms(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page scores launch");
+  sv::count_launches(1);
+  return SV_OK;
+}
+
+sv_status sv_select_pages(int B, int lists, int P, const float *scores, const int32_t *prefix_len,
+                          int page_size, int K, int first, int last, int32_t *out, void *stream) {
+  const CallRange range("sv_select_pages");
+  if (B < 0 || lists < 1 || P < 1 || page_size < 1) return fail(SV_ERR_INVALID_ARG, "B = %d, %d lists of P = %d pages of %d", B, lists, P, page_size);
+  if (P > SV_MAX_SCORE_PAGES) return fail(SV_ERR_UNSUPPORTED, "P = %d pages (supported %d)", P, SV_MAX_SCORE_PAGES);
+  if (K < 1 || first < 0 || last < 0 || (long long)first + last > K)
+    return fail(SV_ERR_INVALID_ARG, "K = %d pages, the first %d and the last %d among them", K, first, last);
+  if ((long long)B * lists > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "B = %d, %d lists", B, lists);
+  if (B == 0) return SV_OK;
+  if (!scores || !prefix_len || !out) return fail(SV_ERR_INVALID_ARG, "scores, prefix_len or out is NULL");
+  const long long n = (long long)B * lists;
+  if (meet(out, n * K * 4, scores, n * P * 4) || meet(out, n * K * 4, prefix_len, 4ll * B))
+    return fail(SV_ERR_INVALID_ARG, "out overlaps an input");
+  sv::SelectParams p{};
+  if (!(p.status = status_word())) return fail(SV_ERR_CUDA, "no CUDA device");
+  p.scores = scores;
+  p.prefix_len = prefix_len;
+  p.out = out;
+  p.lists = lists;
+  p.P = P;
+  p.page_size = page_size;
+  p.K = K;
+  p.first = first;
+  p.last = last;
+  const cudaError_t e = take_injected_failure() ? cudaErrorLaunchFailure
+                                                : sv::launch_select_pages(p, n, num_sms(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page selection launch");
+  sv::count_launches(1);
+  return SV_OK;
+}
+
 // ----------------------------------------------------------------- acceptance
 
 size_t sv_accept_workspace_size(int B, int N, int V, int Dq) {

@@ -48,6 +48,9 @@ struct AttnParams {
   float scale;
   Tree tree;
   unsigned long long wait_ns;  // limit of the tensor-core kernel's waits for progress
+  // listed pages (fp32): [B,sets,Hkv,list_len], a list per set of set_nodes nodes
+  const int32_t *pages;
+  int list_len, sets, set_nodes, page_size;
 };
 
 struct AttnPlan {
@@ -118,6 +121,56 @@ struct WinParams {
   unsigned try_ns;
 };
 cudaError_t launch_window_attention(const AttnParams &p, int num_sms, cudaStream_t s);
+// The query rows of many sequences, or of many nodes, stacked against keys that they all see (bf16): the
+// pieces of the rows' results over those keys.  Two MMA tiles of 128 rows are a unit's rows, by which the
+// pieces are laid out.
+constexpr int kStackRows = 256;
+struct StackParams {
+  CUtensorMap tm_q, tm_k, tm_v;
+  const int32_t *group_start, *shared_len;  // shared prefixes: [groups + 1], [groups]
+  const int32_t *pages;                     // listed pages: [B, Hkv, list_len]
+  const int32_t *prefix_len, *block_table;
+  unsigned int *status;
+  long long *header;  // shared prefixes: the work and, per group, its first work item, key tiles and first unit
+  float *part_o;      // [pieces][kStackRows][D] outputs, unnormalised
+  float2 *part_ml;    // [pieces][kStackRows] maximum (log2 units) and sum
+  int groups, B, N, Hkv, G;
+  int tile_tokens;    // tokens of an MMA tile (G rows each)
+  int list_len, page_size, row_tiles, list_tiles;
+  long long list_work;
+  int Lmax, block_size, max_blocks, num_blocks, cap;
+  int box_rows, grouped;  // rows of a copy of K or V; pages that come with both column halves in one copy
+  float scale_log2;
+  unsigned long long wait_ns;
+};
+cudaError_t launch_stacked(const StackParams &p, int D, bool listed, int grid, cudaStream_t s);
+// A 3-D view (D, heads, rows) of a bf16 tensor with boxes of 64 columns, box_heads heads and box_rows
+// rows; pages of a pool with both 64-column halves in one copy (D = 128).  128-byte swizzle.
+bool tma_heads_map(CUtensorMap *m, const void *base, int D, int heads, long long rows, int box_heads, int box_rows);
+bool tma_pages_map(CUtensorMap *m, const void *base, int heads, long long rows, int page_rows);
+
+// sv_shared_attention and sv_sparse_attention in bf16: the plan, and the launches (counted in *launches).
+struct StackPlan {
+  bool stacked;       // through the stacked kernel and its pieces
+  int grid, tile_tokens, row_tiles, list_tiles;
+  long long pieces;   // at most
+  size_t off_ml, off_o, ws_bytes;
+};
+StackPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int groups, int num_sms);
+StackPlan sparse_plan(int B, int N, int Hq, int Hkv, int D, int page_size, int list_len, int sets, int num_sms);
+struct ListArgs {
+  const int32_t *group_start, *shared_len;
+  int groups;
+  const int32_t *pages;
+  int list_len, sets, page_size;
+};
+// fails(): whether the next launch is to fail without being made (injected failures).
+cudaError_t launch_shared_attention(const AttnParams &a, const ListArgs &l, const StackPlan &pl, void *ws, cudaStream_t s,
+                                    bool (*fails)(), unsigned *launches);
+cudaError_t launch_sparse_attention(const AttnParams &a, const ListArgs &l, const StackPlan &pl, void *ws, int num_sms,
+                                    cudaStream_t s, bool (*fails)(), unsigned *launches);
+// Listed pages in fp32.
+cudaError_t launch_sparse_attention_f32(AttnParams a, const ListArgs &l, int num_sms, cudaStream_t s);
 // The same in fp32 (any number of rows; p.splits is set at the launch: the CTAs per unit).
 cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t s);
 // Whether a windowed bf16 call of these sizes goes to the tensor-core kernel where that takes
@@ -245,6 +298,38 @@ struct RopeParams {
   Tree tree;                           // (tree form; T = B * tree.N)
 };
 cudaError_t launch_qk_norm_rope(sv_dtype dt, int D, RopeParams p, int num_sms, cudaStream_t s);
+
+// ------------------------------------------------------- pages: bounds, scores, selection
+
+struct BoundParams {
+  const void *k;
+  const int32_t *prefix_len, *start;  // start NULL: 0
+  const int32_t *block_table;
+  void *bounds;                       // [pages][Hkv][2][D]
+  unsigned int *status;
+  int Lmax, page_size, max_blocks, num_blocks, cap, seq_pages;
+  int vecs, head_vecs;                // 16-byte pieces of a row and of a head
+};
+cudaError_t launch_page_bounds(sv_dtype dt, BoundParams p, int B, int num_sms, cudaStream_t s);
+
+struct ScoreParams {
+  const void *q, *bounds;
+  const int32_t *prefix_len, *block_table;
+  float *out;                         // [B][sets][Hkv][P]
+  unsigned int *status;
+  int N, Hq, Hkv, G, P, page_size, num_blocks, sets, set_nodes;
+  int set_cols, splits;               // (set at the launch)
+};
+cudaError_t launch_page_scores(sv_dtype dt, int D, ScoreParams p, int B, int num_sms, cudaStream_t s);
+
+struct SelectParams {
+  const float *scores;
+  const int32_t *prefix_len;
+  int32_t *out;
+  unsigned int *status;
+  int lists, P, page_size, K, first, last;  // lists per sequence
+};
+cudaError_t launch_select_pages(const SelectParams &p, long long lists, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- LM head
 

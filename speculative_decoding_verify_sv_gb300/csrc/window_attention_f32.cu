@@ -79,7 +79,8 @@ struct F32Layout {
   static_assert(CHUNK >= R * D, "a warp's outputs merge in the room of its chunk");
 };
 
-template <int D, int R>
+// LISTED: the keys of the unit's listed pages in the place of a window's (sv_sparse_attention).
+template <int D, int R, bool LISTED>
 __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(const __grid_constant__ AttnParams p) {
   using Lay = F32Layout<D, R>;
   constexpr int NW = Lay::NW, KS = Lay::KS, PL = D / 32;
@@ -92,10 +93,11 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned C = p.splits, rank = C > 1 ? cluster_rank() : 0;
   const int blocks = (p.M + R - 1) / R, unit = blockIdx.x / C;
-  const int mb = unit % blocks, kvh = (unit / blocks) % p.Hkv, b = unit / blocks / p.Hkv;
+  const int mb = unit % blocks, kvh = (unit / blocks) % p.Hkv, bs = unit / blocks / p.Hkv;
+  const int b = LISTED ? bs / p.sets : bs, node0 = LISTED ? bs % p.sets * p.set_nodes : 0;
   if (tid < R) {
     const int at = mb * R + tid, node = at / p.G;
-    s_row[tid] = at < p.M ? (b * p.N + node) * p.Hq + kvh * p.G + at - node * p.G : -1;
+    s_row[tid] = at < p.M ? (b * p.N + node0 + node) * p.Hq + kvh * p.G + at - node * p.G : -1;
   }
   __syncthreads();
   wait_previous();
@@ -110,13 +112,14 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   }
   const int parent = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
   if (L < 0 || L > p.cap) {
-    if (unit % (blocks * p.Hkv) == 0 && rank == 0 && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
+    if (unit % (blocks * p.Hkv) == 0 && node0 == 0 && rank == 0 && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
     L = L < 0 ? 0 : p.cap;
   }
-  const int first = window_first(L, p.window), n_sinks = min(p.sinks, first);
+  const int first = LISTED ? 0 : window_first(L, p.window), n_sinks = LISTED ? 0 : min(p.sinks, first);
   // chunks: tree nodes, sinks before the window, window
   const int ct = (p.N + kF32Keys - 1) / kF32Keys, cs = ct + (n_sinks + kF32Keys - 1) / kF32Keys;
-  const int chunks = cs + (L - first + kF32Keys - 1) / kF32Keys;
+  const int listed = LISTED ? p.list_len * p.page_size : 0;  // keys of the list
+  const int chunks = cs + ((LISTED ? listed : L - first) + kF32Keys - 1) / kF32Keys;
   float *sk = sm + warp * Lay::CHUNK, *sv = sk + kF32Keys * KS, *sp = sm + Lay::OFF_P + warp * kF32Keys * R;
   const float *gkt = static_cast<const float *>(p.k_tree), *gvt = static_cast<const float *>(p.v_tree);
   const float *gkc = static_cast<const float *>(p.cache_k), *gvc = static_cast<const float *>(p.cache_v);
@@ -124,7 +127,13 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   // chunk c into this warp's room; true in the lanes whose key is there
   auto fetch = [&](int c) -> bool {
     const int base = c < cs ? kF32Keys * (c < ct ? c : c - ct) : first + kF32Keys * (c - cs);
-    const int key = base + lane, end = c < ct ? p.N : (c < cs ? n_sinks : L);
+    int key = base + lane;
+    const int end = c < ct ? p.N : (c < cs ? n_sinks : L);
+    if (LISTED && c >= ct) {  // place `key` of the list: a position, or none
+      const int page = key < listed ? p.pages[((size_t)bs * p.Hkv + kvh) * p.list_len + key / p.page_size] : -1;
+      const long long at = (long long)page * p.page_size + key % p.page_size;
+      key = page >= 0 && at < L ? (int)at : end;
+    }
     long long row = -1;
     if (key < end) {
       if (c < ct) {
@@ -164,9 +173,11 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
     uint64_t anc = 0;
     int lo = 0, depth;
     if (at < p.M) {
-      if (!tree_walk(s_par, at / p.G, &anc, &depth) && kvh == 0 && rank == 0) set_status(p.status, SV_DEV_BAD_TREE);
-      lo = window_first(L + depth, p.window);
-      anc = window_ancestors(anc, L, p.window, p.sinks);
+      if (!tree_walk(s_par, node0 + at / p.G, &anc, &depth) && kvh == 0 && rank == 0) set_status(p.status, SV_DEV_BAD_TREE);
+      if (!LISTED) {
+        lo = window_first(L + depth, p.window);
+        anc = window_ancestors(anc, L, p.window, p.sinks);
+      }
     }
     s_anc[tid] = anc;
     s_lo[tid] = lo;
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const bool see = there && (c < ct ? ((s_anc[r] >> (key & 63)) & 1ull) != 0
-                                        : (c < cs || key >= s_lo[r] || key < p.sinks));
+                                        : (LISTED || c < cs || key >= s_lo[r] || key < p.sinks));
       const float x = see ? s[r] * p.scale_log2 : -INFINITY;
       const float top = fmaxf(warp_max(x), m[r]);
       const float a = exp2f(m[r] - top);
@@ -287,7 +298,7 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   if (C > 1) cluster_merge<D>(sm, D, s_cm, s_cl, R, C, rank, kF32None, sm + Lay::CHUNK, store);
 }
 
-template <int D, int R>
+template <int D, int R, bool LISTED>
 cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
   using Lay = F32Layout<D, R>;
   static_assert(Lay::SMEM <= 227 * 1024, "shared memory");
@@ -296,7 +307,7 @@ cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr[dev].load()) {
     const cudaError_t e =
-        cudaFuncSetAttribute(window_f32_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+        cudaFuncSetAttribute(window_f32_kernel<D, R, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev].store(true);
   }
@@ -313,25 +324,25 @@ cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, R>, p);
+  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, R, LISTED>, p);
 }
 
-}  // namespace
-
-cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t s) {
+// `kv_units` sequences (or sets of nodes) and KV heads of p.M rows, against up to `keys` keys.
+template <bool LISTED>
+cudaError_t launch_f32(AttnParams p, long long kv_units, long long keys, int num_sms, cudaStream_t s) {
   // Rows of a CTA and CTAs per unit (splits): few rows are done sooner, many read K and V fewer
   // times.  As fitted to measurements (us, 4 to 128 KV heads of 1 to 64 rows, windows 17 to 2049; one
   // CTA per SM): a wave of CTAs takes 3.4 + 0.45 rows and 2.3 + 0.25 rows for every further chunk of
   // its warps, a cluster 2 more.  20 KV heads of 5 rows of 64, window 129: 4.7 us with a row each
   // against 7.8 with eight; 32 of 20 rows of 128, window 2049, 98 with eight (two take 128).
-  const int span = p.window - 1 < p.cap ? p.window - 1 : p.cap, warps = p.D == 64 ? 8 : 4;
-  const int chunks = span / kF32Keys + (p.N + p.sinks) / kF32Keys + 2;
+  const int warps = p.D == 64 ? 8 : 4;
+  const int chunks = (int)(keys / kF32Keys) + (p.N + p.sinks) / kF32Keys + 2;
   int rows = 1;
   long long units = 0;
   double best = 0;
   for (int r = 1; r <= 8 && (r == 1 || r < 2 * p.M); r *= 2)
     for (int c = 1; c <= 8; c *= 2) {
-      const long long u = (long long)p.B * p.Hkv * ((p.M + r - 1) / r);
+      const long long u = kv_units * ((p.M + r - 1) / r);
       if (c == 8 && u * c > num_sms * 2 / 3) break;  // 16 clusters of 8 do not find room together
       const double waves = (double)((u * c + num_sms - 1) / num_sms);
       const int further = (chunks + c * warps - 1) / (c * warps) - 1;
@@ -346,15 +357,32 @@ cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t 
   const long long ctas = units * p.splits;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   switch (rows * 1000 + p.D) {
-    case 1064: return launch_f32_d<64, 1>(p, ctas, s);
-    case 2064: return launch_f32_d<64, 2>(p, ctas, s);
-    case 4064: return launch_f32_d<64, 4>(p, ctas, s);
-    case 8064: return launch_f32_d<64, 8>(p, ctas, s);
-    case 1128: return launch_f32_d<128, 1>(p, ctas, s);
-    case 2128: return launch_f32_d<128, 2>(p, ctas, s);
-    case 4128: return launch_f32_d<128, 4>(p, ctas, s);
-    default: return launch_f32_d<128, 8>(p, ctas, s);
+    case 1064: return launch_f32_d<64, 1, LISTED>(p, ctas, s);
+    case 2064: return launch_f32_d<64, 2, LISTED>(p, ctas, s);
+    case 4064: return launch_f32_d<64, 4, LISTED>(p, ctas, s);
+    case 8064: return launch_f32_d<64, 8, LISTED>(p, ctas, s);
+    case 1128: return launch_f32_d<128, 1, LISTED>(p, ctas, s);
+    case 2128: return launch_f32_d<128, 2, LISTED>(p, ctas, s);
+    case 4128: return launch_f32_d<128, 4, LISTED>(p, ctas, s);
+    default: return launch_f32_d<128, 8, LISTED>(p, ctas, s);
   }
+}
+
+}  // namespace
+
+cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t s) {
+  const int span = p.window - 1 < p.cap ? p.window - 1 : p.cap;
+  return launch_f32<false>(p, (long long)p.B * p.Hkv, span, num_sms, s);
+}
+
+cudaError_t launch_sparse_attention_f32(AttnParams p, const ListArgs &l, int num_sms, cudaStream_t s) {
+  p.pages = l.pages;
+  p.list_len = l.list_len;
+  p.page_size = l.page_size;
+  p.sets = l.sets;
+  p.set_nodes = p.N / l.sets;
+  p.M = p.set_nodes * p.G;
+  return launch_f32<true>(p, (long long)p.B * l.sets * p.Hkv, (long long)l.list_len * l.page_size, num_sms, s);
 }
 
 }  // namespace sv
