@@ -68,19 +68,19 @@ struct JoinedKeys {
       const int a = p.group_start[g], e = p.group_start[g + 1];
       bad |= a < 0 || e < a || e > p.B;
       if (a <= b && b < e) {
-        const int len = min(max(p.shared_len[g], 0), p.cap) & ~15;
         s_group[0] = g;
         s_group[1] = a;
-        s_group[2] = len;
+        s_group[2] = p.shared_len[g];
         found = 1;
-        // a group's shared keys are every member's
-        if (reports && p.shared_len[g] > p.prefix_len[b]) set_status(p.status, SV_DEV_BAD_PREFIX);
       }
     }
     bad = __syncthreads_or(bad);
     found = __syncthreads_or(found);
     if (bad || !found) return {-1, 0, 0};
-    return {s_group[0], s_group[1], s_group[2]};
+    const int len = s_group[2];
+    // (a group's shared keys are every member's)
+    if (reports && threadIdx.x == 0 && len > p.prefix_len[b]) set_status(p.status, SV_DEV_BAD_PREFIX);
+    return {s_group[0], s_group[1], min(max(len, 0), p.cap) & ~15};
   }
   // Where the stacked kernel has left the pieces of a row: its unit's share of the work, cut where a
   // CTA's share ends (of C CTAs CTA c has the work items [W c / C, W (c + 1) / C)).
