@@ -147,7 +147,8 @@ __device__ __forceinline__ bool stack_wait(uint64_t *bar, uint32_t parity, volat
   return true;
 }
 
-template <int D, bool LIST>
+// LIST: listed pages; GROUPED: pages that come with both 64-column halves in one copy, as groups of 8 rows.
+template <int D, bool LIST, bool GROUPED>
 __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __grid_constant__ StackParams p) {
   using Lay = StackLayout<D>;
   constexpr int ST = Lay::ST, KB = Lay::KB;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
         uint8_t *dst = ring + st * Lay::KV_BYTES;
         const CUtensorMap *map = is_v ? &p.tm_v : &p.tm_k;
         if (box) {
-          if (p.grouped) {
+          if (GROUPED) {
             tma_load_5d_hint(dst + lane * 16 * (D * 2), map, 0, 0, 0, c.row >> 3, pc.head, &full[st], policy);
           } else {
 #pragma unroll
@@ -355,75 +356,92 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
           ++tiles;
         }
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9) {
       // ----------------------------------------------------------------- issue
+      // The whole warp walks and waits, so that what the elected thread issues is in uniform registers
+      // (one thread alone in this loop: 147 cycles per MMA instead of XXX).
       constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0, 0), id_o = idesc_bf16(kRows, D, 0, 1);
-      const int block = p.grouped ? 1024 : kKeys * 128, step8 = p.grouped ? KB * 1024 : 1024;
+      constexpr uint32_t kBlock = GROUPED ? 1024 : kKeys * 128, kStep8 = GROUPED ? KB * 1024 : 1024;
       const uint64_t dq = sdesc_sw128(smem_u32(sm), 16, 1024);
-      const uint64_t dk = sdesc_sw128(smem_u32(ring), 16, step8), dv = sdesc_sw128(smem_u32(ring), block, step8);
-      int r = 0, pieces = 0, na = 0, nb = 0;  // stages used, pieces, key tiles of A and of B
-      auto scores = [&](int x, int st) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t a = dq + (uint64_t)((x * Lay::Q_TILE + (k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4);
-          const uint64_t b = dk + (uint64_t)((st * Lay::KV_BYTES + (k >> 2) * block + (k & 3) * 32) >> 4);
-          umma_bf16(tmem + x * kKeys, a, b, id_s, k > 0);
-        }
-        umma_commit(&s_full[x]);
+      const uint64_t dk = sdesc_sw128(smem_u32(ring), 16, kStep8), dv = sdesc_sw128(smem_u32(ring), kBlock, kStep8);
+      int pieces = 0, na = 0, nb = 0;  // pieces, key tiles of A and of B
+      int st = 0, par = 0;             // the next stage and its parity
+      auto next_stage = [&]() {
+        if (++st == ST) st = 0, par ^= 1;
       };
-      auto outputs = [&](int x, int st, bool first, int n) -> bool {
+      auto scores = [&](int x, int at) {
+        const uint64_t a = dq + (uint64_t)(x * Lay::Q_TILE >> 4), b = dk + (uint64_t)(at * (Lay::KV_BYTES >> 4));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            umma_bf16(tmem + x * kKeys, a + (uint64_t)(((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4),
+                      b + (uint64_t)(((k >> 2) * kBlock + (k & 3) * 32) >> 4), id_s, k > 0);
+          umma_commit(&s_full[x]);
+        }
+        __syncwarp();
+      };
+      auto outputs = [&](int x, int at, bool first, int n) -> bool {
+        const uint64_t v = dv + (uint64_t)(at * (Lay::KV_BYTES >> 4));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!stack_wait(h ? &p_full[x] : &p_half[x], n & 1, abort_flag, limit)) return false;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 4 * h; k < 4 * h + 4; ++k)
-            umma_bf16_ts(tmem + 256 + x * D, tmem + x * kKeys + k * 8, dv + (uint64_t)((st * Lay::KV_BYTES + k * 2 * step8) >> 4),
-                         id_o, (!first || k > 0) ? 1u : 0u);
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              umma_bf16_ts(tmem + 256 + x * D, tmem + x * kKeys + k * 8, v + (uint64_t)(k * 2 * kStep8 >> 4), id_o,
+                           (!first || k > 0) ? 1u : 0u);
+          }
+          __syncwarp();
         }
         return true;
+      };
+      auto commit = [&](uint64_t *bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
       };
       StackPiece pc;
       bool ok = true;
       while (ok && next_piece<LIST>(walk, p, tables, pc)) {
         const bool two = pc.tokens > p.tile_tokens;
         const int n = pc.t1 - pc.t0;
-        ok = stack_wait(q_full, pieces & 1, abort_flag, limit) && stack_wait(&full[r % ST], (r / ST) & 1, abort_flag, limit);
+        ok = stack_wait(q_full, pieces & 1, abort_flag, limit) && stack_wait(&full[st], par, abort_flag, limit);
         if (!ok) break;
         tc_fence_after();
-        scores(0, r % ST);
-        if (two) scores(1, r % ST);
-        umma_commit(&empty[r % ST]);
-        if (n == 1) umma_commit(q_empty);
-        ++r;
+        scores(0, st);
+        if (two) scores(1, st);
+        commit(&empty[st]);
+        if (n == 1) commit(q_empty);
+        next_stage();
         for (int i = 0; i < n; ++i) {
-          const int sv = r % ST, sk = (r + 1) % ST;
+          const int sv = st, pv = par;
+          next_stage();
           const bool more = i + 1 < n;
-          ok = stack_wait(&full[sv], (r / ST) & 1, abort_flag, limit) &&
-               (!more || stack_wait(&full[sk], ((r + 1) / ST) & 1, abort_flag, limit)) && outputs(0, sv, i == 0, na);
+          ok = stack_wait(&full[sv], pv, abort_flag, limit) && (!more || stack_wait(&full[st], par, abort_flag, limit)) &&
+               outputs(0, sv, i == 0, na);
           if (!ok) break;
           ++na;
-          if (more) scores(0, sk);
-          else umma_commit(&o_full[0]);
+          if (more) scores(0, st);
+          else commit(&o_full[0]);
           if (two) {
             ok = outputs(1, sv, i == 0, nb);
             if (!ok) break;
             ++nb;
           }
-          umma_commit(&empty[sv]);
+          commit(&empty[sv]);
           if (more) {
-            if (two) scores(1, sk);
-            umma_commit(&empty[sk]);
-            if (i + 2 == n) umma_commit(q_empty);
+            if (two) scores(1, st);
+            commit(&empty[st]);
+            if (i + 2 == n) commit(q_empty);
+            next_stage();
           } else if (two) {
-            umma_commit(&o_full[1]);
+            commit(&o_full[1]);
           }
-          r += more ? 2 : 1;
         }
         ++pieces;
       }
       // every MMA has completed before TMEM is given up
-      umma_commit(drain);
+      commit(drain);
       const unsigned long long t0 = global_ns();
       while (!mbar_try_wait(drain, 0) && global_ns() - t0 < kWaitLimitNs) {
       }
@@ -465,7 +483,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
           for (int i = tid; i < kKeys * (D / 8); i += 128) {
             const int k = i / (D / 8), c = i % (D / 8);
             if ((k & 15) < (int)(keys >> (8 * (k >> 4)) & 31)) continue;
-            uint8_t *at = p.grouped ? v + (k >> 3) * (KB * 1024) + (c >> 3) * 1024 + (k & 7) * 128 + (c & 7) * 16
+            uint8_t *at = GROUPED ? v + (k >> 3) * (KB * 1024) + (c >> 3) * 1024 + (k & 7) * 128 + (c & 7) * 16
                                     : v + (c >> 3) * (kKeys * 128) + k * 128 + (c & 7) * 16;
             // (whole rows are zeroed, so that the swizzle of their 16-byte chunks does not matter)
             *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
@@ -589,13 +607,13 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
   }
 }
 
-template <int D, bool LIST>
+template <int D, bool LIST, bool GROUPED>
 cudaError_t launch_stacked_typed(const StackParams &p, int grid, cudaStream_t s) {
   using Lay = StackLayout<D>;
   static std::atomic<bool> attr[64];
   int dev = 0;
   cudaGetDevice(&dev);
-  auto kern = stacked_attn_kernel<D, LIST>;
+  auto kern = stacked_attn_kernel<D, LIST, GROUPED>;
   if (dev < 0 || dev >= 64 || !attr[dev].load()) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
     if (e != cudaSuccess) return e;
@@ -607,8 +625,9 @@ cudaError_t launch_stacked_typed(const StackParams &p, int grid, cudaStream_t s)
 }  // namespace
 
 cudaError_t launch_stacked(const StackParams &p, int D, bool listed, int grid, cudaStream_t s) {
-  if (D == 128) return listed ? launch_stacked_typed<128, true>(p, grid, s) : launch_stacked_typed<128, false>(p, grid, s);
-  return listed ? launch_stacked_typed<64, true>(p, grid, s) : launch_stacked_typed<64, false>(p, grid, s);
+  if (D == 64) return listed ? launch_stacked_typed<64, true, false>(p, grid, s) : launch_stacked_typed<64, false, false>(p, grid, s);
+  if (p.grouped) return listed ? launch_stacked_typed<128, true, true>(p, grid, s) : launch_stacked_typed<128, false, true>(p, grid, s);
+  return listed ? launch_stacked_typed<128, true, false>(p, grid, s) : launch_stacked_typed<128, false, false>(p, grid, s);
 }
 
 }  // namespace sv

@@ -129,12 +129,6 @@ template <class P>
 __device__ __forceinline__ bool limited_wait(uint64_t *bar, uint32_t parity, volatile int *abort, const P &p) {
   return mbar_try_wait(bar, parity) || limited_wait_slow(bar, parity, abort, p.try_ns, p.wait_ns);
 }
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
-  return one != 0;
-}
 // Transpose of an 8x8 matrix of 16-bit elements held in fragment layout by a warp.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   uint32_t d;
@@ -699,6 +693,52 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
       inv[j][1] = s_inv[r0 + 2 * ft + 1];
     }
   }
+  // the pieces' part of what this slice merges: all loads of a step of 8 rows side by side
+  float4 more[Keys::kPieces ? DO : 1][Keys::kPieces ? NT : 1];
+  if constexpr (Keys::kPieces) {
+    Pieces pc[NT][2];
+    int most = 0;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        pc[j][e] = s_piece[rg * 8 * NT + 8 * j + 2 * ft + e];
+        most = max(most, pc[j][e].count);
+#pragma unroll
+        for (int d = 0; d < DO; ++d) more[d][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    for (int k = 0; k < most; ++k) {
+      // (rows with fewer pieces read their last one again, with weight 0)
+      float a[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = p.part_ml[pc[j][e].row].x;
+          a[j][e] = k < pc[j][e].count ? ex2_approx(x - tops[j][e]) : 0.f;
+        }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float *r0 = p.part_o + (size_t)pc[j][0].row * D + 16 * DO * slice + fg;
+        const float *r1 = p.part_o + (size_t)pc[j][1].row * D + 16 * DO * slice + fg;
+        float4 y[DO];
+#pragma unroll
+        for (int d = 0; d < DO; ++d) y[d] = make_float4(r0[16 * d], r1[16 * d], r0[16 * d + 8], r1[16 * d + 8]);
+#pragma unroll
+        for (int d = 0; d < DO; ++d) {
+          more[d][j].x = fmaf(a[j][0], y[d].x, more[d][j].x);
+          more[d][j].y = fmaf(a[j][1], y[d].y, more[d][j].y);
+          more[d][j].z = fmaf(a[j][0], y[d].z, more[d][j].z);
+          more[d][j].w = fmaf(a[j][1], y[d].w, more[d][j].w);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (k + 1 < pc[j][e].count) pc[j][e].row += kStackRows;
+    }
+  }
 #pragma unroll
   for (int d = 0; d < DT; ++d) {
     if (d / DO != slice) continue;
@@ -718,21 +758,10 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
         v.w += x[j][k].w;
       }
       if constexpr (Keys::kPieces) {
-        if (rank == 0) {
-          const int r0 = rg * 8 * NT + 8 * j + 2 * ft, d0 = 16 * d + fg;
-          auto add = [&](int e, float &lo, float &hi) {
-            const Pieces pc = s_piece[r0 + e];
-            for (int k = 0; k < pc.count; ++k) {
-              const size_t at = pc.row + (size_t)k * kStackRows;
-              const float a = ex2_approx(p.part_ml[at].x - tops[j][e]);
-              const float *row = p.part_o + at * D + d0;
-              lo = fmaf(a, row[0], lo);
-              hi = fmaf(a, row[8], hi);
-            }
-          };
-          add(0, v.x, v.z);
-          add(1, v.y, v.w);
-        }
+        v.x += more[d % DO][j].x;
+        v.y += more[d % DO][j].y;
+        v.z += more[d % DO][j].z;
+        v.w += more[d % DO][j].w;
       }
       if (C == 1) {
         emit(d, rows[j], make_float4(v.x * inv[j][0], v.y * inv[j][1], v.z * inv[j][0], v.w * inv[j][1]));
