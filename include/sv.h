@@ -227,7 +227,7 @@ size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
  * Workspace: sv_shared_attention_workspace_size() bytes, 16-byte aligned (0 for float32); it needs no
  * initial value.  Calls that share one must be stream-ordered.  max_prefix as for
  * sv_tree_attention. */
-#define SV_MAX_SHARED_GROUPS 256
+#define SV_MAX_SHARED_GROUPS 128
 sv_status sv_shared_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
                               const void *k_tree, const void *v_tree, sv_kv_cache cache,
                               const int32_t *parent, int parent_stride, float scale,

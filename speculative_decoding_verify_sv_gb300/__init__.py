@@ -42,7 +42,7 @@ SV_MAX_TREE_NODES = 64
 SV_MAX_SINKS, SV_MAX_TABLE_BATCH = 64, 8192
 SV_DEV_BAD_TOKEN, SV_DEV_BAD_BLOCK, SV_DEV_BAD_PREFIX, SV_DEV_ZERO_DRAFT_PROB = 1, 2, 4, 8
 SV_DEV_TIMEOUT, SV_DEV_LAYOUT, SV_DEV_BAD_TREE, SV_DEV_BAD_GROUP = 0x10, 0x20, 0x40, 0x80
-SV_MAX_SHARED_GROUPS, SV_MAX_SCORE_PAGES = 256, 32768
+SV_MAX_SHARED_GROUPS, SV_MAX_SCORE_PAGES = 128, 32768
 
 _STATUS_NAMES = {1: "SV_ERR_INVALID_ARG", 2: "SV_ERR_UNSUPPORTED", 3: "SV_ERR_WORKSPACE",
                  4: "SV_ERR_CUDA"}

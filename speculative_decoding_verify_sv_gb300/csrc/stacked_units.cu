@@ -7,8 +7,9 @@
 //
 // Pieces: the kernel takes the tree's nodes and a sequence's own keys (those behind what it shares; none
 // with listed pages), and joins the stacked kernel's pieces of the same rows in its merge, as one more part
-// beside those of its own warps.  It is set up while the stacked kernel still runs, reads K and V as soon
-// as an SM is free, and waits for the pieces only then.
+// beside those of its own warps.  A row's first piece is copied to shared memory while the keys are worked
+// on, the others (units that were cut) follow through the ring's room.  (Read straight from memory in the
+// merge, element by element, they took 10 us per CTA.)
 #include "unit_attention.cuh"
 
 namespace sv {
@@ -38,7 +39,7 @@ struct ListedKeys {
   __device__ static __forceinline__ void begin(const Params &) { wait_previous(); }
   __device__ static __forceinline__ int sequence(const Params &p, int bs) { return bs / p.sets; }
   __device__ static __forceinline__ int first_node(const Params &p, int bs) { return bs % p.sets * p.set_nodes; }
-  __device__ static __forceinline__ SharedPart shared_part(const Params &, int, bool) {
+  __device__ static __forceinline__ SharedPart shared_part(const Params &, int, bool, SharedPart *) {
     __syncthreads();
     return {};
   }
@@ -51,68 +52,58 @@ struct ListedKeys {
 struct JoinedKeys {
   using Params = PieceParams;
   static constexpr bool kWindow = false, kListed = false, kPieces = true;
-  // What it reads before the merge was there before the stacked kernel, which lets this one start only
-  // behind its own wait for what came before.
-  __device__ static __forceinline__ void begin(const Params &) {}
+  __device__ static __forceinline__ void begin(const Params &) { wait_previous(); }
   __device__ static __forceinline__ int sequence(const Params &, int bs) { return bs; }
   __device__ static __forceinline__ int first_node(const Params &, int) { return 0; }
-  // The group of sequence b.  A call with a group_start that does not ascend shares nothing.
-  __device__ static __forceinline__ SharedPart shared_part(const Params &p, int b, bool reports) {
-    if (!p.group_start) {
+  // The group of sequence b and its share of the stacked kernel's work, in one round trip to memory.  A call
+  // with a group_start that does not ascend shares nothing.
+  __device__ static __forceinline__ SharedPart shared_part(const Params &p, int b, bool reports, SharedPart *s_part) {
+    if (!p.group_start) {  // listed pages: no own keys
       __syncthreads();
-      return {0, b, INT32_MAX};  // (no own keys)
+      return {b, INT32_MAX, p.list_tiles, p.row_tiles, b * p.Hkv * p.row_tiles, (long long)b * p.Hkv * p.row_tiles * p.list_tiles,
+              (long long)p.B * p.Hkv * p.row_tiles * p.list_tiles};
     }
-    __shared__ int s_group[3];
     int bad = 0, found = 0;
     for (int g = threadIdx.x; g < p.groups; g += kWinThreads) {
-      const int a = p.group_start[g], e = p.group_start[g + 1];
+      const int a = p.group_start[g], e = p.group_start[g + 1], len = p.shared_len[g];
+      const long long first = p.header[1 + 2 * g], at = p.header[2 + 2 * g], total = p.header[0];
       bad |= a < 0 || e < a || e > p.B;
       if (a <= b && b < e) {
-        s_group[0] = g;
-        s_group[1] = a;
-        s_group[2] = p.shared_len[g];
+        const int per = (int)(((long long)(e - a) * p.N + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens));
+        *s_part = {a, len, (int)(at >> 32), per, (int)at, first, total};
         found = 1;
       }
     }
     bad = __syncthreads_or(bad);
     found = __syncthreads_or(found);
-    if (bad || !found) return {-1, 0, 0};
-    const int len = s_group[2];
+    if (bad || !found) return {0, 0, 0, 0, 0, 0, 0};
+    SharedPart part = *s_part;
     // (a group's shared keys are every member's)
-    if (reports && threadIdx.x == 0 && len > p.prefix_len[b]) set_status(p.status, SV_DEV_BAD_PREFIX);
-    return {s_group[0], s_group[1], min(max(len, 0), p.cap) & ~15};
+    if (reports && threadIdx.x == 0 && part.len > p.prefix_len[b]) set_status(p.status, SV_DEV_BAD_PREFIX);
+    part.len = min(max(part.len, 0), p.cap) & ~15;
+    return part;
   }
   // Where the stacked kernel has left the pieces of a row: its unit's share of the work, cut where a
   // CTA's share ends (of C CTAs CTA c has the work items [W c / C, W (c + 1) / C)).
   __device__ static __forceinline__ Pieces pieces_of(const Params &p, int b, int head, int node, int g, const SharedPart &part) {
     Pieces out;
-    long long total, first, unit;
-    int tiles, token = node;
-    if (!p.group_start) {
-      tiles = p.list_tiles;
-      unit = ((long long)b * p.Hkv + head) * p.row_tiles;
-      first = unit * tiles;
-      total = (long long)p.B * p.Hkv * p.row_tiles * tiles;
-    } else {
-      if (part.group < 0) return out;
-      const long long at = p.header[2 + 2 * part.group];
-      tiles = (int)(at >> 32);
-      if (tiles == 0) return out;
-      total = p.header[0];
-      const int members = p.group_start[part.group + 1] - part.start;
-      const int per = (members * p.N + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-      unit = (int)at + (long long)head * per;
-      first = p.header[1 + 2 * part.group] + (long long)head * per * tiles;
-      token += (b - part.start) * p.N;
-    }
-    const int tile = token / (2 * p.tile_tokens), in = token % (2 * p.tile_tokens);
-    unit += tile;
-    first += (long long)tile * tiles;
-    const long long ctas = min((long long)p.grid, total);
-    const int c0 = (int)(((first + 1) * ctas - 1) / total), c1 = (int)(((first + tiles) * ctas - 1) / total);
-    out.row = (int)(unit + c0) * kStackRows + in / p.tile_tokens * 128 + in % p.tile_tokens * p.G + g;
+    if (part.tiles == 0) return out;
+    const int token = (b - part.start) * p.N + node, tile = token / (2 * p.tile_tokens), in = token % (2 * p.tile_tokens);
+    const int unit = head * part.per + tile;  // of the group
+    const long long first = part.first + (long long)unit * part.tiles, ctas = min((long long)p.grid, part.total);
+    auto cta_of = [&](long long item) {
+      const long long x = (item + 1) * ctas - 1;
+      return part.total * ctas <= UINT32_MAX ? (int)((unsigned)x / (unsigned)part.total) : (int)(x / part.total);
+    };
+    const int c0 = cta_of(first), c1 = cta_of(first + part.tiles - 1);
+    out.row = (part.unit + unit + c0) * kStackRows + in / p.tile_tokens * 128 + in % p.tile_tokens * p.G + g;
     out.count = c1 - c0 + 1;
     return out;
+  }
+  // Piece k of a row, 16 bytes u of its D / 4 (a piece is stored by these, rows side by side).
+  template <int D>
+  __device__ static __forceinline__ const float4 *piece(const Params &p, int row, int k, int u) {
+    return reinterpret_cast<const float4 *>(p.part_o) + ((size_t)(row / kStackRows + k) * (D / 4) + u) * kStackRows + row % kStackRows;
   }
   template <int D, int NT, int RG>
   static auto kernel() {

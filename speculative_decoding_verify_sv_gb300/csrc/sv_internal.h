@@ -132,7 +132,7 @@ struct StackParams {
   const int32_t *prefix_len, *block_table;
   unsigned int *status;
   long long *header;  // shared prefixes: the work and, per group, its first work item, key tiles and first unit
-  float *part_o;      // [pieces][kStackRows][D] outputs, unnormalised
+  float *part_o;      // [pieces][D / 4][kStackRows][4] outputs, unnormalised
   float2 *part_ml;    // [pieces][kStackRows] maximum (log2 units) and sum
   int groups, B, N, Hkv, G;
   int tile_tokens;    // tokens of an MMA tile (G rows each)

@@ -65,8 +65,8 @@ struct WinLayout {
   static constexpr int KB = D / 64;             // 64-column blocks of a row
   static constexpr int K_BYTES = kWinGroup * D * 2;
   static constexpr int G_BYTES = 2 * K_BYTES;   // a group's K and V
-  // the slices' rings: what two CTAs per SM leave room for beside their query rows
-  static constexpr int RING = (RG == 2 ? 80 : 96) * 1024;
+  // the slices' rings: what two CTAs per SM leave room for beside their query rows (and their pieces)
+  static constexpr int RING = (Keys::kPieces ? (RG == 2 ? 48 : 64) : (RG == 2 ? 80 : 96)) * 1024;
   static constexpr int ST = RING / (KS * G_BYTES);  // stages of a slice's ring
   static constexpr int RB = 8 * NT * RG;        // query rows of a CTA
   static constexpr int DO = D / 16 / KS;        // 16-dimension tiles of the outputs that a slice merges
@@ -87,10 +87,15 @@ struct WinLayout {
   static constexpr int OFF_PAR = OFF_ROW + RB * 4;      // [64]
   static constexpr int OFF_COPIED = OFF_PAR + kMaxNodes * 4;  // [KS][ST]
   static constexpr int OFF_ABORT = OFF_COPIED + KS * ST * 4;
-  // positions of the groups in the ring [KS][ST] (listed pages); pieces [RB] and their maxima [RB]
-  static constexpr int OFF_MORE = OFF_ABORT + 16;
-  static constexpr int SMEM = OFF_MORE + (Keys::kListed ? KS * ST * 4 : Keys::kPieces ? RB * 12 : 0);
-  static_assert(OFF_JOIN + JOIN <= RING, "the merge goes on in the ring's room");
+  // listed pages: positions of the groups in the ring [KS][ST]; pieces: where the rows' pieces are [RB],
+  // their maxima and sums [RB], the weights of the first two [2][RB] and of those in the ring's room
+  // [CAP][RB], and the outputs of the first ones (and second ones) [PB][RB][D + 4]
+  static constexpr int CAP = RING / (RB * D * 4), PB = RG == 1 ? 2 : 1;
+  static constexpr int OFF_MORE = (OFF_ABORT + 16 + 15) & ~15;
+  static constexpr int OFF_PIECE = OFF_MORE + RB * 24 + CAP * RB * 4 + 64;
+  static constexpr int SMEM = Keys::kListed ? OFF_MORE + KS * ST * 4 : Keys::kPieces ? OFF_PIECE + PB * RB * (D + 4) * 4 : OFF_ABORT + 16;
+  // (with pieces, clusters are for CTAs of up to 24 rows)
+  static_assert((Keys::kPieces && RB > 24 ? OFF_JOIN : OFF_JOIN + JOIN) <= RING, "the merge goes on in the ring's room");
   static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -101,7 +106,9 @@ struct Pieces {
 };
 // What a sequence shares: the group, its first sequence and the number of keys.
 struct SharedPart {
-  int group, start, len;
+  int start, len;          // of its group: the first sequence, the keys
+  int tiles, per, unit;    // key tiles, row tiles of a KV head, first unit (tiles = 0: no pieces)
+  long long first, total;  // first work item of the group, all of the call's
 };
 
 // Wait for the phase of the given parity; false if it ran past the limit (then *abort is raised) or
@@ -168,7 +175,9 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   int *s_row = reinterpret_cast<int *>(sm + Lay::OFF_ROW);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Lay::OFF_ABORT);
   Pieces *s_piece = reinterpret_cast<Pieces *>(sm + Lay::OFF_MORE);
-  float *s_top = reinterpret_cast<float *>(sm + Lay::OFF_MORE + RB * 8);
+  float *s_top = reinterpret_cast<float *>(sm + Lay::OFF_MORE + RB * 8), *s_sum = s_top + RB, *s_w = s_sum + RB, *s_weight = s_w + 2 * RB;
+  float *s_out = reinterpret_cast<float *>(sm + Lay::OFF_PIECE);
+  int *s_most = const_cast<int *>(abort_flag) + 1;  // the most pieces of a row
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (the same in every lane, and known to be)
@@ -201,11 +210,11 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     const int R = mt * RB + tid, node = R / p.G;
     s_row[tid] = R < p.M ? (b * p.N + node0 + node) * p.Hq + kvh * p.G + R - node * p.G : -1;
   }
-  if (tid == 0) *abort_flag = 0;
+  if (tid == 0) *abort_flag = *s_most = 0;
   Keys::begin(p);
   int L = p.prefix_len[b];
   if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
-  const SharedPart shared = Keys::shared_part(p, b, reports);  // (a barrier)
+  const SharedPart shared = Keys::shared_part(p, b, reports, reinterpret_cast<SharedPart *>(sm + Lay::OFF_PIECE - 64));  // (a barrier)
   // query rows as B operands, on their way before the first keys
   uint8_t *s_q = sm + Lay::OFF_Q;
 #pragma unroll
@@ -292,6 +301,17 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     if (elect_one() && (RG == 1 || parity < 0 || limited_wait(&empty[st], parity, abort_flag, p))) copy(i, row, pos, tree, st);
     __syncwarp();
   };
+  // a row's pieces, and the maxima and sums of the first two
+  Pieces pieces;
+  float2 ml0 = make_float2(kWinNone, 0.f), ml1 = ml0;
+  if constexpr (Keys::kPieces) {
+    if (tid < RB && rank == 0 && mt * RB + tid < p.M) {
+      const int R = mt * RB + tid;
+      pieces = Keys::pieces_of(p, b, kvh, R / p.G, R % p.G, shared);
+      if (pieces.count > 0) ml0 = p.part_ml[pieces.row];
+      if (pieces.count > 1) ml1 = p.part_ml[pieces.row + kStackRows];
+    }
+  }
   // The first groups, one after another so that the first one is whole soon (2048 units of 32 rows,
   // window 1025, 169 us against 176 with a lane each); with a lane each only for 33 to 48 rows (512
   // units, window 4097, 179 us against 185; 256 units of 64 rows, window 513, 23.8 against 24.9).
@@ -322,9 +342,37 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     }
     s_anc[tid] = anc;
     s_lo[tid] = lo;
+    if constexpr (Keys::kPieces) {
+      // the maximum and sum of the row's pieces
+      float top = fmaxf(ml0.x, ml1.x), sum = ml0.y * ex2_approx(ml0.x - top) + ml1.y * ex2_approx(ml1.x - top);
+#pragma unroll 8
+      for (int k = 2; k < pieces.count; ++k) {
+        const float2 ml = p.part_ml[pieces.row + (size_t)k * kStackRows];
+        const float up = fmaxf(top, ml.x);
+        sum = sum * ex2_approx(top - up) + ml.y * ex2_approx(ml.x - up);
+        top = up;
+      }
+      s_piece[tid] = pieces;
+      s_top[tid] = top;
+      s_sum[tid] = sum;
+      s_w[tid] = pieces.count > 0 ? ex2_approx(ml0.x - top) : 0.f;
+      s_w[RB + tid] = pieces.count > 1 ? ex2_approx(ml1.x - top) : 0.f;
+      atomicMax(s_most, pieces.count);
+    }
   }
   cp_async_wait<0>();
   __syncthreads();
+  if constexpr (Keys::kPieces) {
+    // the rows' first pieces, on their way while the keys are worked on
+    for (int k = 0; k < Lay::PB; ++k) {
+      if (k > 0 && *s_most <= k) break;
+      for (int i = tid; i < RB * (D / 4); i += kWinThreads) {
+        const int r = i % RB, u = i / RB;
+        cp_async_16(s_out + (k * RB + r) * (D + 4) + 4 * u, Keys::template piece<D>(p, s_piece[r].row, k, u), k < s_piece[r].count);
+      }
+    }
+    cp_async_commit();
+  }
   // Every row sees every key of the groups [plain0, plain1) of this slice: inside the window of all
   // rows (none starts later than the deepest possible node's), before the prefix's end.
   const int lo_last = Keys::kWindow ? window_first(L + p.N - 1, p.window) : lo_root;
@@ -589,18 +637,53 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   float4 *part = reinterpret_cast<float4 *>(sm);      // [KS taker][KS - 1][RG][DO][NT][32]
   float4 *joined = reinterpret_cast<float4 *>(sm + Lay::OFF_JOIN);  // [C][units of this CTA][32]
   float *c_m = reinterpret_cast<float *>(joined + (U + 8) * 32), *c_l = c_m + 8 * RB;  // [C][RB]
-  Pieces pieces;  // of the rows' shared keys, from the previous kernel: one more part of the merge
   if constexpr (Keys::kPieces) {
-    wait_previous();
-    if (tid < RB) {
-      float top = kWinNone;
-      if (rank == 0 && s_row[tid] >= 0) {
-        const int R = mt * RB + tid;
-        pieces = Keys::pieces_of(p, b, kvh, R / p.G, R % p.G, shared);
-        for (int k = 0; k < pieces.count; ++k) top = fmaxf(top, p.part_ml[pieces.row + (size_t)k * kStackRows].x);
+    // One sum of the rows' pieces by their weights against the rows' maxima, in the place of the first
+    // ones; those past the first PB come through the ring's room.
+    cp_async_wait<0>();
+    __syncthreads();  // (every slice is done with its ring)
+    constexpr int CAP = Lay::CAP, PB = Lay::PB, TPR = RB > 32 ? 2 : RB > 16 ? 4 : RB > 8 ? 8 : 16;  // threads of a row
+    const int most = *s_most, r = tid / TPR, r0 = r < RB ? r : RB - 1;
+    auto row_of = [&](int u) { return reinterpret_cast<float4 *>(s_out + r0 * (D + 4) + 4 * u); };
+    if (r < RB) {
+      const float w0 = s_w[r], w1 = s_w[RB + r];
+      for (int u = tid % TPR; u < D / 4; u += TPR) {
+        float4 x = *row_of(u);
+        x = make_float4(x.x * w0, x.y * w0, x.z * w0, x.w * w0);
+        if (PB > 1 && most > 1) {
+          const float4 y = *reinterpret_cast<const float4 *>(s_out + (RB + r) * (D + 4) + 4 * u);
+          x = make_float4(fmaf(w1, y.x, x.x), fmaf(w1, y.y, x.y), fmaf(w1, y.z, x.z), fmaf(w1, y.w, x.w));
+        }
+        *row_of(u) = x;
       }
-      s_piece[tid] = pieces;
-      s_top[tid] = top;
+    }
+    for (int k0 = PB; k0 < most; k0 += CAP) {
+      const int n_k = min(CAP, most - k0);
+      for (int i = tid; i < n_k * RB * (D / 4); i += kWinThreads) {
+        const int q = i % RB, u = i / RB % (D / 4), k = i / (RB * (D / 4));
+        cp_async_16(sm + (k * RB + q) * (D * 4) + ((u ^ (q & 7)) << 4), Keys::template piece<D>(p, s_piece[q].row, k0 + k, u),
+                    k0 + k < s_piece[q].count);
+      }
+      cp_async_commit();
+      for (int i = tid; i < n_k * RB; i += kWinThreads) {
+        const int q = i % RB, k = k0 + i / RB;
+        const Pieces pc = s_piece[q];
+        s_weight[i] = k < pc.count ? ex2_approx(p.part_ml[pc.row + (size_t)k * kStackRows].x - s_top[q]) : 0.f;
+      }
+      cp_async_wait<0>();
+      __syncthreads();
+      if (r < RB) {
+        for (int u = tid % TPR; u < D / 4; u += TPR) {
+          float4 x = *row_of(u);
+          for (int k = 0; k < n_k; ++k) {
+            const float a = s_weight[k * RB + r];
+            const float4 y = *reinterpret_cast<const float4 *>(sm + (k * RB + r) * (D * 4) + ((u ^ (r & 7)) << 4));
+            x = make_float4(fmaf(a, y.x, x.x), fmaf(a, y.y, x.y), fmaf(a, y.z, x.z), fmaf(a, y.w, x.w));
+          }
+          *row_of(u) = x;
+        }
+      }
+      __syncthreads();
     }
   }
   // Done with the ring.  (Room of its own for what the others write and an arrival at the start gain
@@ -621,7 +704,7 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     }
   __syncthreads();  // (and every slice is done with its ring)
   float w[NT][2];   // this slice's weights against the CTA's maximum
-  float tops[Keys::kPieces ? NT : 1][2];
+  float wp[Keys::kPieces ? NT : 1][2];  // the pieces' weight
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -631,7 +714,7 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) top = fmaxf(top, s_m[k * RB + r]);
       w[j][e] = ex2_approx(m[j][e] - top);
-      if constexpr (Keys::kPieces) tops[j][e] = top;
+      if constexpr (Keys::kPieces) wp[j][e] = ex2_approx(s_top[r] - top);
     }
   auto scaled = [&](int d, int j) {
     return make_float4(o[d][j][0] * w[j][0], o[d][j][1] * w[j][1], o[d][j][2] * w[j][0], o[d][j][3] * w[j][1]);
@@ -654,12 +737,7 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     for (int k = 0; k < KS; ++k) top = fmaxf(top, s_m[k * RB + tid]);
 #pragma unroll
     for (int k = 0; k < KS; ++k) sum += ex2_approx(s_m[k * RB + tid] - top) * s_l[k * RB + tid];
-    if constexpr (Keys::kPieces) {
-      for (int k = 0; k < pieces.count; ++k) {
-        const float2 ml = p.part_ml[pieces.row + (size_t)k * kStackRows];
-        sum += ex2_approx(ml.x - top) * ml.y;
-      }
-    }
+    if constexpr (Keys::kPieces) sum += ex2_approx(s_top[tid] - top) * s_sum[tid];
     if (C == 1) s_inv[tid] = sum > 0.f ? 1.f / sum : 0.f;
   }
   __syncthreads();
@@ -693,52 +771,6 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
       inv[j][1] = s_inv[r0 + 2 * ft + 1];
     }
   }
-  // the pieces' part of what this slice merges: all loads of a step of 8 rows side by side
-  float4 more[Keys::kPieces ? DO : 1][Keys::kPieces ? NT : 1];
-  if constexpr (Keys::kPieces) {
-    Pieces pc[NT][2];
-    int most = 0;
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        pc[j][e] = s_piece[rg * 8 * NT + 8 * j + 2 * ft + e];
-        most = max(most, pc[j][e].count);
-#pragma unroll
-        for (int d = 0; d < DO; ++d) more[d][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    for (int k = 0; k < most; ++k) {
-      // (rows with fewer pieces read their last one again, with weight 0)
-      float a[NT][2];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = p.part_ml[pc[j][e].row].x;
-          a[j][e] = k < pc[j][e].count ? ex2_approx(x - tops[j][e]) : 0.f;
-        }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const float *r0 = p.part_o + (size_t)pc[j][0].row * D + 16 * DO * slice + fg;
-        const float *r1 = p.part_o + (size_t)pc[j][1].row * D + 16 * DO * slice + fg;
-        float4 y[DO];
-#pragma unroll
-        for (int d = 0; d < DO; ++d) y[d] = make_float4(r0[16 * d], r1[16 * d], r0[16 * d + 8], r1[16 * d + 8]);
-#pragma unroll
-        for (int d = 0; d < DO; ++d) {
-          more[d][j].x = fmaf(a[j][0], y[d].x, more[d][j].x);
-          more[d][j].y = fmaf(a[j][1], y[d].y, more[d][j].y);
-          more[d][j].z = fmaf(a[j][0], y[d].z, more[d][j].z);
-          more[d][j].w = fmaf(a[j][1], y[d].w, more[d][j].w);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (k + 1 < pc[j][e].count) pc[j][e].row += kStackRows;
-    }
-  }
 #pragma unroll
   for (int d = 0; d < DT; ++d) {
     if (d / DO != slice) continue;
@@ -758,10 +790,11 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
         v.w += x[j][k].w;
       }
       if constexpr (Keys::kPieces) {
-        v.x += more[d % DO][j].x;
-        v.y += more[d % DO][j].y;
-        v.z += more[d % DO][j].z;
-        v.w += more[d % DO][j].w;
+        const float *x0 = s_out + (rg * 8 * NT + 8 * j + 2 * ft) * (D + 4) + 16 * d + fg, *x1 = x0 + D + 4;
+        v.x = fmaf(wp[j][0], x0[0], v.x);
+        v.y = fmaf(wp[j][1], x1[0], v.y);
+        v.z = fmaf(wp[j][0], x0[8], v.z);
+        v.w = fmaf(wp[j][1], x1[8], v.w);
       }
       if (C == 1) {
         emit(d, rows[j], make_float4(v.x * inv[j][0], v.y * inv[j][1], v.z * inv[j][0], v.w * inv[j][1]));
@@ -856,7 +889,7 @@ struct WinPlan {
 };
 
 // M rows against `groups` groups of keys for each of `kv_units` sequences and KV heads.
-inline WinPlan window_plan(long long kv_units, int M, int groups, int num_sms) {
+inline WinPlan window_plan(long long kv_units, int M, int groups, int num_sms, bool pieces = false) {
   WinPlan plan{};
   const double sms = num_sms, moved = (double)kv_units * groups * kWinGroup * 512 * 1e-6;  // K and V, MB
   for (const WinForm &f : kWinForms) {
@@ -872,7 +905,7 @@ inline WinPlan window_plan(long long kv_units, int M, int groups, int num_sms) {
     // such clusters find no room together, 25 us against 13.)
     long long best = 0;
     int cluster = 1;
-    for (int c = 1; c <= 8; c *= 2) {
+    for (int c = 1; c <= (pieces && rows > 24 ? 1 : 8); c *= 2) {
       const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 16);
       if (c == 1 || cost < best) {
         best = cost;
@@ -964,7 +997,7 @@ inline bool unit_params(WinParams &p, const AttnParams &a, int M) {
 // window_plan takes for them.
 template <class Keys>
 cudaError_t launch_units(typename Keys::Params &p, int D, long long kv_units, int groups, int num_sms, cudaStream_t s) {
-  const WinPlan plan = window_plan(kv_units, p.M, groups, num_sms);
+  const WinPlan plan = window_plan(kv_units, p.M, groups, num_sms, Keys::kPieces);
   p.m_tiles = plan.m_tiles;
   p.cluster = plan.cluster;
   const long long ctas = kv_units * p.m_tiles * p.cluster;

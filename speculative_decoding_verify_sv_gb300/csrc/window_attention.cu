@@ -16,7 +16,7 @@ struct WindowKeys {
   __device__ static __forceinline__ void begin(const Params &) { wait_previous(); }
   __device__ static __forceinline__ int sequence(const Params &, int bs) { return bs; }
   __device__ static __forceinline__ int first_node(const Params &, int) { return 0; }
-  __device__ static __forceinline__ SharedPart shared_part(const Params &, int, bool) {
+  __device__ static __forceinline__ SharedPart shared_part(const Params &, int, bool, SharedPart *) {
     __syncthreads();
     return {};
   }
