@@ -108,155 +108,7 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
   }
 }
 
-// ---------------------------------------------------------------------- scores
-
-constexpr int kScorePages = 16;  // pages of a warp's tile
-constexpr int kScoreCols = 256;  // query rows in shared memory at a time
-
-// The columns of a product are query rows: those of a set one after another, padded (with the set's last
-// row again, which changes no maximum) so that no step of 8 columns holds parts of two sets, or else a
-// whole number of sets.
-__host__ __device__ inline int score_set_cols(int rows) {
-  if (rows >= 8) return (rows + 7) & ~7;
-  return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
-}
-
-// bf16 on mma.sync: the pages are the 16-row side, query rows the 8-column side.  A product's columns may
-// be summed in any order: lane t of a quad takes 16 neighbouring channels of each 64 of a page (32 bytes,
-// straight from memory to operand registers) and of a query row.
-template <int D>
-__global__ void __launch_bounds__(256) page_scores_kernel(const __grid_constant__ ScoreParams p) {
-  constexpr int KB = D / 64, STRIDE = D * 2 + 16;  // (16 more bytes: conflict-free 16-byte reads of 8 rows)
-  extern __shared__ __align__(16) uint8_t score_smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int fg = lane >> 2, ft = lane & 3;
-  const int bh = blockIdx.x / p.splits, part = blockIdx.x % p.splits, h = bh % p.Hkv, b = bh / p.Hkv;
-  wait_previous();
-  int L = p.prefix_len[b];
-  const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
-  if (L < 0 || L > most) {
-    if (h == 0 && part == 0 && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
-    L = L < 0 ? 0 : most;
-  }
-  const int pages = (int)(((long long)L + p.page_size - 1) / p.page_size);
-  const int tiles = (p.P + kScorePages - 1) / kScorePages, per = (tiles + p.splits - 1) / p.splits;
-  const int t0 = part * per, t1 = min(tiles, t0 + per);
-  const int rows = p.set_nodes * p.G, cols = p.sets * p.set_cols;  // rows of a set, columns of all sets
-  float *out = p.out + (size_t)b * p.sets * p.Hkv * p.P + (size_t)h * p.P;  // [sets][.][P]
-  for (int c0 = 0; c0 < cols; c0 += kScoreCols) {
-    const int n = min(kScoreCols, cols - c0), n8 = (n + 7) & ~7;
-    if (c0 > 0) __syncthreads();
-    for (int u = tid; u < n8 * (D / 8); u += blockDim.x) {
-      const int c = u / (D / 8), d = u % (D / 8), col = min(c0 + c, cols - 1);
-      const int set = col / p.set_cols, r = min(col % p.set_cols, rows - 1), node = set * p.set_nodes + r / p.G;
-      const size_t row = ((size_t)b * p.N + node) * p.Hq + h * p.G + r % p.G;
-      cp_async_16(score_smem + c * STRIDE + 16 * d, static_cast<const bf16 *>(p.q) + row * D + 8 * d, true);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    for (int t = t0 + warp; t < t1; t += warps) {
-      const int page = t * kScorePages + fg;
-      // this lane's channels of pages `page` and page + 8: least and largest values
-      uint32_t a[2][2][KB][8];
-      bool there[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = page + 8 * i;
-        long long row = -1;
-        if (at < pages) {
-          if (!p.block_table) {
-            row = (long long)b * p.P + at;
-          } else {
-            const int blk = p.block_table[(size_t)b * p.P + at];
-            if (blk >= 0 && blk < p.num_blocks) row = blk;
-            else if (h == 0 && c0 == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
-          }
-        }
-        there[i] = row >= 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(p.bounds) + ((size_t)max(row, 0ll) * p.Hkv + h) * 2 * D) + 2 * ft;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int k = 0; k < KB; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint4 v = there[i] ? src[s * (D / 8) + 8 * k + e] : make_uint4(0, 0, 0, 0);
-              a[i][s][k][4 * e] = v.x;
-              a[i][s][k][4 * e + 1] = v.y;
-              a[i][s][k][4 * e + 2] = v.z;
-              a[i][s][k][4 * e + 3] = v.w;
-            }
-      }
-      float best[2] = {-INFINITY, -INFINITY};
-      for (int j = 0; j < n8 / 8; ++j) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint4 *q = reinterpret_cast<const uint4 *>(score_smem + (8 * j + fg) * STRIDE) + 2 * ft;
-#pragma unroll
-        for (int k = 0; k < KB; ++k) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint4 v = q[8 * k + e];
-            w[4 * e] = v.x;
-            w[4 * e + 1] = v.y;
-            w[4 * e + 2] = v.z;
-            w[4 * e + 3] = v.w;
-          }
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint32_t lo[4] = {a[0][0][k][2 * s], a[1][0][k][2 * s], a[0][0][k][2 * s + 1], a[1][0][k][2 * s + 1]};
-            const uint32_t hi[4] = {a[0][1][k][2 * s], a[1][1][k][2 * s], a[0][1][k][2 * s + 1], a[1][1][k][2 * s + 1]};
-            mma_bf16_16816(acc, hi, max_bf16x2_nan(w[2 * s], 0u), max_bf16x2_nan(w[2 * s + 1], 0u));
-            mma_bf16_16816(acc, lo, min_bf16x2_nan(w[2 * s], 0u), min_bf16x2_nan(w[2 * s + 1], 0u));
-          }
-        }
-        // acc: columns 2 ft, 2 ft + 1 of pages fg and fg + 8
-        const int col = c0 + 8 * j;
-        auto put = [&](int set, float x, float y) {
-          if (set >= p.sets) return;
-          float *to = out + (size_t)set * p.Hkv * p.P;
-          if (page < p.P) to[page] = there[0] ? x : -INFINITY;
-          if (page + 8 < p.P) to[page + 8] = there[1] ? y : -INFINITY;
-        };
-        if (p.set_cols == 1) {
-          put(col + 2 * ft, acc[0], acc[2]);
-          put(col + 2 * ft + 1, acc[1], acc[3]);
-          continue;
-        }
-        float x = max_nan(acc[0], acc[1]), y = max_nan(acc[2], acc[3]);
-        if (p.set_cols == 2) {
-          put(col / 2 + ft, x, y);
-          continue;
-        }
-        x = max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-        y = max_nan(y, __shfl_xor_sync(0xFFFFFFFFu, y, 1));
-        if (p.set_cols == 4) {
-          if ((ft & 1) == 0) put(col / 4 + ft / 2, x, y);
-          continue;
-        }
-        x = max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-        y = max_nan(y, __shfl_xor_sync(0xFFFFFFFFu, y, 2));
-        best[0] = max_nan(best[0], x);
-        best[1] = max_nan(best[1], y);
-        const int set = col / p.set_cols;
-        const bool last = (col + 8) % p.set_cols == 0;
-        if (last || j + 1 == n8 / 8) {
-          if (ft == 0) {
-            // a set whose rows came in parts: the best so far is in memory
-            float *to = out + (size_t)set * p.Hkv * p.P;
-            if (set * p.set_cols < c0) {
-              if (page < p.P) best[0] = max_nan(best[0], to[page]);
-              if (page + 8 < p.P) best[1] = max_nan(best[1], to[page + 8]);
-            }
-            put(set, best[0], best[1]);
-          }
-          best[0] = best[1] = -INFINITY;
-        }
-      }
-    }
-  }
-}
+// -------------------------------------------------- scores (bf16: page_scores_tc.cu)
 
 // fp32: a warp per page, lanes over the channels.
 template <int D>
@@ -449,24 +301,10 @@ cudaError_t launch_page_bounds(sv_dtype dt, BoundParams p, int B, int num_sms, c
                       : launch_close(page_bounds_kernel<false>, grid, kBoundThreads, 0, s, p);
 }
 
-cudaError_t launch_page_scores(sv_dtype dt, int D, ScoreParams p, int B, int num_sms, cudaStream_t s) {
-  const int units = B * p.Hkv, tiles = (p.P + kScorePages - 1) / kScorePages;
-  p.set_cols = score_set_cols(p.set_nodes * p.G);
-  if (dt == SV_F32) {
-    p.splits = std::max(1, std::min((p.P + 7) / 8, (8 * num_sms + units - 1) / units));
-    return D == 128 ? launch_close(page_scores_f32_kernel<128>, dim3((unsigned)units * p.splits), 256, 0, s, p)
-                    : launch_close(page_scores_f32_kernel<64>, dim3((unsigned)units * p.splits), 256, 0, s, p);
-  }
-  p.splits = std::max(1, std::min((tiles + 7) / 8, (4 * num_sms + units - 1) / units));
-  const int cols = (int)std::min<long long>(kScoreCols, ((long long)p.sets * p.set_cols + 7) / 8 * 8);
-  const size_t smem = (size_t)cols * (D * 2 + 16);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = D == 128 ? allow_smem((const void *)page_scores_kernel<128>, kScoreCols * (128 * 2 + 16))
-                                   : allow_smem((const void *)page_scores_kernel<64>, kScoreCols * (64 * 2 + 16));
-    if (e != cudaSuccess) return e;
-  }
-  return D == 128 ? launch_close(page_scores_kernel<128>, dim3((unsigned)units * p.splits), 256, smem, s, p)
-                  : launch_close(page_scores_kernel<64>, dim3((unsigned)units * p.splits), 256, smem, s, p);
+cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream_t s) {
+  p.splits = std::max(1, std::min((p.P + 7) / 8, (8 * num_sms + p.units - 1) / p.units));
+  return D == 128 ? launch_close(page_scores_f32_kernel<128>, dim3((unsigned)p.units * p.splits), 256, 0, s, p)
+                  : launch_close(page_scores_f32_kernel<64>, dim3((unsigned)p.units * p.splits), 256, 0, s, p);
 }
 
 cudaError_t launch_select_pages(const SelectParams &p, long long lists, int num_sms, cudaStream_t s) {

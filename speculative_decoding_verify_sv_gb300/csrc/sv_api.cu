@@ -633,8 +633,10 @@ sv_status sv_page_scores(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, cons
   p.num_blocks = num_blocks;
   p.sets = sets;
   p.set_nodes = N / sets;
+  p.units = B * Hkv;
   const cudaError_t e = take_injected_failure() ? cudaErrorLaunchFailure
-                                                : sv::launch_page_scores(dt, D, p, B, num_sms(), static_cast<cudaStream_t>(stream));
+                        : dt == SV_F32          ? sv::launch_page_scores_f32(D, p, num_sms(), static_cast<cudaStream_t>(stream))
+                                                : sv::launch_page_scores_tc(D, p, num_sms(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "page scores launch");
   sv::count_launches(1);
   return SV_OK;

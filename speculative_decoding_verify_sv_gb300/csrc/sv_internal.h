@@ -318,9 +318,11 @@ struct ScoreParams {
   float *out;                         // [B][sets][Hkv][P]
   unsigned int *status;
   int N, Hq, Hkv, G, P, page_size, num_blocks, sets, set_nodes;
+  int units;                          // sequences x KV heads
   int set_cols, splits;               // (set at the launch)
 };
-cudaError_t launch_page_scores(sv_dtype dt, int D, ScoreParams p, int B, int num_sms, cudaStream_t s);
+cudaError_t launch_page_scores_tc(int D, ScoreParams p, int num_sms, cudaStream_t s);  // bf16
+cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream_t s);
 
 struct SelectParams {
   const float *scores;
