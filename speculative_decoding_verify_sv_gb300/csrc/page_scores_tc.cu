@@ -27,7 +27,7 @@ using namespace tc;
 
 constexpr int kTile = 128;        // pages of a tile
 constexpr int kCols = 256;        // query rows at a time
-constexpr int kScoreThreads = 288;
+constexpr int kScoreThreads = 416;  // maxima, copies (two groups of four warps), issue
 
 // ST: stages of the ring; the more the fewer columns there are
 template <int D, int ST>
@@ -40,8 +40,8 @@ struct ScoreLayout {
   static constexpr int OFF_RING = NQ * Q_BYTES;
   static constexpr int OFF_BAR = OFF_RING + ST * STAGE;
   // full[ST], empty[ST], q_full[NQ], q_empty[NQ], d_full[2], d_empty[2], drain
-  static constexpr int OFF_ROWS = OFF_BAR + (2 * ST + 5 + 2 * NQ) * 8;  // [2][128] rows of the bounds of a tile's pages
-  static constexpr int OFF_THERE = OFF_ROWS + 2 * kTile * 4;   // [8][4] a bit for each page that is there
+  static constexpr int OFF_ROWS = OFF_BAR + (2 * ST + 5 + 2 * NQ) * 8;  // [2][2][128] rows of the bounds of a tile's pages
+  static constexpr int OFF_THERE = OFF_ROWS + 4 * kTile * 4;   // [8][4] a bit for each page that is there
   static constexpr int OFF_MISC = OFF_THERE + 8 * 16;
   static constexpr int SMEM = OFF_MISC + 16;
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == 12) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
@@ -142,16 +142,18 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
   const long long end = layout_ok ? total * (blockIdx.x + 1) / gridDim.x : w;
   ScoreRun run;
 
-  if (warp >= 4 && warp < 8) {
+  if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------------ copies
-    const int me = tid - 128;
-    int k = 0, arrived = 0, segments = 0, tile = 0;  // stages asked for, and landed; row chunks; tiles
+    // two groups of four warps, which take turns at the stages (with one of them 33.5 us against XXX for
+    // scores-decode); the first brings the query rows
+    const int me = tid & 127, group = (warp - 4) >> 2;
+    int k = 0, arrived = 0, segments = 0, tile = 0;  // this group's stages asked for, and landed; row chunks; tiles
     bool ok = true;
     // stages up to `upto` (of those asked for) have landed when `left` younger ones may be on their way
     auto land = [&](int upto) {
       for (; arrived < upto; ++arrived) {
         fence_proxy_async_smem();
-        mbar_arrive(&full[arrived % ST]);
+        mbar_arrive(&full[(2 * arrived + group) % ST]);
       }
     };
     // (A wait that gives up ends the copies but not the walk, whose barriers all four warps have to reach.)
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
         // query rows of this chunk: q- and q+, each column block of 64 in rows of 128 bytes
         const int n16 = (min(COLS, cols - c0) + 15) & ~15, rows = p.set_nodes * p.G;
         const int qb = segments % NQ, q_par = (segments / NQ - 1) & 1;
-        if (segments >= NQ && !mbar_test(&q_empty[qb], q_par)) {
+        if (group == 0 && segments >= NQ && !mbar_test(&q_empty[qb], q_par)) {
           // (what is asked for lands before the products with the buffer's last rows are awaited)
           cp_async_wait<0>();
           land(k);
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
         constexpr int PER = D / 8, AT_ONCE = 8;
         const int d = me % PER;
         uint8_t *to = sm + qb * Lay::Q_BYTES + (d >> 3) * (COLS * 128);
-        for (int q0 = me / PER; ok && q0 < n16; q0 += AT_ONCE * (128 / PER)) {
+        for (int q0 = me / PER; group == 0 && ok && q0 < n16; q0 += AT_ONCE * (128 / PER)) {
           uint4 x[AT_ONCE];
 #pragma unroll
           for (int i = 0; i < AT_ONCE; ++i) {
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
           }
         }
         fence_proxy_async_smem();
-        if (ok) mbar_arrive(&q_full[qb]);
+        if (group == 0 && ok) mbar_arrive(&q_full[qb]);
         ++segments;
         // this thread's page of a tile: its row of the bounds, read a tile ahead and looked at only then
         auto row_of = [&](int t) -> int {
@@ -203,17 +205,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
           int row = next;
           next = row_of(t + 1);
           if (p.block_table && (row < 0 || row >= p.num_blocks)) {
-            if (run.h == 0 && t * kTile + me < run.pages) set_status(p.status, SV_DEV_BAD_BLOCK);
+            if (group == 0 && run.h == 0 && t * kTile + me < run.pages) set_status(p.status, SV_DEV_BAD_BLOCK);
             row = -1;
           }
-          int *s_row = s_rows + (tile & 1) * kTile;
+          int *s_row = s_rows + (2 * group + (tile & 1)) * kTile;
           const unsigned there = __ballot_sync(0xFFFFFFFFu, row >= 0);
           s_row[me] = row;
-          if (lane == 0) s_there[(tile & 7) * 4 + warp - 4] = there;
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          for (int part = 0; part < 2 * KB; ++part) {
-            const int st = k % ST;
-            ok = ok && (k < ST || score_wait(&empty[st], (k / ST - 1) & 1, abort_flag));
+          if (group == 0 && lane == 0) s_there[(tile & 7) * 4 + warp - 4] = there;
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+          for (int part = group; part < 2 * KB; part += 2) {
+            const int at_k = 2 * k + group, st = at_k % ST;
+            ok = ok && (at_k < ST || score_wait(&empty[st], (at_k / ST - 1) & 1, abort_flag));
             if (!ok) break;
             // 16-byte piece c of each 16th page
             uint8_t *dst = ring + st * Lay::STAGE;
@@ -226,8 +228,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
             }
             cp_async_commit();
             ++k;
-            cp_async_wait<ST - 2>();
-            land(k - (ST - 2));
+            cp_async_wait<ST / 2 - 1>();
+            land(k - (ST / 2 - 1));
           }
           __syncwarp();
         }
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
     }
     cp_async_wait<0>();
     land(k);
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     // ------------------------------------------------------------------- issue
     auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
     auto arrived = [&](uint64_t *bar, int parity) -> bool { return __all_sync(0xFFFFFFFFu, score_wait(bar, parity, abort_flag)); };
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
     }
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
