@@ -55,10 +55,12 @@ __device__ __forceinline__ uint32_t high_of(uint32_t a, uint32_t b) {
   else return max_bf16x2_nan(a, b);
 }
 
-// A thread per 16 bytes of a page's rows: consecutive threads read consecutive pieces of a row, and each
-// has the page's rows, 16 at a time, on their way together.
+// A thread per 16 bytes of a page's rows: consecutive threads read consecutive pieces of a row.  A step is 16
+// rows of a page, which go through shared memory of the thread's own (cp.async), the next step's on their
+// way while one is worked on: 192 KB per SM, where registers hold less than half of that.
 template <bool F32>
 __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundParams p) {
+  extern __shared__ __align__(16) uint4 bound_smem[];  // [2][kBoundRows][kBoundThreads]
   wait_previous();
   const int b = blockIdx.y;
   int L = p.prefix_len[b];
@@ -69,43 +71,72 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
   const int start = p.start ? max(p.start[b], 0) : 0;
   if (start >= L) return;
   const int first = start / p.page_size, pages = (L + p.page_size - 1) / p.page_size - first;
-  const long long items = (long long)pages * p.vecs;
-  for (long long i = (long long)blockIdx.x * kBoundThreads + threadIdx.x; i < items; i += (long long)gridDim.x * kBoundThreads) {
-    const int page = first + (int)(i / p.vecs), v = (int)(i % p.vecs);
-    const int rows = min(p.page_size, L - page * p.page_size);
-    long long row, out;
-    if (p.block_table) {
-      const int blk = p.block_table[(size_t)b * p.max_blocks + page];
-      if (blk < 0 || blk >= p.num_blocks) {
-        if (v == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
-        continue;
+  const long long items = (long long)pages * p.vecs, stride = (long long)gridDim.x * kBoundThreads;
+  // an item: a page and a piece of its rows
+  struct Item {
+    const uint4 *src;
+    uint4 *dst;
+    int rows;
+  };
+  long long next = (long long)blockIdx.x * kBoundThreads + threadIdx.x;
+  auto take = [&]() -> Item {
+    for (; next < items; next += stride) {
+      const int page = first + (int)(next / p.vecs), v = (int)(next % p.vecs);
+      long long row = (long long)b * p.Lmax + (long long)page * p.page_size, out = (long long)b * p.seq_pages + page;
+      if (p.block_table) {
+        const int blk = p.block_table[(size_t)b * p.max_blocks + page];
+        if (blk < 0 || blk >= p.num_blocks) {
+          if (v == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
+          continue;
+        }
+        row = (long long)blk * p.page_size;
+        out = blk;
       }
-      row = (long long)blk * p.page_size;
-      out = blk;
+      next += stride;
+      // head h: D least values, then D largest
+      const int h = v / p.head_vecs, d = v % p.head_vecs;
+      return {static_cast<const uint4 *>(p.k) + (size_t)row * p.vecs + v,
+              static_cast<uint4 *>(p.bounds) + ((size_t)out * p.vecs + (size_t)h * p.head_vecs) * 2 + d, min(p.page_size, L - page * p.page_size)};
+    }
+    return {nullptr, nullptr, 0};
+  };
+  uint4 *mine = bound_smem + threadIdx.x;
+  auto ask = [&](const Item &it, int r0, int buf) {
+#pragma unroll
+    for (int r = 0; r < kBoundRows; ++r)
+      if (r0 + r < it.rows) cp_async_16(mine + (buf * kBoundRows + r) * kBoundThreads, it.src + (size_t)(r0 + r) * p.vecs, true);
+    cp_async_commit();
+  };
+  Item cur = take(), ahead{};
+  int r0 = 0, buf = 0;
+  if (cur.rows > 0) ask(cur, 0, 0);
+  uint4 lo, hi;
+  while (cur.rows > 0) {
+    const bool last = r0 + kBoundRows >= cur.rows;
+    if (last) ahead = take();
+    if (last ? ahead.rows > 0 : true) ask(last ? ahead : cur, last ? 0 : r0 + kBoundRows, buf ^ 1);
+    else cp_async_commit();
+    cp_async_wait<1>();
+    const uint4 *x = mine + buf * kBoundRows * kBoundThreads;
+    if (r0 == 0) lo = hi = x[0];
+#pragma unroll
+    for (int r = 0; r < kBoundRows; ++r)
+      if (r0 + r < cur.rows) {
+        const uint4 y = x[r * kBoundThreads];
+        lo = make_uint4(low_of<F32>(lo.x, y.x), low_of<F32>(lo.y, y.y), low_of<F32>(lo.z, y.z), low_of<F32>(lo.w, y.w));
+        hi = make_uint4(high_of<F32>(hi.x, y.x), high_of<F32>(hi.y, y.y), high_of<F32>(hi.z, y.z), high_of<F32>(hi.w, y.w));
+      }
+    if (last) {
+      cur.dst[0] = lo;
+      cur.dst[p.head_vecs] = hi;
+      cur = ahead;
+      r0 = 0;
     } else {
-      row = (long long)b * p.Lmax + (long long)page * p.page_size;
-      out = (long long)b * p.seq_pages + page;
+      r0 += kBoundRows;
     }
-    const uint4 *src = static_cast<const uint4 *>(p.k) + (size_t)row * p.vecs + v;
-    uint4 lo, hi;
-    for (int r0 = 0; r0 < rows; r0 += kBoundRows) {
-      uint4 x[kBoundRows];
-      // (rows past the last one are the last one again)
-#pragma unroll
-      for (int r = 0; r < kBoundRows; ++r) x[r] = load_streamed(src + (size_t)min(r0 + r, rows - 1) * p.vecs);
-      if (r0 == 0) lo = hi = x[0];
-#pragma unroll
-      for (int r = 0; r < kBoundRows; ++r) {
-        lo = make_uint4(low_of<F32>(lo.x, x[r].x), low_of<F32>(lo.y, x[r].y), low_of<F32>(lo.z, x[r].z), low_of<F32>(lo.w, x[r].w));
-        hi = make_uint4(high_of<F32>(hi.x, x[r].x), high_of<F32>(hi.y, x[r].y), high_of<F32>(hi.z, x[r].z), high_of<F32>(hi.w, x[r].w));
-      }
-    }
-    // head h: D least values, then D largest
-    const int per = p.head_vecs, h = v / per, d = v % per;
-    uint4 *dst = static_cast<uint4 *>(p.bounds) + ((size_t)out * p.vecs + (size_t)h * per) * 2 + d;
-    dst[0] = lo;
-    dst[per] = hi;
+    buf ^= 1;
   }
+  cp_async_wait<0>();
 }
 
 // -------------------------------------------------- scores (bf16: page_scores_tc.cu)
@@ -172,16 +203,19 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// A CTA per list.  The threshold is found by digits of 8 bits of the keys, from the highest bit in which
-// they differ at all; what is above it and, of those equal to it, the first ones go out in order.
+// A CTA per list.  The threshold is found by digits of 8 bits of the keys, from the highest bit in which they
+// differ at all, until the keys of the digit fill the places that are left (with random scores after two or
+// three digits, of up to four); what is above it and, of those equal to it, the first ones go out in order,
+// each warp a run of neighbouring pages.
 __global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ uint32_t sel_smem[];
   uint32_t *keys = sel_smem;                      // [P]
-  __shared__ uint32_t hist[256], red[2][32], s_prefix, s_need;
+  __shared__ uint32_t hist[2][256], red[2][32], s_prefix, s_left, s_full;
   __shared__ int above[32], equal[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
   const long long list = blockIdx.x;
   const int b = (int)(list / p.lists);
+  for (int i = tid; i < 256; i += T) hist[0][i] = 0;
   wait_previous();
   int L = p.prefix_len[b];
   const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
@@ -195,10 +229,12 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constan
     for (int i = tid; i < p.K; i += T) out[i] = i < pages ? i : -1;
     return;
   }
-  // pages [m0, m1) compete for `need` places
-  const int m0 = p.first, m1 = pages - p.last, need = p.K - p.first - p.last;
+  // pages [m0, m1) compete for `left` places
+  const int m0 = p.first, m1 = pages - p.last;
+  int left = p.K - p.first - p.last;
   const float *x = p.scores + list * p.P;
   uint32_t any = 0, all = 0xFFFFFFFFu;
+#pragma unroll 8
   for (int i = m0 + tid; i < m1; i += T) {
     const uint32_t k = score_key(x[i]);
     keys[i] = k;
@@ -209,22 +245,21 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constan
   all = __reduce_and_sync(0xFFFFFFFFu, all);
   if (lane == 0) red[0][warp] = any, red[1][warp] = all;
   __syncthreads();
-  any = lane < warps ? red[0][lane] : 0;
-  all = lane < warps ? red[1][lane] : 0xFFFFFFFFu;
-  any = __reduce_or_sync(0xFFFFFFFFu, any);
-  all = __reduce_and_sync(0xFFFFFFFFu, all);
+  any = __reduce_or_sync(0xFFFFFFFFu, lane < warps ? red[0][lane] : 0);
+  all = __reduce_and_sync(0xFFFFFFFFu, lane < warps ? red[1][lane] : 0xFFFFFFFFu);
   int high = 32 - __clz((int)(any ^ all));  // bits below which the keys differ
   uint32_t prefix = high >= 32 ? 0 : (all >> high) << high;
-  int left = need;  // places for keys that begin with the prefix
-  while (high > 0 && left > 0) {
+  bool whole = false;  // every key that begins with the prefix has a place
+  for (int pass = 0; high > 0 && left > 0 && !whole; ++pass) {
     const int low = max(0, high - 8), bins = 1 << (high - low);
-    for (int i = tid; i < bins; i += T) hist[i] = 0;
-    __syncthreads();
+    uint32_t *h = hist[pass & 1];
     const uint32_t mask = high >= 32 ? 0 : ~0u << high;
+#pragma unroll 8
     for (int i = m0 + tid; i < m1; i += T) {
       const uint32_t k = keys[i];
-      if (((k ^ prefix) & mask) == 0) atomicAdd(&hist[(k >> low) & (bins - 1)], 1u);
+      if (((k ^ prefix) & mask) == 0) atomicAdd(&h[(k >> low) & (bins - 1)], 1u);
     }
+    for (int i = tid; i < 256; i += T) hist[(pass & 1) ^ 1][i] = 0;
     __syncthreads();
     if (warp == 0) {
       // bins from the top: the one in which the last place falls
@@ -232,7 +267,7 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int bin = bins - 1 - (8 * lane + e);
-        n[e] = bin >= 0 ? hist[bin] : 0;
+        n[e] = bin >= 0 ? h[bin] : 0;
         sum += n[e];
       }
       uint32_t before = sum;
@@ -246,59 +281,79 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constan
       for (int e = 0; e < 8; ++e) {
         if (before < (uint32_t)left && before + n[e] >= (uint32_t)left) {
           s_prefix = prefix | (uint32_t)(bins - 1 - (8 * lane + e)) << low;
-          s_need = left - before;
+          s_left = left - before;
+          s_full = before + n[e] == (uint32_t)left;
         }
         before += n[e];
       }
     }
     __syncthreads();
     prefix = s_prefix;
-    left = (int)s_need;
+    left = (int)s_left;
+    whole = s_full != 0;
     high = low;
   }
-  // keys above `prefix`, and the first `left` of those equal to it
-  int base = 0, ties = 0;  // what earlier rounds have put out; ties among the earlier ones
-  for (int i0 = 0; i0 < pages; i0 += T) {
-    const int i = i0 + tid;
-    bool over = false, tie = false;
-    if (i < pages) {
-      if (i < m0 || i >= m1) {
-        over = true;
-      } else if (need > 0) {
-        const uint32_t k = keys[i];
-        over = k > prefix;
-        tie = k == prefix;
-      }
+  // keys above `prefix` (or, with the whole digit, from it on), and the first `left` of those equal to it
+  const bool choose = p.K > p.first + p.last;
+  auto kind = [&](int i, bool &over, bool &tie) {
+    over = i < pages && (i < m0 || i >= m1);
+    tie = false;
+    if (choose && i >= m0 && i < m1) {
+      const uint32_t k = keys[i];
+      over = whole ? k >= prefix : k > prefix;
+      tie = !whole && k == prefix;
     }
+  };
+  const int run = ((pages + warps - 1) / warps + 31) & ~31, i0 = warp * run, i1 = min(pages, i0 + run);
+  int n_over = 0, n_tie = 0;
+  for (int i = i0; i < i1; i += 32) {
+    bool over, tie;
+    kind(i + lane, over, tie);
+    n_over += __popc(__ballot_sync(0xFFFFFFFFu, over));
+    n_tie += __popc(__ballot_sync(0xFFFFFFFFu, tie));
+  }
+  if (lane == 0) above[warp] = n_over, equal[warp] = n_tie;
+  __syncthreads();
+  int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? above[lane] : 0);
+  int ties = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? equal[lane] : 0);
+  const unsigned lt = (1u << lane) - 1;
+  for (int i = i0; i < i1; i += 32) {
+    bool over, tie;
+    kind(i + lane, over, tie);
     const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bt = __ballot_sync(0xFFFFFFFFu, tie);
-    if (lane == 0) above[warp] = __popc(bo), equal[warp] = __popc(bt);
-    __syncthreads();
-    int o = lane < warps ? above[lane] : 0, e = lane < warps ? equal[lane] : 0;
-    const int o_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? o : 0), e_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? e : 0);
-    o = __reduce_add_sync(0xFFFFFFFFu, o);
-    e = __reduce_add_sync(0xFFFFFFFFu, e);
-    const unsigned lt = (1u << lane) - 1;
-    const int my_over = base + o_before + __popc(bo & lt), my_ties = ties + e_before + __popc(bt & lt);
-    if (over || (tie && my_ties < left)) out[my_over + min(my_ties, left)] = i;
-    base += o;
-    ties += e;
-    __syncthreads();
+    const int my_ties = ties + __popc(bt & lt);
+    if (over || (tie && my_ties < left)) out[base + __popc(bo & lt) + min(my_ties, left)] = i + lane;
+    base += __popc(bo);
+    ties += __popc(bt);
   }
 }
 
+// Lets a kernel have up to `smem` bytes of shared memory, once per device.
+template <int WHICH>
 cudaError_t allow_smem(const void *kern, size_t smem) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<bool> attr[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && attr[dev].load()) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) attr[dev].store(true);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t launch_page_bounds(sv_dtype dt, BoundParams p, int B, int num_sms, cudaStream_t s) {
-  // enough CTAs for any split of the pages over the sequences; those without a page leave at once
+  // Three CTAs per SM; twice as many, for sequences of different lengths, those without a page leave at
+  // once.  (Six times: 16 prompts of 20000 to 32768 tokens 143.8 us, 256 sequences with 5 new tokens 5.1; three
+  // times 196 and 4.0, twelve times 140.7 and 6.9.)
   const long long most = ((long long)p.cap + p.page_size - 1) / p.page_size * p.vecs;
-  const long long per = std::max(1ll, std::min((most + kBoundThreads - 1) / kBoundThreads, (16ll * num_sms + B - 1) / B));
+  const long long per = std::max(1ll, std::min((most + kBoundThreads - 1) / kBoundThreads, ((long long)6 * num_sms + B - 1) / B));
   const dim3 grid((unsigned)per, (unsigned)B);
-  return dt == SV_F32 ? launch_close(page_bounds_kernel<true>, grid, kBoundThreads, 0, s, p)
-                      : launch_close(page_bounds_kernel<false>, grid, kBoundThreads, 0, s, p);
+  constexpr size_t smem = 2 * kBoundRows * kBoundThreads * 16;
+  const cudaError_t e = dt == SV_F32 ? allow_smem<0>((const void *)page_bounds_kernel<true>, smem) : allow_smem<1>((const void *)page_bounds_kernel<false>, smem);
+  if (e != cudaSuccess) return e;
+  return dt == SV_F32 ? launch_close(page_bounds_kernel<true>, grid, kBoundThreads, smem, s, p)
+                      : launch_close(page_bounds_kernel<false>, grid, kBoundThreads, smem, s, p);
 }
 
 cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream_t s) {
@@ -310,10 +365,11 @@ cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream
 cudaError_t launch_select_pages(const SelectParams &p, long long lists, int num_sms, cudaStream_t s) {
   const size_t smem = (size_t)p.P * 4;
   if (smem > 44 * 1024) {  // (with the kernel's other 1.5 KB more than the default 48)
-    const cudaError_t e = allow_smem((const void *)select_pages_kernel, SV_MAX_SCORE_PAGES * 4);
+    const cudaError_t e = allow_smem<2>((const void *)select_pages_kernel, SV_MAX_SCORE_PAGES * 4);
     if (e != cudaSuccess) return e;
   }
-  const int threads = p.P <= 256 ? 128 : lists <= num_sms || p.P > 8192 ? 1024 : 256;
+  // (2560 lists of 128 of up to 2048 pages: 23.7 us with 128 threads, 32 with 256, 46 with 512)
+  const int threads = p.P <= 256 ? 128 : lists <= num_sms || p.P > 8192 ? 512 : 128;
   return launch_close(select_pages_kernel, dim3((unsigned)lists), threads, smem, s, p);
 }
 
