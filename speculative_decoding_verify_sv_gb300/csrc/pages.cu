@@ -203,19 +203,33 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// A CTA per list.  The threshold is found by digits of 8 bits of the keys, from the highest bit in which they
-// differ at all, until the keys of the digit fill the places that are left (with random scores after two or
-// three digits, of up to four); what is above it and, of those equal to it, the first ones go out in order,
-// each warp a run of neighbouring pages.
-__global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ uint32_t sel_smem[];
-  uint32_t *keys = sel_smem;                      // [P]
-  __shared__ uint32_t hist[2][256], red[2][32], s_prefix, s_left, s_full;
+// A CTA per list.  One histogram of 256 equal parts of the scores' range gives the part in which the last
+// place falls.  What is above it is chosen; what is in it are candidates, few as a rule, of which each counts
+// those before it (or, many of them, digits of 8 bits of their keys decide, and of those equal to the end
+// the lower pages).  (The highest bits in which the keys differ as the first digit: scores of both signs then
+// meet in a few of its words, and 2560 lists of up to 2048 scores take 23 us for the atomics instead of 18.3;
+// without atomics, by counts against seven pivots at a time until few scores are left, 25.3.)
+// The chosen pages are bits of words, from which a lane puts out those of its word.
+constexpr int kSelectThreads = 512;  // at most
+constexpr int kCandidates = 512;     // of a list; more of them are looked up among all scores again
+
+struct SelectWords {
+  uint32_t over, tie;  // chosen; equal to the threshold
+};
+
+__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(8) uint32_t sel_smem[];
+  SelectWords *words = reinterpret_cast<SelectWords *>(sel_smem);                    // [ceil(P / 32)]
+  float *score = reinterpret_cast<float *>(sel_smem) + 2 * ((p.P + 31) / 32);        // [P]
+  __shared__ uint16_t cand[kCandidates];
+  __shared__ uint32_t hist[2][256], s_bin, s_left, s_whole, s_cand;
+  __shared__ float red[2][32];
   __shared__ int above[32], equal[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
   const long long list = blockIdx.x;
   const int b = (int)(list / p.lists);
   for (int i = tid; i < 256; i += T) hist[0][i] = 0;
+  if (tid == 0) s_cand = 0;
   wait_previous();
   int L = p.prefix_len[b];
   const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
@@ -233,41 +247,39 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constan
   const int m0 = p.first, m1 = pages - p.last;
   int left = p.K - p.first - p.last;
   const float *x = p.scores + list * p.P;
-  uint32_t any = 0, all = 0xFFFFFFFFu;
+  float least = FLT_MAX, largest = -FLT_MAX;  // of the finite ones
 #pragma unroll 8
   for (int i = m0 + tid; i < m1; i += T) {
-    const uint32_t k = score_key(x[i]);
-    keys[i] = k;
-    any |= k;
-    all &= k;
-  }
-  any = __reduce_or_sync(0xFFFFFFFFu, any);
-  all = __reduce_and_sync(0xFFFFFFFFu, all);
-  if (lane == 0) red[0][warp] = any, red[1][warp] = all;
-  __syncthreads();
-  any = __reduce_or_sync(0xFFFFFFFFu, lane < warps ? red[0][lane] : 0);
-  all = __reduce_and_sync(0xFFFFFFFFu, lane < warps ? red[1][lane] : 0xFFFFFFFFu);
-  int high = 32 - __clz((int)(any ^ all));  // bits below which the keys differ
-  uint32_t prefix = high >= 32 ? 0 : (all >> high) << high;
-  bool whole = false;  // every key that begins with the prefix has a place
-  for (int pass = 0; high > 0 && left > 0 && !whole; ++pass) {
-    const int low = max(0, high - 8), bins = 1 << (high - low);
-    uint32_t *h = hist[pass & 1];
-    const uint32_t mask = high >= 32 ? 0 : ~0u << high;
-#pragma unroll 8
-    for (int i = m0 + tid; i < m1; i += T) {
-      const uint32_t k = keys[i];
-      if (((k ^ prefix) & mask) == 0) atomicAdd(&h[(k >> low) & (bins - 1)], 1u);
+    const float v = x[i];
+    score[i] = v;
+    if (fabsf(v) <= FLT_MAX) {
+      least = fminf(least, v);
+      largest = fmaxf(largest, v);
     }
-    for (int i = tid; i < 256; i += T) hist[(pass & 1) ^ 1][i] = 0;
-    __syncthreads();
+  }
+  asm volatile("redux.sync.min.f32 %0, %0, 0xFFFFFFFF;" : "+f"(least));
+  asm volatile("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(largest));
+  if (lane == 0) red[0][warp] = least, red[1][warp] = largest;
+  __syncthreads();
+  least = lane < warps ? red[0][lane] : FLT_MAX;
+  largest = lane < warps ? red[1][lane] : -FLT_MAX;
+  asm volatile("redux.sync.min.f32 %0, %0, 0xFFFFFFFF;" : "+f"(least));
+  asm volatile("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(largest));
+  // the part of the range, growing with the score; infinities and NaN are at the ends
+  const float range = largest - least, scale = range > 0.f && range <= FLT_MAX ? 255.f / range : 0.f;
+  auto bin_of = [&](float v) -> int {
+    if (!(fabsf(v) <= FLT_MAX)) return v == -INFINITY ? 0 : 255;
+    return min(255, (int)((v - least) * scale));
+  };
+  bool whole = false;  // all of the part, or digit, have places
+  int pass = 0;
+  // the bin of this pass's histogram in which the last of the `left` places falls
+  auto find = [&]() -> int {
     if (warp == 0) {
-      // bins from the top: the one in which the last place falls
       uint32_t n[8], sum = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int bin = bins - 1 - (8 * lane + e);
-        n[e] = bin >= 0 ? h[bin] : 0;
+        n[e] = hist[pass & 1][255 - (8 * lane + e)];
         sum += n[e];
       }
       uint32_t before = sum;
@@ -280,51 +292,121 @@ __global__ void __launch_bounds__(1024) select_pages_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (before < (uint32_t)left && before + n[e] >= (uint32_t)left) {
-          s_prefix = prefix | (uint32_t)(bins - 1 - (8 * lane + e)) << low;
+          s_bin = 255 - (8 * lane + e);
           s_left = left - before;
-          s_full = before + n[e] == (uint32_t)left;
+          s_whole = before + n[e] == (uint32_t)left;
         }
         before += n[e];
       }
     }
     __syncthreads();
-    prefix = s_prefix;
     left = (int)s_left;
-    whole = s_full != 0;
-    high = low;
-  }
-  // keys above `prefix` (or, with the whole digit, from it on), and the first `left` of those equal to it
-  const bool choose = p.K > p.first + p.last;
-  auto kind = [&](int i, bool &over, bool &tie) {
-    over = i < pages && (i < m0 || i >= m1);
-    tie = false;
-    if (choose && i >= m0 && i < m1) {
-      const uint32_t k = keys[i];
-      over = whole ? k >= prefix : k > prefix;
-      tie = !whole && k == prefix;
-    }
+    whole = s_whole != 0;
+    ++pass;
+    return (int)s_bin;
   };
-  const int run = ((pages + warps - 1) / warps + 31) & ~31, i0 = warp * run, i1 = min(pages, i0 + run);
-  int n_over = 0, n_tie = 0;
-  for (int i = i0; i < i1; i += 32) {
-    bool over, tie;
-    kind(i + lane, over, tie);
-    n_over += __popc(__ballot_sync(0xFFFFFFFFu, over));
-    n_tie += __popc(__ballot_sync(0xFFFFFFFFu, tie));
+  const bool choose = left > 0;
+  int bin = 256;
+  if (choose) {
+#pragma unroll 8
+    for (int i = m0 + tid; i < m1; i += T) atomicAdd(&hist[0][bin_of(score[i])], 1u);
+    for (int i = tid; i < 256; i += T) hist[1][i] = 0;
+    __syncthreads();
+    bin = find();
   }
+  // bits of the pages above the part (and of those that are kept anyhow), and the candidates
+  const int count = (pages + 31) / 32;
+  for (int w = warp; w < count; w += warps) {
+    const int i = 32 * w + lane;
+    bool over = i < pages && (i < m0 || i >= m1), maybe = false;
+    if (choose && i >= m0 && i < m1) {
+      const int k = bin_of(score[i]);
+      over = k > bin || (whole && k == bin);
+      maybe = !whole && k == bin;
+    }
+    const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bm = __ballot_sync(0xFFFFFFFFu, maybe);
+    uint32_t at = 0;
+    if (lane == 0) {
+      words[w] = {bo, 0};
+      if (bm) at = atomicAdd(&s_cand, (uint32_t)__popc(bm));
+    }
+    if (bm) {
+      at = __shfl_sync(0xFFFFFFFFu, at, 0);
+      at += __popc(bm & ((1u << lane) - 1));
+      if (maybe && at < kCandidates) cand[at] = (uint16_t)i;
+    }
+  }
+  __syncthreads();
+  const int n = (int)s_cand;
+  if (n > 0 && n <= kCandidates) {
+    // a candidate has a place if fewer than `left` come before it
+    for (int i = tid; i < n; i += T) {
+      const int at = cand[i];
+      const uint32_t k = score_key(score[at]);
+      int before = 0;
+      for (int c = 0; c < n; ++c) {
+        const int other = cand[c];
+        const uint32_t y = score_key(score[other]);
+        before += y > k || (y == k && other < at);
+      }
+      if (before < left) atomicOr(&words[at >> 5].over, 1u << (at & 31));
+    }
+    __syncthreads();
+  } else if (n > 0) {
+    const int part = bin;
+    uint32_t prefix = 0;
+    int high = 32;
+    whole = false;
+    while (high > 0 && !whole) {
+      const int low = high - 8;
+      const uint32_t mask = high == 32 ? 0 : ~0u << high;
+      for (int i = m0 + tid; i < m1; i += T) {
+        const uint32_t k = score_key(score[i]);
+        if (bin_of(score[i]) == part && ((k ^ prefix) & mask) == 0) atomicAdd(&hist[pass & 1][(k >> low) & 255u], 1u);
+      }
+      for (int i = tid; i < 256; i += T) hist[(pass & 1) ^ 1][i] = 0;
+      __syncthreads();
+      prefix |= (uint32_t)find() << low;
+      high = low;
+    }
+    for (int at = m0 + tid; at < m1; at += T) {
+      if (bin_of(score[at]) != part) continue;
+      const uint32_t k = score_key(score[at]);
+      if (whole ? k >= prefix : k > prefix) atomicOr(&words[at >> 5].over, 1u << (at & 31));
+      else if (!whole && k == prefix) atomicOr(&words[at >> 5].tie, 1u << (at & 31));
+    }
+    __syncthreads();
+  }
+  // a lane per word, each warp a run of them; of the ties the first `left`
+  const int run = (count + T - 1) / T * 32, w0 = warp * run;
+  int n_over = 0, n_tie = 0;
+  for (int w = w0 + lane; w < min(count, w0 + run); w += 32) n_over += __popc(words[w].over), n_tie += __popc(words[w].tie);
+  n_over = __reduce_add_sync(0xFFFFFFFFu, n_over);
+  n_tie = __reduce_add_sync(0xFFFFFFFFu, n_tie);
   if (lane == 0) above[warp] = n_over, equal[warp] = n_tie;
   __syncthreads();
   int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? above[lane] : 0);
   int ties = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? equal[lane] : 0);
-  const unsigned lt = (1u << lane) - 1;
-  for (int i = i0; i < i1; i += 32) {
-    bool over, tie;
-    kind(i + lane, over, tie);
-    const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bt = __ballot_sync(0xFFFFFFFFu, tie);
-    const int my_ties = ties + __popc(bt & lt);
-    if (over || (tie && my_ties < left)) out[base + __popc(bo & lt) + min(my_ties, left)] = i + lane;
-    base += __popc(bo);
-    ties += __popc(bt);
+  for (int w = w0; w < min(count, w0 + run); w += 32) {
+    SelectWords mine{0, 0};
+    if (w + lane < count) mine = words[w + lane];
+    int o = __popc(mine.over), t = __popc(mine.tie);
+    const int my_o = o, my_t = t;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, o, k), z = __shfl_up_sync(0xFFFFFFFFu, t, k);
+      if (lane >= k) o += y, t += z;
+    }
+    int at = base + o - my_o, tie = ties + t - my_t;  // chosen pages and ties before this word
+    at += min(tie, left);
+    for (uint32_t rest = mine.over | mine.tie; rest; rest &= rest - 1) {
+      const int bit = __ffs((int)rest) - 1;
+      const bool is_tie = (mine.tie >> bit) & 1;
+      if (!is_tie || tie < left) out[at++] = 32 * (w + lane) + bit;
+      tie += is_tie;
+    }
+    base += __shfl_sync(0xFFFFFFFFu, o, 31);
+    ties += __shfl_sync(0xFFFFFFFFu, t, 31);
   }
 }
 
@@ -363,14 +445,13 @@ cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream
 }
 
 cudaError_t launch_select_pages(const SelectParams &p, long long lists, int num_sms, cudaStream_t s) {
-  const size_t smem = (size_t)p.P * 4;
-  if (smem > 44 * 1024) {  // (with the kernel's other 1.5 KB more than the default 48)
-    const cudaError_t e = allow_smem<2>((const void *)select_pages_kernel, SV_MAX_SCORE_PAGES * 4);
+  auto bytes = [](int P) { return (size_t)(P + 31) / 32 * 8 + (size_t)P * 4; };
+  if (bytes(p.P) > 44 * 1024) {  // (with the kernel's other 3.6 KB more than the default 48)
+    const cudaError_t e = allow_smem<2>((const void *)select_pages_kernel, bytes(SV_MAX_SCORE_PAGES));
     if (e != cudaSuccess) return e;
   }
-  // (2560 lists of 128 of up to 2048 pages: 23.7 us with 128 threads, 32 with 256, 46 with 512)
-  const int threads = p.P <= 256 ? 128 : lists <= num_sms || p.P > 8192 ? 512 : 128;
-  return launch_close(select_pages_kernel, dim3((unsigned)lists), threads, smem, s, p);
+  const int threads = p.P <= 256 ? 64 : lists <= num_sms || p.P > 8192 ? kSelectThreads : 96;
+  return launch_close(select_pages_kernel, dim3((unsigned)lists), threads, bytes(p.P), s, p);
 }
 
 }  // namespace sv
