@@ -249,8 +249,9 @@ size_t sv_shared_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
  * left out (SV_DEV_BAD_BLOCK).
  * Every other argument, the layouts, the kernels' shapes and the refusals are sv_window_attention's
  * (without window and sinks); Hq / Hkv <= 128, else SV_ERR_UNSUPPORTED.  Rounding as there.
- * Workspace: sv_sparse_attention_workspace_size() bytes, 16-byte aligned (0 for float32 and for few
- * query rows per list); it needs no initial value.  Calls that share one must be stream-ordered. */
+ * Workspace: sv_sparse_attention_workspace_size() bytes, 16-byte aligned (0 for float32, for few query
+ * rows per list and for little to read); it needs no initial value.  Calls that share one must be
+ * stream-ordered. */
 sv_status sv_sparse_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
                               const void *k_tree, const void *v_tree, sv_kv_cache cache,
                               const int32_t *parent, int parent_stride, float scale,

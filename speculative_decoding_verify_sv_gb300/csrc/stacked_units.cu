@@ -5,10 +5,15 @@ namespace sv {
 
 namespace {
 
-// Whether a warp per unit is the better shape, and its tiles of rows: of up to 32, as even as whole steps of
-// 8 allow.
+// Whether a warp per unit is the better shape: with four units per SM or more, where a CTA per unit comes in
+// waves.  Measured on 152 SMs, units of 4 rows (one node, 32:8 heads), us a warp / a CTA per unit:
+//   listed pages   304 units of 128 keys 8.2 / 7.0, of 4096 keys 150 / 94;  608 units 9.7 / 13.7, 192 / 182;
+//                  1216 units 15.5 / 24, 348 / 354
+//   own keys       304 units of 16 keys 19.0 / 15.8, of 512 keys 37 / 26;  608 units 20 / 23, 43 / 42.5;
+//                  1216 units 21 / 36, 64 / 74 (with the shared part, 512 keys, before them)
+// Tiles are of up to 32 rows.
 template <class P>
-bool warp_units_pay(P &p, long long kv_units, int groups, int num_sms) {
+bool warp_units_pay(P &p, long long kv_units, int num_sms) {
   const int tiles = (p.M + 31) / 32;
   const long long units = kv_units * tiles;
   if (units < 4ll * num_sms || units > INT32_MAX) return false;
@@ -80,7 +85,7 @@ cudaError_t launch_joined(const AttnParams &a, const StackParams &st, const Stac
   p.tile_tokens = pl.tile_tokens;
   p.row_tiles = pl.row_tiles;
   p.list_tiles = pl.list_tiles;
-  return warp_units_pay(p, (long long)a.B * a.Hkv, groups_of_keys, pl.grid) ? launch_joined_warps(p, a.D, s)
+  return warp_units_pay(p, (long long)a.B * a.Hkv, pl.grid) ? launch_joined_warps(p, a.D, s)
                                                                            : launch_joined_units(p, a.D, groups_of_keys, pl.grid, s);
 }
 
@@ -96,11 +101,20 @@ StackPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int groups, int num_
   return pl;
 }
 
+// Many rows with one list are worth the stacked kernel, which reads a list's K and V once per 256 rows instead
+// of once per 64 or 32 but leaves pieces to a second kernel, where there is much to read.  Measured, us stacked /
+// in units, pages of 16, 8 KV heads:
+//   104 rows (26 nodes, 4 heads)   16 requests with lists of 256 keys 25 / 16, 1024 keys 37 / 36, 4096 keys 77 / 118;
+//                                  64 requests 55 / 49, 94 / 144, 232 / 521;  one request, 4096 keys, 22 / 17
+//   512 rows                       one request, 1024 keys, 23 / 17, 4096 keys 29 / 39;  16 requests of 256 keys 61 / 55
+//   64 rows                        64 requests of 256 keys 38 / 23, of 4096 keys 212 / 261;  16 of 4096 keys 69 / 64
+//   up to 48 rows                  64 requests of 4096 keys 207 / 191 (40 and 48 rows), 206 / 155 (20 rows)
 StackPlan sparse_plan(int B, int N, int Hq, int Hkv, int D, int page_size, int list_len, int sets, int num_sms) {
   StackPlan pl{};
   const int G = Hq / Hkv;
   pl.grid = num_sms > 0 ? num_sms : 152;
-  if (sets != 1 || N * G <= 32) return pl;
+  const double reads = (double)B * Hkv * ((N * G + 63) / 64) * list_len * page_size;  // keys that units read
+  if (sets != 1 || N * G <= 48 || reads < 2600. * pl.grid) return pl;
   pl.stacked = true;
   pl.tile_tokens = 128 / G;
   pl.row_tiles = (N + 2 * pl.tile_tokens - 1) / (2 * pl.tile_tokens);
@@ -150,7 +164,7 @@ cudaError_t launch_sparse_attention(const AttnParams &a, const ListArgs &l, cons
     p.page_size = l.page_size;
     p.page_groups = l.page_size / kWinGroup;
     const int groups = l.list_len * p.page_groups + a.N / kWinGroup + 1;
-    e = warp_units_pay(p, (long long)a.B * l.sets * a.Hkv, groups, num_sms) ? launch_listed_warps(p, a.D, s)
+    e = warp_units_pay(p, (long long)a.B * l.sets * a.Hkv, num_sms) ? launch_listed_warps(p, a.D, s)
                                                                             : launch_listed_units(p, a.D, groups, num_sms, s);
   }
   if (e == cudaSuccess) ++*launches;

@@ -5,7 +5,7 @@
 // another warp.  A unit's fixed latencies -- lengths, page ids, the first copies, the end -- then
 // overlap with the three other warps' of the CTA and those of the SM's other CTAs, and there is no merge.
 // For 2048 units of 20 rows with 264 keys of their own a CTA per unit takes 90 us (11 us each, of which 4
-// start, 4 keys, 3 end), a warp per unit XXX; few or long units are better off with a CTA (warp_units_pay).
+// start, 4 keys, 3 end), a warp per unit 70; few or long units are better off with a CTA (warp_units_pay).
 //
 // The products and their fragments are those of unit_attention.cuh: S^T = K Q^T, O^T = V^T P^T on
 // mma.sync.

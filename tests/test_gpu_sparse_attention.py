@@ -31,6 +31,23 @@ def lists_of(lens, sets, Hkv, K, page, seed, holes=True):
     return out
 
 
+def padded(inp, pages, page):
+    """The same lists with entries behind them that name nothing, so many that calls with more than 48 rows per
+    list go through the stacked kernel."""
+    B, sets, Hkv, K = pages.shape
+    N, Hq, D = inp["q"].shape[1:]
+    rows = N * Hq // Hkv
+    most = 4000 * torch.cuda.get_device_properties(0).multi_processor_count
+    long = -(-most // (B * Hkv * ((rows + 63) // 64) * page))
+    out = torch.cat([pages, torch.full((B, sets, Hkv, max(0, long - K)), -1, dtype=torch.int32)], 3)
+    assert sv.sv_sparse_attention_workspace_size(BF, B, N, Hq, Hkv, D, page, out.shape[3], 1) > 0
+    return out
+
+
+def stacks(inp, pages):
+    return inp["q"].dtype == BF and pages.shape[1] == 1 and inp["q"].shape[1] * inp["q"].shape[2] // pages.shape[2] > 48
+
+
 def call(inp, parent, pages, page, **kw):
     g = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in inp.items()}
     cache = sv.KVCache(g["cache_k"], g["cache_v"], g["prefix_len"], g["block_table"], page)
@@ -39,7 +56,9 @@ def call(inp, parent, pages, page, **kw):
 
 
 def check(inp, parent, pages, page, **kw):
-    out = call(inp, parent, pages, page, **kw)
+    """The call, and where there are rows enough the same through the stacked kernel too."""
+    outs = [call(inp, parent, p, page, **kw) for p in ([pages, padded(inp, pages, page)] if stacks(inp, pages) else [pages])]
+    out = outs[0]
     torch.cuda.synchronize()
     assert sv.sv_read_device_status() == 0
     D = inp["q"].shape[-1]
@@ -52,9 +71,10 @@ def check(inp, parent, pages, page, **kw):
     size = D ** -0.5 * inp["q"].float().norm(dim=-1).max().item() * max(
         inp["k_tree"].float().norm(dim=-1).max().item(), inp["cache_k"].float().norm(dim=-1).max().item())
     bound = plain_ops.attention_bound(ref, spread, inp["q"].dtype, D, size, pages.shape[3] * page + 64)
-    err = (out.double().cpu() - ref).abs()
-    worst = (err - bound).max().item()
-    assert bool(torch.isfinite(out).all()) and worst <= 0, (worst, err.max().item())
+    for o in outs:
+        err = (o.double().cpu() - ref).abs()
+        worst = (err - bound).max().item()
+        assert bool(torch.isfinite(o).all()) and worst <= 0, (worst, err.max().item())
     return out
 
 
@@ -130,6 +150,8 @@ def test_entries_that_name_no_keys(cuda_ok):
 def test_long_lists_cut_over_many_ctas(cuda_ok, paged):
     inp = wl.attention_inputs(1, 26, 8, 1, 128, [9001], dtype=BF, paged=paged, seed=9)
     check(inp, wl.TREE_T26, lists_of([9001], 1, 1, 500, 16, 9, holes=False), 16)
+    inp = wl.attention_inputs(4, 26, 16, 2, 64, [5003, 4801, 7, 4090], dtype=BF, paged=paged, seed=11)
+    check(inp, wl.TREE_T26, lists_of([5003, 4801, 7, 4090], 1, 2, 300, 16, 12), 16)
     inp = wl.attention_inputs(2, 1, 8, 2, 128, [5000, 4100], dtype=BF, paged=paged, seed=10)
     check(inp, [-1], lists_of([5000, 4100], 1, 2, 256, 16, 10), 16)
 
@@ -143,8 +165,8 @@ def test_trees_of_each_sequence(cuda_ok):
         check(inp, parents, lists_of(lens, 13 if per_node else 1, 2, 6, 16, 11), 16)
 
 
-@pytest.mark.parametrize("N", [2, 26])
-def test_what_is_not_listed_may_hold_anything(cuda_ok, N):
+@pytest.mark.parametrize("N,stacked", [(2, False), (26, False), (26, True)])
+def test_what_is_not_listed_may_hold_anything(cuda_ok, N, stacked):
     """NaN and infinity in unlisted pages and behind the prefix's end, and blocks that are no blocks."""
     parent = wl.TREE_T26 if N == 26 else wl.chain_parent(1)
     lens = [100, 250]
@@ -152,7 +174,10 @@ def test_what_is_not_listed_may_hold_anything(cuda_ok, N):
     pages = torch.full((2, 1, 2, 5), -1, dtype=torch.int32)
     pages[0, 0, :, :3] = torch.tensor([0, 6, 2], dtype=torch.int32)
     pages[1, 0, :, :4] = torch.tensor([15, 3, 8, 1], dtype=torch.int32)
-    clean = check(inp, parent, pages, 16)
+    check(inp, parent, pages, 16)
+    if stacked:
+        pages = padded(inp, pages, 16)
+    clean = call(inp, parent, pages, 16)
     for b, kept in ((0, [0, 2, 6]), (1, [1, 3, 8, 15])):
         for j in range(inp["block_table"].shape[1]):
             blk = int(inp["block_table"][b, j])
@@ -167,12 +192,14 @@ def test_what_is_not_listed_may_hold_anything(cuda_ok, N):
     assert torch.equal(out, clean) and sv.sv_read_device_status() == 0
 
 
-@pytest.mark.parametrize("N,dtype", [(2, BF), (26, BF), (2, F32)])
-def test_bad_pages_are_left_out(cuda_ok, N, dtype):
+@pytest.mark.parametrize("N,dtype,stacked", [(2, BF, False), (26, BF, False), (26, BF, True), (2, F32, False)])
+def test_bad_pages_are_left_out(cuda_ok, N, dtype, stacked):
     parent = wl.TREE_T26 if N == 26 else wl.chain_parent(1)
     inp = wl.attention_inputs(2, N, 8, 2, 128, [100, 250], dtype=dtype, paged=True, seed=13)
     pages = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32).expand(2, 1, 2, 5).contiguous()
     less = torch.tensor([0, -1, 2, -1, 4], dtype=torch.int32).expand(2, 1, 2, 5).contiguous()
+    if stacked:
+        pages, less = padded(inp, pages, 16), padded(inp, less, 16)
     want = call(inp, parent, less, 16)
     assert sv.sv_read_device_status() == 0
     inp["block_table"][:, 1], inp["block_table"][:, 3] = -1, inp["num_blocks"]
@@ -182,10 +209,12 @@ def test_bad_pages_are_left_out(cuda_ok, N, dtype):
 
 
 def test_prefix_outside_the_cache_is_clamped(cuda_ok):
-    for N in (1, 26):
+    for N, stacked in ((1, False), (26, False), (26, True)):
         parent = wl.TREE_T26 if N == 26 else [-1]
         inp = wl.attention_inputs(2, N, 8, 2, 64, [96, 96], dtype=BF, paged=True, extra=0, seed=14)
         pages = torch.arange(6, dtype=torch.int32).expand(2, 1, 2, 6).contiguous()
+        if stacked:
+            pages = padded(inp, pages, 16)
         want = call(inp, parent, pages, 16)
         inp["prefix_len"][0] = 10 ** 6
         got = call(inp, parent, pages, 16)
