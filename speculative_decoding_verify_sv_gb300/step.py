@@ -9,12 +9,15 @@ accepted tokens back.  All arithmetic happens in libsv.so.
 """
 from __future__ import annotations
 
-from typing import Optional, Sequence
+from dataclasses import dataclass
+from typing import Optional, Sequence, Tuple
 
 import torch
 
 from . import (EXACT, GREEDY, Q_LOGITS, KVCache, sv_accept_chain, sv_accept_chain_commit,
                sv_accept_tree, sv_accept_tree_commit, sv_accept_workspace_size, sv_commit_kv,
+               sv_page_bounds, sv_page_scores, sv_select_pages, sv_shared_attention,
+               sv_shared_attention_workspace_size, sv_sparse_attention, sv_sparse_attention_workspace_size,
                sv_tree_attention, sv_tree_attention_workspace_size, sv_window_attention,
                sv_window_attention_workspace_size)
 
@@ -30,19 +33,38 @@ def _depths(parent):
     return d
 
 
+@dataclass
+class SparsePages:
+    """What a step's attention over selected pages looks at: ``count`` pages (of the cache's
+    block_size) of each prefix, the ``first`` and the ``last`` ones and the best scored others, chosen
+    for each KV head and for all nodes together or (per_node) each by itself."""
+    count: int
+    first: int = 1
+    last: int = 1
+    per_node: bool = False
+
+
 class VerifyStep:
     """Buffers and calls of one verify step for a fixed batch shape.
 
     chain=True uses sv_accept_chain (parent must be a chain); otherwise sv_accept_tree.
     window: the layer's sliding window (its attention is then sv_window_attention, with the
     first ``sinks`` positions kept visible); None attends to the whole prefix.
+    shared: (group_start, shared_len), int32 tensors on the device that say which sequences share a
+    prefix (sv_shared_attention); their values may change from step to step.
+    sparse: the attention looks at selected pages only (sv_sparse_attention).  The step keeps the
+    pages' bounds: ``reset_bounds`` makes them from the cache (after prompts were written into it),
+    and each commit brings them up to date.
+    At most one of window, shared and sparse.
     """
 
     def __init__(self, parent: Sequence[int], B: int, Hq: int, Hkv: int, D: int, V: int,
                  cache: KVCache, dtype=torch.bfloat16, mode=EXACT, q_kind=Q_LOGITS,
                  temperature: float = 1.0, top_k: int = 0, chain: bool = False,
                  device: Optional[torch.device] = None, top_p: float = 1.0,
-                 window: Optional[int] = None, sinks: int = 0):
+                 window: Optional[int] = None, sinks: int = 0,
+                 shared: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                 sparse: Optional[SparsePages] = None):
         self.parent = list(parent)
         self.N = len(self.parent)
         self.Dmax = max(_depths(self.parent))
@@ -53,9 +75,17 @@ class VerifyStep:
         self.window, self.sinks = window, sinks
         if window is None and sinks:
             raise ValueError("sinks go with a window")
+        if (window is not None) + (shared is not None) + (sparse is not None) > 1:
+            raise ValueError("at most one of window, shared and sparse")
+        self.shared, self.sparse = shared, sparse
         self.device = device or cache.k.device
         self.scale = D ** -0.5
-        if window is None:
+        if shared is not None:
+            ws = sv_shared_attention_workspace_size(dtype, B, self.N, Hq, Hkv, D, cache.max_prefix,
+                                                    shared[1].shape[0])
+        elif sparse is not None:
+            ws = self._sparse_buffers()
+        elif window is None:
             ws = sv_tree_attention_workspace_size(dtype, B, self.N, Hq, Hkv, D, cache.max_prefix)
         else:
             ws = sv_window_attention_workspace_size(dtype, B, self.N, Hq, Hkv, D, cache.max_prefix, window)
@@ -80,12 +110,60 @@ class VerifyStep:
             pn = torch.arange(W, dtype=torch.int32, device=self.device)
             self.chain_path = pn.unsqueeze(0).expand(B, W).contiguous()
 
+    def _sparse_buffers(self) -> int:
+        """Buffers of the attention over selected pages; its workspace's size."""
+        c, s = self.cache, self.sparse
+        page = int(c.block_size)
+        if c.block_table is None:
+            pages, rows = -(-c.k.shape[1] // page), (self.B, -(-c.k.shape[1] // page))
+        else:
+            pages, rows = c.block_table.shape[1], (c.k.shape[0],)
+        sets = self.N if s.per_node else 1
+        self.bounds = torch.zeros((*rows, self.Hkv, 2, self.D), dtype=c.k.dtype, device=self.device)
+        self.scores = torch.empty((self.B, sets, self.Hkv, pages), dtype=torch.float32, device=self.device)
+        self.pages = torch.empty((self.B, sets, self.Hkv, s.count), dtype=torch.int32, device=self.device)
+        self._committed = torch.zeros(self.B, dtype=torch.int32, device=self.device)
+        return sv_sparse_attention_workspace_size(self.dtype, self.B, self.N, self.Hq, self.Hkv, self.D, page,
+                                                  s.count, sets)
+
+    def reset_bounds(self, stream=None):
+        """The bounds of all pages of the prefixes, from the cache (a step with ``sparse``)."""
+        sv_page_bounds(self.cache, self.bounds, stream=stream)
+
+    def _before_commit(self, stream):
+        if self.sparse is not None:
+            if stream is None:
+                stream = torch.cuda.current_stream(self.device)
+            elif not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), self.device)
+            with torch.cuda.stream(stream):
+                self._committed.copy_(self.cache.prefix_len)
+
+    def _after_commit(self, stream):
+        if self.sparse is not None:
+            sv_page_bounds(self.cache, self.bounds, start=self._committed, stream=stream)
+
     def kernel_launches(self) -> int:
-        """Kernels one step launches: attention, then the two acceptance kernels (the
-        commit runs inside the second)."""
-        return 1 + 2
+        """Kernels one step launches: attention (with shared prefixes, and over pages where many
+        rows have one list, a second for the keys of its own; scores and selection of pages before
+        it and their bounds after the commit), then the two acceptance kernels (the commit runs
+        inside the second)."""
+        if self.shared is None and self.sparse is None:
+            return 1 + 2
+        return (2 if self.attn_splits else 1) + (3 if self.sparse is not None else 0) + 2
 
     def attention(self, q, k_tree, v_tree, stream=None):
+        if self.shared is not None:
+            return sv_shared_attention(q, k_tree, v_tree, self.cache, self.parent, self.scale, *self.shared,
+                                       out=self.out, workspace=self.attn_ws, stream=stream)
+        if self.sparse is not None:
+            c, s = self.cache, self.sparse
+            sv_page_scores(q, self.bounds, c.prefix_len, c.block_size, block_table=c.block_table,
+                           per_node=s.per_node, out=self.scores, stream=stream)
+            sv_select_pages(self.scores, c.prefix_len, c.block_size, s.count, first=s.first, last=s.last,
+                            out=self.pages, stream=stream)
+            return sv_sparse_attention(q, k_tree, v_tree, c, self.parent, self.scale, self.pages, out=self.out,
+                                       workspace=self.attn_ws, stream=stream)
         if self.window is not None:
             return sv_window_attention(q, k_tree, v_tree, self.cache, self.parent, self.scale, self.window,
                                        sinks=self.sinks, out=self.out, workspace=self.attn_ws, stream=stream)
@@ -109,11 +187,19 @@ class VerifyStep:
 
     def commit(self, k_tree, v_tree, stream=None):
         path = self.chain_path if self.chain else self.outs["path_nodes"]
+        self._before_commit(stream)
         sv_commit_kv(k_tree, v_tree, path, self.outs["num_accepted"], self.cache, stream=stream)
+        self._after_commit(stream)
 
     def accept_commit(self, target_logits, q_draft, node_tokens, k_tree, v_tree, seed=0,
                       round_=0, stream=None):
         """Acceptance and the commit of the kept path in one call."""
+        self._before_commit(stream)
+        r = self._accept_commit(target_logits, q_draft, node_tokens, k_tree, v_tree, seed, round_, stream)
+        self._after_commit(stream)
+        return r
+
+    def _accept_commit(self, target_logits, q_draft, node_tokens, k_tree, v_tree, seed, round_, stream):
         if self.chain:
             toks = node_tokens[:, 1:] if node_tokens.shape[1] == self.N else node_tokens
             return sv_accept_chain_commit(
