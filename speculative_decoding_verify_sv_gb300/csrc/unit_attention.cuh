@@ -210,7 +210,8 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     const int R = mt * RB + tid, node = R / p.G;
     s_row[tid] = R < p.M ? (b * p.N + node0 + node) * p.Hq + kvh * p.G + R - node * p.G : -1;
   }
-  if (tid == 0) *abort_flag = *s_most = 0;
+  if (tid == 0) *abort_flag = 0;
+  if (Keys::kPieces && tid == 0) *s_most = 0;
   Keys::begin(p);
   int L = p.prefix_len[b];
   if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
@@ -389,7 +390,6 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = kWinNone, l[j][0] = l[j][1] = 0.f;
 
   const float sc = p.scale_log2;
-  const int sinks = Keys::kWindow ? p.sinks : 0;
   // this lane's row of a group for the two kinds of fragment loads, and its 16-byte chunks
   const int k_row = lane & 15, k_chunk = lane >> 4;
   const int v_row = (lane & 7) + ((lane >> 4) << 3), v_chunk = (lane >> 3) & 1;
@@ -469,13 +469,11 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   auto mask = [&](int i, uint32_t stage, bool bad) {
     const int gi = g0 + slice + KS * i;
     const bool tree = gi < gt;
-    int base;
+    if (!Keys::kListed && !bad && i >= plain0 && i < plain1) return;
+    int base = gi < gs ? kWinGroup * (gi < gt ? gi : gi - gt) : first + kWinGroup * (gi - gs);
     if constexpr (Keys::kListed) {
       base = tree ? kWinGroup * gi : s_pos[(stage - ring_addr) / Lay::G_BYTES];
       if (!bad && !tree && base + kWinGroup <= L) return;
-    } else {
-      if (!bad && i >= plain0 && i < plain1) return;
-      base = gi < gs ? kWinGroup * (gi < gt ? gi : gi - gt) : first + kWinGroup * (gi - gs);
     }
     const int end = bad ? 0 : (tree ? p.N : (gi < gs ? n_sinks : L));
 #pragma unroll
@@ -490,15 +488,15 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
           see1 = seen & 256u;
         } else {
           const int lo = s_lo[r];
-          see0 = key < end && (key >= lo || key < sinks);
-          see1 = key + 8 < end && (key + 8 >= lo || key + 8 < sinks);
+          see0 = key < end && (key >= lo || (Keys::kWindow && key < p.sinks));
+          see1 = key + 8 < end && (key + 8 >= lo || (Keys::kWindow && key + 8 < p.sinks));
         }
         if (!see0) s[j][e] = -INFINITY;
         if (!see1) s[j][e + 2] = -INFINITY;
       }
     // V rows that no row sees may hold anything: zero them, so that 0 * V stays 0
     const int key = base + k_row;
-    const bool live = key < end && (tree || key >= lo_root || key < sinks);
+    const bool live = key < end && (tree || key >= lo_root || (Keys::kWindow && key < p.sinks));
     if (__all_sync(0xFFFFFFFFu, live)) return;
     if (!live) {
       uint8_t *sv = ring + (stage - ring_addr) + Lay::K_BYTES;
