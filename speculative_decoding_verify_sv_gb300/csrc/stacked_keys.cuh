@@ -65,23 +65,37 @@ struct ListedKeys {
 struct JoinedKeys {
   using Params = PieceParams;
   static constexpr bool kWindow = false, kListed = false, kPieces = true;
-  __device__ static __forceinline__ void begin(const Params &) { wait_previous(); }
+  // The stacked kernel lets this one be set up when it has itself waited for everything before it, so that
+  // only what it writes has to be waited for: the first own keys are on their way before (wait_pieces).
+  __device__ static __forceinline__ void begin(const Params &) {}
   __device__ static __forceinline__ int sequence(const Params &, int bs) { return bs; }
   __device__ static __forceinline__ int first_node(const Params &, int) { return 0; }
   // Listed pages: no own keys, and the same work for every list.
   __device__ static __forceinline__ SharedPart listed_part(const Params &p, int b) {
     const int units = p.Hkv * p.row_tiles;
-    return {b, INT32_MAX, p.list_tiles, p.row_tiles, b * units, (long long)b * units * p.list_tiles, (long long)p.B * units * p.list_tiles};
+    return {b, INT32_MAX, p.row_tiles, -1, p.list_tiles, b * units, (long long)b * units * p.list_tiles, (long long)p.B * units * p.list_tiles};
   }
-  // Group g and its share of the stacked kernel's work, in one round trip to memory; *bad if it does not
-  // ascend.  True if it holds sequence b.
+  static __device__ __forceinline__ SharedPart none() { return {0, 0, 0, -1, 0, 0, 0, 0}; }
+  // Group g; *bad if it does not ascend.  True if it holds sequence b.
   __device__ static __forceinline__ bool group_part(const Params &p, int g, int b, SharedPart *part, int *bad) {
     const int a = p.group_start[g], e = p.group_start[g + 1], len = p.shared_len[g];
-    const long long first = p.header[1 + 2 * g], at = p.header[2 + 2 * g], total = p.header[0];
     *bad |= a < 0 || e < a || e > p.B;
-    const int per = (int)(((long long)(e - a) * p.N + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens));
-    *part = {a, len, (int)(at >> 32), per, (int)at, first, total};
+    *part = none();
+    part->start = a;
+    part->len = len;
+    part->per = (int)(((long long)(e - a) * p.N + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens));
+    part->group = g;
     return a <= b && b < e;
+  }
+  // Waits for the stacked kernel; then the group's share of its work.
+  __device__ static __forceinline__ void wait_pieces(const Params &p, SharedPart &part) {
+    wait_previous();
+    if (part.group < 0) return;
+    part.first = p.header[1 + 2 * part.group];
+    const long long at = p.header[2 + 2 * part.group];
+    part.tiles = (int)(at >> 32);
+    part.unit = (int)at;
+    part.total = p.header[0];
   }
   __device__ static __forceinline__ SharedPart checked(const Params &p, int b, bool reports, SharedPart part) {
     // (a group's shared keys are every member's)
@@ -105,14 +119,14 @@ struct JoinedKeys {
       }
     bad = __syncthreads_or(bad);
     found = __syncthreads_or(found);
-    if (bad || !found) return {0, 0, 0, 0, 0, 0, 0};
+    if (bad || !found) return none();
     return checked(p, b, reports && threadIdx.x == 0, *s_part);
   }
   __device__ static __forceinline__ SharedPart shared_part_warp(const Params &p, int b, bool reports) {
     if (!p.group_start) return listed_part(p, b);
     const int lane = threadIdx.x & 31;
     int bad = 0;
-    SharedPart mine{0, 0, 0, 0, 0, 0, 0}, part;
+    SharedPart mine = none(), part;
     bool found = false;
     for (int g = lane; g < p.groups; g += 32)
       if (group_part(p, g, b, &part, &bad)) {
@@ -120,10 +134,14 @@ struct JoinedKeys {
         found = true;
       }
     const unsigned who = __ballot_sync(0xFFFFFFFFu, found);
-    if (__any_sync(0xFFFFFFFFu, bad) || who == 0) return {0, 0, 0, 0, 0, 0, 0};
+    if (__any_sync(0xFFFFFFFFu, bad) || who == 0) return none();
     const int from = __ffs((int)who) - 1;
     auto share = [&](auto v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
-    part = {share(mine.start), share(mine.len), share(mine.tiles), share(mine.per), share(mine.unit), share(mine.first), share(mine.total)};
+    part = none();
+    part.start = share(mine.start);
+    part.len = share(mine.len);
+    part.per = share(mine.per);
+    part.group = share(mine.group);
     return checked(p, b, reports && lane == 0, part);
   }
   // Where the stacked kernel has left the pieces of a row: its unit's share of the work, cut where a

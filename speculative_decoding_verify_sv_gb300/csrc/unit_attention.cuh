@@ -106,9 +106,9 @@ struct Pieces {
 };
 // What a sequence shares: the group, its first sequence and the number of keys.
 struct SharedPart {
-  int start, len;          // of its group: the first sequence, the keys
-  int tiles, per, unit;    // key tiles, row tiles of a KV head, first unit (tiles = 0: no pieces)
-  long long first, total;  // first work item of the group, all of the call's
+  int start, len, per, group;  // of its group: the first sequence, the keys, row tiles of a KV head, its number (-1: none)
+  int tiles, unit;             // key tiles (0: no pieces), first unit
+  long long first, total;      // first work item of the group, all of the call's
 };
 
 // Wait for the phase of the given parity; false if it ran past the limit (then *abort is raised) or
@@ -215,7 +215,7 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   Keys::begin(p);
   int L = p.prefix_len[b];
   if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
-  const SharedPart shared = Keys::shared_part(p, b, reports, reinterpret_cast<SharedPart *>(sm + Lay::OFF_PIECE - 64));  // (a barrier)
+  SharedPart shared = Keys::shared_part(p, b, reports, reinterpret_cast<SharedPart *>(sm + Lay::OFF_PIECE - 64));  // (a barrier)
   // query rows as B operands, on their way before the first keys
   uint8_t *s_q = sm + Lay::OFF_Q;
 #pragma unroll
@@ -302,17 +302,6 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     if (elect_one() && (RG == 1 || parity < 0 || limited_wait(&empty[st], parity, abort_flag, p))) copy(i, row, pos, tree, st);
     __syncwarp();
   };
-  // a row's pieces, and the maxima and sums of the first two
-  Pieces pieces;
-  float2 ml0 = make_float2(kWinNone, 0.f), ml1 = ml0;
-  if constexpr (Keys::kPieces) {
-    if (tid < RB && rank == 0 && mt * RB + tid < p.M) {
-      const int R = mt * RB + tid;
-      pieces = Keys::pieces_of(p, b, kvh, R / p.G, R % p.G, shared);
-      if (pieces.count > 0) ml0 = p.part_ml[pieces.row];
-      if (pieces.count > 1) ml1 = p.part_ml[pieces.row + kStackRows];
-    }
-  }
   // The first groups, one after another so that the first one is whole soon (2048 units of 32 rows,
   // window 1025, 169 us against 176 with a lane each); with a lane each only for 33 to 48 rows (512
   // units, window 4097, 179 us against 185; 256 units of 64 rows, window 513, 23.8 against 24.9).
@@ -324,6 +313,19 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
       __syncwarp();
     } else {
       for (int i = 0; i < min(ST, n); ++i) issue(i, i, -1);
+    }
+  }
+
+  // a row's pieces, and the maxima and sums of the first two
+  Pieces pieces;
+  float2 ml0 = make_float2(kWinNone, 0.f), ml1 = ml0;
+  if constexpr (Keys::kPieces) {
+    Keys::wait_pieces(p, shared);
+    if (tid < RB && rank == 0 && mt * RB + tid < p.M) {
+      const int R = mt * RB + tid;
+      pieces = Keys::pieces_of(p, b, kvh, R / p.G, R % p.G, shared);
+      if (pieces.count > 0) ml0 = p.part_ml[pieces.row];
+      if (pieces.count > 1) ml1 = p.part_ml[pieces.row + kStackRows];
     }
   }
 

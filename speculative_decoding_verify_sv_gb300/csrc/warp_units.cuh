@@ -75,7 +75,7 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
                 row >= 0);
   }
   cp_async_commit();
-  const SharedPart shared = Keys::shared_part_warp(p, b, reports);
+  SharedPart shared = Keys::shared_part_warp(p, b, reports);
   if (L < 0 || L > p.cap) {
     if (reports && lane == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
     L = L < 0 ? 0 : p.cap;
@@ -147,6 +147,8 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
     kept[i] = -1;
     if (i < n) issue(i);
   }
+
+  if constexpr (Keys::kPieces) Keys::wait_pieces(p, shared);
 
   // ---- what each row sees of the tree; its pieces, their maximum and sum
   Pieces pieces;
