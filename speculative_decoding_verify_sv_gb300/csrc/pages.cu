@@ -203,33 +203,46 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// A CTA per list.  One histogram of 256 equal parts of the scores' range gives the part in which the last
-// place falls.  What is above it is chosen; what is in it are candidates, few as a rule, of which each counts
-// those before it (or, many of them, digits of 8 bits of their keys decide, and of those equal to the end
-// the lower pages).  (The highest bits in which the keys differ as the first digit: scores of both signs then
-// meet in a few of its words, and 2560 lists of up to 2048 scores take 23 us for the atomics instead of 18.3;
-// without atomics, by counts against seven pivots at a time until few scores are left, 25.3.)
-// The chosen pages are bits of words, from which a lane puts out those of its word.
-constexpr int kSelectThreads = 512;  // at most
-constexpr int kCandidates = 512;     // of a list; more of them are looked up among all scores again
+// A list is a warp's (many lists) or a CTA's, in whose registers its scores are, up to E per thread.  One histogram
+// of 256 equal parts of the scores' range gives the part in which the last place falls.  What is above it is
+// chosen; what is in it are candidates, few as a rule, of which each counts those before it (or, many of them,
+// digits of 8 bits of their keys decide, and of those equal to the end the lower pages).  The chosen pages are
+// bits of words, which lanes hold and put out.
+// Bound by instructions and their latency: 2560 lists of up to 2048 scores 15.7 us (of 17.8 before the loops ran without
+// branches 3.7 started, 2.1 loaded, 3 found the parts, 2.6 counted, 4.1 sorted out, 2.3 put out); with the scores in
+// shared memory, 4500 instructions per list, 18.3; the highest bits in which the keys differ as the parts, where
+// scores of both signs meet in a few words, 23; without atomics, by counts against seven pivots at a time, 25.3.
+constexpr int kSelectWarps = 2;  // a list each
 
-struct SelectWords {
-  uint32_t over, tie;  // chosen; equal to the threshold
+template <int E, bool WARP>
+struct SelectShared {
+  static constexpr int WARPS = WARP ? 1 : E == 32 ? 32 : 16;  // of a list, at most
+  static constexpr int CAND = WARP ? 128 : 512;  // candidates of a list; more of them are looked up again
+  uint32_t hist[256], key[CAND], over[WARPS * E], tie[WARPS * E], bin, left, whole, count;
+  uint16_t cand[CAND];
+  float least[WARPS], largest[WARPS];
+  int above[WARPS], equal[WARPS];
 };
 
-__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ __align__(8) uint32_t sel_smem[];
-  SelectWords *words = reinterpret_cast<SelectWords *>(sel_smem);                    // [ceil(P / 32)]
-  float *score = reinterpret_cast<float *>(sel_smem) + 2 * ((p.P + 31) / 32);        // [P]
-  __shared__ uint16_t cand[kCandidates];
-  __shared__ uint32_t hist[2][256], s_bin, s_left, s_whole, s_cand;
-  __shared__ float red[2][32];
-  __shared__ int above[32], equal[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, warps = T >> 5;
-  const long long list = blockIdx.x;
+template <int E, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kSelectWarps : 32 * SelectShared<E, WARP>::WARPS)
+    select_pages_kernel(const __grid_constant__ SelectParams p) {
+  using Shared = SelectShared<E, WARP>;
+  constexpr int STEP = E < 8 ? E : 8;
+  __shared__ Shared shared[WARP ? kSelectWarps : 1];
+  const int lane = threadIdx.x & 31, cta_warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0);
+  const int warp = WARP ? 0 : cta_warp, tid = WARP ? lane : (int)threadIdx.x, T = WARP ? 32 : (int)blockDim.x, warps = T >> 5;
+  Shared &sh = shared[WARP ? cta_warp : 0];
+  auto sync = [] {
+    if constexpr (WARP) __syncwarp();
+    else __syncthreads();
+  };
+  const long long list = WARP ? (long long)blockIdx.x * kSelectWarps + cta_warp : blockIdx.x;
   const int b = (int)(list / p.lists);
-  for (int i = tid; i < 256; i += T) hist[0][i] = 0;
-  if (tid == 0) s_cand = 0;
+  if (b >= p.B) return;
+  for (int i = tid; i < 256; i += T) sh.hist[i] = 0;
+  for (int i = tid; i < warps * E; i += T) sh.over[i] = sh.tie[i] = 0;
+  if (tid == 0) sh.count = 0;
   wait_previous();
   int L = p.prefix_len[b];
   const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
@@ -243,44 +256,74 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const __gr
     for (int i = tid; i < p.K; i += T) out[i] = i < pages ? i : -1;
     return;
   }
-  // pages [m0, m1) compete for `left` places
-  const int m0 = p.first, m1 = pages - p.last;
+  // pages [m0, m1) compete for `left` places; this warp's words of 32 pages are [w0, w0 + n), and of this lane's
+  // pages at0 + 32 e those with e in [e0, e1) compete
+  const int m0 = p.first, m1 = pages - p.last, count = (pages + 31) / 32, per = (count + warps - 1) / warps;
+  const int w0 = min(count, warp * per), n = min(count, w0 + per) - w0, at0 = 32 * w0 + lane;
+  const int e0 = (max(m0 - at0, 0) + 31) / 32, e1 = min(n, (max(m1 - at0, 0) + 31) / 32);
   int left = p.K - p.first - p.last;
-  const float *x = p.scores + list * p.P;
-  float least = FLT_MAX, largest = -FLT_MAX;  // of the finite ones
-#pragma unroll 8
-  for (int i = m0 + tid; i < m1; i += T) {
-    const float v = x[i];
-    score[i] = v;
-    if (fabsf(v) <= FLT_MAX) {
-      least = fminf(least, v);
-      largest = fmaxf(largest, v);
+  const float *scores = p.scores + list * p.P;
+  float x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = e >= e0 && e < e1 ? scores[at0 + 32 * e] : __int_as_float(0x7FC00000);
+  // the least and largest finite ones
+  float least[2] = {FLT_MAX, FLT_MAX}, largest[2] = {-FLT_MAX, -FLT_MAX};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    least[e & 1] = fminf(least[e & 1], x[e]);
+    largest[e & 1] = fmaxf(largest[e & 1], x[e]);
+  }
+  float lo = fminf(least[0], least[1]), hi = fmaxf(largest[0], largest[1]);
+  if (lo < -FLT_MAX || hi > FLT_MAX) {
+    lo = FLT_MAX, hi = -FLT_MAX;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (fabsf(x[e]) <= FLT_MAX) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
+  }
+  auto extremes = [&] {
+    asm volatile("redux.sync.min.f32 %0, %0, 0xFFFFFFFF;" : "+f"(lo));
+    asm volatile("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(hi));
+  };
+  __syncwarp();
+  extremes();
+  if constexpr (!WARP) {
+    if (lane == 0) sh.least[warp] = lo, sh.largest[warp] = hi;
+    __syncthreads();
+    lo = lane < warps ? sh.least[lane] : FLT_MAX;
+    hi = lane < warps ? sh.largest[lane] : -FLT_MAX;
+    extremes();
+  }
+  // Parts of the range, growing with the score; infinities and NaN are at the ends.  Without a range (equal
+  // scores, no finite ones, or an overflow) there is one part.
+  const float range = hi - lo, scale = range > 0.f && range <= FLT_MAX ? 255.f / range : 0.f;
+  const bool one_part = !(scale > 0.f && scale <= FLT_MAX), choose = left > 0;
+  int part[E];  // of each score that competes, -1 for the others
+#pragma unroll
+  for (int c = 0; c < E; c += STEP) {
+    if (c < n) {
+#pragma unroll
+      for (int e = c; e < c + STEP; ++e) {
+        const unsigned k = min(255u, __float2uint_rz((x[e] - lo) * scale));  // (-infinity: 0)
+        part[e] = x[e] == x[e] ? (int)k : 255;
+        if (one_part) part[e] = 0;
+        if (e < e0 || e >= e1) part[e] = -1;
+        if (choose && part[e] >= 0) atomicAdd(&sh.hist[part[e]], 1u);
+      }
+    } else {
+#pragma unroll
+      for (int e = c; e < c + STEP; ++e) part[e] = -1;
     }
   }
-  asm volatile("redux.sync.min.f32 %0, %0, 0xFFFFFFFF;" : "+f"(least));
-  asm volatile("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(largest));
-  if (lane == 0) red[0][warp] = least, red[1][warp] = largest;
-  __syncthreads();
-  least = lane < warps ? red[0][lane] : FLT_MAX;
-  largest = lane < warps ? red[1][lane] : -FLT_MAX;
-  asm volatile("redux.sync.min.f32 %0, %0, 0xFFFFFFFF;" : "+f"(least));
-  asm volatile("redux.sync.max.f32 %0, %0, 0xFFFFFFFF;" : "+f"(largest));
-  // the part of the range, growing with the score; infinities and NaN are at the ends
-  const float range = largest - least, scale = range > 0.f && range <= FLT_MAX ? 255.f / range : 0.f;
-  auto bin_of = [&](float v) -> int {
-    if (!(fabsf(v) <= FLT_MAX)) return v == -INFINITY ? 0 : 255;
-    return min(255, (int)((v - least) * scale));
-  };
+  // the bin of the histogram in which the last of the `left` places falls
   bool whole = false;  // all of the part, or digit, have places
-  int pass = 0;
-  // the bin of this pass's histogram in which the last of the `left` places falls
   auto find = [&]() -> int {
+    sync();
     if (warp == 0) {
-      uint32_t n[8], sum = 0;
+      uint32_t m[8], sum = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        n[e] = hist[pass & 1][255 - (8 * lane + e)];
-        sum += n[e];
+        m[e] = sh.hist[255 - (8 * lane + e)];
+        sum += m[e];
       }
       uint32_t before = sum;
 #pragma unroll
@@ -289,124 +332,116 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const __gr
         if (lane >= o) before += y;
       }
       before -= sum;
+      if (before < (uint32_t)left && before + sum >= (uint32_t)left) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (before < (uint32_t)left && before + n[e] >= (uint32_t)left) {
-          s_bin = 255 - (8 * lane + e);
-          s_left = left - before;
-          s_whole = before + n[e] == (uint32_t)left;
+        for (int e = 0; e < 8; ++e) {
+          if (before < (uint32_t)left && before + m[e] >= (uint32_t)left) {
+            sh.bin = 255 - (8 * lane + e);
+            sh.left = left - before;
+            sh.whole = before + m[e] == (uint32_t)left;
+          }
+          before += m[e];
         }
-        before += n[e];
       }
     }
-    __syncthreads();
-    left = (int)s_left;
-    whole = s_whole != 0;
-    ++pass;
-    return (int)s_bin;
+    sync();
+    left = (int)sh.left;
+    whole = sh.whole != 0;
+    return (int)sh.bin;
   };
-  const bool choose = left > 0;
-  int bin = 256;
-  if (choose) {
-#pragma unroll 8
-    for (int i = m0 + tid; i < m1; i += T) atomicAdd(&hist[0][bin_of(score[i])], 1u);
-    for (int i = tid; i < 256; i += T) hist[1][i] = 0;
-    __syncthreads();
-    bin = find();
-  }
-  // bits of the pages above the part (and of those that are kept anyhow), and the candidates
-  const int count = (pages + 31) / 32;
-  for (int w = warp; w < count; w += warps) {
-    const int i = 32 * w + lane;
-    bool over = i < pages && (i < m0 || i >= m1), maybe = false;
-    if (choose && i >= m0 && i < m1) {
-      const int k = bin_of(score[i]);
-      over = k > bin || (whole && k == bin);
-      maybe = !whole && k == bin;
-    }
-    const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bm = __ballot_sync(0xFFFFFFFFu, maybe);
-    uint32_t at = 0;
-    if (lane == 0) {
-      words[w] = {bo, 0};
-      if (bm) at = atomicAdd(&s_cand, (uint32_t)__popc(bm));
-    }
-    if (bm) {
-      at = __shfl_sync(0xFFFFFFFFu, at, 0);
-      at += __popc(bm & ((1u << lane) - 1));
-      if (maybe && at < kCandidates) cand[at] = (uint16_t)i;
-    }
-  }
-  __syncthreads();
-  const int n = (int)s_cand;
-  if (n > 0 && n <= kCandidates) {
-    // a candidate has a place if fewer than `left` come before it
-    for (int i = tid; i < n; i += T) {
-      const int at = cand[i];
-      const uint32_t k = score_key(score[at]);
-      int before = 0;
-      for (int c = 0; c < n; ++c) {
-        const int other = cand[c];
-        const uint32_t y = score_key(score[other]);
-        before += y > k || (y == k && other < at);
+  const int last = choose ? find() : 1000;
+  // this lane's word of the chosen pages, and which of its pages are candidates
+  uint32_t mine = 0, maybe = 0;
+  const int over_from = whole ? last : last + 1, maybe_at = whole || !choose ? 1000 : last;
+#pragma unroll
+  for (int c = 0; c < E; c += STEP) {
+    if (c < n) {
+#pragma unroll
+      for (int e = c; e < c + STEP; ++e) {
+        const unsigned over = __ballot_sync(0xFFFFFFFFu, part[e] >= over_from);
+        if (lane == e) mine = over;
+        if (part[e] == maybe_at) maybe |= 1u << e;
       }
-      if (before < left) atomicOr(&words[at >> 5].over, 1u << (at & 31));
     }
-    __syncthreads();
-  } else if (n > 0) {
-    const int part = bin;
+  }
+  if (maybe) {
+    int at = (int)atomicAdd(&sh.count, (uint32_t)__popc(maybe));
+    for (uint32_t rest = maybe; rest; rest &= rest - 1, ++at) {
+      const int page = at0 + 32 * (__ffs((int)rest) - 1);
+      if (at < Shared::CAND) sh.cand[at] = (uint16_t)page, sh.key[at] = score_key(scores[page]);
+    }
+  }
+  sync();
+  const int candidates = (int)sh.count;
+  if (candidates > 0 && candidates <= Shared::CAND) {
+    // a candidate has a place if fewer than `left` come before it
+    for (int i = tid; i < candidates; i += T) {
+      const int at = sh.cand[i];
+      const uint32_t k = sh.key[i];
+      int before = 0;
+      for (int c = 0; c < candidates; ++c) {
+        const uint32_t y = sh.key[c];
+        before += y > k || (y == k && sh.cand[c] < at);
+      }
+      if (before < left) atomicOr(&sh.over[at >> 5], 1u << (at & 31));
+    }
+    sync();
+  } else if (candidates > 0) {
     uint32_t prefix = 0;
     int high = 32;
+    auto each = [&](auto f) {
+      for (uint32_t rest = maybe; rest; rest &= rest - 1) {
+        const int page = at0 + 32 * (__ffs((int)rest) - 1);
+        f(page, score_key(scores[page]));
+      }
+      __syncwarp();
+    };
     whole = false;
+#pragma unroll 1
     while (high > 0 && !whole) {
       const int low = high - 8;
       const uint32_t mask = high == 32 ? 0 : ~0u << high;
-      for (int i = m0 + tid; i < m1; i += T) {
-        const uint32_t k = score_key(score[i]);
-        if (bin_of(score[i]) == part && ((k ^ prefix) & mask) == 0) atomicAdd(&hist[pass & 1][(k >> low) & 255u], 1u);
-      }
-      for (int i = tid; i < 256; i += T) hist[(pass & 1) ^ 1][i] = 0;
-      __syncthreads();
+      for (int i = tid; i < 256; i += T) sh.hist[i] = 0;
+      sync();
+      each([&](int, uint32_t k) {
+        if (((k ^ prefix) & mask) == 0) atomicAdd(&sh.hist[(k >> low) & 255u], 1u);
+      });
       prefix |= (uint32_t)find() << low;
       high = low;
     }
-    for (int at = m0 + tid; at < m1; at += T) {
-      if (bin_of(score[at]) != part) continue;
-      const uint32_t k = score_key(score[at]);
-      if (whole ? k >= prefix : k > prefix) atomicOr(&words[at >> 5].over, 1u << (at & 31));
-      else if (!whole && k == prefix) atomicOr(&words[at >> 5].tie, 1u << (at & 31));
-    }
-    __syncthreads();
+    each([&](int page, uint32_t k) {
+      if (whole ? k >= prefix : k > prefix) atomicOr(&sh.over[page >> 5], 1u << (page & 31));
+      else if (!whole && k == prefix) atomicOr(&sh.tie[page >> 5], 1u << (page & 31));
+    });
+    sync();
   }
-  // a lane per word, each warp a run of them; of the ties the first `left`
-  const int run = (count + T - 1) / T * 32, w0 = warp * run;
-  int n_over = 0, n_tie = 0;
-  for (int w = w0 + lane; w < min(count, w0 + run); w += 32) n_over += __popc(words[w].over), n_tie += __popc(words[w].tie);
-  n_over = __reduce_add_sync(0xFFFFFFFFu, n_over);
-  n_tie = __reduce_add_sync(0xFFFFFFFFu, n_tie);
-  if (lane == 0) above[warp] = n_over, equal[warp] = n_tie;
-  __syncthreads();
-  int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? above[lane] : 0);
-  int ties = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? equal[lane] : 0);
-  for (int w = w0; w < min(count, w0 + run); w += 32) {
-    SelectWords mine{0, 0};
-    if (w + lane < count) mine = words[w + lane];
-    int o = __popc(mine.over), t = __popc(mine.tie);
-    const int my_o = o, my_t = t;
+  // with the pages that are kept anyhow; of the ties the first `left`
+  uint32_t tied = 0;
+  if (lane < n) {
+    const int page = 32 * (w0 + lane);
+    auto below = [&](int end) { return end <= page ? 0u : end >= page + 32 ? ~0u : (1u << (end - page)) - 1; };
+    mine |= sh.over[w0 + lane] | below(m0) | (below(pages) & ~below(m1));
+    tied = sh.tie[w0 + lane];
+  }
+  int at = __popc(mine), tie = __popc(tied);  // up to this word
 #pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, o, k), z = __shfl_up_sync(0xFFFFFFFFu, t, k);
-      if (lane >= k) o += y, t += z;
-    }
-    int at = base + o - my_o, tie = ties + t - my_t;  // chosen pages and ties before this word
-    at += min(tie, left);
-    for (uint32_t rest = mine.over | mine.tie; rest; rest &= rest - 1) {
-      const int bit = __ffs((int)rest) - 1;
-      const bool is_tie = (mine.tie >> bit) & 1;
-      if (!is_tie || tie < left) out[at++] = 32 * (w + lane) + bit;
-      tie += is_tie;
-    }
-    base += __shfl_sync(0xFFFFFFFFu, o, 31);
-    ties += __shfl_sync(0xFFFFFFFFu, t, 31);
+  for (int s = 1; s < 32; s <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, at, s), z = __shfl_up_sync(0xFFFFFFFFu, tie, s);
+    if (lane >= s) at += y, tie += z;
+  }
+  if constexpr (!WARP) {
+    if (lane == 31) sh.above[warp] = at, sh.equal[warp] = tie;
+    __syncthreads();
+    at += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.above[lane] : 0);
+    tie += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.equal[lane] : 0);
+  }
+  tie -= __popc(tied);
+  at += min(tie, left) - __popc(mine);
+  for (uint32_t rest = mine | tied; rest; rest &= rest - 1) {
+    const int bit = __ffs((int)rest) - 1;
+    const bool is_tie = (tied >> bit) & 1;
+    if (!is_tie || tie < left) out[at++] = 32 * (w0 + lane) + bit;
+    tie += is_tie;
   }
 }
 
@@ -444,14 +479,25 @@ cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream
                   : launch_close(page_scores_f32_kernel<64>, dim3((unsigned)p.units * p.splits), 256, 0, s, p);
 }
 
-cudaError_t launch_select_pages(const SelectParams &p, long long lists, int num_sms, cudaStream_t s) {
-  auto bytes = [](int P) { return (size_t)(P + 31) / 32 * 8 + (size_t)P * 4; };
-  if (bytes(p.P) > 44 * 1024) {  // (with the kernel's other 3.6 KB more than the default 48)
-    const cudaError_t e = allow_smem<2>((const void *)select_pages_kernel, bytes(SV_MAX_SCORE_PAGES));
-    if (e != cudaSuccess) return e;
+// Many lists (four per SM): a warp per list of up to 1024 scores, 16 scores per thread for longer ones; else few scores
+// per thread.  Measured, us a warp / 16 per thread / 4 per thread, 152 SMs:
+//   512 scores    152 lists 4.0 / 5.0 / 3.5;  608 lists 4.1 / 5.1 / 4.2;  2560 lists 5.7 / 7.0 / 9.1
+//   1000 scores   152 lists 5.1 / 5.1 / 3.9;  608 lists 5.4 / 5.6 / 5.3;  2560 lists 8.3 / 10.9 / 15.4
+//   2048 scores   152 lists 9.7 / 5.6 / 4.7;  608 lists 10.2 / 6.7 / 8.4;  2560 lists 20 / 17.1 / 28.9
+cudaError_t launch_select_pages(const SelectParams &p, int num_sms, cudaStream_t s) {
+  const long long lists = (long long)p.B * p.lists;
+  const bool many = lists >= 4ll * num_sms;
+  if (many && p.P <= 1024) {
+    const dim3 grid((unsigned)((lists + kSelectWarps - 1) / kSelectWarps));
+    if (p.P <= 512) return launch_close(select_pages_kernel<16, true>, grid, 32 * kSelectWarps, 0, s, p);
+    return launch_close(select_pages_kernel<32, true>, grid, 32 * kSelectWarps, 0, s, p);
   }
-  const int threads = p.P <= 256 ? 64 : lists <= num_sms || p.P > 8192 ? kSelectThreads : 96;
-  return launch_close(select_pages_kernel, dim3((unsigned)lists), threads, bytes(p.P), s, p);
+  const int e = p.P <= 2048 && !many ? 4 : p.P <= 8192 ? 16 : 32;
+  const dim3 grid((unsigned)lists);
+  const int threads = (p.P + 32 * e - 1) / (32 * e) * 32;
+  if (e == 4) return launch_close(select_pages_kernel<4, false>, grid, threads, 0, s, p);
+  if (e == 16) return launch_close(select_pages_kernel<16, false>, grid, threads, 0, s, p);
+  return launch_close(select_pages_kernel<32, false>, grid, threads, 0, s, p);
 }
 
 }  // namespace sv

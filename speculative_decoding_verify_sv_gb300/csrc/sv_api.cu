@@ -660,6 +660,7 @@ sv_status sv_select_pages(int B, int lists, int P, const float *scores, const in
   p.scores = scores;
   p.prefix_len = prefix_len;
   p.out = out;
+  p.B = B;
   p.lists = lists;
   p.P = P;
   p.page_size = page_size;
@@ -667,7 +668,7 @@ sv_status sv_select_pages(int B, int lists, int P, const float *scores, const in
   p.first = first;
   p.last = last;
   const cudaError_t e = take_injected_failure() ? cudaErrorLaunchFailure
-                                                : sv::launch_select_pages(p, n, num_sms(), static_cast<cudaStream_t>(stream));
+                                                : sv::launch_select_pages(p, num_sms(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "page selection launch");
   sv::count_launches(1);
   return SV_OK;

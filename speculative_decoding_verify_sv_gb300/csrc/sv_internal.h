@@ -329,9 +329,9 @@ struct SelectParams {
   const int32_t *prefix_len;
   int32_t *out;
   unsigned int *status;
-  int lists, P, page_size, K, first, last;  // lists per sequence
+  int B, lists, P, page_size, K, first, last;  // lists per sequence
 };
-cudaError_t launch_select_pages(const SelectParams &p, long long lists, int num_sms, cudaStream_t s);
+cudaError_t launch_select_pages(const SelectParams &p, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- LM head
 
