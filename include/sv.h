@@ -223,9 +223,9 @@ size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
  * prefix_len (the outputs of that sequence are not meaningful).
  * Every other argument, the layouts, the kernels' shapes and the refusals are sv_window_attention's
  * (without window and sinks); Hq / Hkv <= 128, else SV_ERR_UNSUPPORTED.  Rounding as there.  float32
- * calls read each sequence's own rows.
- * Workspace: sv_shared_attention_workspace_size() bytes, 16-byte aligned (0 for float32); it needs no
- * initial value.  Calls that share one must be stream-ordered.  max_prefix as for
+ * calls, and those with little to read in all, read each sequence's own rows.
+ * Workspace: sv_shared_attention_workspace_size() bytes, 16-byte aligned (0 for float32 and for little
+ * to read); it needs no initial value.  Calls that share one must be stream-ordered.  max_prefix as for
  * sv_tree_attention. */
 #define SV_MAX_SHARED_GROUPS 128
 sv_status sv_shared_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,

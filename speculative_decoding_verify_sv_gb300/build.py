@@ -24,7 +24,7 @@ LIB = os.path.join(BUILD, "libsv.so")
 BINDING = os.path.join(BUILD, "sv_binding.so")
 
 SOURCES = ["sv_api.cu", "attention.cu", "attention_tc.cu", "attention_tc_window.cu", "attention_tc_window_paged.cu", "window_attention.cu", "window_attention_f32.cu", "stacked_attention.cu", "stacked_units.cu", "joined_units.cu",
-           "listed_units.cu", "warp_units.cu", "pages.cu", "page_scores_tc.cu",
+           "own_units.cu", "listed_units.cu", "warp_units.cu", "own_warps.cu", "pages.cu", "page_scores_tc.cu",
            "accept.cu", "accept_recursive.cu", "commit.cu", "ngram.cu", "lm_head.cu", "tables.cu", "qk_norm_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

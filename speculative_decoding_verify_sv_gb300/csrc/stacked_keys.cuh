@@ -1,4 +1,4 @@
-// Listed pages, and the own keys behind shared ones, for units of few query rows (sm_103a, bf16): the
+// Listed pages, the own keys behind shared ones, and whole prefixes, for units of few query rows (sm_103a, bf16): the
 // kernels are unit_attention.cuh's (a CTA per unit) and warp_units.cuh's (a warp per unit).
 //
 // Listed pages (sv_sparse_attention): a unit is a sequence, a set of nodes (all of them, or one) and a KV
@@ -18,11 +18,14 @@ namespace sv {
 
 struct ListedParams;
 struct PieceParams;
+struct OwnParams;
 // The launches, each in a file of its own; `groups` of 16 keys per unit (for the choice of shapes).
 cudaError_t launch_listed_units(ListedParams &p, int D, int groups, int num_sms, cudaStream_t s);
-cudaError_t launch_joined_units(PieceParams &p, int D, int groups, int num_sms, cudaStream_t s);
+cudaError_t launch_joined_units(PieceParams &p, int D, int num_sms, cudaStream_t s);
+cudaError_t launch_own_units(OwnParams &p, int D, int groups, int num_sms, cudaStream_t s);
 cudaError_t launch_listed_warps(ListedParams &p, int D, cudaStream_t s);
 cudaError_t launch_joined_warps(PieceParams &p, int D, cudaStream_t s);
+cudaError_t launch_own_warps(OwnParams &p, int D, cudaStream_t s);
 
 struct ListedParams : WinParams {
   const int32_t *pages;  // [B, sets, Hkv, list_len]
@@ -38,8 +41,16 @@ struct PieceParams : WinParams {
   int units;  // (a warp each)
 };
 
+struct OwnParams : WinParams {
+  const int32_t *group_start, *shared_len;
+  int groups;
+  int units;  // (a warp each)
+};
+
 namespace {
 
+template <int D, int NT, int RG>
+__global__ void __launch_bounds__(kWinThreads, 2) own_attn_kernel(const __grid_constant__ OwnParams p);
 template <int D, int NT, int RG>
 __global__ void __launch_bounds__(kWinThreads, 2) listed_attn_kernel(const __grid_constant__ ListedParams p);
 template <int D, int NT, int RG>
@@ -172,6 +183,43 @@ struct JoinedKeys {
   }
 };
 
+// Every key a sequence's own; the groups are only checked, by the first warp of each sequence's first unit.
+struct OwnKeys {
+  using Params = OwnParams;
+  static constexpr bool kWindow = false, kListed = false, kPieces = false;
+  __device__ static __forceinline__ void begin(const Params &) { wait_previous(); }
+  __device__ static __forceinline__ int sequence(const Params &, int bs) { return bs; }
+  __device__ static __forceinline__ int first_node(const Params &, int) { return 0; }
+  __device__ static __forceinline__ SharedPart shared_part_warp(const Params &p, int b, bool reports) {
+    if (!reports) return {};
+    bool bad = false, outside = false, beyond = false;
+    const int L = p.prefix_len[b];
+    for (int g = threadIdx.x & 31; g < p.groups; g += 32) {
+      const int a = p.group_start[g], e = p.group_start[g + 1], len = p.shared_len[g];
+      bad |= a < 0 || e < a || e > p.B;
+      outside |= len < 0 || len > p.cap;
+      beyond |= a <= b && b < e && len > L;
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (bad || outside || beyond)
+      set_status(p.status, (bad ? SV_DEV_BAD_GROUP : 0) | (outside || (beyond && !bad) ? SV_DEV_BAD_PREFIX : 0));
+    return {};
+  }
+  __device__ static __forceinline__ SharedPart shared_part(const Params &p, int b, bool reports, SharedPart *) {
+    if (threadIdx.x < 32) shared_part_warp(p, b, reports);
+    __syncthreads();
+    return {};
+  }
+  template <int D, int NT, int RG>
+  static auto kernel() {
+    return own_attn_kernel<D, NT, RG>;
+  }
+};
+
+template <int D, int NT, int RG>
+__global__ void __launch_bounds__(kWinThreads, 2) own_attn_kernel(const __grid_constant__ OwnParams p) {
+  unit_attention<D, NT, RG, OwnKeys>(p);
+}
 template <int D, int NT, int RG>
 __global__ void __launch_bounds__(kWinThreads, 2) listed_attn_kernel(const __grid_constant__ ListedParams p) {
   unit_attention<D, NT, RG, ListedKeys>(p);

@@ -72,7 +72,7 @@ cudaError_t launch_stack(StackParams &p, const AttnParams &a, const StackPlan &p
   return launch_stacked(p, a.D, listed, pl.grid, s);
 }
 
-cudaError_t launch_joined(const AttnParams &a, const StackParams &st, const StackPlan &pl, int groups_of_keys, cudaStream_t s) {
+cudaError_t launch_joined(const AttnParams &a, const StackParams &st, const StackPlan &pl, cudaStream_t s) {
   PieceParams p{};
   if (!unit_params(p, a, a.M)) return cudaErrorInvalidValue;
   p.group_start = st.group_start;
@@ -86,14 +86,23 @@ cudaError_t launch_joined(const AttnParams &a, const StackParams &st, const Stac
   p.row_tiles = pl.row_tiles;
   p.list_tiles = pl.list_tiles;
   return warp_units_pay(p, (long long)a.B * a.Hkv, pl.grid) ? launch_joined_warps(p, a.D, s)
-                                                                           : launch_joined_units(p, a.D, groups_of_keys, pl.grid, s);
+                                                                           : launch_joined_units(p, a.D, pl.grid, s);
 }
 
 }  // namespace
 
-StackPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int groups, int num_sms) {
+// Shared prefixes are worth the stacked kernel and its pieces where there is much to read, as far as the host can
+// know (the lengths are the device's).  Measured, us stacked / every sequence's own rows, one group, keys of all
+// units in thousands:
+//   one token, 32:8 heads   4 requests of 4096 keys (133) 18.7 / 9.8;  64 of 256 (172) 19 / 13;  16 of 4096 (534) 19 / 22;
+//                           64 of 4096 (2138) 31 / 73
+//   8 nodes, 64:8 heads     16 of 1024 (141) 31 / 21;  256 of 32 (229) 90 / 39;  16 of 4096 (534) 40 / 60
+//   64 nodes, 32:32 heads   16 of 256 (172) 37 / 31;  64 of 32 (229) 108 / 60;  4 of 4096 (534) 47 / 64
+StackPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int max_prefix, int groups, int num_sms) {
   StackPlan pl{};
   pl.grid = num_sms > 0 ? num_sms : 152;
+  const double reads = (double)B * Hkv * (((long long)N * (Hq / Hkv) + 63) / 64) * max_prefix;  // keys that units read
+  if (reads < 1800. * pl.grid || max_prefix <= 128) return pl;
   pl.stacked = true;
   pl.tile_tokens = 128 / (Hq / Hkv);
   const long long units = (((long long)B * N + 2 * pl.tile_tokens - 1) / (2 * pl.tile_tokens) + groups) * Hkv;
@@ -125,16 +134,28 @@ StackPlan sparse_plan(int B, int N, int Hq, int Hkv, int D, int page_size, int l
 
 cudaError_t launch_shared_attention(const AttnParams &a, const ListArgs &l, const StackPlan &pl, void *ws, cudaStream_t s,
                                     bool (*fails)(), unsigned *launches) {
+  if (fails()) return cudaErrorLaunchFailure;
+  if (!pl.stacked) {
+    OwnParams o{};
+    if (!unit_params(o, a, a.M)) return cudaErrorInvalidValue;
+    o.group_start = l.group_start;
+    o.shared_len = l.shared_len;
+    o.groups = l.groups;
+    const cudaError_t e = warp_units_pay(o, (long long)a.B * a.Hkv, pl.grid)
+                              ? launch_own_warps(o, a.D, s)
+                              : launch_own_units(o, a.D, (a.cap + a.N) / kWinGroup + 2, pl.grid, s);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+  }
   StackParams p{};
   p.group_start = l.group_start;
   p.shared_len = l.shared_len;
   p.groups = l.groups;
-  if (fails()) return cudaErrorLaunchFailure;
   cudaError_t e = launch_stack(p, a, pl, ws, false, a.block_table ? box_of(a.block_size) : 128, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (fails()) return cudaErrorLaunchFailure;
-  e = launch_joined(a, p, pl, a.N / kWinGroup + 18, s);
+  e = launch_joined(a, p, pl, s);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
@@ -152,7 +173,7 @@ cudaError_t launch_sparse_attention(const AttnParams &a, const ListArgs &l, cons
     if (e != cudaSuccess) return e;
     ++*launches;
     if (fails()) return cudaErrorLaunchFailure;
-    e = launch_joined(a, p, pl, a.N / kWinGroup + 1, s);
+    e = launch_joined(a, p, pl, s);
   } else {
     ListedParams p{};
     const int set_nodes = a.N / l.sets;

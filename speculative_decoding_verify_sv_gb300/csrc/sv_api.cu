@@ -469,7 +469,7 @@ size_t sv_shared_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
   if (dt != SV_BF16 || B <= 0 || N <= 0 || N > SV_MAX_TREE_NODES || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
       Hq / Hkv > 128 || (D != 64 && D != 128) || max_prefix < 0 || groups < 1 || groups > SV_MAX_SHARED_GROUPS)
     return 0;
-  return sv::shared_plan(B, N, Hq, Hkv, D, groups, num_sms()).ws_bytes;
+  return sv::shared_plan(B, N, Hq, Hkv, D, max_prefix, groups, num_sms()).ws_bytes;
 }
 
 sv_status sv_shared_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, const void *q,
@@ -485,7 +485,7 @@ sv_status sv_shared_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
   if (groups > SV_MAX_SHARED_GROUPS) return fail(SV_ERR_UNSUPPORTED, "%d groups (supported %d)", groups, SV_MAX_SHARED_GROUPS);
   if (B == 0) return SV_OK;
   if (!group_start || !shared_len) return fail(SV_ERR_INVALID_ARG, "group_start or shared_len is NULL");
-  const sv::StackPlan plan = dt == SV_BF16 ? sv::shared_plan(B, N, Hq, Hkv, D, groups, num_sms()) : sv::StackPlan{};
+  const sv::StackPlan plan = dt == SV_BF16 ? sv::shared_plan(B, N, Hq, Hkv, D, p.cap, groups, num_sms()) : sv::StackPlan{};
   if ((st = check_plan(plan, workspace, workspace_bytes)) != SV_OK) return st;
   if (!(p.status = status_word())) return fail(SV_ERR_CUDA, "no CUDA device");
   const sv::ListArgs l{group_start, shared_len, groups, nullptr, 0, 0, 0};

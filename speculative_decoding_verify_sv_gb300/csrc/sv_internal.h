@@ -156,7 +156,7 @@ struct StackPlan {
   long long pieces;   // at most
   size_t off_ml, off_o, ws_bytes;
 };
-StackPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int groups, int num_sms);
+StackPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int max_prefix, int groups, int num_sms);
 StackPlan sparse_plan(int B, int N, int Hq, int Hkv, int D, int page_size, int list_len, int sets, int num_sms);
 struct ListArgs {
   const int32_t *group_start, *shared_len;

@@ -94,8 +94,7 @@ struct WinLayout {
   static constexpr int OFF_MORE = (OFF_ABORT + 16 + 15) & ~15;
   static constexpr int OFF_PIECE = OFF_MORE + RB * 24 + CAP * RB * 4 + 64;
   static constexpr int SMEM = Keys::kListed ? OFF_MORE + KS * ST * 4 : Keys::kPieces ? OFF_PIECE + PB * RB * (D + 4) * 4 : OFF_ABORT + 16;
-  // (with pieces, clusters are for CTAs of up to 24 rows)
-  static_assert((Keys::kPieces && RB > 24 ? OFF_JOIN : OFF_JOIN + JOIN) <= RING, "the merge goes on in the ring's room");
+  static_assert((Keys::kPieces ? OFF_JOIN : OFF_JOIN + JOIN) <= RING, "the merge goes on in the ring's room");
   static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -902,10 +901,11 @@ inline WinPlan window_plan(long long kv_units, int M, int groups, int num_sms, b
     // (its start and merge) beside its share of the window's groups: 512 units of 32 rows, window
     // 4097, go without clusters, 156 us against 181 with clusters of four.  (Clusters of 16 gain
     // little on the longest windows and start later: 8 units of 4 rows, window 1024, 0.6 us more; 16
-    // such clusters find no room together, 25 us against 13.)
+    // such clusters find no room together, 25 us against 13.)  With pieces, whose rows' own keys are few, none:
+    // 4 tokens of one head each, 4096 shared keys, 19 us against 28; 16 tokens 19 against 20.7.
     long long best = 0;
     int cluster = 1;
-    for (int c = 1; c <= (pieces && rows > 24 ? 1 : 8); c *= 2) {
+    for (int c = 1; c <= (pieces ? 1 : 8); c *= 2) {
       const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 16);
       if (c == 1 || cost < best) {
         best = cost;

@@ -86,8 +86,8 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
   const int own = Keys::kPieces ? min(shared.len, L) : 0, first = own & ~(kWinGroup - 1);
   const int gt = (p.N + kWinGroup - 1) / kWinGroup;
   int n = gt;
-  if constexpr (Keys::kPieces) n += own < L ? (L - first + kWinGroup - 1) / kWinGroup : 0;
   if constexpr (Keys::kListed) n += p.list_len * p.page_groups;
+  else n += own < L ? (L - first + kWinGroup - 1) / kWinGroup : 0;
   if (!real || !layout_ok) n = 0;
   const uint64_t stream_policy = l2_policy_evict_first(), tree_policy = l2_policy_evict_normal();
   int desc = -1, desc_pos = 0;  // lane i: row and position of group 32 k + i, k the batch being issued
@@ -409,6 +409,39 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
     if (!layout_ok) set_status(p.status, SV_DEV_LAYOUT);
     else if (*abort_flag) set_status(p.status, SV_DEV_TIMEOUT);
   }
+}
+
+template <int D, int NT, class Keys, class P>
+cudaError_t launch_warps_typed(void (*kern)(P), const P &p, cudaStream_t s) {
+  constexpr int smem = WarpLayout<D, NT, Keys>::SMEM;
+  static std::atomic<bool> attr[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr[dev].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr[dev].store(true);
+  }
+  return launch_close(kern, dim3(((unsigned)p.units + 3) / 4), kWinThreads, (size_t)smem, s, p);
+}
+
+// Launches kernel(D, 8-column steps of a unit's rows).
+template <class Keys, class P, class K>
+cudaError_t launch_warps(const P &p, int D, cudaStream_t s, K kernel) {
+  auto of = [&](auto d) {
+    constexpr int DD = decltype(d)::value;
+    auto step = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      return launch_warps_typed<DD, NT, Keys, P>(kernel(d, nt), p, s);
+    };
+    switch (((p.M + p.m_tiles - 1) / p.m_tiles + 7) / 8) {
+      case 1: return step(std::integral_constant<int, 1>());
+      case 2: return step(std::integral_constant<int, 2>());
+      case 3: return step(std::integral_constant<int, 3>());
+      default: return step(std::integral_constant<int, 4>());
+    }
+  };
+  return D == 128 ? of(std::integral_constant<int, 128>()) : of(std::integral_constant<int, 64>());
 }
 
 }  // namespace

@@ -68,10 +68,11 @@ def test_both_attentions_reject_before_launch(lib):
 
 
 def test_shared_attention_rejects_its_own(lib):
-    need = lib.sv_shared_attention_workspace_size(1, 1, 1, 4, 4, 128, 128, 1)
-    assert need > 0
+    need = lib.sv_shared_attention_workspace_size(1, 1, 1, 4, 4, 128, 1 << 20, 1)
+    assert need > 0 and lib.sv_shared_attention_workspace_size(1, 1, 1, 4, 4, 128, 128, 1) == 0
+    big = dict(cache=_cache(Lmax=1 << 20))
     for code, kw in ((BAD, dict(groups=0)), (BAD, dict(groups=-1)), (NO, dict(groups=129)), (BAD, dict(start=None)), (BAD, dict(length=None)),
-                     (SMALL, dict(ws=None)), (SMALL, dict(ws_bytes=need - 1)), (BAD, dict(ws=ctypes.c_void_p((2 << 40) + 8)))):
+                     (SMALL, dict(big, ws=None)), (SMALL, dict(big, ws_bytes=need - 1)), (BAD, dict(big, ws=ctypes.c_void_p((2 << 40) + 8)))):
         assert _shared(lib, **kw) == code, kw
     sizes = lib.sv_shared_attention_workspace_size
     assert sizes(1, 64, 5, 32, 8, 128, 4096, 128) > sizes(1, 64, 5, 32, 8, 128, 4096, 1) > 0

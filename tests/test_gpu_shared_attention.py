@@ -41,6 +41,26 @@ def shared_inputs(sizes, shared, own, N, Hq, Hkv, D, dtype=BF, page=16, seed=0, 
     return inp
 
 
+def roomy(inp, page):
+    """The same sequences in a cache with room for so many positions that bf16 calls go through the stacked kernel."""
+    B, N, Hq, D = inp["q"].shape
+    Hkv = inp["k_tree"].shape[2]
+    most = 2000 * torch.cuda.get_device_properties(0).multi_processor_count
+    cap = -(-most // (B * Hkv * ((N * Hq // Hkv + 63) // 64)))
+    out = dict(inp)
+    if page:
+        have = inp["block_table"].shape[1]
+        out["block_table"] = torch.cat([inp["block_table"], torch.full((B, max(0, -(-cap // page) - have)), -1, dtype=torch.int32)], 1)
+        cap = out["block_table"].shape[1] * page
+    else:
+        more = max(0, cap - inp["cache_k"].shape[1])
+        for t in ("cache_k", "cache_v"):
+            out[t] = torch.cat([inp[t], torch.full((B, more, Hkv, D), math.nan, dtype=inp[t].dtype)], 1)
+        cap = out["cache_k"].shape[1]
+    assert sv.sv_shared_attention_workspace_size(BF, B, N, Hq, Hkv, D, cap, inp["shared_len"].numel()) > 0
+    return out
+
+
 def call(inp, parent, page=16, **kw):
     g = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in inp.items()}
     cache = sv.KVCache(g["cache_k"], g["cache_v"], g["prefix_len"], g["block_table"], page or 16)
@@ -50,18 +70,22 @@ def call(inp, parent, page=16, **kw):
 
 
 def check(inp, parent, page=16, status=0):
-    out = call(inp, parent, page)
-    torch.cuda.synchronize()
-    assert sv.sv_read_device_status() == status
+    """The call, and in bf16 the same through the stacked kernel, whose result is returned."""
+    outs = []
+    for x in ([inp, roomy(inp, page)] if inp["q"].dtype == BF else [inp]):
+        outs.append(call(x, parent, page))
+        torch.cuda.synchronize()
+        assert sv.sv_read_device_status() == status
     D = inp["q"].shape[-1]
     ref, spread = plain_ops.window_attention(inp["q"], inp["k_tree"], inp["v_tree"], inp["cache_k"], inp["cache_v"],
                                              inp["prefix_len"], parent, D ** -0.5, 2 ** 31, 0, inp["block_table"], page or 16)
     size = D ** -0.5 * inp["q"].float().norm(dim=-1).max().item() * max(
         inp["k_tree"].float().norm(dim=-1).max().item(), inp["cache_k"].float().norm(dim=-1).max().item())
     bound = plain_ops.attention_bound(ref, spread, inp["q"].dtype, D, size, int(inp["prefix_len"].max()) + 64)
-    err = (out.double().cpu() - ref).abs()
-    worst = (err - bound).max().item()
-    assert bool(torch.isfinite(out).all()) and worst <= 0, (worst, err.max().item())
+    for out in outs:
+        err = (out.double().cpu() - ref).abs()
+        worst = (err - bound).max().item()
+        assert bool(torch.isfinite(out).all()) and worst <= 0, (worst, err.max().item())
     return out
 
 
@@ -145,8 +169,9 @@ def test_what_no_row_sees_may_hold_anything(cuda_ok):
                         inp["cache_k"][blk, p % 16], inp["cache_v"][blk, p % 16] = math.nan, math.inf
             else:
                 inp["cache_k"][b, L:], inp["cache_v"][b, L:] = math.inf, math.nan
-        out = call(inp, wl.chain_parent(4), page)
+        out = call(roomy(inp, page), wl.chain_parent(4), page)
         assert torch.equal(out, clean) and sv.sv_read_device_status() == 0
+        assert bool(call(inp, wl.chain_parent(4), page).isfinite().all()) and sv.sv_read_device_status() == 0
 
 
 def test_bad_groups_share_nothing(cuda_ok):
@@ -161,21 +186,23 @@ def test_shared_lengths_outside_the_cache(cuda_ok):
     inp["shared_len"] = torch.tensor([200, -5], dtype=torch.int32)  # (as 0)
     check(inp, wl.chain_parent(4), status=sv.SV_DEV_BAD_PREFIX)
     # beyond a member's prefix: that sequence alone is off
-    inp["shared_len"] = torch.tensor([200, 112], dtype=torch.int32)
-    inp["prefix_len"][3] = 100
-    out = call(inp, wl.chain_parent(4))
-    assert sv.sv_read_device_status() == sv.SV_DEV_BAD_PREFIX
-    inp["shared_len"] = torch.tensor([200, 0], dtype=torch.int32)
-    want = call(inp, wl.chain_parent(4))
-    assert sv.sv_read_device_status() == 0
-    assert torch.equal(out[:3], want[:3])
+    for room in (False, True):
+        inp["shared_len"] = torch.tensor([200, 112], dtype=torch.int32)
+        inp["prefix_len"][3] = 100
+        out = call(roomy(inp, 16) if room else inp, wl.chain_parent(4))
+        assert sv.sv_read_device_status() == sv.SV_DEV_BAD_PREFIX
+        inp["shared_len"] = torch.tensor([200, 0], dtype=torch.int32)
+        want = call(roomy(inp, 16) if room else inp, wl.chain_parent(4))
+        assert sv.sv_read_device_status() == 0
+        assert torch.equal(out[:3], want[:3])
 
 
-def test_bad_pages_of_the_shared_part_are_left_out(cuda_ok):
+@pytest.mark.parametrize("room", [True, False])
+def test_bad_pages_of_the_shared_part_are_left_out(cuda_ok, room):
     """Reported; the keys of the page are no keys of the group's sequences."""
     inp = shared_inputs([3], [192], [0, 5, 33], 5, 8, 2, 128, seed=15)
     inp["block_table"][:, 4] = inp["num_blocks"] + 7
-    out = call(inp, wl.chain_parent(4))
+    out = call(roomy(inp, 16) if room else inp, wl.chain_parent(4))
     assert sv.sv_read_device_status() == sv.SV_DEV_BAD_BLOCK
     keep = [j for j in range(inp["block_table"].shape[1]) if j != 4]
     inp["block_table"] = inp["block_table"][:, keep].contiguous()

@@ -61,12 +61,14 @@ def test_sparse_steps(cuda_ok, dtype, paged, per_node, parent, Hq, Hkv):
     assert int((cache.prefix_len.cpu() - inp["prefix_len"]).max()) >= 4
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dtype,room", [(BF, False), (BF, True), (F32, False)])
 @pytest.mark.parametrize("parent", [wl.chain_parent(4), wl.TREE_T26])
-def test_shared_steps(cuda_ok, dtype, parent):
-    """Two groups behind prompts of their own, step after step, as a captured graph too."""
+def test_shared_steps(cuda_ok, dtype, room, parent):
+    """Two groups behind prompts of their own, step after step."""
     N, Hq, Hkv, D = len(parent), 8, 2, 64
     inp = shared.shared_inputs([3, 2], [130, 64], [0, 9, 33, 70, 1], N, Hq, Hkv, D, dtype=dtype, seed=10, extra=N * 3)
+    if room:
+        inp = shared.roomy(inp, 16)
     cache = sv.KVCache(inp["cache_k"].cuda(), inp["cache_v"].cuda(), inp["prefix_len"].cuda(), inp["block_table"].cuda(), 16)
     group = (inp["group_start"].cuda(), inp["shared_len"].cuda())
     step = VerifyStep(parent, 5, Hq, Hkv, D, V, cache, dtype=dtype, mode=sv.GREEDY, shared=group)
@@ -81,10 +83,11 @@ def test_shared_steps(cuda_ok, dtype, parent):
         assert torch.equal(cache.prefix_len.cpu(), before + outs["num_accepted"].cpu() + 1)
         now = {"q": q, "k_tree": k, "v_tree": v, "cache_k": cache.k.cpu(), "cache_v": cache.v.cpu(), "prefix_len": before,
                "block_table": inp["block_table"], "group_start": inp["group_start"], "shared_len": inp["shared_len"]}
-        assert torch.equal(shared.check(now, parent), out)
+        shared.check(now, parent)
+        assert torch.equal(shared.call(now, parent), out)
 
 
-@pytest.mark.parametrize("kind", ["shared", "sparse"])
+@pytest.mark.parametrize("kind", ["shared", "stacked", "sparse"])
 def test_captured_steps_follow_the_lengths(cuda_ok, kind):
     """A step captured once and replayed: prefix lengths, bounds and pages move on by themselves."""
     parent, Hq, Hkv, D = wl.chain_parent(4), 8, 2, 64
@@ -92,8 +95,10 @@ def test_captured_steps_follow_the_lengths(cuda_ok, kind):
 
     def make():
         inp = shared.shared_inputs([3, 2], [130, 64], [0, 9, 33, 70, 1], N, Hq, Hkv, D, seed=10, extra=N * 4)
+        if kind == "stacked":
+            inp = shared.roomy(inp, 16)
         cache = sv.KVCache(inp["cache_k"].cuda(), inp["cache_v"].cuda(), inp["prefix_len"].cuda(), inp["block_table"].cuda(), 16)
-        kw = dict(shared=(inp["group_start"].cuda(), inp["shared_len"].cuda())) if kind == "shared" else dict(sparse=SparsePages(5))
+        kw = dict(shared=(inp["group_start"].cuda(), inp["shared_len"].cuda())) if kind != "sparse" else dict(sparse=SparsePages(5))
         step = VerifyStep(parent, 5, Hq, Hkv, D, V, cache, mode=sv.GREEDY, **kw)
         if kind == "sparse":
             step.reset_bounds()
