@@ -46,7 +46,7 @@ def roomy(inp, page):
     B, N, Hq, D = inp["q"].shape
     Hkv = inp["k_tree"].shape[2]
     most = 2000 * torch.cuda.get_device_properties(0).multi_processor_count
-    cap = -(-most // (B * Hkv * ((N * Hq // Hkv + 63) // 64)))
+    cap = max(256, -(-most // (B * Hkv * ((N * Hq // Hkv + 63) // 64))))
     out = dict(inp)
     if page:
         have = inp["block_table"].shape[1]
