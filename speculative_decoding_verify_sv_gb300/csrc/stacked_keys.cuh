@@ -5,11 +5,12 @@
 // head, and its keys are the tree's nodes and the pages of its list, in groups of 16 that none of them
 // crosses.  Pages that many rows see together go through the stacked kernel instead, see sparse_plan.
 //
-// Pieces: the kernel takes the tree's nodes and a sequence's own keys (those behind what it shares; none
-// with listed pages), and joins the stacked kernel's pieces of the same rows in its merge, as one more part
-// beside those of its own warps.  A row's first piece is copied to shared memory while the keys are worked
-// on, the others (units that were cut) follow through the ring's room.  (Read straight from memory in the
-// merge, element by element, they took 10 us per CTA.)
+// Pieces: the kernel takes the tree's nodes and a sequence's own keys (those behind what it shares; none with
+// listed pages), and its rows begin with the stacked kernel's pieces instead of nothing, the slices of a CTA
+// with every fourth (or second) each.  They are read straight to the registers that the products add to, while
+// the first keys are on their way.  (One more part of the merge at the end, through shared memory: one token of
+// 8 requests behind 8192 keys, 19 pieces a row, 25.8 us instead of 22.7; read element by element there, 10 us
+// more per CTA.)
 #pragma once
 
 #include "unit_attention.cuh"

@@ -9,8 +9,8 @@ namespace {
 // waves.  Measured on 152 SMs, units of 4 rows (one node, 32:8 heads), us a warp / a CTA per unit:
 //   listed pages   304 units of 128 keys 8.2 / 7.0, of 4096 keys 150 / 94;  608 units 9.7 / 13.7, 192 / 182;
 //                  1216 units 15.5 / 24, 348 / 354
-//   own keys       304 units of 16 keys 19.0 / 15.8, of 512 keys 37 / 26;  608 units 20 / 23, 43 / 42.5;
-//                  1216 units 21 / 36, 64 / 74 (with the shared part, 512 keys, before them)
+//   own keys       304 units of 16 keys 15.7 / 15.5, of 512 keys 34 / 24;  608 units 16.8 / 22.5, 40 / 42;
+//                  1216 units 18.2 / 35, 60 / 73 (with the shared part, 512 keys, before them)
 // Tiles are of up to 32 rows.
 template <class P>
 bool warp_units_pay(P &p, long long kv_units, int num_sms) {
@@ -113,17 +113,17 @@ StackPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int max_prefix, int 
 // Many rows with one list are worth the stacked kernel, which reads a list's K and V once per 256 rows instead
 // of once per 64 or 32 but leaves pieces to a second kernel, where there is much to read.  Measured, us stacked /
 // in units, pages of 16, 8 KV heads:
-//   104 rows (26 nodes, 4 heads)   16 requests with lists of 256 keys 25 / 16, 1024 keys 37 / 36, 4096 keys 77 / 118;
-//                                  64 requests 55 / 49, 94 / 144, 232 / 521;  one request, 4096 keys, 22 / 17
-//   512 rows                       one request, 1024 keys, 23 / 17, 4096 keys 29 / 39;  16 requests of 256 keys 61 / 55
-//   64 rows                        64 requests of 256 keys 38 / 23, of 4096 keys 212 / 261;  16 of 4096 keys 69 / 64
-//   up to 48 rows                  64 requests of 4096 keys 207 / 191 (40 and 48 rows), 206 / 155 (20 rows)
+//   104 rows (26 nodes, 4 heads)   16 requests with lists of 256 keys 24 / 16, 1024 keys 37 / 36, 4096 keys 76 / 118;
+//                                  64 requests 46 / 49, 85 / 144, 223 / 521;  one request, 4096 keys, 21 / 17
+//   512 rows                       one request, 1024 keys, 23 / 17, 4096 keys 29 / 39;  16 requests of 256 keys 49 / 55
+//   64 rows                        64 requests of 256 keys 32 / 23, of 2048 keys 118 / 134;  16 of 4096 keys 70 / 64
+//   up to 48 rows                  64 requests of 4096 keys 205 / 191 (48 rows), 208 / 155 (20 rows)
 StackPlan sparse_plan(int B, int N, int Hq, int Hkv, int D, int page_size, int list_len, int sets, int num_sms) {
   StackPlan pl{};
   const int G = Hq / Hkv;
   pl.grid = num_sms > 0 ? num_sms : 152;
   const double reads = (double)B * Hkv * ((N * G + 63) / 64) * list_len * page_size;  // keys that units read
-  if (sets != 1 || N * G <= 48 || reads < 2600. * pl.grid) return pl;
+  if (sets != 1 || N * G <= 48 || reads < (N * G > 64 ? 1800. : 4000.) * pl.grid) return pl;
   pl.stacked = true;
   pl.tile_tokens = 128 / G;
   pl.row_tiles = (N + 2 * pl.tile_tokens - 1) / (2 * pl.tile_tokens);

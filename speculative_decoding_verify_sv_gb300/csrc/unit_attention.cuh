@@ -65,8 +65,8 @@ struct WinLayout {
   static constexpr int KB = D / 64;             // 64-column blocks of a row
   static constexpr int K_BYTES = kWinGroup * D * 2;
   static constexpr int G_BYTES = 2 * K_BYTES;   // a group's K and V
-  // the slices' rings: what two CTAs per SM leave room for beside their query rows (and their pieces)
-  static constexpr int RING = (Keys::kPieces ? (RG == 2 ? 48 : 64) : (RG == 2 ? 80 : 96)) * 1024;
+  // the slices' rings: what two CTAs per SM leave room for beside their query rows
+  static constexpr int RING = (RG == 2 ? 80 : 96) * 1024;
   static constexpr int ST = RING / (KS * G_BYTES);  // stages of a slice's ring
   static constexpr int RB = 8 * NT * RG;        // query rows of a CTA
   static constexpr int DO = D / 16 / KS;        // 16-dimension tiles of the outputs that a slice merges
@@ -87,14 +87,12 @@ struct WinLayout {
   static constexpr int OFF_PAR = OFF_ROW + RB * 4;      // [64]
   static constexpr int OFF_COPIED = OFF_PAR + kMaxNodes * 4;  // [KS][ST]
   static constexpr int OFF_ABORT = OFF_COPIED + KS * ST * 4;
-  // listed pages: positions of the groups in the ring [KS][ST]; pieces: where the rows' pieces are [RB],
-  // their maxima and sums [RB], the weights of the first two [2][RB] and of those in the ring's room
-  // [CAP][RB], and the outputs of the first ones (and second ones) [PB][RB][D + 4]
-  static constexpr int CAP = RING / (RB * D * 4), PB = RG == 1 ? 2 : 1;
+  // listed pages: positions of the groups in the ring [KS][ST]; pieces: where the rows' pieces are [RB], what the
+  // sequence shares
   static constexpr int OFF_MORE = (OFF_ABORT + 16 + 15) & ~15;
-  static constexpr int OFF_PIECE = OFF_MORE + RB * 24 + CAP * RB * 4 + 64;
-  static constexpr int SMEM = Keys::kListed ? OFF_MORE + KS * ST * 4 : Keys::kPieces ? OFF_PIECE + PB * RB * (D + 4) * 4 : OFF_ABORT + 16;
-  static_assert((Keys::kPieces ? OFF_JOIN : OFF_JOIN + JOIN) <= RING, "the merge goes on in the ring's room");
+  static constexpr int OFF_SHARED = OFF_MORE + RB * 8;
+  static constexpr int SMEM = Keys::kListed ? OFF_MORE + KS * ST * 4 : Keys::kPieces ? OFF_SHARED + 64 : OFF_ABORT + 16;
+  static_assert(OFF_JOIN + JOIN <= RING, "the merge goes on in the ring's room");
   static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -161,6 +159,60 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// Rows begin with their pieces k0, k0 + step, ..., straight from memory to where the products add to them: this
+// lane's part of rows 8 j + 2 (lane mod 4) + e.  count: the pieces of row `lane`.  (A row's sum is one of 8 lanes.)
+template <int D, int NT, class Keys>
+__device__ __forceinline__ void begin_with_pieces(const typename Keys::Params &p, const Pieces *rows, int count, int k0, int step,
+                                                  float (&o)[D / 16][NT][4], float (&m)[NT][2], float (&l)[NT][2]) {
+  constexpr int DT = D / 16;
+  const int lane = threadIdx.x & 31, fg = lane >> 2, ft = lane & 3;
+  const int most = __reduce_max_sync(0xFFFFFFFFu, count);
+  if (k0 < most) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const Pieces pc = rows[8 * j + 2 * ft + e];
+        const bool there = k0 < pc.count;
+        const float2 ml = there ? p.part_ml[pc.row + (size_t)k0 * kStackRows] : make_float2(kWinNone, 0.f);
+        const float *from = reinterpret_cast<const float *>(Keys::template piece<D>(p, pc.row, k0, fg >> 2)) + (fg & 3);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) o[d][j][e + 2 * h] = there ? from[(size_t)(4 * d + 2 * h) * (4 * kStackRows)] : 0.f;
+        m[j][e] = ml.x;
+        l[j][e] = fg == 0 ? ml.y : 0.f;
+      }
+  }
+#pragma unroll 1
+  for (int k = k0 + step; k < most; k += step) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float x[DT][4], w[2], c[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const Pieces pc = rows[8 * j + 2 * ft + e];
+        const bool there = k < pc.count;
+        const float2 ml = there ? p.part_ml[pc.row + (size_t)k * kStackRows] : make_float2(kWinNone, 0.f);
+        const float *from = reinterpret_cast<const float *>(Keys::template piece<D>(p, pc.row, k, fg >> 2)) + (fg & 3);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) x[d][e + 2 * h] = there ? from[(size_t)(4 * d + 2 * h) * (4 * kStackRows)] : 0.f;
+        const float top = fmaxf(m[j][e], ml.x);
+        w[e] = ex2_approx(m[j][e] - top);
+        c[e] = ex2_approx(ml.x - top);
+        m[j][e] = top;
+        l[j][e] = l[j][e] * w[e] + (fg == 0 ? c[e] * ml.y : 0.f);
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][j][i] = o[d][j][i] * w[i & 1] + c[i & 1] * x[d][i];
+    }
+  }
+}
+
 template <int D, int NT, int RG, class Keys>
 __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   using Lay = WinLayout<D, NT, RG, Keys>;
@@ -174,9 +226,6 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   int *s_row = reinterpret_cast<int *>(sm + Lay::OFF_ROW);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Lay::OFF_ABORT);
   Pieces *s_piece = reinterpret_cast<Pieces *>(sm + Lay::OFF_MORE);
-  float *s_top = reinterpret_cast<float *>(sm + Lay::OFF_MORE + RB * 8), *s_sum = s_top + RB, *s_w = s_sum + RB, *s_weight = s_w + 2 * RB;
-  float *s_out = reinterpret_cast<float *>(sm + Lay::OFF_PIECE);
-  int *s_most = const_cast<int *>(abort_flag) + 1;  // the most pieces of a row
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (the same in every lane, and known to be)
@@ -210,11 +259,10 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     s_row[tid] = R < p.M ? (b * p.N + node0 + node) * p.Hq + kvh * p.G + R - node * p.G : -1;
   }
   if (tid == 0) *abort_flag = 0;
-  if (Keys::kPieces && tid == 0) *s_most = 0;
   Keys::begin(p);
   int L = p.prefix_len[b];
   if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
-  SharedPart shared = Keys::shared_part(p, b, reports, reinterpret_cast<SharedPart *>(sm + Lay::OFF_PIECE - 64));  // (a barrier)
+  SharedPart shared = Keys::shared_part(p, b, reports, reinterpret_cast<SharedPart *>(sm + Lay::OFF_SHARED));  // (a barrier)
   // query rows as B operands, on their way before the first keys
   uint8_t *s_q = sm + Lay::OFF_Q;
 #pragma unroll
@@ -315,18 +363,7 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     }
   }
 
-  // a row's pieces, and the maxima and sums of the first two
-  Pieces pieces;
-  float2 ml0 = make_float2(kWinNone, 0.f), ml1 = ml0;
-  if constexpr (Keys::kPieces) {
-    Keys::wait_pieces(p, shared);
-    if (tid < RB && rank == 0 && mt * RB + tid < p.M) {
-      const int R = mt * RB + tid;
-      pieces = Keys::pieces_of(p, b, kvh, R / p.G, R % p.G, shared);
-      if (pieces.count > 0) ml0 = p.part_ml[pieces.row];
-      if (pieces.count > 1) ml1 = p.part_ml[pieces.row + kStackRows];
-    }
-  }
+  if constexpr (Keys::kPieces) Keys::wait_pieces(p, shared);
 
   // ---- what each row sees
   if (tid < RB) {
@@ -345,36 +382,13 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     s_anc[tid] = anc;
     s_lo[tid] = lo;
     if constexpr (Keys::kPieces) {
-      // the maximum and sum of the row's pieces
-      float top = fmaxf(ml0.x, ml1.x), sum = ml0.y * ex2_approx(ml0.x - top) + ml1.y * ex2_approx(ml1.x - top);
-#pragma unroll 8
-      for (int k = 2; k < pieces.count; ++k) {
-        const float2 ml = p.part_ml[pieces.row + (size_t)k * kStackRows];
-        const float up = fmaxf(top, ml.x);
-        sum = sum * ex2_approx(top - up) + ml.y * ex2_approx(ml.x - up);
-        top = up;
-      }
+      Pieces pieces;
+      if (R < p.M) pieces = Keys::pieces_of(p, b, kvh, R / p.G, R % p.G, shared);
       s_piece[tid] = pieces;
-      s_top[tid] = top;
-      s_sum[tid] = sum;
-      s_w[tid] = pieces.count > 0 ? ex2_approx(ml0.x - top) : 0.f;
-      s_w[RB + tid] = pieces.count > 1 ? ex2_approx(ml1.x - top) : 0.f;
-      atomicMax(s_most, pieces.count);
     }
   }
   cp_async_wait<0>();
   __syncthreads();
-  if constexpr (Keys::kPieces) {
-    // the rows' first pieces, on their way while the keys are worked on
-    for (int k = 0; k < Lay::PB; ++k) {
-      if (k > 0 && *s_most <= k) break;
-      for (int i = tid; i < RB * (D / 4); i += kWinThreads) {
-        const int r = i % RB, u = i / RB;
-        cp_async_16(s_out + (k * RB + r) * (D + 4) + 4 * u, Keys::template piece<D>(p, s_piece[r].row, k, u), k < s_piece[r].count);
-      }
-    }
-    cp_async_commit();
-  }
   // Every row sees every key of the groups [plain0, plain1) of this slice: inside the window of all
   // rows (none starts later than the deepest possible node's), before the prefix's end.
   const int lo_last = Keys::kWindow ? window_first(L + p.N - 1, p.window) : lo_root;
@@ -389,6 +403,11 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   float m[NT][2], l[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = kWinNone, l[j][0] = l[j][1] = 0.f;
+  // (the rows begin with their pieces, those of a row in turn with the slices)
+  if constexpr (Keys::kPieces) {
+    const Pieces *rows = s_piece + rg * 8 * NT;
+    begin_with_pieces<D, NT, Keys>(p, rows, lane < 8 * NT ? rows[lane].count : 0, slice, KS, o, m, l);
+  }
 
   const float sc = p.scale_log2;
   // this lane's row of a group for the two kinds of fragment loads, and its 16-byte chunks
@@ -636,55 +655,6 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   float4 *part = reinterpret_cast<float4 *>(sm);      // [KS taker][KS - 1][RG][DO][NT][32]
   float4 *joined = reinterpret_cast<float4 *>(sm + Lay::OFF_JOIN);  // [C][units of this CTA][32]
   float *c_m = reinterpret_cast<float *>(joined + (U + 8) * 32), *c_l = c_m + 8 * RB;  // [C][RB]
-  if constexpr (Keys::kPieces) {
-    // One sum of the rows' pieces by their weights against the rows' maxima, in the place of the first
-    // ones; those past the first PB come through the ring's room.
-    cp_async_wait<0>();
-    __syncthreads();  // (every slice is done with its ring)
-    constexpr int CAP = Lay::CAP, PB = Lay::PB, TPR = RB > 32 ? 2 : RB > 16 ? 4 : RB > 8 ? 8 : 16;  // threads of a row
-    const int most = *s_most, r = tid / TPR, r0 = r < RB ? r : RB - 1;
-    auto row_of = [&](int u) { return reinterpret_cast<float4 *>(s_out + r0 * (D + 4) + 4 * u); };
-    if (r < RB) {
-      const float w0 = s_w[r], w1 = s_w[RB + r];
-      for (int u = tid % TPR; u < D / 4; u += TPR) {
-        float4 x = *row_of(u);
-        x = make_float4(x.x * w0, x.y * w0, x.z * w0, x.w * w0);
-        if (PB > 1 && most > 1) {
-          const float4 y = *reinterpret_cast<const float4 *>(s_out + (RB + r) * (D + 4) + 4 * u);
-          x = make_float4(fmaf(w1, y.x, x.x), fmaf(w1, y.y, x.y), fmaf(w1, y.z, x.z), fmaf(w1, y.w, x.w));
-        }
-        *row_of(u) = x;
-      }
-    }
-    for (int k0 = PB; k0 < most; k0 += CAP) {
-      const int n_k = min(CAP, most - k0);
-      for (int i = tid; i < n_k * RB * (D / 4); i += kWinThreads) {
-        const int q = i % RB, u = i / RB % (D / 4), k = i / (RB * (D / 4));
-        cp_async_16(sm + (k * RB + q) * (D * 4) + ((u ^ (q & 7)) << 4), Keys::template piece<D>(p, s_piece[q].row, k0 + k, u),
-                    k0 + k < s_piece[q].count);
-      }
-      cp_async_commit();
-      for (int i = tid; i < n_k * RB; i += kWinThreads) {
-        const int q = i % RB, k = k0 + i / RB;
-        const Pieces pc = s_piece[q];
-        s_weight[i] = k < pc.count ? ex2_approx(p.part_ml[pc.row + (size_t)k * kStackRows].x - s_top[q]) : 0.f;
-      }
-      cp_async_wait<0>();
-      __syncthreads();
-      if (r < RB) {
-        for (int u = tid % TPR; u < D / 4; u += TPR) {
-          float4 x = *row_of(u);
-          for (int k = 0; k < n_k; ++k) {
-            const float a = s_weight[k * RB + r];
-            const float4 y = *reinterpret_cast<const float4 *>(sm + (k * RB + r) * (D * 4) + ((u ^ (r & 7)) << 4));
-            x = make_float4(fmaf(a, y.x, x.x), fmaf(a, y.y, x.y), fmaf(a, y.z, x.z), fmaf(a, y.w, x.w));
-          }
-          *row_of(u) = x;
-        }
-      }
-      __syncthreads();
-    }
-  }
   // Done with the ring.  (Room of its own for what the others write and an arrival at the start gain
   // nothing.)
   if (C > 1) cluster_arrive();
@@ -703,17 +673,15 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
     }
   __syncthreads();  // (and every slice is done with its ring)
   float w[NT][2];   // this slice's weights against the CTA's maximum
-  float wp[Keys::kPieces ? NT : 1][2];  // the pieces' weight
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = rg * 8 * NT + 8 * j + 2 * ft + e;
-      float top = Keys::kPieces ? s_top[r] : kWinNone;
+      float top = kWinNone;
 #pragma unroll
       for (int k = 0; k < KS; ++k) top = fmaxf(top, s_m[k * RB + r]);
       w[j][e] = ex2_approx(m[j][e] - top);
-      if constexpr (Keys::kPieces) wp[j][e] = ex2_approx(s_top[r] - top);
     }
   auto scaled = [&](int d, int j) {
     return make_float4(o[d][j][0] * w[j][0], o[d][j][1] * w[j][1], o[d][j][2] * w[j][0], o[d][j][3] * w[j][1]);
@@ -731,12 +699,10 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   }
   float top = kWinNone, sum = 0.f;
   if (tid < RB) {
-    if constexpr (Keys::kPieces) top = s_top[tid];
 #pragma unroll
     for (int k = 0; k < KS; ++k) top = fmaxf(top, s_m[k * RB + tid]);
 #pragma unroll
     for (int k = 0; k < KS; ++k) sum += ex2_approx(s_m[k * RB + tid] - top) * s_l[k * RB + tid];
-    if constexpr (Keys::kPieces) sum += ex2_approx(s_top[tid] - top) * s_sum[tid];
     if (C == 1) s_inv[tid] = sum > 0.f ? 1.f / sum : 0.f;
   }
   __syncthreads();
@@ -787,13 +753,6 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
         v.y += x[j][k].y;
         v.z += x[j][k].z;
         v.w += x[j][k].w;
-      }
-      if constexpr (Keys::kPieces) {
-        const float *x0 = s_out + (rg * 8 * NT + 8 * j + 2 * ft) * (D + 4) + 16 * d + fg, *x1 = x0 + D + 4;
-        v.x = fmaf(wp[j][0], x0[0], v.x);
-        v.y = fmaf(wp[j][1], x1[0], v.y);
-        v.z = fmaf(wp[j][0], x0[8], v.z);
-        v.w = fmaf(wp[j][1], x1[8], v.w);
       }
       if (C == 1) {
         emit(d, rows[j], make_float4(v.x * inv[j][0], v.y * inv[j][1], v.z * inv[j][0], v.w * inv[j][1]));

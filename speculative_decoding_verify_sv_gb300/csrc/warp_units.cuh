@@ -151,7 +151,7 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
   if constexpr (Keys::kPieces) Keys::wait_pieces(p, shared);
 
   // ---- what each row sees of the tree; its pieces
-  int most = 0;
+  int count = 0;
   if (lane < RB) {
     uint64_t anc = 0;
     if (my_row >= 0) {
@@ -163,7 +163,7 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
       Pieces pieces;
       if (real && my_row >= 0) pieces = Keys::pieces_of(p, b, kvh, node, g, shared);
       s_piece[lane] = pieces;
-      most = pieces.count;
+      count = pieces.count;
     }
   }
   __syncwarp();
@@ -177,52 +177,9 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
 #pragma unroll
   for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = kWinNone, l[j][0] = l[j][1] = 0.f;
   if constexpr (Keys::kPieces) {
-    // The rows begin with their pieces, straight from memory to where the products add to them, while the first keys
-    // are on their way (through shared memory at the end: Medusa trees
-    // behind one prompt 143 us instead of 135, 26-node trees over 256 pages 88.5 instead of 81).
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const Pieces pc = s_piece[8 * j + 2 * ft + e];
-        const bool there = pc.count > 0;
-        const float2 ml = there ? p.part_ml[pc.row] : make_float2(kWinNone, 0.f);
-        const float *from = reinterpret_cast<const float *>(Keys::template piece<D>(p, pc.row, 0, fg >> 2)) + (fg & 3);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) o[d][j][e + 2 * h] = there ? from[(size_t)(4 * d + 2 * h) * (4 * kStackRows)] : 0.f;
-        m[j][e] = ml.x;
-        l[j][e] = fg == 0 ? ml.y : 0.f;  // (a sum of the 8 lanes with this row)
-      }
-#pragma unroll 1
-    for (int k = 1; k < most; ++k) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float x[DT][4], w[2], c[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const Pieces pc = s_piece[8 * j + 2 * ft + e];
-          const bool there = k < pc.count;
-          const float2 ml = there ? p.part_ml[pc.row + (size_t)k * kStackRows] : make_float2(kWinNone, 0.f);
-          const float *from = reinterpret_cast<const float *>(Keys::template piece<D>(p, pc.row, k, fg >> 2)) + (fg & 3);
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) x[d][e + 2 * h] = there ? from[(size_t)(4 * d + 2 * h) * (4 * kStackRows)] : 0.f;
-          const float top = fmaxf(m[j][e], ml.x);
-          w[e] = ex2_approx(m[j][e] - top);
-          c[e] = ex2_approx(ml.x - top);
-          m[j][e] = top;
-          l[j][e] = l[j][e] * w[e] + (fg == 0 ? c[e] * ml.y : 0.f);
-        }
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[d][j][i] = o[d][j][i] * w[i & 1] + c[i & 1] * x[d][i];
-      }
-    }
+    // (pieces through shared memory at the end: Medusa trees behind one prompt 143 us instead of 135, 26-node
+    // trees over 256 pages 88.5 instead of 81)
+    begin_with_pieces<D, NT, Keys>(p, s_piece, count, 0, 1, o, m, l);
   }
   cp_async_wait<0>();
   __syncwarp();
