@@ -220,7 +220,7 @@ size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
  * captured call follows them.  1 <= groups <= SV_MAX_SHARED_GROUPS.
  * Device status: SV_DEV_BAD_GROUP for a group_start that does not ascend within [0, B] (nothing is
  * shared then), SV_DEV_BAD_PREFIX for a shared_len outside the cache (clamped) or beyond a member's
- * prefix_len (the outputs of that sequence are not meaningful).
+ * prefix_len (the outputs of that group are not meaningful).
  * Every other argument, the layouts, the kernels' shapes and the refusals are sv_window_attention's
  * (without window and sinks); Hq / Hkv <= 128, else SV_ERR_UNSUPPORTED.  Rounding as there.  float32
  * calls, and those with little to read in all, read each sequence's own rows.

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
   }
   const int start = p.start ? max(p.start[b], 0) : 0;
   if (start >= L) return;
-  const int first = start / p.page_size, pages = (L + p.page_size - 1) / p.page_size - first;
+  const int first = start / p.page_size, pages = (int)(((long long)L + p.page_size - 1) / p.page_size) - first;
   const long long items = (long long)pages * p.vecs, stride = (long long)gridDim.x * kBoundThreads;
   // an item: a page and a piece of its rows
   struct Item {

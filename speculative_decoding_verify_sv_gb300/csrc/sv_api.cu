@@ -609,6 +609,7 @@ sv_status sv_page_scores(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, cons
   if (block_table && num_blocks < 1) return fail(SV_ERR_INVALID_ARG, "num_blocks = %d", num_blocks);
   if ((long long)B * N * Hq > kMaxRows || (long long)B * Hkv * ((long long)P / 8 + 2) > kMaxRows || (long long)Hkv * D > kMaxRows / 8)
     return fail(SV_ERR_UNSUPPORTED, "B = %d, N = %d, Hq = %d, P = %d: too many rows", B, N, Hq, P);
+  if (!block_table && (long long)B * P > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "B = %d, P = %d: too many pages", B, P);
   if (B == 0) return SV_OK;
   if (!q || !bounds || !prefix_len || !out) return fail(SV_ERR_INVALID_ARG, "q, bounds, prefix_len or out is NULL");
   if (!aligned16(q) || !aligned16(bounds) || !aligned16(out)) return fail(SV_ERR_INVALID_ARG, "q, bounds and out must be 16-byte aligned");

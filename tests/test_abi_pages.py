@@ -115,7 +115,7 @@ def test_page_scores_reject_before_launch(lib):
         return lib.sv_page_scores(dt, B, N, Hq, Hkv, D, q, bounds, length, page, pages, table, blocks, sets, out, None)
     for code, kw in ((NO, dict(dt=2)), (BAD, dict(B=-1)), (BAD, dict(Hq=6)), (BAD, dict(Hkv=0)), (NO, dict(D=80)), (NO, dict(Hq=129, Hkv=1)),
                      (BAD, dict(N=0)), (NO, dict(N=65)), (BAD, dict(page=0)), (BAD, dict(pages=0)), (BAD, dict(sets=2)),
-                     (BAD, dict(table=P, blocks=0)), (NO, dict(B=2 ** 26, N=8)), (NO, dict(pages=2 ** 31 - 1, B=64)), (BAD, dict(q=None)),
+                     (BAD, dict(table=P, blocks=0)), (NO, dict(B=2 ** 26, N=8)), (NO, dict(pages=2 ** 31 - 1, B=64)), (NO, dict(pages=2 ** 20, B=2 ** 13, Hq=1, Hkv=1)), (BAD, dict(q=None)),
                      (BAD, dict(bounds=None)), (BAD, dict(length=None)), (BAD, dict(out=None)), (BAD, dict(q=ctypes.c_void_p(20))),
                      (BAD, dict(out=ctypes.c_void_p((1 << 40) + 4))), (BAD, dict(out=P)), (BAD, dict(out=FAR2)), (BAD, dict(out=FAR3)),
                      (BAD, dict(bounds=ctypes.c_void_p((1 << 40) + 128))), (BAD, dict(table=FAR, blocks=4))):

@@ -41,6 +41,19 @@ def test_bounds(cuda_ok, dtype, page, paged, Hkv, D):
         assert torch.equal(new[-1, 0].cpu(), want[-1, 0])
 
 
+def test_pages_larger_than_the_cache(cuda_ok):
+    """One page holds all of a sequence, up to the largest size that there is."""
+    inp = wl.attention_inputs(3, 1, 2, 2, 64, [40, 0, 33], paged=False, extra=8, seed=5)
+    cache = sv.KVCache(inp["cache_k"].cuda(), inp["cache_v"].cuda(), inp["prefix_len"].cuda(), None, 2 ** 31 - 1)
+    bounds = sv.sv_page_bounds(cache, torch.zeros(3, 1, 2, 2, 64, dtype=BF, device="cuda"))
+    want = plain_pages.page_bounds(torch.zeros(3, 1, 2, 2, 64, dtype=BF), inp["cache_k"], inp["prefix_len"], None, None, 2 ** 31 - 1)
+    assert torch.equal(bounds.cpu(), want)
+    _scores(inp["q"], want, inp["prefix_len"], 2 ** 31 - 1, None, False)
+    out = sv.sv_select_pages(torch.zeros(3, 1, 2, 1, device="cuda"), cache.prefix_len, 2 ** 31 - 1, 2)
+    assert out.cpu().tolist() == [[[[0, -1]] * 2], [[[-1, -1]] * 2], [[[0, -1]] * 2]]
+    assert sv.sv_read_device_status() == 0
+
+
 def test_bounds_keep_what_is_no_number(cuda_ok):
     for dtype in (BF, F32):
         k = torch.randn(1, 48, 2, 64).to(dtype)
