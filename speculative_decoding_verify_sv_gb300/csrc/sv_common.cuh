@@ -37,6 +37,16 @@ __device__ __forceinline__ uint4 load_streamed(const uint4 *p) {
   return v;
 }
 
+// The entries of a list of pages up to the last that is one (the same in every lane): lists of short
+// prefixes are mostly empty at the end.
+__device__ __forceinline__ int listed_length(const int32_t *list, int n) {
+  int used = 0;
+#pragma unroll 8
+  for (int i = threadIdx.x & 31; i < n; i += 32)
+    if (list[i] >= 0) used = i + 1;
+  return __reduce_max_sync(0xFFFFFFFFu, used);
+}
+
 inline cudaLaunchAttribute close_launch() {
   cudaLaunchAttribute a;
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -260,7 +260,8 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   }
   if (tid == 0) *abort_flag = 0;
   Keys::begin(p);
-  int L = p.prefix_len[b];
+  int L = p.prefix_len[b], entries = 0;
+  if constexpr (Keys::kListed) entries = listed_length(p.pages + ((size_t)bs * p.Hkv + kvh) * p.list_len, p.list_len);
   if (tid < kMaxNodes) s_par[tid] = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
   SharedPart shared = Keys::shared_part(p, b, reports, reinterpret_cast<SharedPart *>(sm + Lay::OFF_SHARED));  // (a barrier)
   // query rows as B operands, on their way before the first keys
@@ -285,7 +286,7 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   const int gt = (p.N + kWinGroup - 1) / kWinGroup, gs = gt + (n_sinks + kWinGroup - 1) / kWinGroup;
   int groups = gs + (L - first + kWinGroup - 1) / kWinGroup;
   if constexpr (Keys::kPieces) groups = lo_root < L ? groups : gs;
-  if constexpr (Keys::kListed) groups = gs + p.list_len * p.page_groups;
+  if constexpr (Keys::kListed) groups = gs + entries * p.page_groups;
   const int per = (groups + (int)C - 1) / (int)C;
   const int g0 = min((int)rank * per, groups), g1 = min(g0 + per, groups);
   const int n = g1 - g0 > slice ? (g1 - g0 - slice + KS - 1) / KS : 0;  // this slice's groups

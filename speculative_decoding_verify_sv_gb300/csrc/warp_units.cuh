@@ -65,7 +65,8 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
   const int R = mt * RB + lane, node = R / p.G, g = R - node * p.G;
   const int my_row = lane < RB && R < p.M ? (b * p.N + node0 + node) * p.Hq + kvh * p.G + g : -1;
   Keys::begin(p);
-  int L = p.prefix_len[b];
+  int L = p.prefix_len[b], entries = 0;
+  if constexpr (Keys::kListed) entries = listed_length(p.pages + ((size_t)bs * p.Hkv + kvh) * p.list_len, p.list_len);
   for (int i = lane; i < kMaxNodes; i += 32) s_par[i] = i < p.N ? tree_parent(p.tree, b, i) : -1;
   // query rows as B operands
 #pragma unroll
@@ -86,7 +87,7 @@ __device__ __forceinline__ void warp_units(const typename Keys::Params &p) {
   const int own = Keys::kPieces ? min(shared.len, L) : 0, first = own & ~(kWinGroup - 1);
   const int gt = (p.N + kWinGroup - 1) / kWinGroup;
   int n = gt;
-  if constexpr (Keys::kListed) n += p.list_len * p.page_groups;
+  if constexpr (Keys::kListed) n += entries * p.page_groups;
   else n += own < L ? (L - first + kWinGroup - 1) / kWinGroup : 0;
   if (!real || !layout_ok) n = 0;
   const uint64_t stream_policy = l2_policy_evict_first(), tree_policy = l2_policy_evict_normal();

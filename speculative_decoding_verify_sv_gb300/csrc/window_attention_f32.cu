@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   const int first = LISTED ? 0 : window_first(L, p.window), n_sinks = LISTED ? 0 : min(p.sinks, first);
   // chunks: tree nodes, sinks before the window, window
   const int ct = (p.N + kF32Keys - 1) / kF32Keys, cs = ct + (n_sinks + kF32Keys - 1) / kF32Keys;
-  const int listed = LISTED ? p.list_len * p.page_size : 0;  // keys of the list
+  int listed = 0;  // keys of the list
+  if constexpr (LISTED) listed = listed_length(p.pages + ((size_t)bs * p.Hkv + kvh) * p.list_len, p.list_len) * p.page_size;
   const int chunks = cs + ((LISTED ? listed : L - first) + kF32Keys - 1) / kF32Keys;
   float *sk = sm + warp * Lay::CHUNK, *sv = sk + kF32Keys * KS, *sp = sm + Lay::OFF_P + warp * kF32Keys * R;
   const float *gkt = static_cast<const float *>(p.k_tree), *gvt = static_cast<const float *>(p.v_tree);
