@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cmath>
 
 #include "sv_common.cuh"
 #include "sv_internal.h"
@@ -413,6 +414,19 @@ int set_columns(int rows) {
 }
 
 }  // namespace
+
+// A tile of 128 pages costs the same however few of them there are.  As fitted to measurements (us, heads of 64 and
+// 128, 1 to 128 pages of 1 to 256 sequences): this kernel 4.6 and 2.6 per tile of an SM, the other one 0.65 for a
+// thousand steps of eight rows and a page, and 1.2 for each of a set's.  E.g. one token, 32:8 heads, 64 sequences:
+// 4 pages 13.2 here against 3.5, 16 pages 13.2 against 7.6, 64 pages 13.2 against 25; a set for each of 26 nodes
+// of 8 heads: 8 sequences of 4 pages 9.8 against 6.0, of 16 9.8 against 17.5.
+bool page_scores_prefer_tc(const ScoreParams &p, int num_sms) {
+  const double cols = (double)p.sets * set_columns(p.set_nodes * p.G);
+  const double tiles = std::ceil((double)p.units * ((p.P + kTile - 1) / kTile) / num_sms);
+  const double here = 2.0 + 2.6 * tiles + 0.016 * cols * tiles;
+  const double steps = (p.set_nodes * p.G + 7) / 8, all = 1e-3 * p.units * p.P * p.sets * steps * 152 / num_sms;
+  return here <= 2.2 + std::max(1.2 * steps, 0.65 * all);
+}
 
 cudaError_t launch_page_scores_tc(int D, ScoreParams p, int num_sms, cudaStream_t s) {
   p.set_cols = set_columns(p.set_nodes * p.G);

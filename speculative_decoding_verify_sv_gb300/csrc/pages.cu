@@ -139,14 +139,16 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
   cp_async_wait<0>();
 }
 
-// -------------------------------------------------- scores (bf16: page_scores_tc.cu)
+// ------------------------------------------ scores without the tensor cores (page_scores_tc.cu: with)
 
-// fp32: a warp per page, lanes over the channels.
-template <int D>
-__global__ void __launch_bounds__(256) page_scores_f32_kernel(const __grid_constant__ ScoreParams p) {
+// A warp per page and set, a lane's channels next to one another.  Eight rows are summed over the lanes together: each
+// exchange halves the rows of a lane.  For fp32, and for bf16 where a tile of 128 pages would be mostly
+// empty (page_scores_prefer_tc).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) page_scores_plain_kernel(const __grid_constant__ ScoreParams p) {
   constexpr int PL = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int bh = blockIdx.x / p.splits, part = blockIdx.x % p.splits, h = bh % p.Hkv, b = bh / p.Hkv;
+  const int bh = blockIdx.x / p.splits, part = blockIdx.x % p.splits, h = bh % p.Hkv, b = bh / p.Hkv, warps = blockDim.x >> 5;
   wait_previous();
   int L = p.prefix_len[b];
   const int most = (int)min((long long)INT_MAX, (long long)p.P * p.page_size);
@@ -156,7 +158,14 @@ __global__ void __launch_bounds__(256) page_scores_f32_kernel(const __grid_const
   }
   const int pages = (int)(((long long)L + p.page_size - 1) / p.page_size);
   float *out = p.out + (size_t)b * p.sets * p.Hkv * p.P + (size_t)h * p.P;
-  for (int page = part * 8 + warp; page < p.P; page += p.splits * 8) {
+  // PL neighbouring elements
+  struct alignas(sizeof(T) * PL) Piece {
+    T x[PL];
+  };
+  const int rows = p.set_nodes * p.G;
+  const long long jobs = (long long)p.P * p.sets;
+  for (long long job = (long long)part * warps + warp; job < jobs; job += (long long)p.splits * warps) {
+    const int set = (int)(job / p.P), page = (int)(job - (long long)set * p.P);
     long long row = -1;
     if (page < pages) {
       if (!p.block_table) {
@@ -164,33 +173,48 @@ __global__ void __launch_bounds__(256) page_scores_f32_kernel(const __grid_const
       } else {
         const int blk = p.block_table[(size_t)b * p.P + page];
         if (blk >= 0 && blk < p.num_blocks) row = blk;
-        else if (h == 0 && lane == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
+        else if (h == 0 && set == 0 && lane == 0) set_status(p.status, SV_DEV_BAD_BLOCK);
       }
     }
-    float lo[PL], hi[PL];
-    const float *src = static_cast<const float *>(p.bounds) + ((size_t)max(row, 0ll) * p.Hkv + h) * 2 * D + lane;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      lo[i] = row >= 0 ? src[32 * i] : 0.f;
-      hi[i] = row >= 0 ? src[D + 32 * i] : 0.f;
+    if (row < 0) {
+      if (lane == 0) out[(size_t)set * p.Hkv * p.P + page] = -INFINITY;
+      continue;
     }
-    for (int set = 0; set < p.sets; ++set) {
-      float best = -INFINITY;
-      for (int r = 0; r < p.set_nodes * p.G && row >= 0; ++r) {
-        const float *q = static_cast<const float *>(p.q) + (((size_t)b * p.N + set * p.set_nodes + r / p.G) * p.Hq + h * p.G + r % p.G) * D + lane;
-        float x = 0.f;
+    const T *src = static_cast<const T *>(p.bounds) + ((size_t)row * p.Hkv + h) * 2 * D + PL * lane;
+    const Piece lo = *reinterpret_cast<const Piece *>(src), hi = *reinterpret_cast<const Piece *>(src + D);
+    float best = -INFINITY;  // of the rows r0 + k, a k for each four lanes
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = min(r0 + k, rows - 1), node = r / p.G;
+        const Piece q = *reinterpret_cast<const Piece *>(
+            static_cast<const T *>(p.q) + (((size_t)b * p.N + set * p.set_nodes + node) * p.Hq + h * p.G + r - node * p.G) * D + PL * lane);
+        x[k] = 0.f;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-          const float y = q[32 * i];
-          x = fmaf(max_nan(y, 0.f), hi[i], x);
-          x = fmaf(min_nan(y, 0.f), lo[i], x);
+          const float y = (float)q.x[i];
+          x[k] = fmaf(max_nan(y, 0.f), (float)hi.x[i], x[k]);
+          x[k] = fmaf(min_nan(y, 0.f), (float)lo.x[i], x[k]);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-        best = max_nan(best, x);
       }
-      if (lane == 0) out[(size_t)set * p.Hkv * p.P + page] = best;
+      // (rows past the last are it once more, which changes no maximum)
+#pragma unroll
+      for (int half = 4; half > 0; half >>= 1) {
+        const bool upper = lane & (4 * half);
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+          const float keep = upper ? x[k + half] : x[k], send = upper ? x[k] : x[k + half];
+          x[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, 4 * half);
+        }
+      }
+      x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], 2);
+      x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
+      best = max_nan(best, x[0]);
     }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) best = max_nan(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+    if (lane == 0) out[(size_t)set * p.Hkv * p.P + page] = best;
   }
 }
 
@@ -473,10 +497,16 @@ cudaError_t launch_page_bounds(sv_dtype dt, BoundParams p, int B, int num_sms, c
                       : launch_close(page_bounds_kernel<false>, grid, kBoundThreads, smem, s, p);
 }
 
-cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream_t s) {
-  p.splits = std::max(1, std::min((p.P + 7) / 8, (8 * num_sms + p.units - 1) / p.units));
-  return D == 128 ? launch_close(page_scores_f32_kernel<128>, dim3((unsigned)p.units * p.splits), 256, 0, s, p)
-                  : launch_close(page_scores_f32_kernel<64>, dim3((unsigned)p.units * p.splits), 256, 0, s, p);
+cudaError_t launch_page_scores_plain(sv_dtype dt, int D, ScoreParams p, int num_sms, cudaStream_t s) {
+  const long long jobs = (long long)p.P * p.sets;
+  const int warps = (int)std::min<long long>(8, jobs);
+  p.splits = (int)std::max<long long>(1, std::min<long long>((jobs + warps - 1) / warps, (64ll / warps * num_sms + p.units - 1) / p.units));
+  const dim3 grid((unsigned)((long long)p.units * p.splits));
+  if (dt == SV_F32)
+    return D == 128 ? launch_close(page_scores_plain_kernel<float, 128>, grid, 32 * warps, 0, s, p)
+                    : launch_close(page_scores_plain_kernel<float, 64>, grid, 32 * warps, 0, s, p);
+  return D == 128 ? launch_close(page_scores_plain_kernel<bf16, 128>, grid, 32 * warps, 0, s, p)
+                  : launch_close(page_scores_plain_kernel<bf16, 64>, grid, 32 * warps, 0, s, p);
 }
 
 // Many lists (four per SM): a warp per list of up to 1024 scores, 16 scores per thread for longer ones; else few scores

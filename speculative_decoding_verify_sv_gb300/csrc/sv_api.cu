@@ -636,8 +636,9 @@ sv_status sv_page_scores(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, cons
   p.set_nodes = N / sets;
   p.units = B * Hkv;
   const cudaError_t e = take_injected_failure() ? cudaErrorLaunchFailure
-                        : dt == SV_F32          ? sv::launch_page_scores_f32(D, p, num_sms(), static_cast<cudaStream_t>(stream))
-                                                : sv::launch_page_scores_tc(D, p, num_sms(), static_cast<cudaStream_t>(stream));
+                        : dt == SV_BF16 && sv::page_scores_prefer_tc(p, num_sms())
+                            ? sv::launch_page_scores_tc(D, p, num_sms(), static_cast<cudaStream_t>(stream))
+                            : sv::launch_page_scores_plain(dt, D, p, num_sms(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "page scores launch");
   sv::count_launches(1);
   return SV_OK;

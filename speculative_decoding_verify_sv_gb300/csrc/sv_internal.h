@@ -322,7 +322,8 @@ struct ScoreParams {
   int set_cols, splits;               // (set at the launch)
 };
 cudaError_t launch_page_scores_tc(int D, ScoreParams p, int num_sms, cudaStream_t s);  // bf16
-cudaError_t launch_page_scores_f32(int D, ScoreParams p, int num_sms, cudaStream_t s);
+bool page_scores_prefer_tc(const ScoreParams &p, int num_sms);
+cudaError_t launch_page_scores_plain(sv_dtype dt, int D, ScoreParams p, int num_sms, cudaStream_t s);
 
 struct SelectParams {
   const float *scores;

@@ -116,6 +116,21 @@ def test_scores(cuda_ok, dtype, paged, per_node, N, Hq, Hkv, D):
     _scores(q, bounds, lens, page, bt, per_node)
 
 
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("per_node", [False, True])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 8, 8, 64), (5, 6, 2, 128), (26, 16, 2, 128), (64, 12, 1, 64), (64, 20, 1, 128)])
+def test_scores_of_many_pages(cuda_ok, paged, per_node, N, Hq, Hkv, D):
+    """Tiles that are full, partly full and behind the prefix, where the tensor cores are worth it."""
+    g = torch.Generator().manual_seed(N + Hq)
+    lens = torch.tensor([0, 1, 100, 16 * 700, 16 * 128, 16 * 511 + 3], dtype=torch.int32)
+    P, page = 700, 16
+    q = torch.randn(6, N, Hq, D, generator=g).to(BF)
+    bt = torch.randperm(6 * P, generator=g).to(torch.int32).view(6, P) if paged else None
+    x = torch.randn(*((6 * P,) if paged else (6, P)), Hkv, 2, D, generator=g).to(BF)
+    bounds = torch.stack([x.amin(-2), x.amax(-2)], -2).contiguous()
+    _scores(q, bounds, lens, page, bt, per_node)
+
+
 def test_scores_bound_every_key(cuda_ok):
     """The chain of operators: no key of a page has a larger product with any row than the page's score."""
     inp = wl.attention_inputs(3, 5, 8, 2, 128, [50, 161, 300], paged=True, seed=9)
@@ -145,6 +160,16 @@ def test_scores_of_bad_pages_prefixes_and_numbers(cuda_ok):
             s = sv.sv_page_scores(q.to(dtype), bounds.to(dtype).cuda(), torch.full_like(L, n), 16, block_table=bt.clamp(0, 7)).cpu()
             assert sv.sv_read_device_status() == sv.SV_DEV_BAD_PREFIX
             assert bool(s.isneginf().all()) == (n < 0) and (n < 0 or not bool(s.isneginf().any()))
+    # the same entries in a long table, for the tensor cores
+    wide = torch.cat([bt] + [bt.clamp(0, 7)] * 399, 1)
+    s = sv.sv_page_scores(q, bounds.cuda(), torch.full_like(L, 32000), 16, block_table=wide).cpu()
+    assert sv.sv_read_device_status() == sv.SV_DEV_BAD_BLOCK
+    assert bool(s[0, 0, :, [1, 3]].isneginf().all()) and bool(s[0, 0, 0, 4:].isfinite().all())
+    assert bool(s[0, 0, 1, 2].isnan()) and bool(s[0, 0, 0, 2].isfinite()) and bool(s[0, 0, 1, 7::5].isnan().all())
+    for n in (10 ** 6, -1):
+        s = sv.sv_page_scores(q, bounds.cuda(), torch.full_like(L, n), 16, block_table=wide.clamp(0, 7)).cpu()
+        assert sv.sv_read_device_status() == sv.SV_DEV_BAD_PREFIX
+        assert bool(s.isneginf().all()) == (n < 0) and (n < 0 or not bool(s.isneginf().any()))
 
 
 @pytest.mark.parametrize("P,count,first,last", [(1, 1, 0, 0), (5, 3, 1, 1), (40, 1, 0, 0), (40, 1, 1, 0), (40, 2, 1, 1), (300, 64, 4, 2),
