@@ -63,10 +63,13 @@ __device__ __forceinline__ void get(const float *p, float (&v)[R]) {
   }
 }
 
-// R: query rows of a CTA (1, 2, 4 or 8)
-template <int D, int R>
+// R: query rows of a CTA (1, 2, 4 or 8); NW: its warps, what one chunk each leaves room for, or two where
+// several CTAs share an SM
+template <int D>
+constexpr int kF32Warps = D == 64 ? 8 : 4;
+template <int D, int R, int NW_>
 struct F32Layout {
-  static constexpr int NW = D == 64 ? 8 : 4;      // warps: what one chunk each leaves room for
+  static constexpr int NW = NW_;
   static constexpr int KS = D + 4;                // row stride of K (floats)
   static constexpr int CHUNK = kF32Keys * (KS + D);  // floats of a warp's chunk
   static constexpr int OFF_P = NW * CHUNK;        // [NW][32][8] weights
@@ -80,9 +83,9 @@ struct F32Layout {
 };
 
 // LISTED: the keys of the unit's listed pages in the place of a window's (sv_sparse_attention).
-template <int D, int R, bool LISTED>
-__global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(const __grid_constant__ AttnParams p) {
-  using Lay = F32Layout<D, R>;
+template <int D, int R, int NW_, bool LISTED>
+__global__ void __launch_bounds__(NW_ * 32) window_f32_kernel(const __grid_constant__ AttnParams p) {
+  using Lay = F32Layout<D, R, NW_>;
   constexpr int NW = Lay::NW, KS = Lay::KS, PL = D / 32;
   extern __shared__ __align__(16) float f32_smem[];
   float *sm = f32_smem;
@@ -299,16 +302,16 @@ __global__ void __launch_bounds__(F32Layout<D, R>::NW * 32) window_f32_kernel(co
   if (C > 1) cluster_merge<D>(sm, D, s_cm, s_cl, R, C, rank, kF32None, sm + Lay::CHUNK, store);
 }
 
-template <int D, int R, bool LISTED>
+template <int D, int R, int NW, bool LISTED>
 cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
-  using Lay = F32Layout<D, R>;
+  using Lay = F32Layout<D, R, NW>;
   static_assert(Lay::SMEM <= 227 * 1024, "shared memory");
   static std::atomic<bool> attr[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr[dev].load()) {
     const cudaError_t e =
-        cudaFuncSetAttribute(window_f32_kernel<D, R, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+        cudaFuncSetAttribute(window_f32_kernel<D, R, NW, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev].store(true);
   }
@@ -325,7 +328,7 @@ cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, R, LISTED>, p);
+  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, R, NW, LISTED>, p);
 }
 
 // `kv_units` sequences (or sets of nodes) and KV heads of p.M rows, against up to `keys` keys.
@@ -336,36 +339,55 @@ cudaError_t launch_f32(AttnParams p, long long kv_units, long long keys, int num
   // CTA per SM): a wave of CTAs takes 3.4 + 0.45 rows and 2.3 + 0.25 rows for every further chunk of
   // its warps, a cluster 2 more.  20 KV heads of 5 rows of 64, window 129: 4.7 us with a row each
   // against 7.8 with eight; 32 of 20 rows of 128, window 2049, 98 with eight (two take 128).
-  const int warps = p.D == 64 ? 8 : 4;
+  // Many short lists (26 nodes of 8 heads of 128 with a page of 16 each, 8 sequences: 1664 units of two
+  // chunks, 20.6 us against 49.7) have two warps to a CTA, of which three (heads of 64: six) share an SM.
+  const int full = p.D == 64 ? 8 : 4;
   const int chunks = (int)(keys / kF32Keys) + (p.N + p.sinks) / kF32Keys + 2;
-  int rows = 1;
+  int rows = 1, warps = full;
   long long units = 0;
   double best = 0;
-  for (int r = 1; r <= 8 && (r == 1 || r < 2 * p.M); r *= 2)
-    for (int c = 1; c <= 8; c *= 2) {
-      const long long u = kv_units * ((p.M + r - 1) / r);
-      if (c == 8 && u * c > num_sms * 2 / 3) break;  // 16 clusters of 8 do not find room together
-      const double waves = (double)((u * c + num_sms - 1) / num_sms);
-      const int further = (chunks + c * warps - 1) / (c * warps) - 1;
-      const double cost = waves * (3.4 + 0.45 * r + further * (2.3 + 0.25 * r) + (c > 1 ? 2 : 0));
-      if (units == 0 || cost < best) {
-        best = cost;
-        rows = r;
-        units = u;
-        p.splits = c;
+  for (int w = full; w >= (LISTED ? 2 : full); w = w > 2 ? 2 : 0)
+    for (int r = 1; r <= 8 && (r == 1 || r < 2 * p.M); r *= 2)
+      for (int c = 1; c <= (w == full ? 8 : 1); c *= 2) {
+        const long long u = kv_units * ((p.M + r - 1) / r);
+        if (c == 8 && u * c > num_sms * 2 / 3) break;  // 16 clusters of 8 do not find room together
+        const long long places = (long long)num_sms * (w == full ? 1 : p.D == 64 ? 6 : 3);
+        const double waves = (double)((u * c + places - 1) / places);
+        const int further = (chunks + c * w - 1) / (c * w) - 1;
+        const double cost = waves * (3.4 + 0.45 * r + further * (2.3 + 0.25 * r) + (c > 1 ? 2 : 0));
+        if (units == 0 || cost < best) {
+          best = cost;
+          rows = r;
+          units = u;
+          warps = w;
+          p.splits = c;
+        }
       }
-    }
   const long long ctas = units * p.splits;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  if constexpr (LISTED) {
+    if (warps == 2) {
+      switch (rows * 1000 + p.D) {
+        case 1064: return launch_f32_d<64, 1, 2, true>(p, ctas, s);
+        case 2064: return launch_f32_d<64, 2, 2, true>(p, ctas, s);
+        case 4064: return launch_f32_d<64, 4, 2, true>(p, ctas, s);
+        case 8064: return launch_f32_d<64, 8, 2, true>(p, ctas, s);
+        case 1128: return launch_f32_d<128, 1, 2, true>(p, ctas, s);
+        case 2128: return launch_f32_d<128, 2, 2, true>(p, ctas, s);
+        case 4128: return launch_f32_d<128, 4, 2, true>(p, ctas, s);
+        default: return launch_f32_d<128, 8, 2, true>(p, ctas, s);
+      }
+    }
+  }
   switch (rows * 1000 + p.D) {
-    case 1064: return launch_f32_d<64, 1, LISTED>(p, ctas, s);
-    case 2064: return launch_f32_d<64, 2, LISTED>(p, ctas, s);
-    case 4064: return launch_f32_d<64, 4, LISTED>(p, ctas, s);
-    case 8064: return launch_f32_d<64, 8, LISTED>(p, ctas, s);
-    case 1128: return launch_f32_d<128, 1, LISTED>(p, ctas, s);
-    case 2128: return launch_f32_d<128, 2, LISTED>(p, ctas, s);
-    case 4128: return launch_f32_d<128, 4, LISTED>(p, ctas, s);
-    default: return launch_f32_d<128, 8, LISTED>(p, ctas, s);
+    case 1064: return launch_f32_d<64, 1, kF32Warps<64>, LISTED>(p, ctas, s);
+    case 2064: return launch_f32_d<64, 2, kF32Warps<64>, LISTED>(p, ctas, s);
+    case 4064: return launch_f32_d<64, 4, kF32Warps<64>, LISTED>(p, ctas, s);
+    case 8064: return launch_f32_d<64, 8, kF32Warps<64>, LISTED>(p, ctas, s);
+    case 1128: return launch_f32_d<128, 1, kF32Warps<128>, LISTED>(p, ctas, s);
+    case 2128: return launch_f32_d<128, 2, kF32Warps<128>, LISTED>(p, ctas, s);
+    case 4128: return launch_f32_d<128, 4, kF32Warps<128>, LISTED>(p, ctas, s);
+    default: return launch_f32_d<128, 8, kF32Warps<128>, LISTED>(p, ctas, s);
   }
 }
 

@@ -73,3 +73,15 @@ def test_trees_of_each_sequence(cuda_ok):
     lens = [i % 70 for i in range(B)]
     inp = wl.attention_inputs(B, 6, 16, 8, 64, lens, dtype=BF, seed=7)
     sparse.check(inp, parents, sparse.lists_of(lens, 1, 8, 3, 16, 11), 16)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D,per_node", [(64, 4, 4, 64, True), (26, 8, 8, 128, True), (5, 16, 4, 64, True), (5, 32, 4, 128, True),
+                                                 (1, 8, 8, 128, False), (33, 3, 3, 64, False)])
+@pytest.mark.parametrize("paged", [True, False])
+def test_listed_units_of_float32(cuda_ok, N, Hq, Hkv, D, per_node, paged):
+    """CTAs of two warps, of which several share an SM, each with one to eight rows."""
+    B = batch(2 * Hkv * (N if per_node else 1)) if N > 1 else batch(Hkv)
+    lens = [(0, 1, 15, 16, 17, 40, 29, 33)[i % 8] for i in range(B)]
+    par = wl.TREE_T64 if N == 64 else wl.TREE_T26 if N == 26 else wl.chain_parent(N - 1)
+    inp = wl.attention_inputs(B, N, Hq, Hkv, D, lens, dtype=torch.float32, paged=paged, seed=N)
+    sparse.check(inp, par, sparse.lists_of(lens, N if per_node else 1, Hkv, 2, 16, N), 16)
