@@ -6,11 +6,11 @@
 // crosses.  Pages that many rows see together go through the stacked kernel instead, see sparse_plan.
 //
 // Pieces: the kernel takes the tree's nodes and a sequence's own keys (those behind what it shares; none with
-// listed pages), and its rows begin with the stacked kernel's pieces instead of nothing, the slices of a CTA
-// with every fourth (or second) each.  They are read straight to the registers that the products add to, while
-// the first keys are on their way.  (One more part of the merge at the end, through shared memory: one token of
-// 8 requests behind 8192 keys, 19 pieces a row, 25.8 us instead of 22.7; read element by element there, 10 us
-// more per CTA.)
+// listed pages), and its rows begin with the stacked kernel's pieces instead of nothing, shared out over the
+// slices of the unit's CTAs.  They are read straight to the registers that the products add to, while the first
+// keys are on their way.  (One token of 8 requests behind 8192 keys, 19 pieces a row: 19.9 us; without clusters
+// 21.9; as one more part of the merge at the end, through shared memory, 25.8; read element by element there,
+// 10 us more per CTA.)
 #pragma once
 
 #include "unit_attention.cuh"

@@ -404,10 +404,10 @@ __device__ __forceinline__ void unit_attention(const typename Keys::Params &p) {
   float m[NT][2], l[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = kWinNone, l[j][0] = l[j][1] = 0.f;
-  // (the rows begin with their pieces, those of a row in turn with the slices)
+  // (the rows begin with their pieces, those of a row in turn with the slices of all CTAs)
   if constexpr (Keys::kPieces) {
     const Pieces *rows = s_piece + rg * 8 * NT;
-    begin_with_pieces<D, NT, Keys>(p, rows, lane < 8 * NT ? rows[lane].count : 0, slice, KS, o, m, l);
+    begin_with_pieces<D, NT, Keys>(p, rows, lane < 8 * NT ? rows[lane].count : 0, (int)rank * KS + slice, (int)C * KS, o, m, l);
   }
 
   const float sc = p.scale_log2;
@@ -848,7 +848,7 @@ struct WinPlan {
 };
 
 // M rows against `groups` groups of keys for each of `kv_units` sequences and KV heads.
-inline WinPlan window_plan(long long kv_units, int M, int groups, int num_sms, bool pieces = false) {
+inline WinPlan window_plan(long long kv_units, int M, int groups, int num_sms) {
   WinPlan plan{};
   const double sms = num_sms, moved = (double)kv_units * groups * kWinGroup * 512 * 1e-6;  // K and V, MB
   for (const WinForm &f : kWinForms) {
@@ -861,11 +861,10 @@ inline WinPlan window_plan(long long kv_units, int M, int groups, int num_sms, b
     // (its start and merge) beside its share of the window's groups: 512 units of 32 rows, window
     // 4097, go without clusters, 156 us against 181 with clusters of four.  (Clusters of 16 gain
     // little on the longest windows and start later: 8 units of 4 rows, window 1024, 0.6 us more; 16
-    // such clusters find no room together, 25 us against 13.)  With pieces, whose rows' own keys are few, none:
-    // 4 tokens of one head each, 4096 shared keys, 19 us against 28; 16 tokens 19 against 20.7.
+    // such clusters find no room together, 25 us against 13.)
     long long best = 0;
     int cluster = 1;
-    for (int c = 1; c <= (pieces ? 1 : 8); c *= 2) {
+    for (int c = 1; c <= 8; c *= 2) {
       const long long cost = (units * c + slots - 1) / slots * ((groups + c - 1) / c + 16);
       if (c == 1 || cost < best) {
         best = cost;
@@ -957,7 +956,7 @@ inline bool unit_params(WinParams &p, const AttnParams &a, int M) {
 // window_plan takes for them.
 template <class Keys>
 cudaError_t launch_units(typename Keys::Params &p, int D, long long kv_units, int groups, int num_sms, cudaStream_t s) {
-  const WinPlan plan = window_plan(kv_units, p.M, groups, num_sms, Keys::kPieces);
+  const WinPlan plan = window_plan(kv_units, p.M, groups, num_sms);
   p.m_tiles = plan.m_tiles;
   p.cluster = plan.cluster;
   const long long ctas = kv_units * p.m_tiles * p.cluster;
