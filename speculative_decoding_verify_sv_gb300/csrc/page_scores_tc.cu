@@ -32,13 +32,13 @@ constexpr int kTile = 128;        // pages of a tile
 constexpr int kCols = 256;        // query rows at a time
 constexpr int kScoreThreads = 416;  // maxima, copies (two groups of four warps), issue
 
-// ST: stages of the ring; the more the fewer columns there are
-template <int D, int ST>
+// ST: stages of the ring; COLS: columns of a product; NQ: buffers of query rows
+template <int D, int ST, int COLS_, int NQ_>
 struct ScoreLayout {
   static constexpr int KB = D / 64;
   static constexpr int STAGE = kTile * 128;  // a tile's pages, 64 channels of lo or hi
-  static constexpr int COLS = ST <= 6 ? kCols : 64;
-  static constexpr int NQ = ST <= 6 ? 1 : 2;    // buffers of query rows [2 KB][COLS][64], 128-byte swizzle
+  static constexpr int COLS = COLS_;
+  static constexpr int NQ = NQ_;                // [2 KB][COLS][64] each, 128-byte swizzle
   static constexpr int Q_BYTES = COLS * D * 4;
   static constexpr int OFF_RING = NQ * Q_BYTES;
   static constexpr int OFF_BAR = OFF_RING + ST * STAGE;
@@ -100,9 +100,9 @@ __device__ __forceinline__ bool next_run(long long &w, long long end, const Scor
   return true;
 }
 
-template <int D, int ST>
+template <int D, int ST, int COLS_, int NQ_>
 __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const __grid_constant__ ScoreParams p) {
-  using Lay = ScoreLayout<D, ST>;
+  using Lay = ScoreLayout<D, ST, COLS_, NQ_>;
   constexpr int KB = Lay::KB, COLS = Lay::COLS, NQ = Lay::NQ;
   extern __shared__ __align__(1024) uint8_t score_tc_smem[];
   uint8_t *sm = score_tc_smem, *ring = sm + Lay::OFF_RING;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
   if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------------ copies
     // two groups of four warps, which take turns at the stages (with one of them 33.5 us against 27.2 for
-    // scores-decode); the first brings the query rows
+    // one token of 16 sequences of 2000 pages); the first brings the query rows
     const int me = tid & 127, group = (warp - 4) >> 2;
     int k = 0, arrived = 0, segments = 0, tile = 0;  // this group's stages asked for, and landed; row chunks; tiles
     bool ok = true;
@@ -390,13 +390,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
   }
 }
 
-template <int D, int ST>
+template <int D, int ST, int COLS, int NQ>
 cudaError_t launch_typed(const ScoreParams &p, int grid, cudaStream_t s) {
-  using Lay = ScoreLayout<D, ST>;
+  using Lay = ScoreLayout<D, ST, COLS, NQ>;
   static std::atomic<bool> attr[64];
   int dev = 0;
   cudaGetDevice(&dev);
-  auto kern = page_scores_tc_kernel<D, ST>;
+  auto kern = page_scores_tc_kernel<D, ST, COLS, NQ>;
   if (dev < 0 || dev >= 64 || !attr[dev].load()) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
     if (e != cudaSuccess) return e;
@@ -432,11 +432,14 @@ cudaError_t launch_page_scores_tc(int D, ScoreParams p, int num_sms, cudaStream_
   p.set_cols = set_columns(p.set_nodes * p.G);
   const long long tiles = (long long)p.units * ((p.P + kTile - 1) / kTile);
   const int grid = (int)std::min<long long>(num_sms, tiles);
-  // few columns leave room for a deeper ring (one token, 32:8 heads, 2048 pages, 16 requests: 26.5 us against 27.2;
-  // 8 requests, 32:32 heads, 46.3 against 48.2)
-  const bool few = (long long)p.sets * p.set_cols <= 64;
-  if (D == 128) return few ? launch_typed<128, 10>(p, grid, s) : launch_typed<128, 6>(p, grid, s);
-  return few ? launch_typed<64, 10>(p, grid, s) : launch_typed<64, 6>(p, grid, s);
+  // Two buffers of query rows where there is room for them, so that a sequence or head can be prepared beside the one
+  // before it, then stages: 26 nodes, 64:8 heads of 64, 16 sequences of 2048 pages 21.4 us against 28.2 with one
+  // buffer (and 31.0 with one and ten stages), 64 sequences of 200 pages 21.7 against 40.7; 32:8 heads of 128,
+  // 104 columns, 29.9 against 31.1; one token, 32:8 heads of 128, ten stages 26.5 against six 27.2.
+  const long long cols = (long long)p.sets * p.set_cols;
+  if (D == 64) return cols <= 128 ? launch_typed<64, 10, 128, 2>(p, grid, s) : launch_typed<64, 6, 256, 2>(p, grid, s);
+  if (cols <= 64) return launch_typed<128, 10, 64, 2>(p, grid, s);
+  return cols <= 128 ? launch_typed<128, 6, 128, 2>(p, grid, s) : launch_typed<128, 6, 256, 1>(p, grid, s);
 }
 
 }  // namespace sv
