@@ -5,14 +5,15 @@
 // up to 256 at a time).  A page is a lane of TMEM then, so that the maximum over the rows of a set is taken
 // in a thread, and a warp writes the scores of 32 neighbouring pages of a set side by side.
 //
-// Persistent CTAs split the (sequence, KV head, tile of 128 pages) space evenly.  Four warps bring the bounds
-// (cp.async: a page of a paged cache is 512 bytes somewhere in the pool) through a ring whose stages are 64
-// channels of a tile's pages, and make q- and q+ whenever the sequence or head changes; one warp issues; four
-// read the products, double buffered in TMEM.
+// Persistent CTAs split the (sequence, KV head, tile of 128 pages) space evenly.  Two groups of four warps bring the
+// bounds (cp.async: a page of a paged cache is 512 bytes somewhere in the pool) through a ring whose stages are 64
+// channels of a tile's pages, the first of them also q- and q+ whenever the sequence or head changes; one warp
+// issues; four read the products, double buffered in TMEM.
 //
-// Bound by HBM for few rows: 16 requests, one token, 2048 pages of 8 heads of 128, 26.6 us, 4.9 TB/s, 72 % of the
-// measured copy rate (one group of copying warps 33.5 us, mma.sync 34); for many by the products, which HBM's time does not
-// hide: 26 nodes, 64:8 heads, 208 columns per page, 37 us (one group of copying warps 43, mma.sync 184).
+// Bound by HBM for few rows: 16 requests, one token, 2000 pages of 8 heads of 128, 26.6 us, 4.9 TB/s, 72 % of the
+// measured copy rate, of which start and end are 5 us (one group of copying warps 33.5 us, mma.sync 34, gathers
+// of four pages by TMA 64: 7 bytes per clock and SM); for many by the products, which HBM's time does not hide: 26
+// nodes, 64:8 heads, 208 columns per page, 37 us (one group of copying warps 43, gathers 80, mma.sync 184).
 #include <algorithm>
 #include <atomic>
 #include <climits>

@@ -7,7 +7,7 @@
 // matrix products like a prompt's, and K and V are read once for all instead of once per sequence.
 // What differs by row (a sequence's own keys, the tree's mask) is not here: this kernel leaves each
 // row's unnormalised output, maximum and sum over the keys that it has worked on, and the kernel of
-// stacked_units.cu, which takes the own keys and the tree, joins them by softmax's rule
+// stacked_keys.cuh, which takes the own keys and the tree, joins them by softmax's rule
 //   m = max m_i,  l = sum 2^(m_i - m) l_i,  o = sum 2^(m_i - m) o_i / l.
 //
 // Work: a unit is a KV head and up to 256 rows of a group (two MMA tiles A and B of 128), against the
@@ -22,10 +22,11 @@
 // may be issued over P as soon as P V has been, without waiting for it.
 //
 // Bound by the CTA's chain of products and softmax: 32 sequences with 64 nodes each behind one prompt of 4099 keys,
-// 32:32 heads of 128, 95 us, 1.45 PFLOP/s, the tensor pipe 61 % active at first (105 us) and 67 % now, exponents
-// 30 %.  Half the MMAs left out 84.5 us, the exponents left out no change.  What was tried: 16 softmax warps, half
+// 32:32 heads of 128, 95 us, 1.45 PFLOP/s, the tensor pipe about two thirds active, the unit of the exponents a third.
+// (With half of the MMAs left out 84.5 us, with the exponents left out no change.)  What was tried: 16 softmax warps, half
 // a row each, 102 us against 96; weights of the first half against the maximum of the tile before 100.6
-// against 95.6; four stages of the ring and page ids tile by tile, 256 requests in four groups, 104 against 98.
+// against 95.6; four stages of the ring and page ids tile by tile, 256 requests in four groups, 104 against 98; tiles
+// prefetched to the L2 115 against 97.
 #include <atomic>
 #include <cfloat>
 
