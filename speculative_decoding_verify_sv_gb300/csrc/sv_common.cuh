@@ -22,7 +22,8 @@ __device__ __forceinline__ void set_status(unsigned int *status, unsigned int bi
 
 // Kernels that a call with this attribute launches begin with wait_previous(): the launch may then
 // be set up while the stream's previous kernel still runs, and nothing is read or written before
-// that kernel has completed.  Back to back an empty kernel costs 1.4 us launched this way and 2.05
+// that kernel has completed (a kernel that follows one of the same call, which has itself waited before it
+// let this one start, waits only before what that one writes).  Back to back an empty kernel costs 1.4 us launched this way and 2.05
 // us the plain way, and kernels of a few us are spared the rounding up to that step.
 // Such a grid may be resident while the previous kernel still writes, so that nothing of it is
 // read-only for the grid's lifetime: what it reads behind the wait it reads with ordinary loads, never
