@@ -462,6 +462,10 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t ts = tmem + lanes + x * kKeys, to = tmem + lanes + 256 + x * D;
     const float sc = p.scale_log2;
+    // (a warp goes on or leaves as a whole: behind each wait are operations that all of its lanes take part in)
+    auto arrived = [&](uint64_t *bar, int parity) -> bool {
+      return __all_sync(0xFFFFFFFFu, stack_wait(bar, parity, abort_flag, limit));
+    };
     int r = 0, tiles = 0, n = 0, done = 0;  // stages, key tiles of the CTA, of this MMA tile, pieces of this MMA tile
     StackPiece pc;
     bool ok = true;
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
       const bool idle = wq * 32 >= rows;  // padding: the barriers only
       float m = kStackNone, l = 0.f;
       for (int t = pc.t0; t < pc.t1; ++t, ++tiles, ++n, r += 2) {
-        if (!stack_wait(&s_full[x], n & 1, abort_flag, limit)) {
+        if (!arrived(&s_full[x], n & 1)) {
           ok = false;
           break;
         }
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
         if (keys != kAllKeys && x == 0) {
           // V rows that are no keys may hold anything: zero, so that 0 * V stays 0
           const int sv = (r + 1) % ST;
-          if (!stack_wait(&full[sv], ((r + 1) / ST) & 1, abort_flag, limit)) {
+          if (!arrived(&full[sv], ((r + 1) / ST) & 1)) {
             ok = false;
             break;
           }
@@ -576,7 +580,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
         }
       }
       if (!ok) break;
-      if (!stack_wait(&o_full[x], done & 1, abort_flag, limit)) break;
+      if (!arrived(&o_full[x], done & 1)) break;
       ++done;
       tc_fence_after();
       if (!idle) {
