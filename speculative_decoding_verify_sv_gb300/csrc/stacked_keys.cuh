@@ -192,18 +192,7 @@ struct OwnKeys {
   __device__ static __forceinline__ int sequence(const Params &, int bs) { return bs; }
   __device__ static __forceinline__ int first_node(const Params &, int) { return 0; }
   __device__ static __forceinline__ SharedPart shared_part_warp(const Params &p, int b, bool reports) {
-    if (!reports) return {};
-    bool bad = false, outside = false, beyond = false;
-    const int L = p.prefix_len[b];
-    for (int g = threadIdx.x & 31; g < p.groups; g += 32) {
-      const int a = p.group_start[g], e = p.group_start[g + 1], len = p.shared_len[g];
-      bad |= a < 0 || e < a || e > p.B;
-      outside |= len < 0 || len > p.cap;
-      beyond |= a <= b && b < e && len > L;
-    }
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    if (bad || outside || beyond)
-      set_status(p.status, (bad ? SV_DEV_BAD_GROUP : 0) | (outside || (beyond && !bad) ? SV_DEV_BAD_PREFIX : 0));
+    if (reports) report_groups(p.group_start, p.shared_len, p.groups, p.B, p.cap, b, p.prefix_len[b], p.status);
     return {};
   }
   __device__ static __forceinline__ SharedPart shared_part(const Params &p, int b, bool reports, SharedPart *) {

@@ -492,7 +492,7 @@ sv_status sv_shared_attention(sv_dtype dt, int B, int N, int Hq, int Hkv, int D,
   unsigned launches = 0;
   cudaError_t e = cudaErrorLaunchFailure;
   if (dt == SV_F32) {
-    if (!take_injected_failure() && (e = sv::launch_window_attention_f32(p, num_sms(), static_cast<cudaStream_t>(stream))) == cudaSuccess)
+    if (!take_injected_failure() && (e = sv::launch_shared_attention_f32(p, l, num_sms(), static_cast<cudaStream_t>(stream))) == cudaSuccess)
       ++launches;
   } else {
     e = sv::launch_shared_attention(p, l, plan, workspace, static_cast<cudaStream_t>(stream), take_injected_failure, &launches);

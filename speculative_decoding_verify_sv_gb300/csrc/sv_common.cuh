@@ -48,6 +48,22 @@ __device__ __forceinline__ int listed_length(const int32_t *list, int n) {
   return __reduce_max_sync(0xFFFFFFFFu, used);
 }
 
+// (a warp) Reports groups that are none, and shared lengths outside the cache or beyond sequence b's prefix
+// length L, for calls in which every sequence's own rows are read.
+__device__ __forceinline__ void report_groups(const int32_t *group_start, const int32_t *shared_len, int groups, int B, int cap,
+                                              int b, int L, unsigned int *status) {
+  bool bad = false, outside = false, beyond = false;
+  for (int g = threadIdx.x & 31; g < groups; g += 32) {
+    const int a = group_start[g], e = group_start[g + 1], len = shared_len[g];
+    bad |= a < 0 || e < a || e > B;
+    outside |= len < 0 || len > cap;
+    beyond |= a <= b && b < e && len > L;
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (bad || outside || beyond)
+    set_status(status, (bad ? SV_DEV_BAD_GROUP : 0) | (outside || (beyond && !bad) ? SV_DEV_BAD_PREFIX : 0));
+}
+
 inline cudaLaunchAttribute close_launch() {
   cudaLaunchAttribute a;
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;

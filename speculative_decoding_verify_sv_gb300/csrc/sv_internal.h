@@ -51,6 +51,9 @@ struct AttnParams {
   // listed pages (fp32): [B,sets,Hkv,list_len], a list per set of set_nodes nodes
   const int32_t *pages;
   int list_len, sets, set_nodes, page_size;
+  // groups that share prefixes (fp32, which only reports what is wrong with them)
+  const int32_t *group_start, *shared_len;
+  int groups;
 };
 
 struct AttnPlan {
@@ -169,7 +172,8 @@ cudaError_t launch_shared_attention(const AttnParams &a, const ListArgs &l, cons
                                     bool (*fails)(), unsigned *launches);
 cudaError_t launch_sparse_attention(const AttnParams &a, const ListArgs &l, const StackPlan &pl, void *ws, int num_sms,
                                     cudaStream_t s, bool (*fails)(), unsigned *launches);
-// Listed pages in fp32.
+// Every sequence's whole prefix, and listed pages, in fp32.
+cudaError_t launch_shared_attention_f32(AttnParams a, const ListArgs &l, int num_sms, cudaStream_t s);
 cudaError_t launch_sparse_attention_f32(AttnParams a, const ListArgs &l, int num_sms, cudaStream_t s);
 // The same in fp32 (any number of rows; p.splits is set at the launch: the CTAs per unit).
 cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t s);

@@ -82,10 +82,14 @@ struct F32Layout {
   static_assert(CHUNK >= R * D, "a warp's outputs merge in the room of its chunk");
 };
 
-// LISTED: the keys of the unit's listed pages in the place of a window's (sv_sparse_attention).
-template <int D, int R, int NW_, bool LISTED>
+// The keys: a window's (sv_window_attention), those of the unit's listed pages (sv_sparse_attention), or the sequence's
+// whole prefix (sv_shared_attention), which also reports groups that are none.  (Instances of their own: with that
+// report for no groups in the window's, 4 requests of 5 nodes, 32:8 heads of 128, window 2049, take 105 us against 98.)
+enum F32Kind { kWindowKeys, kListedKeys, kSharedKeys };
+template <int D, int R, int NW_, F32Kind KEYS>
 __global__ void __launch_bounds__(NW_ * 32) window_f32_kernel(const __grid_constant__ AttnParams p) {
   using Lay = F32Layout<D, R, NW_>;
+  constexpr bool LISTED = KEYS == kListedKeys;
   constexpr int NW = Lay::NW, KS = Lay::KS, PL = D / 32;
   extern __shared__ __align__(16) float f32_smem[];
   float *sm = f32_smem;
@@ -114,6 +118,8 @@ __global__ void __launch_bounds__(NW_ * 32) window_f32_kernel(const __grid_const
     qv[k] = row >= 0 ? static_cast<const float *>(p.q)[(size_t)row * D + i % D] : 0.f;
   }
   const int parent = tid < p.N ? tree_parent(p.tree, b, tid) : -1;
+  if (KEYS == kSharedKeys && tid < 32 && rank == 0 && unit % (blocks * p.Hkv) == 0)
+    report_groups(p.group_start, p.shared_len, p.groups, p.B, p.cap, b, L, p.status);
   if (L < 0 || L > p.cap) {
     if (unit % (blocks * p.Hkv) == 0 && node0 == 0 && rank == 0 && tid == 0) set_status(p.status, SV_DEV_BAD_PREFIX);
     L = L < 0 ? 0 : p.cap;
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(NW_ * 32) window_f32_kernel(const __grid_const
   if (C > 1) cluster_merge<D>(sm, D, s_cm, s_cl, R, C, rank, kF32None, sm + Lay::CHUNK, store);
 }
 
-template <int D, int R, int NW, bool LISTED>
+template <int D, int R, int NW, F32Kind KEYS>
 cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
   using Lay = F32Layout<D, R, NW>;
   static_assert(Lay::SMEM <= 227 * 1024, "shared memory");
@@ -311,7 +317,7 @@ cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr[dev].load()) {
     const cudaError_t e =
-        cudaFuncSetAttribute(window_f32_kernel<D, R, NW, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+        cudaFuncSetAttribute(window_f32_kernel<D, R, NW, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev].store(true);
   }
@@ -328,11 +334,11 @@ cudaError_t launch_f32_d(const AttnParams &p, long long ctas, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, R, NW, LISTED>, p);
+  return cudaLaunchKernelEx(&cfg, window_f32_kernel<D, R, NW, KEYS>, p);
 }
 
 // `kv_units` sequences (or sets of nodes) and KV heads of p.M rows, against up to `keys` keys.
-template <bool LISTED>
+template <F32Kind KEYS>
 cudaError_t launch_f32(AttnParams p, long long kv_units, long long keys, int num_sms, cudaStream_t s) {
   // Rows of a CTA and CTAs per unit (splits): few rows are done sooner, many read K and V fewer
   // times.  As fitted to measurements (us, 4 to 128 KV heads of 1 to 64 rows, windows 17 to 2049; one
@@ -346,7 +352,7 @@ cudaError_t launch_f32(AttnParams p, long long kv_units, long long keys, int num
   int rows = 1, warps = full;
   long long units = 0;
   double best = 0;
-  for (int w = full; w >= (LISTED ? 2 : full); w = w > 2 ? 2 : 0)
+  for (int w = full; w >= (KEYS == kListedKeys ? 2 : full); w = w > 2 ? 2 : 0)
     for (int r = 1; r <= 8 && (r == 1 || r < 2 * p.M); r *= 2)
       for (int c = 1; c <= (w == full ? 8 : 1); c *= 2) {
         const long long u = kv_units * ((p.M + r - 1) / r);
@@ -365,29 +371,29 @@ cudaError_t launch_f32(AttnParams p, long long kv_units, long long keys, int num
       }
   const long long ctas = units * p.splits;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  if constexpr (LISTED) {
+  if constexpr (KEYS == kListedKeys) {
     if (warps == 2) {
       switch (rows * 1000 + p.D) {
-        case 1064: return launch_f32_d<64, 1, 2, true>(p, ctas, s);
-        case 2064: return launch_f32_d<64, 2, 2, true>(p, ctas, s);
-        case 4064: return launch_f32_d<64, 4, 2, true>(p, ctas, s);
-        case 8064: return launch_f32_d<64, 8, 2, true>(p, ctas, s);
-        case 1128: return launch_f32_d<128, 1, 2, true>(p, ctas, s);
-        case 2128: return launch_f32_d<128, 2, 2, true>(p, ctas, s);
-        case 4128: return launch_f32_d<128, 4, 2, true>(p, ctas, s);
-        default: return launch_f32_d<128, 8, 2, true>(p, ctas, s);
+        case 1064: return launch_f32_d<64, 1, 2, kListedKeys>(p, ctas, s);
+        case 2064: return launch_f32_d<64, 2, 2, kListedKeys>(p, ctas, s);
+        case 4064: return launch_f32_d<64, 4, 2, kListedKeys>(p, ctas, s);
+        case 8064: return launch_f32_d<64, 8, 2, kListedKeys>(p, ctas, s);
+        case 1128: return launch_f32_d<128, 1, 2, kListedKeys>(p, ctas, s);
+        case 2128: return launch_f32_d<128, 2, 2, kListedKeys>(p, ctas, s);
+        case 4128: return launch_f32_d<128, 4, 2, kListedKeys>(p, ctas, s);
+        default: return launch_f32_d<128, 8, 2, kListedKeys>(p, ctas, s);
       }
     }
   }
   switch (rows * 1000 + p.D) {
-    case 1064: return launch_f32_d<64, 1, kF32Warps<64>, LISTED>(p, ctas, s);
-    case 2064: return launch_f32_d<64, 2, kF32Warps<64>, LISTED>(p, ctas, s);
-    case 4064: return launch_f32_d<64, 4, kF32Warps<64>, LISTED>(p, ctas, s);
-    case 8064: return launch_f32_d<64, 8, kF32Warps<64>, LISTED>(p, ctas, s);
-    case 1128: return launch_f32_d<128, 1, kF32Warps<128>, LISTED>(p, ctas, s);
-    case 2128: return launch_f32_d<128, 2, kF32Warps<128>, LISTED>(p, ctas, s);
-    case 4128: return launch_f32_d<128, 4, kF32Warps<128>, LISTED>(p, ctas, s);
-    default: return launch_f32_d<128, 8, kF32Warps<128>, LISTED>(p, ctas, s);
+    case 1064: return launch_f32_d<64, 1, kF32Warps<64>, KEYS>(p, ctas, s);
+    case 2064: return launch_f32_d<64, 2, kF32Warps<64>, KEYS>(p, ctas, s);
+    case 4064: return launch_f32_d<64, 4, kF32Warps<64>, KEYS>(p, ctas, s);
+    case 8064: return launch_f32_d<64, 8, kF32Warps<64>, KEYS>(p, ctas, s);
+    case 1128: return launch_f32_d<128, 1, kF32Warps<128>, KEYS>(p, ctas, s);
+    case 2128: return launch_f32_d<128, 2, kF32Warps<128>, KEYS>(p, ctas, s);
+    case 4128: return launch_f32_d<128, 4, kF32Warps<128>, KEYS>(p, ctas, s);
+    default: return launch_f32_d<128, 8, kF32Warps<128>, KEYS>(p, ctas, s);
   }
 }
 
@@ -395,7 +401,14 @@ cudaError_t launch_f32(AttnParams p, long long kv_units, long long keys, int num
 
 cudaError_t launch_window_attention_f32(AttnParams p, int num_sms, cudaStream_t s) {
   const int span = p.window - 1 < p.cap ? p.window - 1 : p.cap;
-  return launch_f32<false>(p, (long long)p.B * p.Hkv, span, num_sms, s);
+  return launch_f32<kWindowKeys>(p, (long long)p.B * p.Hkv, span, num_sms, s);
+}
+
+cudaError_t launch_shared_attention_f32(AttnParams p, const ListArgs &l, int num_sms, cudaStream_t s) {
+  p.group_start = l.group_start;
+  p.shared_len = l.shared_len;
+  p.groups = l.groups;
+  return launch_f32<kSharedKeys>(p, (long long)p.B * p.Hkv, p.cap, num_sms, s);
 }
 
 cudaError_t launch_sparse_attention_f32(AttnParams p, const ListArgs &l, int num_sms, cudaStream_t s) {
@@ -405,7 +418,7 @@ cudaError_t launch_sparse_attention_f32(AttnParams p, const ListArgs &l, int num
   p.sets = l.sets;
   p.set_nodes = p.N / l.sets;
   p.M = p.set_nodes * p.G;
-  return launch_f32<true>(p, (long long)p.B * l.sets * p.Hkv, (long long)l.list_len * l.page_size, num_sms, s);
+  return launch_f32<kListedKeys>(p, (long long)p.B * l.sets * p.Hkv, (long long)l.list_len * l.page_size, num_sms, s);
 }
 
 }  // namespace sv
