@@ -646,13 +646,15 @@ const char *sv_version(void);
  * all threads); the difference around a region counts the region's launches. */
 uint64_t sv_kernel_launches(void);
 
-/* The time after which a wait for progress inside the tensor-core attention kernel gives
- * up (a copy, an MMA, or another CTA's piece of a split unit that does not arrive): the
- * kernel then lets its copies and MMAs in flight land, frees its tensor memory, sets
+/* The time after which a wait for progress inside a bf16 attention kernel (sv_tree_attention,
+ * sv_window_attention, sv_shared_attention, sv_sparse_attention) or the tensor-core kernel of
+ * sv_page_scores gives up (a copy, an MMA, or another CTA's piece of a split unit that does not
+ * arrive): the kernel then lets its copies and MMAs in flight land, frees its tensor memory, sets
  * SV_DEV_TIMEOUT and returns; the workspace stays usable for the next call.  Default 2 s;
- * 0 restores it.  Process-wide, read at each sv_tree_attention call.  A limit shorter
- * than the kernel's normal waits makes the calls fail with SV_DEV_TIMEOUT: it exists to
- * exercise that path. */
+ * 0 restores it.  Process-wide, read at each of these calls; the other kernels' waits (sv_lm_head,
+ * the acceptances) keep 2 s.  A wait is tried once, for a time of the hardware's choice, before
+ * the limit counts.  A limit shorter than the kernel's normal waits makes the calls fail with
+ * SV_DEV_TIMEOUT: it exists to exercise that path. */
 void sv_set_wait_limit_ns(uint64_t ns);
 uint64_t sv_get_wait_limit_ns(void);
 

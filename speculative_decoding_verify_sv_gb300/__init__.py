@@ -699,7 +699,7 @@ def sv_accept_typical(target_logits, parent, node_tokens, temperature=1.0, epsil
 
 
 def sv_set_wait_limit_ns(ns: int) -> None:
-    """Limit of the tensor-core attention kernel's waits for progress (0: the default 2 s)."""
+    """Limit of the waits for progress in the bf16 attentions and the page scores (0: the default 2 s)."""
     load_library().sv_set_wait_limit_ns(int(ns))
 
 

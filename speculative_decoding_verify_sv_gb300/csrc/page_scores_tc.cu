@@ -51,12 +51,14 @@ struct ScoreLayout {
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ bool score_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+// Wait for the phase of the given parity; false if it ran past the limit (then *abort is raised) or *abort was
+// raised.
+__device__ __forceinline__ bool score_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned long long limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*abort) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
+    if (global_ns() - t0 > limit) {
       *abort = 1;
       return false;
     }
@@ -114,6 +116,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + Lay::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(s_tmem + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const unsigned long long limit = p.wait_ns;
   const bool layout_ok = (smem_u32(sm) & 1023u) == 0;
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
           // (what is asked for lands before the products with the buffer's last rows are awaited)
           cp_async_wait<0>();
           land(k);
-          ok = ok && score_wait(&q_empty[qb], q_par, abort_flag);
+          ok = ok && score_wait(&q_empty[qb], q_par, abort_flag, limit);
         }
         constexpr int PER = D / 8, AT_ONCE = 8;
         const int d = me % PER;
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
           asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
           for (int part = group; part < 2 * KB; part += 2) {
             const int at_k = 2 * k + group, st = at_k % ST;
-            ok = ok && (at_k < ST || score_wait(&empty[st], (at_k / ST - 1) & 1, abort_flag));
+            ok = ok && (at_k < ST || score_wait(&empty[st], (at_k / ST - 1) & 1, abort_flag, limit));
             if (!ok) break;
             // 16-byte piece c of each 16th page
             uint8_t *dst = ring + st * Lay::STAGE;
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
   } else if (warp == 12) {
     // ------------------------------------------------------------------- issue
     auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-    auto arrived = [&](uint64_t *bar, int parity) -> bool { return __all_sync(0xFFFFFFFFu, score_wait(bar, parity, abort_flag)); };
+    auto arrived = [&](uint64_t *bar, int parity) -> bool { return __all_sync(0xFFFFFFFFu, score_wait(bar, parity, abort_flag, limit)); };
     auto commit = [&](uint64_t *bar) {
       if (elect_one()) umma_commit(bar);
       __syncwarp();
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) page_scores_tc_kernel(const 
         const int n = min(COLS, cols - c0), n16 = (n + 15) & ~15;
         for (int t = run.t0; t < t1; ++t, ++tile) {
           const int buf = tile & 1, page = t * kTile + tid;
-          if (!__all_sync(0xFFFFFFFFu, score_wait(&d_full[buf], (tile / 2) & 1, abort_flag))) {
+          if (!__all_sync(0xFFFFFFFFu, score_wait(&d_full[buf], (tile / 2) & 1, abort_flag, limit))) {
             ok = false;
             break;
           }

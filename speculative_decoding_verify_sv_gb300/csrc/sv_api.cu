@@ -635,6 +635,7 @@ sv_status sv_page_scores(sv_dtype dt, int B, int N, int Hq, int Hkv, int D, cons
   p.sets = sets;
   p.set_nodes = N / sets;
   p.units = B * Hkv;
+  p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   const cudaError_t e = take_injected_failure() ? cudaErrorLaunchFailure
                         : dt == SV_BF16 && sv::page_scores_prefer_tc(p, num_sms())
                             ? sv::launch_page_scores_tc(D, p, num_sms(), static_cast<cudaStream_t>(stream))

@@ -324,6 +324,7 @@ struct ScoreParams {
   int N, Hq, Hkv, G, P, page_size, num_blocks, sets, set_nodes;
   int units;                          // sequences x KV heads
   int set_cols, splits;               // (set at the launch)
+  unsigned long long wait_ns;         // limit of the tensor-core kernel's waits for progress
 };
 cudaError_t launch_page_scores_tc(int D, ScoreParams p, int num_sms, cudaStream_t s);  // bf16
 bool page_scores_prefer_tc(const ScoreParams &p, int num_sms);
