@@ -53,8 +53,10 @@ class VerifyStep:
     shared: (group_start, shared_len), int32 tensors on the device that say which sequences share a
     prefix (sv_shared_attention); their values may change from step to step.
     sparse: the attention looks at selected pages only (sv_sparse_attention).  The step keeps the
-    pages' bounds: ``reset_bounds`` makes them from the cache (after prompts were written into it),
-    and each commit brings them up to date.
+    pages' bounds: the first attention makes them from the cache, unless ``reset_bounds`` has, and each
+    commit brings them up to date.  Call ``reset_bounds`` whenever something else has written the cache
+    (another request's prompt), and before the first attention is captured into a graph, which would make
+    all of them at each replay.
     At most one of window, shared and sparse.
     """
 
@@ -123,20 +125,29 @@ class VerifyStep:
         self.scores = torch.empty((self.B, sets, self.Hkv, pages), dtype=torch.float32, device=self.device)
         self.pages = torch.empty((self.B, sets, self.Hkv, s.count), dtype=torch.int32, device=self.device)
         self._committed = torch.zeros(self.B, dtype=torch.int32, device=self.device)
+        self._bounds_made = False
         return sv_sparse_attention_workspace_size(self.dtype, self.B, self.N, self.Hq, self.Hkv, self.D, page,
                                                   s.count, sets)
 
-    def reset_bounds(self, stream=None):
-        """The bounds of all pages of the prefixes, from the cache (a step with ``sparse``)."""
-        sv_page_bounds(self.cache, self.bounds, stream=stream)
+    def reset_bounds(self, stream=None, start=None):
+        """The bounds of the prefixes' pages, from the cache (a step with ``sparse``): of all of them, or of
+        those with positions from ``start`` on (CUDA int32 [B]; 0 for a sequence that was replaced, its
+        prefix length for one that was not)."""
+        if self.sparse is None:
+            raise ValueError("a step without sparse keeps no bounds")
+        sv_page_bounds(self.cache, self.bounds, start=start, stream=stream)
+        with torch.cuda.stream(self._torch_stream(stream)):
+            if start is None and not torch.cuda.is_current_stream_capturing():  # (a capture makes nothing yet)
+                self._bounds_made = True
+
+    def _torch_stream(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.device)
+        return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), self.device)
 
     def _before_commit(self, stream):
         if self.sparse is not None:
-            if stream is None:
-                stream = torch.cuda.current_stream(self.device)
-            elif not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), self.device)
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(self._torch_stream(stream)):
                 self._committed.copy_(self.cache.prefix_len)
 
     def _after_commit(self, stream):
@@ -147,7 +158,8 @@ class VerifyStep:
         """Kernels one step launches: attention (with shared prefixes, and over pages where many
         rows have one list, a second for the keys of its own; scores and selection of pages before
         it and their bounds after the commit), then the two acceptance kernels (the commit runs
-        inside the second)."""
+        inside the second).  Not counted: the bounds of all pages, made once before the first
+        attention, and a step's copy of the prefix lengths, which is no kernel of the library's."""
         if self.shared is None and self.sparse is None:
             return 1 + 2
         return (2 if self.attn_splits else 1) + (3 if self.sparse is not None else 0) + 2
@@ -158,6 +170,8 @@ class VerifyStep:
                                        out=self.out, workspace=self.attn_ws, stream=stream)
         if self.sparse is not None:
             c, s = self.cache, self.sparse
+            if not self._bounds_made:
+                self.reset_bounds(stream)
             sv_page_scores(q, self.bounds, c.prefix_len, c.block_size, block_table=c.block_table,
                            per_node=s.per_node, out=self.scores, stream=stream)
             sv_select_pages(self.scores, c.prefix_len, c.block_size, s.count, first=s.first, last=s.last,
