@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) lm_head_kernel(const __grid_const
     int i = 0;
     for (int t = blockIdx.x; t < T; t += gridDim.x, ++i) {
       const int acc = i & 1, m = t % p.mtiles, n = t / p.mtiles;
-      if (!mbar_wait(&acc_full[acc], (uint32_t)((i >> 1) & 1), abort_flag)) break;
+      if (!mbar_wait_warp(&acc_full[acc], (uint32_t)((i >> 1) & 1), abort_flag)) break;
       tc_fence_after();
       const int row = m * kBM + q * 32 + lane;
       const bool live = row < p.R;

@@ -84,6 +84,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   return mbar_wait_slow(bar, parity, abort, limit_ns);
 }
 
+// The same for a whole warp, which goes on or leaves together: lanes that part would wait for one another at the
+// next operation that takes all of them (tcgen05.ld, a vote, a warp barrier), which has no limit.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                               unsigned long long limit_ns = kWaitLimitNs) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, limit_ns));
+}
+
 // --------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, int c0, int c1,

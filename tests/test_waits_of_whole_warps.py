@@ -42,3 +42,19 @@ def test_a_wait_of_each_lane_is_found():
     assert parting(["if (!stack_wait(&full[sv], 0, abort_flag, limit)) ", "ok = ok && stack_wait(bar, 0, a, l)"], "stack_wait") != []
     assert parting(["if (copied >= ST && lane == 0) ok = stack_wait(&empty[st], 0, a, l)",
                     "return __all_sync(0xFFFFFFFFu, stack_wait(bar, 0, a, l))"], "stack_wait") == []
+
+
+def part(name, begin, end=None):
+    """The code of a file from one text to another."""
+    with open(os.path.join(svbuild.CSRC, name)) as f:
+        text = f.read()
+    assert text.count(begin) == 1, begin
+    text = text[text.index(begin):]
+    text = text[:text.index(end)] if end else text
+    return re.split(r"[;{}]", re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S))
+
+
+def test_the_lm_heads_epilogue_decides_as_a_whole():
+    code = part("lm_head.cu", "---- epilogue")
+    assert any("mbar_wait_warp(" in s for s in code)
+    assert not parting(code, "mbar_wait")
