@@ -477,6 +477,9 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
         continue;
       }
       const bool idle = wq * 32 >= rows;  // padding: the barriers only
+      // (the other rows of a tile hold another sequence's queries, or what was in shared memory before: they move no
+      // maximum of the warp's)
+      const bool real = row < rows;
       float m = kStackNone, l = 0.f;
       for (int t = pc.t0; t < pc.t1; ++t, ++tiles, ++n, r += 2) {
         if (!arrived(&s_full[x], n & 1)) {
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
             for (int i = 2; i < 32; i += 2) top[c] = fmax3(top[c], s[c][i], s[c][i + 1]);
           }
           const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
-          const bool moves = best > m + kStackRescale;
+          const bool moves = real && best > m + kStackRescale;
           if (__any_sync(0xFFFFFFFFu, moves)) {
             const float to_m = fmaxf(best, m), w = ex2_approx(m - to_m);
             m = to_m;
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
       tc_fence_after();
       if (!idle) {
         const int in = x * kRows + row;
-        if (row < rows) p.part_ml[(size_t)pc.slot * kStackRows + in] = make_float2(m, l);
+        if (real) p.part_ml[(size_t)pc.slot * kStackRows + in] = make_float2(m, l);
         // by 16 bytes of all rows, so that a warp's stores are 512 bytes side by side (row by row: 2 us more
         // per piece)
         float4 *to_o = reinterpret_cast<float4 *>(p.part_o) + (size_t)pc.slot * (D / 4) * kStackRows + in;
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(kStackThreads, 1) stacked_attn_kernel(const __
           float o[32];
           tmem_ld32(to + c, o);
           tmem_wait_ld();
-          if (row < rows) {
+          if (real) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) to_o[(size_t)((c + i) / 4) * kStackRows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
