@@ -221,6 +221,10 @@ size_t sv_window_attention_workspace_size(sv_dtype dt, int B, int N, int Hq, int
  * Device status: SV_DEV_BAD_GROUP for a group_start that does not ascend within [0, B] (nothing is
  * shared then), SV_DEV_BAD_PREFIX for a shared_len outside the cache (clamped) or beyond a member's
  * prefix_len (the outputs of that group are not meaningful).
+ * When to call it: with up to 20 rows (N * Hq / Hkv) it was the faster of the two wherever measured; for wide
+ * trees (50 rows and more) where the shared part is several times the sequences' own keys.  Long own parts of
+ * wide trees are sv_tree_attention's (26 nodes, 64:8 heads, 16 sequences with 4096 own keys behind 512 shared: 101
+ * us there, 269 here).
  * Every other argument, the layouts, the kernels' shapes and the refusals are sv_window_attention's
  * (without window and sinks); Hq / Hkv <= 128, else SV_ERR_UNSUPPORTED.  Rounding as there.  float32
  * calls, and those with little to read in all, read each sequence's own rows.

@@ -351,7 +351,7 @@ def sv_shared_attention(q, k_tree, v_tree, cache: KVCache, parent, scale, group_
     Sequences group_start[g] .. group_start[g+1] - 1 hold the same K and V at the cache positions
     [0, shared_len[g]) (the same pages, or copies), which are worked on once for all of them; positions
     from there to prefix_len are each sequence's own.  group_start [groups+1], shared_len [groups]: CUDA
-    int32 tensors."""
+    int32 tensors.  For wide trees with long parts of their own sv_tree_attention is the faster."""
     return load_binding().shared_attention(q, k_tree, v_tree, cache.k, cache.v, cache.prefix_len, cache.block_table,
                                            cache.block_size, parent, scale, group_start, shared_len, out, workspace, stream)
 

@@ -4,7 +4,7 @@
 //
 // Sequences that share a prefix have, at each of its keys, K and V in common, so that their query rows
 // (tokens x group heads) stack up to one matrix per KV head: S = Q K^T and O = P V over the prefix are
-// matrix products like a prompt's, and K and V are read once for all instead of once per sequence.
+// matrix products like a prompt's, and K and V are read once per 256 rows instead of once per sequence.
 // What differs by row (a sequence's own keys, the tree's mask) is not here: this kernel leaves each
 // row's unnormalised output, maximum and sum over the keys that it has worked on, and the kernel of
 // stacked_keys.cuh, which takes the own keys and the tree, joins them by softmax's rule
@@ -22,7 +22,8 @@
 // may be issued over P as soon as P V has been, without waiting for it.
 //
 // Bound by the CTA's chain of products and softmax: 32 sequences with 64 nodes each behind one prompt of 4099 keys,
-// 32:32 heads of 128, 95 us, 1.45 PFLOP/s, the tensor pipe about two thirds active, the unit of the exponents a third.
+// 32:32 heads of 128, 94 us, 1.45 PFLOP/s, the tensor pipe 68 % active, the unit of the exponents a third (pages of 16
+// instead of a contiguous cache: 7 % more; over lists the pipe is 51 % active, for reasons not found).
 // (With half of the MMAs left out 84.5 us, with the exponents left out no change.)  What was tried: 16 softmax warps, half
 // a row each, 102 us against 96; weights of the first half against the maximum of the tile before 100.6
 // against 95.6; four stages of the ring and page ids tile by tile, 256 requests in four groups, 104 against 98; tiles

@@ -51,7 +51,8 @@ class VerifyStep:
     window: the layer's sliding window (its attention is then sv_window_attention, with the
     first ``sinks`` positions kept visible); None attends to the whole prefix.
     shared: (group_start, shared_len), int32 tensors on the device that say which sequences share a
-    prefix (sv_shared_attention); their values may change from step to step.
+    prefix (sv_shared_attention); their values may change from step to step.  (Not for wide trees whose
+    own parts are about as long as the shared one: the plain step is the faster there.)
     sparse: the attention looks at selected pages only (sv_sparse_attention).  The step keeps the
     pages' bounds: the first attention makes them from the cache, unless ``reset_bounds`` has, and each
     commit brings them up to date.  Call ``reset_bounds`` whenever something else has written the cache
