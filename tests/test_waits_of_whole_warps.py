@@ -7,7 +7,7 @@ import pytest
 
 from speculative_decoding_verify_sv_gb300 import build as svbuild
 
-# file -> (the wait's name, calls that it has)
+# file -> the name of its wait
 SOURCES = {"stacked_attention.cu": "stack_wait", "unit_attention.cuh": "limited_wait", "warp_units.cuh": "limited_wait"}
 
 
